@@ -1,7 +1,8 @@
 /*
  * fp8q.h -- C ABI of libfp8q: FP8 delayed-scaling quantization on one GPU.
  *
- * Nine operations, each one kernel launch on the caller's stream:
+ * Fourteen operations, each one kernel launch on the caller's stream (the last,
+ * where it sums gradients over rows, two):
  *   fp8q_quantize_amax        bf16 -> FP8 bytes, fused with amax = max|x|
  *   fp8q_multi_quantize_amax  the same over a ragged list of tensors
  *   fp8q_dequantize           FP8 bytes -> bf16
@@ -13,6 +14,13 @@
  *   fp8q_layernorm_quantize_amax  LayerNorm producer fused with quantize + amax
  *   fp8q_amax_scale_update_ring_quantize  the ring update fused with the next
  *                             step's first quantize
+ *   fp8q_fp4_quantize_amax    bf16 -> microscaled 4-bit operands (of a matrix,
+ *                             its transpose, or both), fused with amax
+ *   fp8q_fp4_dequantize       microscaled 4-bit -> bf16
+ *   fp8q_fp4_matmul           the product of two microscaled 4-bit operands
+ *   fp8q_residual_norm_quantize_amax  RMS norm after a block, gate, residual
+ *                             add, RMS norm before the next block, quantize
+ *   fp8q_residual_norm_backward  its gradients
  *
  * Sources (web pages, by title and section):
  *   "User Guide on Native XLA-FP8" (NVIDIA JAX-Toolbox): opening section
@@ -60,8 +68,18 @@ extern "C" {
 
 typedef enum {
     FP8Q_E4M3FN = 0, /* 1-4-3, bias 7, no inf, max 448 (forward pass) */
-    FP8Q_E5M2 = 1    /* 1-5-2, bias 15, IEEE inf/NaN, max 57344 (gradients) */
+    FP8Q_E5M2 = 1,   /* 1-5-2, bias 15, IEEE inf/NaN, max 57344 (gradients) */
+    /* microscaled 4-bit formats: e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and
+     * their negatives) with a scale for each block of a row; taken by the
+     * fp8q_fp4_* and fp8q_residual_norm_* calls only */
+    FP8Q_MXFP4 = 2,  /* blocks of 32, scales are powers of two (ue8m0) */
+    FP8Q_NVFP4 = 3   /* blocks of 16, e4m3 scales, and a binary32 tensor scale */
 } fp8q_format;
+
+typedef enum {
+    FP8Q_OUT_BF16 = 0,
+    FP8Q_OUT_F32 = 1
+} fp8q_out_type;
 
 typedef enum {
     FP8Q_ALGO_MAX = 0,        /* amax = max over the (rolled) history window */
@@ -313,6 +331,181 @@ fp8q_status fp8q_amax_scale_update_ring_quantize(float* amax_history, const int3
                                                  fp8q_amax_algo algo, int32_t margin, const void* x_bf16,
                                                  uint8_t* q, int64_t n, int32_t slot, float* amax,
                                                  void* stream);
+
+/*
+ * Microscaled 4-bit operands.  A packed operand of an [rows, cols] matrix is
+ *   codes   rows x fp8q_fp4_row_bytes(cols) bytes: two e2m1 codes a byte (the
+ *           even column in the low four bits), each row filled up with zero
+ *           codes to a multiple of 32 columns;
+ *   scales  fp8q_fp4_scale_bytes(rows, cols, fmt) bytes: one for each block of
+ *           32 (FP8Q_MXFP4) or 16 (FP8Q_NVFP4) columns, in tiles of 128 rows x
+ *           4 blocks of 512 bytes, tiles row by row; within a tile the scale
+ *           of (row, block) lies at (row % 32) * 16 + (row % 128) / 32 * 4 +
+ *           block % 4.  A row's blocks are filled up to a multiple of 4 with
+ *           zero scales; rows that fill up the last tile are neither written
+ *           nor used.
+ * Both arrays start on 16-byte boundaries.
+ */
+int64_t fp8q_fp4_row_bytes(int64_t cols);
+int64_t fp8q_fp4_scale_bytes(int64_t rows, int64_t cols, fp8q_format fmt);
+
+/*
+ * bf16 -> microscaled 4 bits with amax, in one pass over x, which is [rows,
+ * cols], row-major.  q, sf: the packed operand of x (blocks along a row).  qt,
+ * sft: the packed operand of x's transpose, [cols, rows] (blocks down a
+ * column): what the products of a backward pass read.  Either pair may be
+ * NULL, not both.  With a = max|x| of a block:
+ *   FP8Q_MXFP4  scale 2^e, e = max(-127, floor(log2 a) - 2); an infinite a
+ *               counts as the largest finite bf16; a NaN in the block makes
+ *               its scale NaN (0xFF).  code = e2m1(x / 2^e).
+ *   FP8Q_NVFP4  with the tensor scale s: block scale sb = e4m3(RN(a / RN(6 s))),
+ *               held at 448, d = RN(sb s), code = e2m1(RN(x / d)), signed zeros
+ *               where d is 0; RN is a rounding to binary32.  A NaN in the
+ *               block, or an s whose RN(6 s) is not positive and finite, makes
+ *               sb NaN (0x7F), but a block of zeros always has scale and
+ *               codes 0.
+ * e2m1 rounds to nearest, ties to the even code, held at +-6; infinities become
+ * +-6.  *amax = max(*amax, max|x|) as for fp8q_quantize_amax.
+ * scale: one float (device), or NULL for 1; NULL for FP8Q_MXFP4.  amax / 2688
+ * (the largest element 6 times the largest block scale 448) uses the whole
+ * range.  amax: one float (device), or NULL where it is not wanted.
+ * Errors: INVALID_ARG for another fmt, rows or cols < 0, a NULL x_bf16, no
+ *         output or half a pair, a scale with FP8Q_MXFP4, or a misaligned
+ *         x_bf16, scale or amax; UNSUPPORTED for q, sf, qt or sft off a
+ *         16-byte boundary, or rows or cols above 2^31 - 128.
+ */
+fp8q_status fp8q_fp4_quantize_amax(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q, uint8_t* sf,
+                                   uint8_t* qt, uint8_t* sft, fp8q_format fmt, const float* scale, float* amax,
+                                   void* stream);
+
+/*
+ * Microscaled 4 bits -> bf16: y = bf16(RN(code * block scale * s)), y [rows,
+ * cols] row-major; the product of code and block scale is exact.  scale: one
+ * float (device), or NULL for 1; NULL for FP8Q_MXFP4.  Errors: as for
+ * fp8q_fp4_quantize_amax.
+ */
+fp8q_status fp8q_fp4_dequantize(const uint8_t* q, const uint8_t* sf, void* y_bf16, int64_t rows, int64_t cols,
+                                fp8q_format fmt, const float* scale, void* stream);
+
+/*
+ * The product of two microscaled 4-bit operands of the same format, both
+ * packed along k:
+ *   d[i][j] = RN_out( (sum_k a[i][k] b[j][k]) * RN(a_scale * b_scale) )
+ * a is [m, k], b is [n, k], d is [m, n], row-major, bf16 or binary32.  A linear
+ * layer's output is the product of its input and its weight; its input's
+ * gradient that of the output's gradient and the weight's transpose; its
+ * weight's gradient that of the output's gradient's and the input's
+ * transposes.  Products are exact; sums are held in binary32.
+ * a_scale, b_scale: the tensor scales, one float each (device), or NULL for 1;
+ * NULL for FP8Q_MXFP4.  Calls with the same arguments give the same bits.
+ * Errors: INVALID_ARG for another fmt or out, m, n or k < 0, k == 0 with m and
+ *         n > 0, a NULL operand or d, a scale with FP8Q_MXFP4, or a misaligned
+ *         d or scale; UNSUPPORTED for an operand off a 16-byte boundary or
+ *         m, n or k above 2^31 - 128.  m == 0 or n == 0 launches nothing.
+ */
+fp8q_status fp8q_fp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, void* d,
+                            int64_t m, int64_t n, int64_t k, fp8q_format fmt, fp8q_out_type out,
+                            const float* a_scale, const float* b_scale, void* stream);
+
+/*
+ * The RMS norms after and before a transformer block, fused with the block's
+ * gate, the residual scale and the quantization of the next block's input.
+ * Row by row, in binary32:
+ *   y  = b / sqrt(mean(b^2) + eps) * post_weight     (y = b without post_weight)
+ *   r' = bf16(residual + alpha * gate * y)           (r' = residual without block)
+ *   h  = bf16(r' / sqrt(mean(r'^2) + eps) * pre_weight)    of the rounded r'
+ *   q  = the codes of h in fmt, exactly those of fp8q_quantize_amax or
+ *        fp8q_fp4_quantize_amax;  *amax = max(*amax, max|h|)
+ * A NaN, or an infinity where it is normalised, makes its row NaN.  Any part
+ * may be left out by NULL: block (then no post_weight and gate), post_weight,
+ * gate (1), residual_out (without block only), pre_weight (then no h, q and
+ * amax), h or q (one of them with pre_weight), sf (FP8 formats), scale (NULL
+ * for FP8Q_MXFP4; 1 for FP8Q_NVFP4 without), amax, rstd_post, rstd_pre.
+ */
+typedef struct {
+    int64_t rows;             /* tokens */
+    int32_t hidden;           /* a multiple of 16 from 16 to 32768 */
+    fp8q_format fmt;          /* of q */
+    const void* residual;     /* [rows, hidden] bf16 */
+    const void* block;        /* [rows, hidden] bf16: the block's output */
+    const float* post_weight; /* [hidden] */
+    const void* gate;         /* [ceil(rows / rows_per_gate), hidden] binary32 or bf16 */
+    int64_t rows_per_gate;    /* consecutive rows that share a row of gate: 1, a sequence, or all */
+    int32_t gate_is_bf16;
+    float alpha;              /* the residual scale */
+    float eps;
+    const float* pre_weight;  /* [hidden] */
+    void* residual_out;       /* [rows, hidden] bf16; may be residual */
+    void* h;                  /* [rows, hidden] bf16 */
+    uint8_t* q;               /* FP8: [rows, hidden] bytes; 4 bits: a packed operand's codes */
+    uint8_t* sf;              /* 4 bits: its scales */
+    const float* scale;       /* one float */
+    float* amax;              /* one float, max-accumulated */
+    float* rstd_post;         /* [rows]: 1 / sqrt(mean(b^2) + eps), for the backward pass */
+    float* rstd_pre;          /* [rows]: 1 / sqrt(mean(r'^2) + eps) */
+} fp8q_residual_norm;
+
+/*
+ * Errors: INVALID_ARG for a NULL args, another fmt, rows < 0, hidden < 16 or
+ *         not a multiple of 16, rows_per_gate < 1 with gate, parts missing or
+ *         left over as listed above, or a misaligned scale, amax or rstd;
+ *         UNSUPPORTED for hidden > 32768, rows above 2^31 - 128 or another
+ *         pointer off a 16-byte boundary.  rows == 0 launches nothing.
+ */
+fp8q_status fp8q_residual_norm_quantize_amax(const fp8q_residual_norm* args, void* stream);
+
+/*
+ * Gradients of the call above (the quantization counts as the identity).  With
+ * n1 = block * rstd_post (block without post_weight), n2 = r' * rstd_pre,
+ * dn = d_h * pre_weight:
+ *   D             = d_residual_out + rstd_pre (dn - n2 mean(dn n2))
+ *   d_residual    = bf16(D)                      (d_residual_out's and d_h's share)
+ *   e             = alpha * gate * D
+ *   d_block       = bf16(rstd_post (e post_weight - n1 mean(e post_weight n1)))
+ *                                                (bf16(e) without post_weight)
+ *   d_pre_weight  = sum over rows of d_h n2
+ *   d_post_weight = sum over rows of e n1
+ *   d_gate        = sum over the rows of a gate's row of alpha D n1 post_weight
+ * D is not rounded on the way to the others.  Sums are taken in binary32 in a
+ * fixed order: the same arguments give the same bits.
+ */
+typedef struct {
+    int64_t rows;
+    int32_t hidden;
+    int32_t gate_is_bf16;
+    const void* d_residual_out; /* [rows, hidden] bf16, or NULL for zeros */
+    const void* d_h;            /* [rows, hidden] bf16, or NULL without pre_weight */
+    const void* residual_out;   /* r', [rows, hidden] bf16 (with d_h) */
+    const float* rstd_pre;      /* [rows] (with d_h) */
+    const float* pre_weight;    /* [hidden] (with d_h) */
+    const void* block;          /* [rows, hidden] bf16, or NULL */
+    const float* rstd_post;     /* [rows] (with post_weight) */
+    const float* post_weight;   /* [hidden], or NULL */
+    const void* gate;           /* as in the forward call, or NULL */
+    int64_t rows_per_gate;
+    float alpha;
+    void* d_residual;           /* [rows, hidden] bf16, or NULL */
+    void* d_block;              /* [rows, hidden] bf16, or NULL */
+    float* d_pre_weight;        /* [hidden], or NULL */
+    float* d_post_weight;       /* [hidden], or NULL */
+    void* d_gate;               /* gate's shape and type, or NULL */
+    void* workspace;            /* fp8q_residual_norm_backward_workspace bytes */
+    int64_t workspace_bytes;
+} fp8q_residual_norm_grad;
+
+/* Bytes of workspace (16-byte aligned, contents irrelevant) for the gradients
+ * of weights and of a gate that rows share; one call at a time may use it.
+ * rows_per_gate: 0 without gate. */
+int64_t fp8q_residual_norm_backward_workspace(int64_t rows, int32_t hidden, int64_t rows_per_gate);
+
+/*
+ * Errors: INVALID_ARG for a NULL args, rows < 0, hidden < 16 or not a multiple
+ *         of 16, neither gradient given, parts missing or left over, too small
+ *         a workspace, or a misaligned rstd; UNSUPPORTED for hidden > 32768,
+ *         rows above 2^31 - 128 or another pointer off a 16-byte boundary.
+ *         rows == 0 launches nothing (and writes no sums).
+ */
+fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* args, void* stream);
 
 /* Static, human-readable name of a status. */
 const char* fp8q_status_string(fp8q_status status);

@@ -1,0 +1,271 @@
+// fp4_quantize.cu -- bf16 -> microscaled 4-bit operands, of a matrix and of its
+// transpose in one pass, and back.
+//
+// Both kernels stream HBM.  A CTA takes a tile of 128 rows x 128 columns: 128
+// rows are what a scale tile spans, so a CTA writes whole scale tiles (512
+// contiguous bytes) and, for the transpose, 64 contiguous bytes of each of its
+// 128 code rows.  A thread quantizes 16 columns of a row from registers; the
+// transpose reads the same tile back from shared memory by pairs of columns.
+
+#include "fp4.cuh"
+
+namespace {
+
+constexpr int kTile = 128;  // rows and columns of a CTA's tile
+
+struct Fp4QuantArgs {
+    const uint16_t* x;
+    uint8_t *q, *sf, *qt, *sft;
+    const float* scale;
+    float* amax;
+    int64_t rows, cols, tile_cols;
+    int vec;  // rows start on 32-byte boundaries and hold whole 16-column chunks
+};
+
+// The 512-byte scale tiles gathered in `s` go out by 32-bit words (four blocks
+// of one row); words of rows at or past `rows` and tiles past the last are not
+// written.
+template <int FMT>
+__device__ __forceinline__ void store_sf(uint8_t* sf, const uint32_t* s, int64_t r0, int64_t rows, int64_t c0,
+                                         int64_t cols) {
+    constexpr int kTiles = kTile / Fp4<FMT>::kSfCols;
+    const int64_t across = fp4_sf_tiles<FMT>(cols), t0 = c0 / Fp4<FMT>::kSfCols;
+    const int i = threadIdx.x & 127, t = threadIdx.x >> 7;
+    if (t < kTiles && t0 + t < across && r0 + (i & 3) * 32 + (i >> 2) < rows)
+        reinterpret_cast<uint32_t*>(sf)[((r0 / 128) * across + t0 + t) * 128 + i] = s[t * 128 + i];
+}
+
+__device__ __forceinline__ int sf_byte(int row, int block) {
+    return (block >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4 + (block & 3);
+}
+
+template <int FMT, bool ROW, bool COL>
+__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantArgs a) {
+    constexpr int kBlock = Fp4<FMT>::kBlock;
+    __shared__ uint32_t red[kThreads / 32];
+    __shared__ __align__(16) uint32_t sfs[2 * 128];
+    __shared__ __align__(16) uint32_t xs[COL ? kTile * kTile / 2 : 4];
+    __shared__ __align__(16) uint2 qts[COL ? kTile * 9 : 1];  // 72 bytes a code row: 2-way conflicts at most
+    const int tid = threadIdx.x;
+    const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
+    const int64_t r0 = tr * kTile, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kTile;
+
+    uint32_t w[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int id = u * kThreads + tid;
+        const int64_t r = r0 + (id >> 3), c = c0 + (id & 7) * 16;
+        const uint16_t* p = a.x + r * a.cols + c;
+        if (a.vec) {
+            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+            if (r < a.rows && c < a.cols) ld_stream_v8(p, lo, hi);
+            w[u][0] = lo.x; w[u][1] = lo.y; w[u][2] = lo.z; w[u][3] = lo.w;
+            w[u][4] = hi.x; w[u][5] = hi.y; w[u][6] = hi.z; w[u][7] = hi.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t v = 0;
+                if (r < a.rows && c + 2 * i < a.cols) v = p[2 * i];
+                if (r < a.rows && c + 2 * i + 1 < a.cols) v |= (uint32_t)p[2 * i + 1] << 16;
+                w[u][i] = v;
+            }
+        }
+    }
+    const Fp4Scale sc = make_fp4_scale(a.scale);
+
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int id = u * kThreads + tid, row = id >> 3, ck = id & 7;
+        const uint32_t m = absmax16(w[u]);
+        m2 = bf16x2_absmax(m2, m);
+        if (ROW) {
+            uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
+            if (FMT == FP8Q_MXFP4) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+            const BlockScale b = block_scale<FMT>(am, sc);
+            const uint2 o = block_codes<FMT>(w[u], b);
+            const int64_t c = c0 + ck * 16;
+            if (r0 + row < a.rows && c < 2 * fp4_row_bytes(a.cols))
+                *reinterpret_cast<uint2*>(a.q + (r0 + row) * fp4_row_bytes(a.cols) + c / 2) = o;
+            if (FMT == FP8Q_NVFP4 || (ck & 1) == 0)
+                reinterpret_cast<uint8_t*>(sfs)[sf_byte(row, ck * 16 / kBlock)] = (uint8_t)b.code;
+        }
+        if (COL) {
+            uint4* d = reinterpret_cast<uint4*>(xs + row * (kTile / 2) + ck * 8);
+            d[0] = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
+            d[1] = make_uint4(w[u][4], w[u][5], w[u][6], w[u][7]);
+        }
+    }
+    __syncthreads();
+    if (ROW) store_sf<FMT>(a.sf, sfs, r0, a.rows, c0, a.cols);
+    if (COL) {
+        if (ROW) __syncthreads();  // sfs is used again
+        constexpr int kHalves = kBlock / 16, kUnits = kTile / kBlock;  // blocks down a column
+#pragma unroll 1
+        for (int id = tid; id < kUnits * (kTile / 2); id += kThreads) {
+            const int p = id & 63, rb = id >> 6;  // column pair, block of rows
+            uint32_t lo[kHalves][8], hi[kHalves][8];
+            uint32_t m = 0;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t v0 = xs[(rb * kBlock + h * 16 + 2 * i) * (kTile / 2) + p];
+                    const uint32_t v1 = xs[(rb * kBlock + h * 16 + 2 * i + 1) * (kTile / 2) + p];
+                    m = bf16x2_absmax(m, bf16x2_absmax(v0, v1));
+                    lo[h][i] = __byte_perm(v0, v1, 0x5410);
+                    hi[h][i] = __byte_perm(v0, v1, 0x7632);
+                }
+            const BlockScale bl = block_scale<FMT>(m & 0x7FFFu, sc), bh = block_scale<FMT>((m >> 16) & 0x7FFFu, sc);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                qts[(2 * p) * 9 + rb * kHalves + h] = block_codes<FMT>(lo[h], bl);
+                qts[(2 * p + 1) * 9 + rb * kHalves + h] = block_codes<FMT>(hi[h], bh);
+            }
+            reinterpret_cast<uint8_t*>(sfs)[sf_byte(2 * p, rb)] = (uint8_t)bl.code;
+            reinterpret_cast<uint8_t*>(sfs)[sf_byte(2 * p + 1, rb)] = (uint8_t)bh.code;
+        }
+        __syncthreads();
+        store_sf<FMT>(a.sft, sfs, c0, a.cols, r0, a.rows);
+        const int64_t ldt = fp4_row_bytes(a.rows);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int id = u * kThreads + tid, col = id >> 3, k = id & 7;
+            if (c0 + col < a.cols && r0 / 2 + k * 8 < ldt)
+                *reinterpret_cast<uint2*>(a.qt + (c0 + col) * ldt + r0 / 2 + k * 8) = qts[col * 9 + k];
+        }
+    }
+    if (a.amax) flush_amax(m2, 0u, a.amax, red);
+}
+
+struct Fp4DequantArgs {
+    const uint8_t *q, *sf;
+    uint16_t* y;
+    const float* scale;
+    int64_t rows, cols, tile_cols;
+    int vec;
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4DequantArgs a) {
+    constexpr int kBlock = Fp4<FMT>::kBlock, kTiles = kTile / Fp4<FMT>::kSfCols;
+    __shared__ __align__(16) uint32_t sfs[2 * 128];
+    const int tid = threadIdx.x;
+    const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
+    const int64_t r0 = tr * kTile, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kTile;
+    const int64_t ld = fp4_row_bytes(a.cols), across = fp4_sf_tiles<FMT>(a.cols), t0 = c0 / Fp4<FMT>::kSfCols;
+    uint2 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int id = u * kThreads + tid;
+        const int64_t r = r0 + (id >> 3), c = c0 + (id & 7) * 16;
+        w[u] = make_uint2(0, 0);
+        if (r < a.rows && c < a.cols) w[u] = ld_stream_v2(a.q + r * ld + c / 2);
+    }
+    {
+        const int i = tid & 127, t = tid >> 7;
+        if (t < kTiles && t0 + t < across && r0 + (i & 3) * 32 + (i >> 2) < a.rows)
+            sfs[t * 128 + i] = reinterpret_cast<const uint32_t*>(a.sf)[(tr * across + t0 + t) * 128 + i];
+    }
+    const float s = a.scale ? __ldg(a.scale) : 1.0f;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int id = u * kThreads + tid, row = id >> 3, ck = id & 7;
+        const int64_t r = r0 + row, c = c0 + ck * 16;
+        if (r >= a.rows || c >= a.cols) continue;
+        const float b = sf_value<FMT>(reinterpret_cast<const uint8_t*>(sfs)[sf_byte(row, ck * 16 / kBlock)]);
+        uint32_t h[8], o[8];
+        e2m1x8_to_f16(w[u].x, *reinterpret_cast<uint32_t(*)[4]>(h));
+        e2m1x8_to_f16(w[u].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = cvt_bf16x2(__fmul_rn(__fmul_rn(f16_lo(h[i]), b), s), __fmul_rn(__fmul_rn(f16_hi(h[i]), b), s));
+        uint16_t* y = a.y + r * a.cols + c;
+        if (a.vec) {
+            st_v4(y, make_uint4(o[0], o[1], o[2], o[3]));
+            st_v4(y + 8, make_uint4(o[4], o[5], o[6], o[7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < a.cols) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
+template <int FMT>
+fp8q_status launch_quantize(const Fp4QuantArgs& a, unsigned grid, cudaStream_t s) {
+    auto kern = a.q ? (a.qt ? fp4_quantize_kernel<FMT, true, true> : fp4_quantize_kernel<FMT, true, false>)
+                    : fp4_quantize_kernel<FMT, false, true>;
+    return launch_kernel(kern, dim3(grid), dim3(kThreads), 0, s, "fp4_quantize_kernel", a);
+}
+
+// Tiles of an [rows, cols] matrix; 0 where there are more than a grid holds.
+unsigned tile_grid(int64_t rows, int64_t cols) {
+    const int64_t tr = (rows + kTile - 1) / kTile, tc = (cols + kTile - 1) / kTile;
+    return tr <= 0x7FFFFFFF / tc ? (unsigned)(tr * tc) : 0u;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8q_fp4_row_bytes(int64_t cols) { return cols > 0 ? fp4_row_bytes(cols) : 0; }
+
+int64_t fp8q_fp4_scale_bytes(int64_t rows, int64_t cols, fp8q_format fmt) {
+    if (rows <= 0 || cols <= 0 || !valid_fp4(fmt)) return 0;
+    return (rows + 127) / 128 * (fmt == FP8Q_MXFP4 ? fp4_sf_tiles<FP8Q_MXFP4>(cols) : fp4_sf_tiles<FP8Q_NVFP4>(cols)) * 512;
+}
+
+fp8q_status fp8q_fp4_quantize_amax(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q, uint8_t* sf, uint8_t* qt,
+                                   uint8_t* sft, fp8q_format fmt, const float* scale, float* amax, void* stream) {
+    if (!valid_fp4(fmt) || rows < 0 || cols < 0) return FP8Q_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return FP8Q_OK;
+    if (rows > kFp4MaxDim || cols > kFp4MaxDim) return FP8Q_ERR_UNSUPPORTED;
+    if (!x_bf16 || (!q != !sf) || (!qt != !sft) || (!q && !qt)) return FP8Q_ERR_INVALID_ARG;
+    if (fmt == FP8Q_MXFP4 && scale) return FP8Q_ERR_INVALID_ARG;
+    if (((uintptr_t)x_bf16 & 1u) || ((uintptr_t)scale & 3u) || ((uintptr_t)amax & 3u)) return FP8Q_ERR_INVALID_ARG;
+    if (((uintptr_t)q | (uintptr_t)sf | (uintptr_t)qt | (uintptr_t)sft) & 15u) return FP8Q_ERR_UNSUPPORTED;
+    const unsigned grid = tile_grid(rows, cols);
+    if (!grid) return FP8Q_ERR_UNSUPPORTED;
+    Fp4QuantArgs a;
+    a.x = static_cast<const uint16_t*>(x_bf16);
+    a.q = q;
+    a.sf = sf;
+    a.qt = qt;
+    a.sft = sft;
+    a.scale = scale;
+    a.amax = amax;
+    a.rows = rows;
+    a.cols = cols;
+    a.tile_cols = (cols + kTile - 1) / kTile;
+    a.vec = cols % 16 == 0 && ((uintptr_t)x_bf16 & 31u) == 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return fmt == FP8Q_MXFP4 ? launch_quantize<FP8Q_MXFP4>(a, grid, s) : launch_quantize<FP8Q_NVFP4>(a, grid, s);
+}
+
+fp8q_status fp8q_fp4_dequantize(const uint8_t* q, const uint8_t* sf, void* y_bf16, int64_t rows, int64_t cols,
+                                fp8q_format fmt, const float* scale, void* stream) {
+    if (!valid_fp4(fmt) || rows < 0 || cols < 0) return FP8Q_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return FP8Q_OK;
+    if (rows > kFp4MaxDim || cols > kFp4MaxDim) return FP8Q_ERR_UNSUPPORTED;
+    if (!q || !sf || !y_bf16 || (fmt == FP8Q_MXFP4 && scale)) return FP8Q_ERR_INVALID_ARG;
+    if (((uintptr_t)y_bf16 & 1u) || ((uintptr_t)scale & 3u)) return FP8Q_ERR_INVALID_ARG;
+    if (((uintptr_t)q | (uintptr_t)sf) & 15u) return FP8Q_ERR_UNSUPPORTED;
+    const unsigned grid = tile_grid(rows, cols);
+    if (!grid) return FP8Q_ERR_UNSUPPORTED;
+    Fp4DequantArgs a;
+    a.q = q;
+    a.sf = sf;
+    a.y = static_cast<uint16_t*>(y_bf16);
+    a.scale = scale;
+    a.rows = rows;
+    a.cols = cols;
+    a.tile_cols = (cols + kTile - 1) / kTile;
+    a.vec = cols % 16 == 0 && ((uintptr_t)y_bf16 & 15u) == 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto kern = fmt == FP8Q_MXFP4 ? fp4_dequantize_kernel<FP8Q_MXFP4> : fp4_dequantize_kernel<FP8Q_NVFP4>;
+    return launch_kernel(kern, dim3(grid), dim3(kThreads), 0, s, "fp4_dequantize_kernel", a);
+}
+
+}  // extern "C"

@@ -13,6 +13,8 @@ import os
 
 E4M3FN = 0
 E5M2 = 1
+MXFP4 = 2
+NVFP4 = 3
 ALGO_MAX = 0
 ALGO_MOST_RECENT = 1
 MAX_TENSORS = 512
@@ -24,8 +26,9 @@ STATUS = {0: "FP8Q_OK", 1: "FP8Q_ERR_INVALID_ARG", 2: "FP8Q_ERR_UNSUPPORTED", 3:
 EXPORTS = ("fp8q_quantize_amax", "fp8q_multi_quantize_amax", "fp8q_dequantize",
            "fp8q_amax_scale_update", "fp8q_qdq_amax", "fp8q_amax_scale_update_ring",
            "fp8q_gelu_quantize_amax", "fp8q_layernorm_quantize_amax",
-           "fp8q_amax_scale_update_ring_quantize", "fp8q_status_string",
-           "fp8q_last_cuda_error")
+           "fp8q_amax_scale_update_ring_quantize", "fp8q_fp4_quantize_amax", "fp8q_fp4_dequantize",
+           "fp8q_fp4_matmul", "fp8q_residual_norm_quantize_amax", "fp8q_residual_norm_backward",
+           "fp8q_status_string", "fp8q_last_cuda_error")
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8q.so")
 
@@ -43,6 +46,27 @@ class Tensor(ctypes.Structure):
     """fp8q_tensor: one entry of a ragged list."""
     _fields_ = [("x_bf16", ctypes.c_void_p), ("q", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("scale", ctypes.c_void_p), ("amax", ctypes.c_void_p)]
+
+
+class ResidualNorm(ctypes.Structure):
+    """fp8q_residual_norm: the arguments of fp8q_residual_norm_quantize_amax."""
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int32), ("fmt", ctypes.c_int), ("residual", ctypes.c_void_p),
+                ("block", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("rows_per_gate", ctypes.c_int64), ("gate_is_bf16", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("pre_weight", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("q", ctypes.c_void_p), ("sf", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("amax", ctypes.c_void_p), ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p)]
+
+
+class ResidualNormGrad(ctypes.Structure):
+    """fp8q_residual_norm_grad: the arguments of fp8q_residual_norm_backward."""
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int32), ("gate_is_bf16", ctypes.c_int32),
+                ("d_residual_out", ctypes.c_void_p), ("d_h", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+                ("rstd_pre", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p), ("block", ctypes.c_void_p),
+                ("rstd_post", ctypes.c_void_p), ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("rows_per_gate", ctypes.c_int64), ("alpha", ctypes.c_float), ("d_residual", ctypes.c_void_p),
+                ("d_block", ctypes.c_void_p), ("d_pre_weight", ctypes.c_void_p), ("d_post_weight", ctypes.c_void_p),
+                ("d_gate", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -69,10 +93,18 @@ def lib() -> ctypes.CDLL:
                                                    vp, vp, vp]
         L.fp8q_amax_scale_update_ring_quantize.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, vp, c_int, c_int,
                                                            i32, vp, vp, i64, i32, vp, vp]
+        L.fp8q_fp4_quantize_amax.argtypes = [vp, i64, i64, vp, vp, vp, vp, c_int, vp, vp, vp]
+        L.fp8q_fp4_dequantize.argtypes = [vp, vp, vp, i64, i64, c_int, vp, vp]
+        L.fp8q_fp4_matmul.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, c_int, c_int, vp, vp, vp]
+        L.fp8q_residual_norm_quantize_amax.argtypes = [vp, vp]
+        L.fp8q_residual_norm_backward.argtypes = [vp, vp]
+        L.fp8q_residual_norm_backward_workspace.argtypes = [i64, i32, i64]
+        L.fp8q_residual_norm_backward_workspace.restype = i64
         for f in ("fp8q_quantize_amax", "fp8q_multi_quantize_amax", "fp8q_dequantize",
                   "fp8q_amax_scale_update", "fp8q_qdq_amax", "fp8q_amax_scale_update_ring",
                   "fp8q_gelu_quantize_amax", "fp8q_layernorm_quantize_amax",
-                  "fp8q_amax_scale_update_ring_quantize"):
+                  "fp8q_amax_scale_update_ring_quantize", "fp8q_fp4_quantize_amax", "fp8q_fp4_dequantize",
+                  "fp8q_fp4_matmul", "fp8q_residual_norm_quantize_amax", "fp8q_residual_norm_backward"):
             getattr(L, f).restype = c_int
         L.fp8q_status_string.argtypes = [c_int]
         L.fp8q_status_string.restype = ctypes.c_char_p
@@ -347,6 +379,208 @@ def fp8q_amax_scale_update_ring_quantize(history, head_in, head_out, amax_new, s
         _ptr(history), _ptr(head_in), _ptr(head_out), H, S, _ptr(amax_new), _ptr(scale), _ptr(scale_inv),
         _ptr(slot_format), fmt, algo, margin, _ptr(x), _ptr(q), n, slot, _ptr(amax), _stream(stream)),
         "fp8q_amax_scale_update_ring_quantize")
+
+
+_KINDS = None
+_raw_stream = None
+
+
+def _devs(*triples):
+    """_dev for (tensor, kind, name) triples, None passed over: the common case in one
+    expression a tensor, anything else gets _dev's message.  Returns the device."""
+    global _KINDS, _raw_stream
+    if _KINDS is None:
+        import torch
+        _dev(None, "bf16", "")
+        _KINDS = {"bf16": (torch.bfloat16,), "u8": _FP8_DTYPES, "f32": (torch.float32,),
+                  "gate": (torch.float32, torch.bfloat16), "current": torch.cuda.current_device}
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    cur = None
+    for t, kind, name in triples:
+        if t is None:
+            continue
+        if cur is None and t.is_cuda:
+            cur = _KINDS["current"]()
+        if t.dtype not in _KINDS[kind] or t.get_device() != cur or not t.is_contiguous():
+            if kind == "gate":
+                kind = "bf16" if t.dtype == _KINDS["bf16"][0] else "f32"
+            _dev(t, kind, name)
+    return cur
+
+
+def _on(stream, device):
+    """The stream's handle: the device's current stream where none is given."""
+    return _raw_stream(device) if stream is None else _stream(stream)
+
+
+def fp4_row_bytes(cols):
+    """Bytes of a row's codes in a packed 4-bit operand: two codes a byte, rows of whole 32-column groups."""
+    return (cols + 31) // 32 * 16
+
+
+def fp4_scale_bytes(rows, cols, fmt):
+    """Bytes of a packed 4-bit operand's block scales: tiles of 128 rows x 4 blocks."""
+    return (rows + 127) // 128 * ((cols + 127) // 128 if fmt == MXFP4 else (cols + 63) // 64) * 512
+
+
+def fp4_empty(rows, cols, fmt, device="cuda"):
+    """Room for a packed 4-bit operand of an [rows, cols] matrix: (codes [rows, row bytes], scales)."""
+    import torch
+    if fmt not in (MXFP4, NVFP4):
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    return (torch.empty((rows, fp4_row_bytes(cols)), dtype=torch.uint8, device=device),
+            torch.empty(fp4_scale_bytes(rows, cols, fmt), dtype=torch.uint8, device=device))
+
+
+def _packed(q, sf, rows, cols, fmt, name):
+    if q.numel() != rows * fp4_row_bytes(cols) or sf is None or sf.numel() != fp4_scale_bytes(rows, cols, fmt):
+        raise ValueError(f"{name} is not a packed operand of [{rows}, {cols}]: see fp4_empty")
+
+
+def _one(t, name):
+    if t is not None and t.numel() != 1:
+        raise ValueError(f"{name} must have one element")
+
+
+def fp8q_fp4_quantize_amax(x, q, sf, fmt, scale=None, amax=None, qt=None, sft=None, stream=None):
+    """The packed 4-bit operand (q, sf) of x [rows, cols], and (qt, sft) of its transpose, either
+    pair None, with amax = max(amax, max|x|), in one launch.  scale (NVFP4): the tensor scale, None for 1."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    dev = _devs((x, "bf16", "x"), (q, "u8", "q"), (sf, "u8", "sf"), (qt, "u8", "qt"), (sft, "u8", "sft"),
+                (scale, "f32", "scale"), (amax, "f32", "amax"))
+    if q is not None:
+        _packed(q, sf, rows, cols, fmt, "(q, sf)")
+    if qt is not None:
+        _packed(qt, sft, cols, rows, fmt, "(qt, sft)")
+    _one(scale, "scale")
+    _one(amax, "amax")
+    st = lib().fp8q_fp4_quantize_amax(x.data_ptr(), rows, cols, _ptr(q), _ptr(sf), _ptr(qt), _ptr(sft), fmt, _ptr(scale),
+                                      _ptr(amax), _on(stream, dev))
+    if st:
+        _check(st, "fp8q_fp4_quantize_amax")
+
+
+def fp8q_fp4_dequantize(q, sf, y, fmt, scale=None, stream=None):
+    """y [rows, cols] = bf16 of what the packed 4-bit operand (q, sf) stands for."""
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, cols]")
+    rows, cols = y.shape
+    dev = _devs((q, "u8", "q"), (sf, "u8", "sf"), (y, "bf16", "y"), (scale, "f32", "scale"))
+    _packed(q, sf, rows, cols, fmt, "(q, sf)")
+    _one(scale, "scale")
+    st = lib().fp8q_fp4_dequantize(q.data_ptr(), sf.data_ptr(), y.data_ptr(), rows, cols, fmt, _ptr(scale), _on(stream, dev))
+    if st:
+        _check(st, "fp8q_fp4_dequantize")
+
+
+def fp8q_fp4_matmul(a, a_sf, b, b_sf, d, k, fmt, a_scale=None, b_scale=None, stream=None):
+    """d [m, n] (bf16 or float32) = A [m, k] times the transpose of B [n, k], both packed 4-bit operands."""
+    if d.dim() != 2:
+        raise ValueError("d must be [m, n]")
+    m, n = d.shape
+    dev = _devs((a, "u8", "a"), (a_sf, "u8", "a_sf"), (b, "u8", "b"), (b_sf, "u8", "b_sf"), (d, "gate", "d"),
+                (a_scale, "f32", "a_scale"), (b_scale, "f32", "b_scale"))
+    _packed(a, a_sf, m, k, fmt, "(a, a_sf)")
+    _packed(b, b_sf, n, k, fmt, "(b, b_sf)")
+    _one(a_scale, "a_scale")
+    _one(b_scale, "b_scale")
+    st = lib().fp8q_fp4_matmul(a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), d.data_ptr(), m, n, k, fmt,
+                               d.element_size() == 4, _ptr(a_scale), _ptr(b_scale), _on(stream, dev))
+    if st:
+        _check(st, "fp8q_fp4_matmul")
+
+
+def _gate_rows(gate, rows, hidden, rows_per_gate):
+    if rows_per_gate < 1:
+        raise ValueError("rows_per_gate must be at least 1")
+    groups = (rows + rows_per_gate - 1) // rows_per_gate
+    if gate.numel() != groups * hidden:
+        raise ValueError(f"gate must be [{groups}, {hidden}]")
+
+
+def _sizes(n, what, *pairs):
+    for t, name in pairs:
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} must have {what}={n} elements")
+
+
+def fp8q_residual_norm_quantize_amax(residual, residual_out, block=None, post_weight=None, gate=None, rows_per_gate=0,
+                                     alpha=1.0, pre_weight=None, h=None, q=None, sf=None, fmt=E4M3FN, scale=None,
+                                     amax=None, rstd_post=None, rstd_pre=None, eps=1e-6, stream=None):
+    """residual_out = residual + alpha * gate * RMSnorm(block) * post_weight, and of it
+    h = RMSnorm(residual_out) * pre_weight, its codes q (FP8, or 4 bits with sf) and amax, one launch.
+
+    ``residual`` is bf16 [rows, hidden]; ``gate`` is float32 or bf16 [ceil(rows / rows_per_gate), hidden].
+    Parts left None are left out (no ``post_weight``: block is added as it is); ``residual_out`` may be
+    ``residual``.  ``rstd_post`` and ``rstd_pre`` (float32 [rows]) keep what the backward pass needs.
+    """
+    if residual.dim() != 2:
+        raise ValueError("residual must be [rows, hidden]")
+    rows, hidden = residual.shape
+    dev = _devs((residual, "bf16", "residual"), (residual_out, "bf16", "residual_out"), (block, "bf16", "block"),
+                (post_weight, "f32", "post_weight"), (gate, "gate", "gate"), (pre_weight, "f32", "pre_weight"),
+                (h, "bf16", "h"), (q, "u8", "q"), (sf, "u8", "sf"), (scale, "f32", "scale"), (amax, "f32", "amax"),
+                (rstd_post, "f32", "rstd_post"), (rstd_pre, "f32", "rstd_pre"))
+    n = rows * hidden
+    _sizes(n, "rows * hidden", (residual_out, "residual_out"), (block, "block"), (h, "h"))
+    _sizes(hidden, "hidden", (post_weight, "post_weight"), (pre_weight, "pre_weight"))
+    _sizes(rows, "rows", (rstd_post, "rstd_post"), (rstd_pre, "rstd_pre"))
+    if gate is not None:
+        _gate_rows(gate, rows, hidden, rows_per_gate)
+    if q is not None:
+        if fmt in (MXFP4, NVFP4):
+            _packed(q, sf, rows, hidden, fmt, "(q, sf)")
+        else:
+            _sizes(n, "rows * hidden", (q, "q"))
+    _one(scale, "scale")
+    _one(amax, "amax")
+    args = ResidualNorm(rows, hidden, fmt, residual.data_ptr(), _ptr(block), _ptr(post_weight), _ptr(gate), rows_per_gate,
+                        gate is not None and gate.element_size() == 2, alpha, eps, _ptr(pre_weight), _ptr(residual_out),
+                        _ptr(h), _ptr(q), _ptr(sf), _ptr(scale), _ptr(amax), _ptr(rstd_post), _ptr(rstd_pre))
+    st = lib().fp8q_residual_norm_quantize_amax(ctypes.byref(args), _on(stream, dev))
+    if st:
+        _check(st, "fp8q_residual_norm_quantize_amax")
+
+
+def residual_norm_backward_workspace(rows, hidden, rows_per_gate=0):
+    """Bytes of workspace of fp8q_residual_norm_backward (rows_per_gate 0: no gate)."""
+    return lib().fp8q_residual_norm_backward_workspace(rows, hidden, rows_per_gate)
+
+
+def fp8q_residual_norm_backward(d_residual_out, d_h, residual_out, rstd_pre, pre_weight, d_residual, d_pre_weight,
+                                block=None, rstd_post=None, post_weight=None, gate=None, rows_per_gate=0, alpha=1.0,
+                                d_block=None, d_post_weight=None, d_gate=None, workspace=None, stream=None):
+    """Gradients of fp8q_residual_norm_quantize_amax.  ``d_residual_out`` and ``d_h`` (with residual_out,
+    rstd_pre and pre_weight) come from what follows, either may be None; gradients left None are not
+    computed.  ``workspace``: residual_norm_backward_workspace bytes (uint8), for one call at a time.
+    """
+    d = d_residual_out if d_residual_out is not None else d_h
+    if d is None or d.dim() != 2:
+        raise ValueError("d_residual_out or d_h must be [rows, hidden]")
+    rows, hidden = d.shape
+    dev = _devs((d_residual_out, "bf16", "d_residual_out"), (d_h, "bf16", "d_h"), (residual_out, "bf16", "residual_out"),
+                (rstd_pre, "f32", "rstd_pre"), (pre_weight, "f32", "pre_weight"), (d_residual, "bf16", "d_residual"),
+                (d_pre_weight, "f32", "d_pre_weight"), (block, "bf16", "block"), (rstd_post, "f32", "rstd_post"),
+                (post_weight, "f32", "post_weight"), (gate, "gate", "gate"), (d_block, "bf16", "d_block"),
+                (d_post_weight, "f32", "d_post_weight"), (d_gate, "gate", "d_gate"), (workspace, "u8", "workspace"))
+    _sizes(rows * hidden, "rows * hidden", (d_residual_out, "d_residual_out"), (d_h, "d_h"), (residual_out, "residual_out"),
+           (block, "block"), (d_residual, "d_residual"), (d_block, "d_block"))
+    _sizes(hidden, "hidden", (pre_weight, "pre_weight"), (post_weight, "post_weight"), (d_pre_weight, "d_pre_weight"),
+           (d_post_weight, "d_post_weight"))
+    _sizes(rows, "rows", (rstd_pre, "rstd_pre"), (rstd_post, "rstd_post"))
+    if gate is not None:
+        _gate_rows(gate, rows, hidden, rows_per_gate)
+        if d_gate is not None and (d_gate.numel() != gate.numel() or d_gate.dtype != gate.dtype):
+            raise ValueError("d_gate must have gate's shape and type")
+    args = ResidualNormGrad(rows, hidden, gate is not None and gate.element_size() == 2, _ptr(d_residual_out), _ptr(d_h),
+                            _ptr(residual_out), _ptr(rstd_pre), _ptr(pre_weight), _ptr(block), _ptr(rstd_post),
+                            _ptr(post_weight), _ptr(gate), rows_per_gate, alpha, _ptr(d_residual), _ptr(d_block),
+                            _ptr(d_pre_weight), _ptr(d_post_weight), _ptr(d_gate), _ptr(workspace), _numel(workspace))
+    st = lib().fp8q_residual_norm_backward(ctypes.byref(args), _on(stream, dev))
+    if st:
+        _check(st, "fp8q_residual_norm_backward")
 
 
 def status_string(status: int) -> str:
