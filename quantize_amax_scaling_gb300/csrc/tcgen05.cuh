@@ -1,0 +1,136 @@
+// tcgen05.cuh -- the fifth-generation tensor core's instructions that the 4-bit
+// product uses: tensor memory, block-scaled multiply-add, and the copies that
+// feed it.  Documented PTX only.
+
+#pragma once
+
+#include "fp4.cuh"
+#include "mbarrier.cuh"
+
+#include <cuda.h>
+
+namespace {
+
+// ----------------------------------------------------------------------------
+// Tensor memory
+
+// A whole warp.  The only allocation of its CTA: others on the SM may go on at once.
+template <int PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+    if (PAIR == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+
+template <int PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {  // a whole warp
+    if (PAIR == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Sixteen consecutive columns of the calling warp's 32 lanes, one lane a thread.
+// The values are there after tmem_wait().
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ----------------------------------------------------------------------------
+// Shared-memory descriptors
+
+// Rows of 128 bytes along k, 128-byte swizzle, atoms of 8 rows (1024 bytes) one
+// after another.  A step of 64 codes along k adds 32 bytes to the start.
+__device__ __forceinline__ uint64_t desc_codes(uint32_t at) {
+    return (uint64_t)((at & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// One scale tile: 32 lines of 16 bytes, no swizzle, 8 lines (128 bytes) to the next.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t at) {
+    return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+// ----------------------------------------------------------------------------
+// Instructions
+
+// A scale tile (512 bytes of shared memory) to four columns of tensor memory,
+// repeated for each of the four groups of 32 lanes.
+template <int PAIR>
+__device__ __forceinline__ void tc_copy_scales(uint32_t at, uint64_t desc) {
+    if (PAIR == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(at), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(at), "l"(desc) : "memory");
+}
+
+// Instruction descriptor: e2m1 operands along k, N columns, M rows, the scale
+// format, and which pair of the four scale bytes is used (32-blocks only).
+template <int FMT>
+__host__ __device__ constexpr uint32_t mma_desc(uint32_t m, uint32_t n, uint32_t pair) {
+    return (pair << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((FMT == FP8Q_MXFP4 ? 1u : 0u) << 23) | ((m >> 4) << 24) |
+           (pair << 29);
+}
+
+// d (+)= A B^T over 64 codes with their block scales.
+template <int FMT, int PAIR>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t add) {
+#define FP8Q_MMA(group, kind)                                                                                       \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                  \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),  \
+                 "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(add)                                           \
+                 : "memory")
+    if (FMT == FP8Q_MXFP4) {
+        if (PAIR == 2)
+            FP8Q_MMA("2", "mxf4.block_scale.scale_vec::2X");
+        else
+            FP8Q_MMA("1", "mxf4.block_scale.scale_vec::2X");
+    } else {
+        if (PAIR == 2)
+            FP8Q_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+        else
+            FP8Q_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    }
+#undef FP8Q_MMA
+}
+
+// *bar completes a phase when everything this thread has given to the tensor core is done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// ----------------------------------------------------------------------------
+// Copies
+
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void block_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+}  // namespace
