@@ -7,8 +7,8 @@
 // tensor-map copies (256 codes of k a step, 128 bytes a row, 128-byte swizzle,
 // zeros beyond the edges), block scales by plain bulk copies of whole scale
 // tiles, which already lie as tensor memory takes them; one thread issues the
-// copies, another the scale copies to tensor memory and the block-scaled
-// multiply-adds, and four warps carry the accumulators out.
+// copies, another the block-scaled multiply-adds; other warps
+// store the scales to tensor memory and carry the accumulators out.
 
 #include "tcgen05.cuh"
 
@@ -38,19 +38,14 @@ struct MmArgs {
 template <int FMT, int BN>
 struct MmGeom {
     static constexpr int kSfTiles = FMT == FP8Q_MXFP4 ? 2 : 4;  // scale tiles a step and 128 rows
-    static constexpr int kQSf = (BN + 127) / 128;
     static constexpr int kPBytes = 128 * kStepBytes, kQBytes = BN * kStepBytes;
-    static constexpr int kStageBytes = kPBytes + kQBytes + (1 + kQSf) * kSfTiles * 512;
+    static constexpr int kStageBytes = kPBytes + kQBytes + 2 * kSfTiles * 512;
     static constexpr int kSmem = kStages * kStageBytes + 1024;  // and room to start on 1024 bytes
     static constexpr int kAccCols = BN < 32 ? 32 : BN;
-    static constexpr int kSfCols = kSfTiles * 4 * (1 + kQSf);   // tensor memory columns a stage
+    static constexpr int kSfCols = kSfTiles * 4 * 2;          // tensor memory columns a stage
     static constexpr int kNeed = kAccCols + kStages * kSfCols;
     static constexpr int kCols = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
 };
-
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t at, uint32_t rank) {
     uint32_t r;
@@ -95,7 +90,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
                                                          const MmArgs a) {
     using G = MmGeom<FMT, BN>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[kStages], empty[kStages], done;
+    __shared__ uint64_t full[kStages], scaled[kStages], empty[kStages], done;
     __shared__ uint32_t tmem_slot, loads;
     __shared__ int gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -111,6 +106,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i]);
+            mbar_init_count(&scaled[i], 4);
             mbar_init(&empty[i]);
         }
         mbar_init(&done);
@@ -125,7 +121,6 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     const uint32_t tmem = tmem_slot;
 
     if (warp == 4 && lane == 0) {
-        const int q_sf_tiles = min(G::kQSf, (a.q_rows - q0 + 127) / 128);  // scale tiles of Q's rows that exist
         const uint8_t* psf = a.p_sf + (int64_t)(p0 / 128) * a.sf_across * 512;
         const uint8_t* qsf = a.q_sf + (int64_t)(q0 / 128) * a.sf_across * 512;
         uint32_t n = 0;
@@ -136,42 +131,53 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
                 break;
             }
             const int t0 = s * G::kSfTiles, nt = min(G::kSfTiles, a.sf_across - t0);
-            expect_bytes(&full[st], G::kPBytes + G::kQBytes + nt * 512 * (1 + q_sf_tiles));
+            expect_bytes(&full[st], G::kPBytes + G::kQBytes + nt * 512 * 2);
             tile_load(at, &map_p, s * kStepBytes, p0, &full[st]);
             tile_load(at + G::kPBytes, &map_q, s * kStepBytes, q0, &full[st]);
             const uint32_t sf = at + G::kPBytes + G::kQBytes;
             block_load(sf, psf + (int64_t)t0 * 512, nt * 512, &full[st]);
-            for (int j = 0; j < q_sf_tiles; ++j)
-                block_load(sf + (1 + j) * G::kSfTiles * 512, qsf + ((int64_t)j * a.sf_across + t0) * 512, nt * 512, &full[st]);
+            block_load(sf + G::kSfTiles * 512, qsf + (int64_t)t0 * 512, nt * 512, &full[st]);
         }
         loads = n;
     } else if (warp == 5 && lane == 0) {
         uint32_t n = 0;
         for (int s = s0; s < s1; ++s, ++n) {
             const uint32_t st = n % kStages, at = base + st * G::kStageBytes;
-            if (!mbar_wait(&full[st], (n / kStages) & 1)) {
+            if (!mbar_wait(&full[st], (n / kStages) & 1) || !mbar_wait(&scaled[st], (n / kStages) & 1)) {
                 gave_up = 1;
                 break;
             }
             tc_fence_after();
-            const int nk = min(4, a.ksteps - s * 4), nt = min(G::kSfTiles, a.sf_across - s * G::kSfTiles);
-            const uint32_t sf = at + G::kPBytes + G::kQBytes;
+            const int nk = min(4, a.ksteps - s * 4);
             const uint32_t tp = tmem + G::kAccCols + st * G::kSfCols, tq = tp + G::kSfTiles * 4;
-            for (int t = 0; t < nt; ++t) {
-                tc_copy_scales<1>(tp + t * 4, desc_scales(sf + t * 512));
-#pragma unroll
-                for (int j = 0; j < G::kQSf; ++j)
-                    tc_copy_scales<1>(tq + t * 4 * G::kQSf + j * 4, desc_scales(sf + ((1 + j) * G::kSfTiles + t) * 512));
-            }
             for (int k = 0; k < nk; ++k) {
                 const int t = FMT == FP8Q_MXFP4 ? k >> 1 : k;
                 const uint32_t idesc = FMT == FP8Q_MXFP4 && (k & 1) ? mma_desc<FMT>(128, BN, 2) : mma_desc<FMT>(128, BN, 0);
-                tc_mma<FMT, 1>(tmem, desc_codes(at + k * 32), desc_codes(at + G::kPBytes + k * 32), idesc, tp + t * 4,
-                               tq + t * 4 * G::kQSf, n | k);
+                tc_mma<FMT, 1>(tmem, desc_codes(at + k * 32), desc_codes(at + G::kPBytes + k * 32), idesc, tp + t * 4, tq + t * 4, n | k);
             }
             tc_commit(&empty[st]);
         }
         tc_commit(&done);
+    } else if (warp < 4) {
+        uint32_t n = 0;
+        for (int s = s0; s < s1; ++s, ++n) {
+            const uint32_t st = n % kStages;
+            if (!mbar_wait(&full[st], (n / kStages) & 1)) {
+                gave_up = 1;
+                break;
+            }
+            __syncwarp();
+            const uint32_t sf = base + st * G::kStageBytes + G::kPBytes + G::kQBytes;
+            const uint32_t to = tmem + ((uint32_t)(warp * 32) << 16) + G::kAccCols + st * G::kSfCols;
+            if constexpr (FMT == FP8Q_MXFP4) {
+                store_scales4(to, sf, 512);  // P's and Q's two
+            } else {
+                store_scales4(to, sf, 512);
+                store_scales4(to + 16, sf + 2048, 512);
+            }
+            scales_stored();
+            if (lane == 0) arrive_local(&scaled[st]);
+        }
     }
     __syncwarp();
     if (warp < 4 && !mbar_wait(&done, 0)) gave_up = 1;
@@ -242,6 +248,230 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
 }
 
 // ----------------------------------------------------------------------------
+// Pairs: two CTAs of a cluster share tiles of 256 x 256.  Each holds 128 rows of
+// P and of Q and the accumulators of its own rows of P; the first issues the
+// multiply-adds for both, so a row of Q is read from shared memory once for 256
+// rows of P.  Persistent: the copies of the next tile run on while this one's
+// accumulators go out, and the tensor cores wait only until these are in
+// registers.
+
+constexpr int kPairStages = 5;
+constexpr int kPairThreads = 576;  // 8 warps carry results out, 8 store scales, one copies, one multiplies
+
+template <int FMT>
+struct PairGeom {
+    static constexpr int kSfTiles = FMT == FP8Q_MXFP4 ? 2 : 4;
+    static constexpr int kCodeBytes = 128 * kStepBytes;  // of P and of Q
+    static constexpr int kStageBytes = 2 * kCodeBytes + 3 * kSfTiles * 512;
+    static constexpr int kSmem = kPairStages * kStageBytes + 1024;
+    static constexpr int kSfCols = 3 * kSfTiles * 4;
+};
+
+template <int FMT, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+    fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                           const __grid_constant__ CUtensorMap map_psf, const __grid_constant__ CUtensorMap map_qsf, const MmArgs a) {
+    using G = PairGeom<FMT>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[kPairStages], sf_full[kPairStages], scaled[kPairStages], empty[kPairStages], done, drained;
+    __shared__ uint32_t tmem_slot, loads;
+    __shared__ int gave_up;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t rank = cluster_rank();
+    const int tiles = (a.p_rows + 255) / 256 * a.q_tiles, stride = gridDim.x / 2;
+    const int steps = (a.ksteps + 3) / 4;
+
+    if (warp == 9) tmem_alloc<2>(&tmem_slot, 512);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(&full[i]);
+            mbar_init(&sf_full[i]);
+            mbar_init_count(&scaled[i], 8);
+            mbar_init(&empty[i]);
+        }
+        mbar_init(&done);
+        mbar_init_count(&drained, 16);
+        loads = 0;
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are there
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
+                const int p0 = tile / a.q_tiles * 256, q0 = tile % a.q_tiles * 256;
+                for (int s = 0; s < steps; ++s, ++n) {
+                    const uint32_t st = n % kPairStages, at = base + st * G::kStageBytes;
+                    if (!mbar_wait(&empty[st], ((n / kPairStages) & 1) ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) expect_bytes(&full[st], 4 * G::kCodeBytes);
+                    expect_bytes(&sf_full[st], 3 * G::kSfTiles * 512);
+                    const uint32_t bar = in_cluster(smem_addr(&full[st]), 0);
+                    tile_load_pair(at, &map_p, s * kStepBytes, p0 + (int)rank * 128, bar);
+                    tile_load_pair(at + G::kCodeBytes, &map_q, s * kStepBytes, q0 + (int)rank * 128, bar);
+                    const uint32_t sf = at + 2 * G::kCodeBytes;
+                    tile_load(sf, &map_psf, s * G::kSfTiles * 64, p0 / 128 + (int)rank, &sf_full[st]);
+                    tile_load(sf + G::kSfTiles * 512, &map_qsf, s * G::kSfTiles * 64, q0 / 128, &sf_full[st]);
+                }
+            }
+            if (!ok) gave_up = 1;
+            loads = n;
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && rank == 0) {
+            uint32_t n = 0, it = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride, ++it) {
+                if (it > 0 && !mbar_wait(&drained, (it - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int s = 0; s < steps; ++s, ++n) {
+                    const uint32_t st = n % kPairStages, at = base + st * G::kStageBytes;
+                    if (!mbar_wait(&full[st], (n / kPairStages) & 1) || !mbar_wait(&scaled[st], (n / kPairStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int nk = min(4, a.ksteps - s * 4);
+                    const uint32_t tp = tmem + 256 + st * G::kSfCols, tq = tp + G::kSfTiles * 4;
+                    for (int k = 0; k < nk; ++k) {
+                        const int t = FMT == FP8Q_MXFP4 ? k >> 1 : k;
+                        const uint32_t idesc = FMT == FP8Q_MXFP4 && (k & 1) ? mma_desc<FMT>(256, 256, 2) : mma_desc<FMT>(256, 256, 0);
+                        tc_mma<FMT, 2>(tmem, desc_codes(at + k * 32), desc_codes(at + G::kCodeBytes + k * 32), idesc, tp + t * 4,
+                                       tq + t * 8, s | k);
+                    }
+                    tc_commit_pair(&empty[st], 3);
+                }
+                tc_commit_pair(&done, 3);
+            }
+            if (!ok) {
+                tc_commit_pair(&done, 3);
+                gave_up = 1;
+            }
+        }
+    } else if (warp >= 10) {
+        // scale stores, two groups of four warps in turn: warps 10 to 13 reach lane groups 2, 3, 0, 1
+        const int group = (warp - 10) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256;
+        uint32_t n = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
+            for (int s = 0; s < steps; ++s, ++n) {
+                if ((n & 1) != (uint32_t)group) continue;
+                const uint32_t st = n % kPairStages;
+                if (!mbar_wait(&sf_full[st], (n / kPairStages) & 1)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                const uint32_t sf = base + st * G::kStageBytes + 2 * G::kCodeBytes, to = lanes + st * G::kSfCols;
+                // Q's scales for its first and second 128 rows lie side by side for each step of 64
+                if constexpr (FMT == FP8Q_MXFP4) {
+                    store_scales2(to, sf);
+                    store_scales4(to + 8, sf + 1024, 1024);
+                } else {
+                    store_scales4(to, sf, 512);
+                    store_scales4(to + 16, sf + 2048, 2048);
+                    store_scales4(to + 32, sf + 3072, 2048);
+                }
+                scales_stored();
+                if (lane == 0) arrive_cluster(in_cluster(smem_addr(&scaled[st]), 0));
+            }
+        }
+        if (!ok) gave_up = 1;
+    } else {
+        const float alpha = __fmul_rn(a.sa ? __ldg(a.sa) : 1.0f, a.sb ? __ldg(a.sb) : 1.0f);
+        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * 128;
+        const uint32_t bar = in_cluster(smem_addr(&drained), 0);
+        bool ok = true;
+        uint32_t it = 0;
+        for (int tile = blockIdx.x / 2; tile < tiles; tile += stride, ++it) {
+            const int p = tile / a.q_tiles * 256 + (int)rank * 128 + (warp & 3) * 32 + lane;
+            const int q = tile % a.q_tiles * 256 + (warp >> 2) * 128, left = a.q_rows - q;
+            ok = ok && mbar_wait(&done, it & 1);
+            if (!ok) gave_up = 1;
+            __syncwarp();
+            tc_fence_after();
+            const float nan = __uint_as_float(0x7FFFFFFFu);  // a wait that ran out shows as NaN in the tile
+            if constexpr (F32) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                    float v[16];
+                    tmem_load16(from + c, v);
+                    if (c == 112) {
+                        tc_fence_before();
+                        if (lane == 0) arrive_cluster(bar);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = ok ? __fmul_rn(v[i], alpha) : nan;
+                    if (p < a.p_rows && left > c) {
+                        if (a.p_is_m) {
+                            store_row16<true>(a.d, (int64_t)p * a.ld + q + c, v, left - c, a.vec);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (c + i < left) store_one<true>(a.d, (int64_t)(q + c + i) * a.ld + p, v[i]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            } else {
+                uint32_t o[64];
+#pragma unroll
+                for (int c = 0; c < 128; c += 16) {
+                    float v[16];
+                    tmem_load16(from + c, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[c / 2 + i] = ok ? cvt_bf16x2(__fmul_rn(v[2 * i], alpha), __fmul_rn(v[2 * i + 1], alpha)) : 0x7FFF7FFFu;
+                }
+                tc_fence_before();
+                if (lane == 0) arrive_cluster(bar);  // the accumulators are in registers
+                if (p < a.p_rows && left > 0) {
+                    uint16_t* d = static_cast<uint16_t*>(a.d);
+                    if (a.p_is_m && a.vec && left >= 128) {
+                        uint4* out = reinterpret_cast<uint4*>(d + (int64_t)p * a.ld + q);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } else {
+                        const int64_t step = a.p_is_m ? 1 : a.ld;
+                        uint16_t* out = a.p_is_m ? d + (int64_t)p * a.ld + q : d + (int64_t)q * a.ld + p;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i < left) out[i * step] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (gave_up && threadIdx.x == 0)  // copies still under way end before their CTAs do
+        for (uint32_t n = loads > kPairStages ? loads - kPairStages : 0; n < loads; ++n) {
+            if (rank == 0) mbar_wait(&full[n % kPairStages], (n / kPairStages) & 1);
+            mbar_wait(&sf_full[n % kPairStages], (n / kPairStages) & 1);
+        }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 9) tmem_free<2>(tmem, 512);
+}
+
+// ----------------------------------------------------------------------------
 // Host
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -273,6 +503,16 @@ bool codes_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t cols, i
     const cuuint32_t box[2] = {kStepBytes, (cuuint32_t)box_rows}, one[2] = {1, 1};
     return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(q), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Block scales: rows of scale tiles along k, boxes of `tiles` of them x box_rows, zeros beyond the edges.
+bool scales_map(CUtensorMap* map, const uint8_t* sf, int64_t rows, int64_t across, int tiles, int box_rows) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dim[2] = {(cuuint64_t)across * 64, (cuuint64_t)((rows + 127) / 128)}, stride[1] = {(cuuint64_t)across * 512};
+    const cuuint32_t box[2] = {(cuuint32_t)tiles * 64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(sf), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A kernel's shared-memory limit, set on its first call on each device.
@@ -308,6 +548,37 @@ fp8q_status launch_tiles(const CUtensorMap& mp, const CUtensorMap& mq, const MmA
     return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "fp4_matmul_kernel");
 }
 
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 152;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) n = 152;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <int FMT, bool F32>
+fp8q_status launch_pairs(const uint8_t* p, const uint8_t* q, int64_t k, MmArgs g, cudaStream_t s) {
+    static std::atomic<uint64_t> devices{0};
+    using G = PairGeom<FMT>;
+    auto kern = fp4_matmul_pair_kernel<FMT, F32>;
+    const cudaError_t e = allow_smem(kern, G::kSmem, devices);
+    if (e != cudaSuccess) return cuda_fail(e, "fp4_matmul_pair_kernel setup");
+    CUtensorMap mp, mq, ms, mt;
+    if (!codes_map(&mp, p, g.p_rows, k, 128) || !codes_map(&mq, q, g.q_rows, k, 128) ||
+        !scales_map(&ms, g.p_sf, g.p_rows, g.sf_across, G::kSfTiles, 1) || !scales_map(&mt, g.q_sf, g.q_rows, g.sf_across, G::kSfTiles, 2))
+        return cuda_fail(cudaErrorInvalidValue, "fp4_matmul_pair_kernel tensor map");
+    g.q_tiles = (g.q_rows + 255) / 256;
+    const int64_t tiles = (int64_t)((g.p_rows + 255) / 256) * g.q_tiles;
+    if (tiles > 0x3FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
+    const int64_t pairs = sm_count() / 2;
+    const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+    return launch_kernel(kern, dim3(grid), dim3(kPairThreads), G::kSmem, s, "fp4_matmul_pair_kernel", mp, mq, ms, mt, g);
+}
+
 template <int FMT, bool F32>
 fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, void* d, int64_t m, int64_t n, int64_t k,
                    const float* sa, const float* sb, cudaStream_t s) {
@@ -327,7 +598,8 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     g.q_sf = g.p_is_m ? b_sf : a_sf;
     g.p_rows = (int32_t)(g.p_is_m ? m : n);
     g.q_rows = (int32_t)(g.p_is_m ? n : m);
-    const int bn = g.q_rows <= 16 ? 16 : g.q_rows <= 32 ? 32 : g.q_rows <= 64 ? 64 : g.q_rows <= 128 ? 128 : 256;
+    if ((int64_t)((g.p_rows + 255) / 256) * ((g.q_rows + 255) / 256) >= 64) return launch_pairs<FMT, F32>(p, q, k, g, s);
+    const int bn = g.q_rows <= 16 ? 16 : g.q_rows <= 32 ? 32 : g.q_rows <= 64 ? 64 : 128;
     g.q_tiles = (g.q_rows + bn - 1) / bn;
     const int64_t tiles = (int64_t)((g.p_rows + 127) / 128) * g.q_tiles;
     const int steps = (g.ksteps + 3) / 4;
@@ -343,8 +615,7 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
         case 16: return launch_tiles<FMT, 16, F32>(mp, mq, g, grid, s);
         case 32: return launch_tiles<FMT, 32, F32>(mp, mq, g, grid, s);
         case 64: return launch_tiles<FMT, 64, F32>(mp, mq, g, grid, s);
-        case 128: return launch_tiles<FMT, 128, F32>(mp, mq, g, grid, s);
-        default: return launch_tiles<FMT, 256, F32>(mp, mq, g, grid, s);
+        default: return launch_tiles<FMT, 128, F32>(mp, mq, g, grid, s);
     }
 }
 

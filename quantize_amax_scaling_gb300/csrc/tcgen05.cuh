@@ -60,22 +60,48 @@ __device__ __forceinline__ uint64_t desc_codes(uint32_t at) {
     return (uint64_t)((at & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// One scale tile: 32 lines of 16 bytes, no swizzle, 8 lines (128 bytes) to the next.
-__device__ __forceinline__ uint64_t desc_scales(uint32_t at) {
-    return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-}
-
 // ----------------------------------------------------------------------------
 // Instructions
 
-// A scale tile (512 bytes of shared memory) to four columns of tensor memory,
-// repeated for each of the four groups of 32 lanes.
-template <int PAIR>
-__device__ __forceinline__ void tc_copy_scales(uint32_t at, uint64_t desc) {
-    if (PAIR == 2)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(at), "l"(desc) : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(at), "l"(desc) : "memory");
+// Four scale tiles (512 bytes each) to sixteen columns of the calling warp's 32
+// lanes: line l of a tile, 16 bytes, is lane l's four columns.  The tiles lie one
+// behind another (gap 512), or the second and fourth `gap` behind the first and
+// third, which lie one behind the other.  Each of the four warps that reach the four groups of
+// lanes stores the same.  Copying them by the tensor core's own shared-to-tensor
+// memory copies holds up the multiply-adds behind them (1162 cycles for four
+// multiply-adds of 256x256x64 and their twelve tiles, 512 without); stored by
+// eight warps beside them, twelve tiles take 445.
+__device__ __forceinline__ void store_scales4(uint32_t to, uint32_t from, uint32_t gap) {
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3])
+                     : "r"(from + (gap == 512 ? i * 512 : (i >> 1) * 512 + (i & 1) * gap) + (threadIdx.x & 31) * 16)
+                     : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(to),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+        "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void store_scales2(uint32_t to, uint32_t from) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3])
+                     : "r"(from + i * 512 + (threadIdx.x & 31) * 16)
+                     : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void scales_stored() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    tc_fence_before();
 }
 
 // Instruction descriptor: e2m1 operands along k, N columns, M rows, the scale
@@ -113,6 +139,45 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// The same for the pair: the barrier at this place in each CTA of `mask`.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint32_t mask) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+                 "h"((uint16_t)mask)
+                 : "memory");
+}
+
+// ----------------------------------------------------------------------------
+// Clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The address in the cluster of what lies at `at` in the CTA of that rank.
+__device__ __forceinline__ uint32_t in_cluster(uint32_t at, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void arrive_local(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void mbar_init_count(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+}
+
 // ----------------------------------------------------------------------------
 // Copies
 
@@ -124,6 +189,15 @@ __device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, 
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The same in a pair: the barrier, a cluster address, may lie in either of its CTAs.
+__device__ __forceinline__ void tile_load_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 

@@ -172,7 +172,8 @@ def test_dequantize(dev, r, c, fmt):
 MATMULS = [(1, 1, 1), (1, 8, 16), (1, 4096, 4096), (2, 130, 31), (3, 1000, 257), (7, 16, 16384), (8, 129, 64), (16, 256, 96),
            (17, 300, 130), (24, 512, 2048), (33, 77, 640), (64, 128, 65), (65, 200, 1033), (100, 333, 333), (128, 128, 128), (129, 257, 192),
            (255, 256, 256), (256, 512, 320), (300, 1000, 1033), (513, 520, 1024), (1024, 768, 4096), (1555, 640, 257), (2048, 1, 512),
-           (4096, 40, 72), (640, 2056, 1536), (2000, 2304, 96)]
+           (4096, 40, 72), (640, 2056, 1536), (2000, 2304, 96),
+           (2100, 2050, 257), (4100, 1104, 1056), (200, 17000, 96), (2304, 2400, 640), (1030, 4099, 33)]
 
 
 def product_bound(a, b, want, k, alpha, out_eps):
@@ -206,7 +207,8 @@ def test_matmul(dev, m, n, k, fmt):
 
 
 @pytest.mark.parametrize("fmt", [R.MXFP4, R.NVFP4])
-@pytest.mark.parametrize("m,n,k", [(1, 640, 4096), (5, 384, 1000), (40, 256, 8192), (200, 300, 2048), (700, 1100, 1056), (512, 512, 512)])
+@pytest.mark.parametrize("m,n,k", [(1, 640, 4096), (5, 384, 1000), (40, 256, 8192), (200, 300, 2048), (700, 1100, 1056), (512, 512, 512),
+                                   (2300, 2112, 1100), (2200, 2051, 2048), (16384, 520, 256), (2560, 8192, 128)])
 def test_matmul_exact_sums(dev, m, n, k, fmt):
     """Scales of 1, 2 and 4 and few enough terms: every partial sum is a multiple of 1/4 below 2^22, exact in
     binary32 in any order, so the product is exact: a wrong code, scale or place shows in the last bit."""
