@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
         uint32_t n = 0;
         for (int s = s0; s < s1; ++s, ++n) {
             const uint32_t st = n % kStages;
-            if (!mbar_wait(&full[st], (n / kStages) & 1)) {
+            if (!mbar_wait_warp(&full[st], (n / kStages) & 1, 0)) {
                 gave_up = 1;
                 break;
             }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
         }
     }
     __syncwarp();
-    if (warp < 4 && !mbar_wait(&done, 0)) gave_up = 1;
+    if (warp < 4 && !mbar_wait_warp(&done, 0, 0)) gave_up = 1;
     __syncthreads();
     tc_fence_after();
     const float alpha = __fmul_rn(a.sa ? __ldg(a.sa) : 1.0f, a.sb ? __ldg(a.sb) : 1.0f);
@@ -256,43 +256,57 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
 // registers.
 
 constexpr int kPairStages = 5;
-constexpr int kPairThreads = 576;  // 8 warps carry results out, 8 store scales, one copies, one multiplies
+constexpr int kPairThreads = 608;  // warps 0-7 carry results out, 8 copies codes, 9 multiplies, 10-17 store scales, 18 copies scales
 
 template <int FMT>
 struct PairGeom {
     static constexpr int kSfTiles = FMT == FP8Q_MXFP4 ? 2 : 4;
     static constexpr int kCodeBytes = 128 * kStepBytes;  // of P and of Q
     static constexpr int kStageBytes = 2 * kCodeBytes + 3 * kSfTiles * 512;
-    static constexpr int kSmem = kPairStages * kStageBytes + 1024;
+    static constexpr int kOutBytes = 8 * 4096;  // 32 rows of 128 bytes for each warp that carries results out
+    static constexpr int kSmem = kPairStages * kStageBytes + kOutBytes + 1024;
     static constexpr int kSfCols = 3 * kSfTiles * 4;
 };
+
+// Tiles go in bands of eight along P, along Q within a band, so that the tiles
+// under way at one time share rows of both operands in L2.
+struct PairTile {
+    int p, q;
+};
+__device__ __forceinline__ PairTile pair_tile(int tile, int p_tiles, int q_tiles) {
+    const int band = tile / (8 * q_tiles), in = tile - band * 8 * q_tiles;
+    const int high = min(8, p_tiles - band * 8);
+    return {(band * 8 + in % high) * 256, in / high * 256};
+}
 
 template <int FMT, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
-                           const __grid_constant__ CUtensorMap map_psf, const __grid_constant__ CUtensorMap map_qsf, const MmArgs a) {
+                           const __grid_constant__ CUtensorMap map_psf, const __grid_constant__ CUtensorMap map_qsf,
+                           const __grid_constant__ CUtensorMap map_d, const MmArgs a) {
     using G = PairGeom<FMT>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[kPairStages], sf_full[kPairStages], scaled[kPairStages], empty[kPairStages], done, drained;
-    __shared__ uint32_t tmem_slot, loads;
+    // full: the codes of a stage are there in both CTAs and its scales in both tensor memories (the first CTA's counts);
+    // sf_full: this CTA's scales are in shared memory; empty: the stage has been used
+    __shared__ uint64_t full[kPairStages], sf_full[kPairStages], empty[kPairStages], done, drained;
+    __shared__ uint32_t tmem_slot, loads, sf_loads;
     __shared__ int gave_up;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t rank = cluster_rank();
-    const int tiles = (a.p_rows + 255) / 256 * a.q_tiles, stride = gridDim.x / 2;
+    const int p_tiles = (a.p_rows + 255) / 256, tiles = p_tiles * a.q_tiles, stride = gridDim.x / 2;
     const int steps = (a.ksteps + 3) / 4;
 
     if (warp == 9) tmem_alloc<2>(&tmem_slot, 512);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPairStages; ++i) {
-            mbar_init(&full[i]);
+            mbar_init_count(&full[i], 1 + 8);
             mbar_init(&sf_full[i]);
-            mbar_init_count(&scaled[i], 8);
             mbar_init(&empty[i]);
         }
         mbar_init(&done);
         mbar_init_count(&drained, 16);
-        loads = 0;
+        loads = sf_loads = 0;
         gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -304,91 +318,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     const uint32_t tmem = tmem_slot;
 
     if (warp == 8) {
-        if (lane == 0) {
-            uint32_t n = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
-                const int p0 = tile / a.q_tiles * 256, q0 = tile % a.q_tiles * 256;
-                for (int s = 0; s < steps; ++s, ++n) {
-                    const uint32_t st = n % kPairStages, at = base + st * G::kStageBytes;
-                    if (!mbar_wait(&empty[st], ((n / kPairStages) & 1) ^ 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (rank == 0) expect_bytes(&full[st], 4 * G::kCodeBytes);
-                    expect_bytes(&sf_full[st], 3 * G::kSfTiles * 512);
-                    const uint32_t bar = in_cluster(smem_addr(&full[st]), 0);
-                    tile_load_pair(at, &map_p, s * kStepBytes, p0 + (int)rank * 128, bar);
-                    tile_load_pair(at + G::kCodeBytes, &map_q, s * kStepBytes, q0 + (int)rank * 128, bar);
-                    const uint32_t sf = at + 2 * G::kCodeBytes;
-                    tile_load(sf, &map_psf, s * G::kSfTiles * 64, p0 / 128 + (int)rank, &sf_full[st]);
-                    tile_load(sf + G::kSfTiles * 512, &map_qsf, s * G::kSfTiles * 64, q0 / 128, &sf_full[st]);
+        uint32_t st = 0, round = 0, n = 0;
+        bool ok = true;
+        const uint32_t bars = in_cluster(smem_addr(&full[0]), 0);
+        for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
+            const PairTile t = pair_tile(tile, p_tiles, a.q_tiles);
+            const int p0 = t.p + (int)rank * 128, q0 = t.q + (int)rank * 128;
+            for (int s = 0; s < steps; ++s, ++n) {
+                if (!mbar_wait(&empty[st], (round & 1) ^ 1)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t at = base + st * G::kStageBytes, bar = bars + st * 8;
+                if (elect_lane()) {
+                    if (rank == 0) expect_bytes(&full[st], 4 * G::kCodeBytes);
+                    tile_load_pair(at, &map_p, s * kStepBytes, p0, bar);
+                    tile_load_pair(at + G::kCodeBytes, &map_q, s * kStepBytes, q0, bar);
+                }
+                __syncwarp();
+                if (++st == kPairStages) st = 0, ++round;
             }
+        }
+        if (lane == 0) {
             if (!ok) gave_up = 1;
             loads = n;
         }
+    } else if (warp == 18) {
+        uint32_t st = 0, round = 0, n = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
+            const PairTile t = pair_tile(tile, p_tiles, a.q_tiles);
+            for (int s = 0; s < steps; ++s, ++n) {
+                if (!mbar_wait(&empty[st], (round & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sf = base + st * G::kStageBytes + 2 * G::kCodeBytes;
+                if (elect_lane()) {
+                    expect_bytes(&sf_full[st], 3 * G::kSfTiles * 512);
+                    tile_load(sf, &map_psf, s * G::kSfTiles * 64, t.p / 128 + (int)rank, &sf_full[st]);
+                    tile_load(sf + G::kSfTiles * 512, &map_qsf, s * G::kSfTiles * 64, t.q / 128, &sf_full[st]);
+                }
+                __syncwarp();
+                if (++st == kPairStages) st = 0, ++round;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) gave_up = 1;
+            sf_loads = n;
+        }
     } else if (warp == 9) {
-        if (lane == 0 && rank == 0) {
-            uint32_t n = 0, it = 0;
+        if (rank == 0) {
+            uint32_t st = 0, round = 0, it = 0;
             bool ok = true;
             for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride, ++it) {
                 if (it > 0 && !mbar_wait(&drained, (it - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                for (int s = 0; s < steps; ++s, ++n) {
-                    const uint32_t st = n % kPairStages, at = base + st * G::kStageBytes;
-                    if (!mbar_wait(&full[st], (n / kPairStages) & 1) || !mbar_wait(&scaled[st], (n / kPairStages) & 1)) {
+                for (int s = 0; s < steps; ++s) {
+                    if (!mbar_wait(&full[st], round & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const int nk = min(4, a.ksteps - s * 4);
+                    const uint32_t at = base + st * G::kStageBytes;
+                    const uint64_t dp = desc_codes(at), dq = desc_codes(at + G::kCodeBytes);
                     const uint32_t tp = tmem + 256 + st * G::kSfCols, tq = tp + G::kSfTiles * 4;
-                    for (int k = 0; k < nk; ++k) {
-                        const int t = FMT == FP8Q_MXFP4 ? k >> 1 : k;
-                        const uint32_t idesc = FMT == FP8Q_MXFP4 && (k & 1) ? mma_desc<FMT>(256, 256, 2) : mma_desc<FMT>(256, 256, 0);
-                        tc_mma<FMT, 2>(tmem, desc_codes(at + k * 32), desc_codes(at + G::kCodeBytes + k * 32), idesc, tp + t * 4,
-                                       tq + t * 8, s | k);
+                    if (elect_lane()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = FMT == FP8Q_MXFP4 ? k >> 1 : k;
+                            constexpr uint32_t kEven = mma_desc<FMT>(256, 256, 0), kOdd = mma_desc<FMT>(256, 256, 2);
+                            if (k < nk)  // a step of 64 codes is 32 bytes on
+                                tc_mma<FMT, 2>(tmem, dp + k * 2, dq + k * 2, FMT == FP8Q_MXFP4 && (k & 1) ? kOdd : kEven, tp + t * 4,
+                                               tq + t * 8, s | k);
+                        }
+                        tc_commit_pair(&empty[st], 3);
+                        if (s == steps - 1) tc_commit_pair(&done, 3);
                     }
-                    tc_commit_pair(&empty[st], 3);
+                    __syncwarp();
+                    if (++st == kPairStages) st = 0, ++round;
                 }
-                tc_commit_pair(&done, 3);
             }
-            if (!ok) {
+            if (!ok && elect_lane()) {
                 tc_commit_pair(&done, 3);
                 gave_up = 1;
             }
         }
     } else if (warp >= 10) {
-        // scale stores, two groups of four warps in turn: warps 10 to 13 reach lane groups 2, 3, 0, 1
-        const int group = (warp - 10) >> 2;
+        // two groups of four warps in turn; a warp reaches the lanes of its number modulo 4
+        const uint32_t group = (warp - 10) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256;
-        uint32_t n = 0;
+        const uint32_t bars = in_cluster(smem_addr(&full[0]), 0);
+        uint32_t st = 0, round = 0, n = 0;
         bool ok = true;
         for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
             for (int s = 0; s < steps; ++s, ++n) {
-                if ((n & 1) != (uint32_t)group) continue;
-                const uint32_t st = n % kPairStages;
-                if (!mbar_wait(&sf_full[st], (n / kPairStages) & 1)) {
-                    ok = false;
-                    break;
+                if ((n & 1) == group) {
+                    if (!mbar_wait(&sf_full[st], round & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sf = base + st * G::kStageBytes + 2 * G::kCodeBytes, to = lanes + st * G::kSfCols;
+                    // Q's scales for its first and second 128 rows lie side by side for each step of 64
+                    if constexpr (FMT == FP8Q_MXFP4) {
+                        store_scales2(to, sf);
+                        store_scales4(to + 8, sf + 1024, 1024);
+                    } else {
+                        store_scales4(to, sf, 512);
+                        store_scales4(to + 16, sf + 2048, 2048);
+                        store_scales4(to + 32, sf + 3072, 2048);
+                    }
+                    scales_stored();
+                    if (lane == 0) arrive_cluster(bars + st * 8);
                 }
-                __syncwarp();
-                const uint32_t sf = base + st * G::kStageBytes + 2 * G::kCodeBytes, to = lanes + st * G::kSfCols;
-                // Q's scales for its first and second 128 rows lie side by side for each step of 64
-                if constexpr (FMT == FP8Q_MXFP4) {
-                    store_scales2(to, sf);
-                    store_scales4(to + 8, sf + 1024, 1024);
-                } else {
-                    store_scales4(to, sf, 512);
-                    store_scales4(to + 16, sf + 2048, 2048);
-                    store_scales4(to + 32, sf + 3072, 2048);
-                }
-                scales_stored();
-                if (lane == 0) arrive_cluster(in_cluster(smem_addr(&scaled[st]), 0));
+                if (++st == kPairStages) st = 0, ++round;
             }
         }
         if (!ok) gave_up = 1;
@@ -398,73 +444,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         const uint32_t bar = in_cluster(smem_addr(&drained), 0);
         bool ok = true;
         uint32_t it = 0;
+        constexpr int kLine = F32 ? 32 : 64;  // columns of a 128-byte line
+        const uint32_t out = base + kPairStages * G::kStageBytes + warp * 4096, line = out + lane * 128;
         for (int tile = blockIdx.x / 2; tile < tiles; tile += stride, ++it) {
-            const int p = tile / a.q_tiles * 256 + (int)rank * 128 + (warp & 3) * 32 + lane;
-            const int q = tile % a.q_tiles * 256 + (warp >> 2) * 128, left = a.q_rows - q;
-            ok = ok && mbar_wait(&done, it & 1);
+            const PairTile t = pair_tile(tile, p_tiles, a.q_tiles);
+            const int p_first = t.p + (int)rank * 128 + (warp & 3) * 32, p = p_first + lane;
+            const int q = t.q + (warp >> 2) * 128, left = a.q_rows - q;
+            ok = ok && mbar_wait_warp(&done, it & 1, 32);
             if (!ok) gave_up = 1;
-            __syncwarp();
             tc_fence_after();
-            const float nan = __uint_as_float(0x7FFFFFFFu);  // a wait that ran out shows as NaN in the tile
-            if constexpr (F32) {
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 16) {
-                    float v[16];
-                    tmem_load16(from + c, v);
-                    if (c == 112) {
-                        tc_fence_before();
-                        if (lane == 0) arrive_cluster(bar);
-                    }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = ok ? __fmul_rn(v[i], alpha) : nan;
-                    if (p < a.p_rows && left > c) {
-                        if (a.p_is_m) {
-                            store_row16<true>(a.d, (int64_t)p * a.ld + q + c, v, left - c, a.vec);
-                        } else {
+            for (int c = 0; c < 128; c += kLine) {
+                uint32_t o[32];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (c + i < left) store_one<true>(a.d, (int64_t)(q + c + i) * a.ld + p, v[i]);
-                        }
-                    }
-                    __syncwarp();
-                }
-            } else {
-                uint32_t o[64];
+                for (int h = 0; h < kLine; h += 32) {
+                    float v[32];
+                    tmem_load32(from + c + h, v);
+                    // a wait that ran out shows as NaN in the tile
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
-                    float v[16];
-                    tmem_load16(from + c, v);
+                    for (int i = 0; i < 32; ++i) v[i] = ok ? __fmul_rn(v[i], alpha) : __uint_as_float(0x7FFFFFFFu);
+                    if constexpr (F32) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[c / 2 + i] = ok ? cvt_bf16x2(__fmul_rn(v[2 * i], alpha), __fmul_rn(v[2 * i + 1], alpha)) : 0x7FFF7FFFu;
-                }
-                tc_fence_before();
-                if (lane == 0) arrive_cluster(bar);  // the accumulators are in registers
-                if (p < a.p_rows && left > 0) {
-                    uint16_t* d = static_cast<uint16_t*>(a.d);
-                    if (a.p_is_m && a.vec && left >= 128) {
-                        uint4* out = reinterpret_cast<uint4*>(d + (int64_t)p * a.ld + q);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) out[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(v[i]);
                     } else {
-                        const int64_t step = a.p_is_m ? 1 : a.ld;
-                        uint16_t* out = a.p_is_m ? d + (int64_t)p * a.ld + q : d + (int64_t)q * a.ld + p;
 #pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (i < left) out[i * step] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+                        for (int i = 0; i < 16; ++i) o[h / 2 + i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
                     }
+                }
+                if (c + kLine == 128) {  // the accumulators are in registers
+                    tc_fence_before();
+                    if (lane == 0) arrive_cluster(bar);
+                }
+                if (a.p_is_m && a.vec) {
+                    // through shared memory (128-byte swizzle), out by a tensor-map store
+                    if (lane == 0) store_read_wait();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((j ^ (lane & 7)) << 4)), "r"(o[4 * j]),
+                                     "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
+                                     : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0 && left > c && p_first < a.p_rows) tile_store(&map_d, q + c, p_first, out);
+                } else if (p < a.p_rows) {
+                    const int64_t step = a.p_is_m ? 1 : a.ld;
+                    const int64_t first = a.p_is_m ? (int64_t)p * a.ld + q + c : (int64_t)(q + c) * a.ld + p;
+#pragma unroll
+                    for (int i = 0; i < kLine; ++i)
+                        if (c + i < left) {
+                            if constexpr (F32)
+                                static_cast<uint32_t*>(a.d)[first + i * step] = o[i];
+                            else
+                                static_cast<uint16_t*>(a.d)[first + i * step] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+                        }
                 }
                 __syncwarp();
             }
         }
+        if (lane == 0) store_wait();
     }
     __syncwarp();
     __syncthreads();
-    if (gave_up && threadIdx.x == 0)  // copies still under way end before their CTAs do
-        for (uint32_t n = loads > kPairStages ? loads - kPairStages : 0; n < loads; ++n) {
-            if (rank == 0) mbar_wait(&full[n % kPairStages], (n / kPairStages) & 1);
+    if (gave_up && threadIdx.x == 0) {  // copies still under way end before their CTAs do
+        for (uint32_t n = loads > kPairStages ? loads - kPairStages : 0; n < loads && rank == 0; ++n)
+            mbar_wait(&full[n % kPairStages], (n / kPairStages) & 1);
+        for (uint32_t n = sf_loads > kPairStages ? sf_loads - kPairStages : 0; n < sf_loads; ++n)
             mbar_wait(&sf_full[n % kPairStages], (n / kPairStages) & 1);
-        }
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -513,6 +560,19 @@ bool scales_map(CUtensorMap* map, const uint8_t* sf, int64_t rows, int64_t acros
     const cuuint32_t box[2] = {(cuuint32_t)tiles * 64, (cuuint32_t)box_rows}, one[2] = {1, 1};
     return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(sf), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// D: boxes of 32 rows of 128 bytes.
+template <bool F32>
+bool result_map(CUtensorMap* map, void* d, int64_t rows, int64_t cols) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    constexpr int kBytes = F32 ? 4 : 2;
+    const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)cols * kBytes};
+    const cuuint32_t box[2] = {128 / kBytes, 32}, one[2] = {1, 1};
+    return f(map, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, dim, stride, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A kernel's shared-memory limit, set on its first call on each device.
@@ -567,16 +627,18 @@ fp8q_status launch_pairs(const uint8_t* p, const uint8_t* q, int64_t k, MmArgs g
     auto kern = fp4_matmul_pair_kernel<FMT, F32>;
     const cudaError_t e = allow_smem(kern, G::kSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp4_matmul_pair_kernel setup");
-    CUtensorMap mp, mq, ms, mt;
+    CUtensorMap mp, mq, ms, mt, md = {};
     if (!codes_map(&mp, p, g.p_rows, k, 128) || !codes_map(&mq, q, g.q_rows, k, 128) ||
         !scales_map(&ms, g.p_sf, g.p_rows, g.sf_across, G::kSfTiles, 1) || !scales_map(&mt, g.q_sf, g.q_rows, g.sf_across, G::kSfTiles, 2))
+        return cuda_fail(cudaErrorInvalidValue, "fp4_matmul_pair_kernel tensor map");
+    if (g.p_is_m && g.vec && !result_map<F32>(&md, g.d, g.p_rows, g.q_rows))
         return cuda_fail(cudaErrorInvalidValue, "fp4_matmul_pair_kernel tensor map");
     g.q_tiles = (g.q_rows + 255) / 256;
     const int64_t tiles = (int64_t)((g.p_rows + 255) / 256) * g.q_tiles;
     if (tiles > 0x3FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
     const int64_t pairs = sm_count() / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_kernel(kern, dim3(grid), dim3(kPairThreads), G::kSmem, s, "fp4_matmul_pair_kernel", mp, mq, ms, mt, g);
+    return launch_kernel(kern, dim3(grid), dim3(kPairThreads), G::kSmem, s, "fp4_matmul_pair_kernel", mp, mq, ms, mt, md, g);
 }
 
 template <int FMT, bool F32>
@@ -592,13 +654,14 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     g.vec = ((uintptr_t)d & 15u) == 0 && n % (F32 ? 4 : 8) == 0;
     // P, the 128 lanes, is the operand with more rows; with D's rows too short for whole
     // vectors the lanes run along D's rows, so that a warp's stores are contiguous
-    g.p_is_m = m >= n && g.vec;
+    const bool pairs = (m + 255) / 256 * ((n + 255) / 256) >= 64;
+    g.p_is_m = g.vec && (pairs || m >= n);
     const uint8_t *p = g.p_is_m ? a : b, *q = g.p_is_m ? b : a;
     g.p_sf = g.p_is_m ? a_sf : b_sf;
     g.q_sf = g.p_is_m ? b_sf : a_sf;
     g.p_rows = (int32_t)(g.p_is_m ? m : n);
     g.q_rows = (int32_t)(g.p_is_m ? n : m);
-    if ((int64_t)((g.p_rows + 255) / 256) * ((g.q_rows + 255) / 256) >= 64) return launch_pairs<FMT, F32>(p, q, k, g, s);
+    if (pairs) return launch_pairs<FMT, F32>(p, q, k, g, s);
     const int bn = g.q_rows <= 16 ? 16 : g.q_rows <= 32 ? 32 : g.q_rows <= 64 ? 64 : 128;
     g.q_tiles = (g.q_rows + bn - 1) / bn;
     const int64_t tiles = (int64_t)((g.p_rows + 127) / 128) * g.q_tiles;

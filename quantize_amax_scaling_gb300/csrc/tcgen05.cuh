@@ -11,6 +11,42 @@
 
 namespace {
 
+// mbar_wait() for a whole warp: one lane looks at the barrier (32 lanes looking,
+// in many warps, take the barriers' time from the threads that everything waits
+// for), with pauses of `pause` ns where the wait is long anyway.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t pause) {
+    uint32_t ok = 0;
+    if ((threadIdx.x & 31) == 0) {
+        const uint32_t at = smem_addr(bar);
+        uint64_t t0 = 0;
+        for (;;) {
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(at), "r"(parity)
+                : "memory");
+            if (ok) break;
+            if (pause) __nanosleep(pause);
+            const uint64_t t = global_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kWaitLimitNs) break;
+        }
+    }
+    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
+// One lane of a converged warp.  The warps that issue copies and multiply-adds
+// run their loops whole and let one lane issue: addresses and descriptors then
+// stay in uniform registers, and a step costs its issuer tens of cycles, not
+// hundreds.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ----------------------------------------------------------------------------
 // Tensor memory
 
@@ -49,6 +85,22 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Thirty-two columns.
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // ----------------------------------------------------------------------------
@@ -206,5 +258,16 @@ __device__ __forceinline__ void block_load(uint32_t dst, const void* src, uint32
                  "r"(bytes), "r"(smem_addr(bar))
                  : "memory");
 }
+
+// A box from shared memory, clipped at the tensor's edges; one thread's stores
+// are done reading shared memory after store_read_wait(), done altogether after
+// store_wait().
+__device__ __forceinline__ void tile_store(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 }  // namespace
