@@ -138,6 +138,9 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
             block_load(sf, psf + (int64_t)t0 * 512, nt * 512, &full[st]);
             block_load(sf + G::kSfTiles * 512, qsf + (int64_t)t0 * 512, nt * 512, &full[st]);
         }
+        // the tensor core's last arrivals land before the CTA may go
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n && !gave_up; ++i)
+            if (!mbar_wait(&empty[i % kStages], (i / kStages) & 1)) gave_up = 1;
         loads = n;
     } else if (warp == 5 && lane == 0) {
         uint32_t n = 0;
@@ -339,6 +342,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                 if (++st == kPairStages) st = 0, ++round;
             }
         }
+        // The tensor cores' last arrivals land before this CTA may go.
+        for (uint32_t i = 0; i < kPairStages && i < n && ok; ++i) {
+            st = st ? st - 1 : kPairStages - 1;
+            ok = mbar_wait(&empty[st], ((n - 1 - i) / kPairStages) & 1);
+        }
         if (lane == 0) {
             if (!ok) gave_up = 1;
             loads = n;
@@ -402,6 +410,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                     if (++st == kPairStages) st = 0, ++round;
                 }
             }
+            // The other CTA's last arrivals land before this one may go.
+            if (ok && it > 0) ok = mbar_wait(&drained, (it - 1) & 1);
             if (!ok && elect_lane()) {
                 tc_commit_pair(&done, 3);
                 gave_up = 1;
@@ -417,7 +427,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
             for (int s = 0; s < steps; ++s, ++n) {
                 if ((n & 1) == group) {
-                    if (!mbar_wait(&sf_full[st], round & 1)) {
+                    // The stage's last round went to the other group; its use has to be over before a
+                    // parity tells this round's scales from the last but one's.
+                    if (!mbar_wait(&empty[st], (round & 1) ^ 1) || !mbar_wait(&sf_full[st], round & 1)) {
                         ok = false;
                         break;
                     }
@@ -516,6 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     __syncthreads();
     cluster_sync_all();
     if (warp == 9) tmem_free<2>(tmem, 512);
+    cluster_sync_all();
 }
 
 // ----------------------------------------------------------------------------

@@ -285,3 +285,31 @@ def test_on_another_stream_and_in_a_graph(dev, fmt):
         d.zero_()
         g.replay()
         assert torch.equal(d, y)
+
+
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.NVFP4])
+@pytest.mark.parametrize("m,n,k", [(64, 16384, 4096), (1100, 4352, 2816)])
+def test_matmul_from_cold_memory(dev, m, n, k, fmt):
+    """Operands that come from memory in any order, many calls one behind another: the same exact sums each time."""
+    g = torch.Generator(device=dev)
+    g.manual_seed(k)
+    one = 127 if fmt == R.MXFP4 else 0x38
+    grid = torch.tensor(R.VALUE, dtype=torch.float32, device=dev)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=dev)
+    sets = []
+    for _ in range(3):
+        ops, vals = [], []
+        for r in (m, n):
+            q, s = fp8q.fp4_empty(r, k, fmt, dev)
+            q.copy_(torch.randint(0, 256, q.shape, generator=g, device=dev, dtype=torch.uint8))
+            s.fill_(one)
+            ops.append((q, s))
+            vals.append(grid[torch.stack((q & 15, q >> 4), -1).view(r, -1)[:, :k].int()])
+        sets.append((ops, vals[0].double() @ vals[1].double().t()))
+    d = [torch.empty((m, n), device=dev) for _ in sets]
+    for i in range(10):
+        flush.zero_()
+        for (ops, _), out in zip(sets, d):
+            fp8q.fp8q_fp4_matmul(*ops[0], *ops[1], out, k, fmt)
+        for (_, want), out in zip(sets, d):
+            assert torch.equal(out.double(), want)
