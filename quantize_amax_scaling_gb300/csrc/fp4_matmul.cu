@@ -47,11 +47,9 @@ struct MmGeom {
     static constexpr int kCols = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t at, uint32_t rank) {
-    uint32_t r;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
 
@@ -93,7 +91,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     __shared__ uint64_t full[kStages], scaled[kStages], empty[kStages], done;
     __shared__ uint32_t tmem_slot, loads;
     __shared__ int gave_up;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
     const int tile = blockIdx.x / a.split;
@@ -102,8 +100,9 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     const int steps = (a.ksteps + 3) / 4;
     const int s0 = (int)((int64_t)steps * rank / a.split), s1 = (int)((int64_t)steps * (rank + 1) / a.split);
 
-    if (warp == 5) tmem_alloc<1>(&tmem_slot, G::kCols);
-    if (threadIdx.x == 0) {
+    if (warp == 5) {
+        tmem_alloc<1>(&tmem_slot, G::kCols);
+    } else if (threadIdx.x == 128) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i]);
             mbar_init_count(&scaled[i], 4);
@@ -120,56 +119,74 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
-    if (warp == 4 && lane == 0) {
+    if (warp == 4) {
         const uint8_t* psf = a.p_sf + (int64_t)(p0 / 128) * a.sf_across * 512;
         const uint8_t* qsf = a.q_sf + (int64_t)(q0 / 128) * a.sf_across * 512;
-        uint32_t n = 0;
+        uint32_t st = 0, round = 0, n = 0;
+        bool ok = true;
         for (int s = s0; s < s1; ++s, ++n) {
-            const uint32_t st = n % kStages, at = base + st * G::kStageBytes;
-            if (!mbar_wait(&empty[st], ((n / kStages) & 1) ^ 1)) {
-                gave_up = 1;
+            if (!mbar_wait(&empty[st], (round & 1) ^ 1)) {
+                ok = false;
                 break;
             }
+            const uint32_t at = base + st * G::kStageBytes, sf = at + G::kPBytes + G::kQBytes;
             const int t0 = s * G::kSfTiles, nt = min(G::kSfTiles, a.sf_across - t0);
-            expect_bytes(&full[st], G::kPBytes + G::kQBytes + nt * 512 * 2);
-            tile_load(at, &map_p, s * kStepBytes, p0, &full[st]);
-            tile_load(at + G::kPBytes, &map_q, s * kStepBytes, q0, &full[st]);
-            const uint32_t sf = at + G::kPBytes + G::kQBytes;
-            block_load(sf, psf + (int64_t)t0 * 512, nt * 512, &full[st]);
-            block_load(sf + G::kSfTiles * 512, qsf + (int64_t)t0 * 512, nt * 512, &full[st]);
+            if (elect_lane()) {
+                expect_bytes(&full[st], G::kPBytes + G::kQBytes + nt * 512 * 2);
+                tile_load(at, &map_p, s * kStepBytes, p0, &full[st]);
+                tile_load(at + G::kPBytes, &map_q, s * kStepBytes, q0, &full[st]);
+                block_load(sf, psf + (int64_t)t0 * 512, nt * 512, &full[st]);
+                block_load(sf + G::kSfTiles * 512, qsf + (int64_t)t0 * 512, nt * 512, &full[st]);
+            }
+            __syncwarp();
+            if (++st == kStages) st = 0, ++round;
         }
         // the tensor core's last arrivals land before the CTA may go
-        for (uint32_t i = n > kStages ? n - kStages : 0; i < n && !gave_up; ++i)
-            if (!mbar_wait(&empty[i % kStages], (i / kStages) & 1)) gave_up = 1;
-        loads = n;
-    } else if (warp == 5 && lane == 0) {
-        uint32_t n = 0;
-        for (int s = s0; s < s1; ++s, ++n) {
-            const uint32_t st = n % kStages, at = base + st * G::kStageBytes;
-            if (!mbar_wait(&full[st], (n / kStages) & 1) || !mbar_wait(&scaled[st], (n / kStages) & 1)) {
-                gave_up = 1;
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n && ok; ++i) ok = mbar_wait(&empty[i % kStages], (i / kStages) & 1);
+        if (lane == 0) {
+            if (!ok) gave_up = 1;
+            loads = n;
+        }
+    } else if (warp == 5) {
+        uint32_t st = 0, round = 0;
+        bool ok = true;
+        for (int s = s0; s < s1; ++s) {
+            if (!mbar_wait(&full[st], round & 1) || !mbar_wait(&scaled[st], round & 1)) {
+                ok = false;
                 break;
             }
             tc_fence_after();
             const int nk = min(4, a.ksteps - s * 4);
+            const uint32_t at = base + st * G::kStageBytes;
+            const uint64_t dp = desc_codes(at), dq = desc_codes(at + G::kPBytes);
             const uint32_t tp = tmem + G::kAccCols + st * G::kSfCols, tq = tp + G::kSfTiles * 4;
-            for (int k = 0; k < nk; ++k) {
-                const int t = FMT == FP8Q_MXFP4 ? k >> 1 : k;
-                const uint32_t idesc = FMT == FP8Q_MXFP4 && (k & 1) ? mma_desc<FMT>(128, BN, 2) : mma_desc<FMT>(128, BN, 0);
-                tc_mma<FMT, 1>(tmem, desc_codes(at + k * 32), desc_codes(at + G::kPBytes + k * 32), idesc, tp + t * 4, tq + t * 4, n | k);
-            }
-            tc_commit(&empty[st]);
-        }
-        tc_commit(&done);
-    } else if (warp < 4) {
-        uint32_t n = 0;
-        for (int s = s0; s < s1; ++s, ++n) {
-            const uint32_t st = n % kStages;
-            if (!mbar_wait_warp(&full[st], (n / kStages) & 1, 0)) {
-                gave_up = 1;
-                break;
+            if (elect_lane()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = FMT == FP8Q_MXFP4 ? k >> 1 : k;
+                    constexpr uint32_t kEven = mma_desc<FMT>(128, BN, 0), kOdd = mma_desc<FMT>(128, BN, 2);
+                    if (k < nk)  // a step of 64 codes is 32 bytes on
+                        tc_mma<FMT, 1>(tmem, dp + k * 2, dq + k * 2, FMT == FP8Q_MXFP4 && (k & 1) ? kOdd : kEven, tp + t * 4, tq + t * 4,
+                                       (s - s0) | k);
+                }
+                tc_commit(&empty[st]);
+                if (s == s1 - 1) tc_commit(&done);
             }
             __syncwarp();
+            if (++st == kStages) st = 0, ++round;
+        }
+        if (!ok && elect_lane()) {
+            tc_commit(&done);
+            gave_up = 1;
+        }
+    } else {
+        uint32_t st = 0, round = 0;
+        bool ok = true;
+        for (int s = s0; s < s1; ++s) {
+            if (!mbar_wait(&full[st], round & 1)) {
+                ok = false;
+                break;
+            }
             const uint32_t sf = base + st * G::kStageBytes + G::kPBytes + G::kQBytes;
             const uint32_t to = tmem + ((uint32_t)(warp * 32) << 16) + G::kAccCols + st * G::kSfCols;
             if constexpr (FMT == FP8Q_MXFP4) {
@@ -180,25 +197,27 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
             }
             scales_stored();
             if (lane == 0) arrive_local(&scaled[st]);
+            if (++st == kStages) st = 0, ++round;
         }
+        if (!mbar_wait_warp(&done, 0, 0) || !ok) gave_up = 1;
     }
     __syncwarp();
-    if (warp < 4 && !mbar_wait_warp(&done, 0, 0)) gave_up = 1;
     __syncthreads();
     tc_fence_after();
     const float alpha = __fmul_rn(a.sa ? __ldg(a.sa) : 1.0f, a.sb ? __ldg(a.sb) : 1.0f);
     // A wait that ran out (correct operation never gets there) shows as NaN in the whole tile.
     const float nan = __uint_as_float(0x7FFFFFFFu);
-    const int p = p0 + warp * 32 + lane;
+    const int bad = gave_up;
     if (a.split == 1) {
         if (warp < 4) {
+            const int p = p0 + warp * 32 + lane;
             const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16);
 #pragma unroll 1
             for (int c = 0; c < BN; c += 16) {
                 float v[16];
                 tmem_load16(row + c, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = gave_up ? nan : __fmul_rn(v[i], alpha);
+                for (int i = 0; i < 16; ++i) v[i] = bad ? nan : __fmul_rn(v[i], alpha);
                 const int left = a.q_rows - (q0 + c);
                 if (p < a.p_rows && left > 0) {
                     if (a.p_is_m) {
@@ -213,37 +232,48 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
             }
         }
     } else {
-        // the partial sums in shared memory, a column's 128 rows side by side; each CTA adds
-        // its share of the columns over the cluster in rank order
-        float* part = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
+        // the partial sums in shared memory, a column's 128 rows side by side; each CTA adds its
+        // share of them over the cluster in rank order, four rows a thread
         if (warp < 4) {
+            float* part = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
             const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16);
 #pragma unroll 1
             for (int c = 0; c < BN; c += 16) {
                 float v[16];
                 tmem_load16(row + c, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) part[(c + i) * 128 + warp * 32 + lane] = gave_up ? nan : v[i];
+                for (int i = 0; i < 16; ++i) part[(c + i) * 128 + warp * 32 + lane] = bad ? nan : v[i];
             }
         }
         cluster_sync_all();
-        if (warp < 4) {
-            for (int c = rank; c < BN && q0 + c < a.q_rows; c += a.split) {
-                const uint32_t at = base + (c * 128 + warp * 32 + lane) * 4;
-                float v = 0.0f;
-                for (int r = 0; r < a.split; ++r) v += ld_cluster_f32(at, r);
-                v = __fmul_rn(v, alpha);
-                if (p < a.p_rows) {
-                    if (a.p_is_m)
-                        store_one<F32>(a.d, (int64_t)p * a.ld + q0 + c, v);
-                    else
-                        store_one<F32>(a.d, (int64_t)(q0 + c) * a.ld + p, v);
-                }
+        const int share = BN * 32 / a.split;
+        for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += 192) {
+            const int q = q0 + (i >> 5), p = p0 + (i & 31) * 4;
+            float4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < a.split) v[r] = ld_cluster_f32x4(in_cluster(base + i * 16, r));
+            float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < a.split) f[0] += v[r].x, f[1] += v[r].y, f[2] += v[r].z, f[3] += v[r].w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = __fmul_rn(f[k], alpha);
+            const int64_t at = (int64_t)q * a.ld + p;  // split tiles have D's rows along P
+            if (q < a.q_rows && a.vec && p < a.p_rows) {
+                if (F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.d) + at) = make_float4(f[0], f[1], f[2], f[3]);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.d) + at) = make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
+            } else if (q < a.q_rows) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (p + k < a.p_rows) store_one<F32>(a.d, at + k, f[k]);
             }
         }
         cluster_sync_all();  // no CTA's sums go away while another reads them
     }
-    if (gave_up && threadIdx.x == 0)  // copies still under way end before the CTA does
+    if (bad && threadIdx.x == 0)  // copies still under way end before the CTA does
         for (uint32_t n = loads > kStages ? loads - kStages : 0; n < loads; ++n) mbar_wait(&full[n % kStages], (n / kStages) & 1);
     tc_fence_before();
     __syncthreads();
@@ -665,29 +695,38 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     g.ksteps = (int32_t)((k + 63) / 64);
     g.sf_across = (int32_t)fp4_sf_tiles<FMT>(k);
     g.vec = ((uintptr_t)d & 15u) == 0 && n % (F32 ? 4 : 8) == 0;
-    // P, the 128 lanes, is the operand with more rows; with D's rows too short for whole
-    // vectors the lanes run along D's rows, so that a warp's stores are contiguous
-    const bool pairs = (m + 255) / 256 * ((n + 255) / 256) >= 64;
-    g.p_is_m = g.vec && (pairs || m >= n);
+    // Pairs of CTAs where 128-row tiles of one CTA each would not all be resident at once.
+    const int sms = sm_count();
+    const bool pairs = m > 128 && n > 128 && (m + 127) / 128 * ((n + 127) / 128) > sms;
+    // Otherwise few tiles share out their sums over clusters, while every CTA is resident (two an SM up to 32
+    // rows of Q; clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and keeps four steps or more: 1x4096x4096 takes 7.4 us
+    // on 32 CTAs, 5.8 on clusters of 4; 128x4096x4096 9.6 and 8.2.
+    const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, steps = (g.ksteps + 3) / 4;
+    int split = 1;
+    if (!pairs) {
+        const int64_t tiles = (n + 127) / 128 * ((m + bn - 1) / bn), room = (bn <= 32 ? 2 : 1) * sms;
+        while (split < 8 && tiles * split * 2 <= room * (split == 1 ? 20 : split == 2 ? 19 : 16) / 20 && steps >= split * 8) split *= 2;
+    }
+    g.split = split;
+    // P, whose rows are the accumulators' 128 lanes, is A, and a thread holds part of a row of D, where
+    // D's rows hold whole vectors; otherwise the lanes run along D's rows, so that a warp's stores are
+    // contiguous, as they are where few rows of A leave the lanes to B.
+    g.p_is_m = g.vec && split == 1 && (pairs || m >= n);
     const uint8_t *p = g.p_is_m ? a : b, *q = g.p_is_m ? b : a;
     g.p_sf = g.p_is_m ? a_sf : b_sf;
     g.q_sf = g.p_is_m ? b_sf : a_sf;
     g.p_rows = (int32_t)(g.p_is_m ? m : n);
     g.q_rows = (int32_t)(g.p_is_m ? n : m);
     if (pairs) return launch_pairs<FMT, F32>(p, q, k, g, s);
-    const int bn = g.q_rows <= 16 ? 16 : g.q_rows <= 32 ? 32 : g.q_rows <= 64 ? 64 : 128;
-    g.q_tiles = (g.q_rows + bn - 1) / bn;
+    const int qn = g.p_is_m ? (n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128) : bn;
+    g.q_tiles = (g.q_rows + qn - 1) / qn;
     const int64_t tiles = (int64_t)((g.p_rows + 127) / 128) * g.q_tiles;
-    const int steps = (g.ksteps + 3) / 4;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * 152 && steps >= split * 4) split *= 2;
-    g.split = split;
     if (tiles * split > 0x7FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
     CUtensorMap mp, mq;
-    if (!codes_map(&mp, p, g.p_rows, k, 128) || !codes_map(&mq, q, g.q_rows, k, bn))
+    if (!codes_map(&mp, p, g.p_rows, k, 128) || !codes_map(&mq, q, g.q_rows, k, qn))
         return cuda_fail(cudaErrorInvalidValue, "fp4_matmul_kernel tensor map");
     const unsigned grid = (unsigned)(tiles * split);
-    switch (bn) {
+    switch (qn) {
         case 16: return launch_tiles<FMT, 16, F32>(mp, mq, g, grid, s);
         case 32: return launch_tiles<FMT, 32, F32>(mp, mq, g, grid, s);
         case 64: return launch_tiles<FMT, 64, F32>(mp, mq, g, grid, s);
