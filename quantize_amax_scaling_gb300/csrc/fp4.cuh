@@ -17,7 +17,21 @@
 
 #include "fp8q_common.cuh"
 
+#include <atomic>
+
 namespace {
+
+// A kernel's shared-memory limit, set on its first call on each device.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& devices) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (devices.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) devices.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
 
 inline bool valid_fp4(int fmt) { return fmt == FP8Q_MXFP4 || fmt == FP8Q_NVFP4; }
 
@@ -33,6 +47,10 @@ __host__ __device__ inline int64_t fp4_row_bytes(int64_t cols) { return (cols + 
 template <int FMT>
 __host__ __device__ inline int64_t fp4_sf_tiles(int64_t cols) {  // scale tiles a row of tiles
     return (cols + Fp4<FMT>::kSfCols - 1) / Fp4<FMT>::kSfCols;
+}
+
+__device__ __forceinline__ void st_v2(void* p, uint2 v) {
+    asm volatile("st.global.cs.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // Four pairs of binary32 values -> eight e2m1 codes (nearest, ties to even,

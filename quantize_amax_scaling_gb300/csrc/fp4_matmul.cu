@@ -618,18 +618,6 @@ bool result_map(CUtensorMap* map, void* d, int64_t rows, int64_t cols) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A kernel's shared-memory limit, set on its first call on each device.
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& devices) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && (devices.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64) devices.fetch_or(1ull << dev, std::memory_order_release);
-    return e;
-}
-
 template <int FMT, int BN, bool F32>
 fp8q_status launch_tiles(const CUtensorMap& mp, const CUtensorMap& mq, const MmArgs& a, unsigned grid, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};

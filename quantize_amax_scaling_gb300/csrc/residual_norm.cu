@@ -13,9 +13,11 @@
 // so one reduction of three sums gives both means.
 //   dg2 = sum dh n2, dg1 = sum alpha gate D n1, dgate = sum alpha D n1 g1.
 //
-// Both kernels stream HBM; a thread holds 16 columns of a row in registers as
-// four groups of four (8-byte loads of the bf16 tensors, 16-byte loads of the
-// binary32 weights, both contiguous across a warp; the weights come from L1).
+// Both kernels stream HBM.  Rows are dealt out in strips of consecutive rows, a
+// strip to each T threads; a thread has 16 (or 32) columns of a row, in groups of
+// eight, and brings the next rows of its strip into shared memory by asynchronous
+// copies of its own (it alone reads them, so they need no barrier), while the
+// weights of its columns stay in registers.
 
 #include "fp4.cuh"
 
@@ -35,32 +37,61 @@ struct RnArgs {
     const float *post, *pre, *scale;
     const void* gate;
     float *amax, *rstd_post, *rstd_pre;
-    int64_t rows, per;
+    int64_t rows, per, per_strip;
     int32_t H, T, gate_bf16;
     float alpha, eps;
 };
 
-__device__ __forceinline__ void widen4(uint2 v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
 }
 
-__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
+    return make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p)), w = __ldg(reinterpret_cast<const float4*>(p) + 1);
     f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    f[4] = w.x; f[5] = w.y; f[6] = w.z; f[7] = w.w;
 }
 
-__device__ __forceinline__ void load_gate4(const void* g, int is_bf16, int64_t at, float (&f)[4]) {
+__device__ __forceinline__ void load_gate8(const void* g, int is_bf16, int64_t at, float (&f)[8]) {
     if (is_bf16)
-        widen4(__ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + at)), f);
+        widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + at)), f);
     else
-        load4(static_cast<const float*>(g) + at, f);
+        load8(static_cast<const float*>(g) + at, f);
 }
 
-__device__ __forceinline__ void st_v2(void* p, uint2 v) {
-    asm volatile("st.global.cs.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+// Sixteen bytes from global to shared memory, or zeros (then nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// Eight gate values that lie in the ring: one 16-byte slot of bf16, or two of binary32.
+__device__ __forceinline__ void ring_gate8(uint32_t at, uint32_t step, int is_bf16, float (&f)[8]) {
+    const uint4 v = ld_shared(at);
+    if (is_bf16) {
+        widen8(v, f);
+    } else {
+        const uint4 w = ld_shared(at + step);
+        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+        f[4] = __uint_as_float(w.x); f[5] = __uint_as_float(w.y); f[6] = __uint_as_float(w.z); f[7] = __uint_as_float(w.w);
+    }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -70,8 +101,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sum over the T threads of a row (T a multiple of 32; every thread of the CTA
-// calls it).  `part` holds one float a warp and is not used again before the
-// next barrier.
+// calls it).  `part` holds one float a warp and is not written again before the
+// next barrier but one.
 __device__ __forceinline__ float row_sum(float v, int T, float* part) {
     v = warp_sum(v);
     if (T == 32) return v;
@@ -83,125 +114,215 @@ __device__ __forceinline__ float row_sum(float v, int T, float* part) {
     return v;
 }
 
-// Codes of four columns of h (bf16 pairs in w), a warp together, as
-// fp8q_quantize_amax or fp8q_fp4_quantize_amax give them.
+// Codes of eight columns of h, a warp together, as fp8q_quantize_amax or
+// fp8q_fp4_quantize_amax give them.
 template <int FMT>
-__device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, const Fp4Scale& c4, int64_t row, int64_t col,
-                                            bool live, uint2 w) {
+__device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, const Fp4Scale& c4, int64_t row, int col, bool live,
+                                            const uint4& w) {
     if constexpr (FMT == FP8Q_E4M3FN || FMT == FP8Q_E5M2) {
-        const uint32_t o = c8.fast ? quant_quad<FMT, true>(w.x, w.y, c8) : quant_quad<FMT, false>(w.x, w.y, c8);
-        if (live && col < a.H) *reinterpret_cast<uint32_t*>(a.q + row * a.H + col) = o;
+        uint2 o;
+        if (c8.fast)
+            o = make_uint2(quant_quad<FMT, true>(w.x, w.y, c8), quant_quad<FMT, true>(w.z, w.w, c8));
+        else
+            o = make_uint2(quant_quad<FMT, false>(w.x, w.y, c8), quant_quad<FMT, false>(w.z, w.w, c8));
+        if (live && col < a.H) st_v2(a.q + row * a.H + col, o);
     } else if constexpr (FMT == FP8Q_MXFP4 || FMT == FP8Q_NVFP4) {
-        constexpr int kLanes = Fp4<FMT>::kBlock / 4;  // lanes a block
-        const uint32_t m = bf16x2_absmax(w.x, w.y);
+        constexpr int kLanes = Fp4<FMT>::kBlock / 8;  // lanes a block
+        const uint32_t m = bf16x2_absmax(bf16x2_absmax(w.x, w.y), bf16x2_absmax(w.z, w.w));
         uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
         const BlockScale b = block_scale<FMT>(am, c4);
-        const uint32_t full[8] = {w.x, w.y, 0, 0, 0, 0, 0, 0};
-        const uint32_t mine = block_codes<FMT>(full, b).x & 0xFFFFu;
-        const uint32_t both = mine | (__shfl_down_sync(0xFFFFFFFFu, mine, 1) << 16);
+        const uint32_t full[8] = {w.x, w.y, w.z, w.w, 0, 0, 0, 0};
+        const uint32_t mine = block_codes<FMT>(full, b).x;
         const int64_t ld = fp4_row_bytes(a.H);
-        if (live && (threadIdx.x & 1) == 0 && col < 2 * ld)
-            *reinterpret_cast<uint32_t*>(a.q + row * ld + col / 2) = both;
+        if (live && col < 2 * ld) *reinterpret_cast<uint32_t*>(a.q + row * ld + col / 2) = mine;
         uint32_t s = b.code;
         s |= __shfl_down_sync(0xFFFFFFFFu, b.code, kLanes) << 8;
         s |= __shfl_down_sync(0xFFFFFFFFu, b.code, 2 * kLanes) << 16;
         s |= __shfl_down_sync(0xFFFFFFFFu, b.code, 3 * kLanes) << 24;
         const int64_t across = fp4_sf_tiles<FMT>(a.H), tile = col / Fp4<FMT>::kSfCols;
         if (live && (threadIdx.x & 31) % (4 * kLanes) == 0 && tile < across)
-            *reinterpret_cast<uint32_t*>(a.sf + ((row / 128) * across + tile) * 512 + (row % 32) * 16 +
-                                         (row % 128) / 32 * 4) = s;
+            *reinterpret_cast<uint32_t*>(a.sf + ((row / 128) * across + tile) * 512 + (row % 32) * 16 + (row % 128) / 32 * 4) = s;
     }
 }
 
-// U groups of four columns a thread; a row takes T threads, a CTA blockDim / T rows.
-template <int FMT, int U>
-__global__ void __launch_bounds__(1024) residual_norm_kernel(const RnArgs a) {
-    __shared__ float part[2][32];
+// U groups of eight columns a thread.  WREG: the weights stay in registers (rows
+// of up to 512 threads); longer rows, with 64 registers a thread, read them from
+// L1 for each row, and the longest have room for one row ahead in shared memory.
+template <int FMT, int U, bool WREG>
+__global__ void __launch_bounds__(WREG ? 512 : 1024) residual_norm_kernel(const RnArgs a) {
+    extern __shared__ __align__(16) uint8_t ring_raw[];
+    __shared__ float part[4][32];
     __shared__ uint32_t red[32];
     const int T = a.T, t = threadIdx.x % T;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
-    const bool live = row < a.rows;
-    uint2 b[U], r[U];
+    const int64_t strip = (int64_t)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
+    const int64_t row0 = strip * a.per_strip, row1 = min(row0 + a.per_strip, a.rows);
+    constexpr int kStages = U == 2 ? 3 : 1;  // rows under way
+    const bool ring_gate = WREG && a.gate && a.per == 1;
+    const uint32_t step = blockDim.x * 16;  // from one slot to the next
+    const uint32_t slots = 1 + (a.b != nullptr) + (ring_gate ? (a.gate_bf16 ? 1 : 2) : 0);
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) + threadIdx.x * 16;
+
+    auto fetch = [&](int64_t row, uint32_t stage) {
+        const bool live = row < row1;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int col = (u * T + t) * 4;
-        b[u] = r[u] = make_uint2(0, 0);
-        if (live && col < a.H) {
-            r[u] = ld_stream_v2(a.r + row * a.H + col);
-            if (a.b) b[u] = ld_stream_v2(a.b + row * a.H + col);
-        }
-    }
-    if (a.b) {
-        float rstd = 1.0f;
-        if (a.post) {
-            float s = 0.0f;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float f[4];
-                widen4(b[u], f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s = fmaf(f[i], f[i], s);
+        for (int u = 0; u < U; ++u) {
+            const int col = (u * T + t) * 8;
+            const bool on = live && col < a.H;
+            const int64_t at = on ? row * a.H + col : 0;
+            uint32_t dst = ring + (stage * U + u) * slots * step;
+            copy16(dst, a.r + at, on);
+            if (a.b) copy16(dst += step, a.b + at, on);
+            if (ring_gate) {
+                if (a.gate_bf16) {
+                    copy16(dst += step, static_cast<const uint16_t*>(a.gate) + at, on);
+                } else {
+                    copy16(dst += step, static_cast<const float*>(a.gate) + at, on);
+                    copy16(dst += step, static_cast<const float*>(a.gate) + at + (on ? 4 : 0), on);
+                }
             }
-            s = row_sum(s, T, part[0]);
-            rstd = __frcp_rn(__fsqrt_rn(s / (float)a.H + a.eps));
-            if (a.rstd_post && live && t == 0) a.rstd_post[row] = rstd;
         }
-        const int64_t g0 = a.gate && live ? row / a.per * a.H : 0;
+        copies_commit();
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int col = (u * T + t) * 4;
-            if (!live || col >= a.H) continue;
-            float f[4], x[4], p[4] = {1, 1, 1, 1}, g[4] = {1, 1, 1, 1};
-            widen4(b[u], f);
-            widen4(r[u], x);
-            if (a.post) load4(a.post + col, p);
-            if (a.gate) load_gate4(a.gate, a.gate_bf16, g0 + col, g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = fmaf(a.alpha * g[i], f[i] * rstd * p[i], x[i]);
-            r[u] = make_uint2(cvt_bf16x2(x[0], x[1]), cvt_bf16x2(x[2], x[3]));
-        }
-    }
-    if (a.ro) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int col = (u * T + t) * 4;
-            if (live && col < a.H) st_v2(a.ro + row * a.H + col, r[u]);
-        }
-    }
-    if (!a.pre) return;
-    float s = 0.0f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float f[4];
-        widen4(r[u], f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fmaf(f[i], f[i], s);
-    }
-    s = row_sum(s, T, part[1]);
-    const float rstd = __frcp_rn(__fsqrt_rn(s / (float)a.H + a.eps));
-    if (a.rstd_pre && live && t == 0) a.rstd_pre[row] = rstd;
+    for (int i = 0; i < kStages; ++i) fetch(i < a.per_strip ? row0 + i : row1, i);
+
     QScale c8;
     Fp4Scale c4;
     if constexpr (FMT == FP8Q_E4M3FN || FMT == FP8Q_E5M2) c8 = make_qscale(a.scale);
     if constexpr (FMT == FP8Q_MXFP4 || FMT == FP8Q_NVFP4) c4 = make_fp4_scale(a.scale);
-    uint32_t m2 = 0;
+    // alpha * gate * post of a column, without the gate where it comes with the row
+    auto weight = [&](int u, int64_t group, float (&w)[8]) {
+        const int col = (u * T + t) * 8;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int col = (u * T + t) * 4;
-        uint2 o = make_uint2(0, 0);
-        if (live && col < a.H) {
-            float f[4], g[4];
-            widen4(r[u], f);
-            load4(a.pre + col, g);
+        for (int i = 0; i < 8; ++i) w[i] = a.alpha;
+        if (col >= a.H) return;
+        float f[8];
+        if (a.gate && !ring_gate) {
+            load_gate8(a.gate, a.gate_bf16, group * a.H + col, f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = f[i] * rstd * g[i];
-            o = make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
-            m2 = bf16x2_absmax(m2, bf16x2_absmax(o.x, o.y));
-            if (a.h) st_v2(a.h + row * a.H + col, o);
+            for (int i = 0; i < 8; ++i) w[i] *= f[i];
         }
-        if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, col, live, o);
+        if (a.post) {
+            load8(a.post + col, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] *= f[i];
+        }
+    };
+    float W[WREG ? U : 1][8], P[WREG ? U : 1][8];
+    int64_t group = a.gate && !ring_gate ? row0 / a.per : 0, gend = a.gate && !ring_gate ? (group + 1) * a.per : a.rows;
+    if constexpr (WREG) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (a.b && row0 < a.rows) weight(u, group, W[u]);
+            if (a.pre && (u * T + t) * 8 < a.H) load8(a.pre + (u * T + t) * 8, P[u]);
+        }
+    }
+    const float inv_h = 1.0f / (float)a.H;
+    uint32_t m2 = 0, stage = 0;
+    for (int64_t it = 0; it < a.per_strip; ++it) {
+        const int64_t row = row0 + it;
+        const bool live = row < row1;
+        if (row == gend) {
+            ++group;
+            gend += a.per;
+            if constexpr (WREG) {
+                if (live)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) weight(u, group, W[u]);
+            }
+        }
+        copies_wait<kStages - 1>();
+        uint4 r[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t at = ring + (stage * U + u) * slots * step;
+            r[u] = ld_shared(at);
+            b[u] = a.b ? ld_shared(at + step) : make_uint4(0, 0, 0, 0);
+        }
+        if (a.b) {
+            float rstd = 1.0f;
+            if (a.post) {
+                float s = 0.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[8];
+                    widen8(b[u], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
+                }
+                s = row_sum(s, T, part[(it & 1) * 2]);
+                rstd = __frcp_rn(__fsqrt_rn(fmaf(s, inv_h, a.eps)));
+                if (a.rstd_post && live && t == 0) a.rstd_post[row] = rstd;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[8], x[8], g[8], w[8];
+                widen8(b[u], f);
+                widen8(r[u], x);
+                if constexpr (WREG) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = W[u][i];
+                } else if (live) {
+                    weight(u, group, w);
+                }
+                if (ring_gate) {
+                    ring_gate8(ring + ((stage * U + u) * slots + 2) * step, step, a.gate_bf16, g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] *= g[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fmaf(w[i], f[i] * rstd, x[i]);
+                r[u] = narrow8(x);
+            }
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int col = (u * T + t) * 8;
+            if (!live || col >= a.H) r[u] = make_uint4(0, 0, 0, 0);
+            float f[8];
+            widen8(r[u], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
+        }
+        // everything of this stage has been used: the row after the next ones into it
+        fetch(it + kStages < a.per_strip ? row + kStages : row1, stage);
+        if (++stage == kStages) stage = 0;
+        if (a.ro && live) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int col = (u * T + t) * 8;
+                if (col < a.H) st_v4(a.ro + row * a.H + col, r[u]);
+            }
+        }
+        if (!a.pre) continue;
+        s = row_sum(s, T, part[(it & 1) * 2 + 1]);
+        const float rstd = __frcp_rn(__fsqrt_rn(fmaf(s, inv_h, a.eps)));
+        if (a.rstd_pre && live && t == 0) a.rstd_pre[row] = rstd;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int col = (u * T + t) * 8;
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (live && col < a.H) {
+                float f[8];
+                widen8(r[u], f);
+                if constexpr (WREG) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * P[u][i];
+                } else {
+                    float g[8];
+                    load8(a.pre + col, g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
+                }
+                o = narrow8(f);
+                m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(o.x, o.y), bf16x2_absmax(o.z, o.w)));
+                if (a.h) st_v4(a.h + row * a.H + col, o);
+            }
+            if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, col, live, o);
+        }
     }
     if (a.amax) {
         uint32_t m = max(abs_bits_lo(m2), m2 & 0x7FFF0000u);
@@ -213,6 +334,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const RnArgs a) {
             atomicMax(reinterpret_cast<int*>(a.amax), (int)m);  // ordered like the values (flush_amax)
         }
     }
+    copies_wait<0>();
 }
 
 // ----------------------------------------------------------------------------
@@ -256,16 +378,28 @@ struct RnBwdArgs {
     float alpha;
 };
 
-__device__ __forceinline__ void store_gate4(void* p, int is_bf16, int64_t at, const float (&f)[4]) {
-    if (is_bf16)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
-    else
-        *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-template <bool CLUSTER>
-__global__ void __launch_bounds__(256) residual_norm_backward_kernel(const RnBwdArgs a) {
+__device__ __forceinline__ void store_gate8(void* p, int is_bf16, int64_t at, const float (&f)[8]) {
+    if (is_bf16)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = narrow8(f);
+    else
+        store8(static_cast<float*>(p) + at, f);
+}
+
+// Per row: one pass for the three sums, one for the gradients, both from shared
+// memory (kept in registers between them, a row would spill).  With X = D n1 and W = alpha gate g1 of a column, a row
+// adds X to the one sum S that dgate and dg1 share: a gate's row of dgate is
+// alpha g1 S, and dg1 takes alpha gate S whenever a gate's rows end.  RING_GATE:
+// each row has its own gate, which comes with it.
+template <bool CLUSTER, bool RING_GATE>
+__global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const RnBwdArgs a) {
     namespace cg = cooperative_groups;
+    constexpr int kStages = RING_GATE ? 2 : 3;
+    extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float part[2][8][3];
     __shared__ float sums[2][8][3];  // of each CTA of the cluster
     const int T = a.T, t = threadIdx.x % T, warp = threadIdx.x >> 5;
@@ -278,50 +412,97 @@ __global__ void __launch_bounds__(256) residual_norm_backward_kernel(const RnBwd
     const int64_t row0 = strip * a.per_strip, row1 = min(row0 + a.per_strip, a.rows);
     const int c0 = slice * a.width, c1 = min(c0 + a.width, a.H);  // this CTA's columns
     const float inv_h = 1.0f / (float)a.H;
+    // ring: a stage holds, for each of two groups of eight columns, a slot of b, r', dr', dh and one
+    // or two of the gate; behind it this thread's sums of dg1
+    constexpr uint32_t kStep = 256 * 16;
+    const uint32_t slots = RING_GATE ? (a.gate_bf16 ? 5 : 6) : 4;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) + threadIdx.x * 16;
+    float4* const post_sum = reinterpret_cast<float4*>(ring_raw + kStages * 2 * slots * kStep) + threadIdx.x;
 
-    float apre[4][4] = {}, apost[4][4] = {}, agate[4][4] = {};
+    auto fetch = [&](int64_t row, uint32_t stage) {
+        const bool live = row < row1;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int col = c0 + (u * T + t) * 8;
+            const bool on = live && col < c1;
+            const int64_t at = on ? row * a.H + col : 0;
+            const uint32_t dst = ring + (stage * 2 + u) * slots * kStep;
+            if (a.b) copy16(dst, a.b + at, on);
+            if (a.dh) {
+                copy16(dst + kStep, a.ro + at, on);
+                copy16(dst + 3 * kStep, a.dh + at, on);
+            }
+            if (a.dro) copy16(dst + 2 * kStep, a.dro + at, on);
+            if (RING_GATE) {
+                if (a.gate_bf16) {
+                    copy16(dst + 4 * kStep, static_cast<const uint16_t*>(a.gate) + at, on);
+                } else {
+                    copy16(dst + 4 * kStep, static_cast<const float*>(a.gate) + at, on);
+                    copy16(dst + 5 * kStep, static_cast<const float*>(a.gate) + at + (on ? 4 : 0), on);
+                }
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(i < a.per_strip ? row0 + i : row1, i);
+
     int64_t group = a.gate ? row0 / a.per : 0;
-    int64_t gend = a.gate ? (group + 1) * a.per : 0;  // first row behind the group
-    bool whole = a.gate && group * a.per >= row0;     // the group began in this strip
+    int64_t gend = a.gate ? (group + 1) * a.per : a.rows;  // first row behind the group
+    bool whole = a.gate && group * a.per >= row0;          // the group began in this strip
+    float Q[2][8], W[2][8], S[2][8] = {}, apre[2][8] = {};
+    // alpha * gate * post of a column, without a gate that comes with the row
+    auto weight = [&](int u) {
+        const int col = c0 + (u * T + t) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) W[u][i] = a.alpha;
+        if (col >= c1) return;
+        float f[8];
+        if (a.post) {
+            load8(a.post + col, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) W[u][i] *= f[i];
+        }
+        if (a.gate && !RING_GATE) {
+            load_gate8(a.gate, a.gate_bf16, group * a.H + col, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) W[u][i] *= f[i];
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int col = c0 + (u * T + t) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) Q[u][i] = 0.0f;
+        if (a.dh && col < c1) load8(a.pre + col, Q[u]);
+        if (row0 < a.rows) weight(u);
+        post_sum[(2 * u) * 256] = post_sum[(2 * u + 1) * 256] = make_float4(0, 0, 0, 0);
+    }
 
+    uint32_t stage = 0;
     for (int64_t it = 0; it < a.per_strip; ++it) {
         const int64_t row = row0 + it;
         const bool live = row < row1;
-        uint2 vb[4], vo[4], vd[4], vh[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int col = c0 + (u * T + t) * 4;
-            const int64_t at = row * a.H + col;
-            vb[u] = vo[u] = vd[u] = vh[u] = make_uint2(0, 0);
-            if (live && col < c1) {
-                if (a.dro) vd[u] = ld_stream_v2(a.dro + at);
-                if (a.dh) {
-                    vh[u] = ld_stream_v2(a.dh + at);
-                    vo[u] = ld_stream_v2(a.ro + at);
-                }
-                if (a.b) vb[u] = ld_stream_v2(a.b + at);
-            }
-        }
-        const float rstd2 = a.dh && live ? a.rstd_pre[row] : 0.0f;
-        const float rstd1 = a.post && live ? a.rstd_post[row] : 1.0f;
-        const int64_t g0 = group * a.H;
+        const float rstd2 = a.dh && live ? __ldg(a.rstd_pre + row) : 0.0f;
+        const float rstd1 = a.post && live ? __ldg(a.rstd_post + row) : 1.0f;
+        copies_wait<kStages - 1>();
+        const uint32_t at_stage = ring + stage * 2 * slots * kStep;
+        const uint4 none = make_uint4(0, 0, 0, 0);
         float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int col = c0 + (u * T + t) * 4;
-            if (!live || col >= c1) continue;
-            float fo[4], fh[4], fd[4], fb[4], p[4] = {1, 1, 1, 1}, q[4] = {1, 1, 1, 1}, g[4] = {1, 1, 1, 1};
-            widen4(vo[u], fo);
-            widen4(vh[u], fh);
-            widen4(vd[u], fd);
-            widen4(vb[u], fb);
-            if (a.dh) load4(a.pre + col, q);
-            if (a.post) load4(a.post + col, p);
-            if (a.gate) load_gate4(a.gate, a.gate_bf16, g0 + col, g);
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t at = at_stage + u * slots * kStep;
+            float fb[8], fo[8], fd[8], fh[8], g[8];
+            widen8(a.b ? ld_shared(at) : none, fb);
+            widen8(a.dh ? ld_shared(at + kStep) : none, fo);
+            widen8(a.dro ? ld_shared(at + 2 * kStep) : none, fd);
+            widen8(a.dh ? ld_shared(at + 3 * kStep) : none, fh);
+            if (RING_GATE) ring_gate8(at + 4 * kStep, kStep, a.gate_bf16, g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float n2 = fo[i] * rstd2, dn = fh[i] * q[i];
-                const float w = a.alpha * g[i] * p[i] * (fb[i] * rstd1);
+            for (int i = 0; i < 8; ++i) {
+                const float n2 = fo[i] * rstd2, dn = fh[i] * Q[u][i];
+                float w = W[u][i] * (fb[i] * rstd1);
+                if (RING_GATE) w *= g[i];
                 s0 = fmaf(dn, n2, s0);
                 s1 = fmaf(w, fmaf(rstd2, dn, fd[i]), s1);
                 s2 = fmaf(w, n2, s2);
@@ -366,73 +547,90 @@ __global__ void __launch_bounds__(256) residual_norm_backward_kernel(const RnBwd
         }
         const float c2 = s0 * inv_h;
         const float m1 = a.post ? (s1 - rstd2 * c2 * s2) * inv_h : 0.0f;  // mean(w D); no term without g1
-        const bool flush = a.gate && live && (row + 1 == gend || row + 1 == row1);
+        const bool flush = live && a.b && (row + 1 == gend || row + 1 == row1);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int col = c0 + (u * T + t) * 4;
-            if (!live || col >= c1) continue;
+        for (int u = 0; u < 2; ++u) {
+            const int col = c0 + (u * T + t) * 8;
+            const bool on = live && col < c1;
             const int64_t at = row * a.H + col;
-            float fo[4], fh[4], D[4], fb[4], p[4] = {1, 1, 1, 1}, q[4] = {1, 1, 1, 1}, g[4] = {1, 1, 1, 1}, e[4];
-            widen4(vo[u], fo);
-            widen4(vh[u], fh);
-            widen4(vd[u], D);
-            widen4(vb[u], fb);
-            if (a.dh) load4(a.pre + col, q);
+            float fb[8], fo[8], D[8], fh[8], e[8], g[8];
+            const uint32_t from = at_stage + u * slots * kStep;
+            widen8(a.b ? ld_shared(from) : none, fb);
+            widen8(a.dh ? ld_shared(from + kStep) : none, fo);
+            widen8(a.dro ? ld_shared(from + 2 * kStep) : none, D);
+            widen8(a.dh ? ld_shared(from + 3 * kStep) : none, fh);
+            if (RING_GATE) ring_gate8(from + 4 * kStep, kStep, a.gate_bf16, g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float n2 = fo[i] * rstd2;
-                D[i] = fmaf(rstd2, fmaf(-n2, c2, fh[i] * q[i]), D[i]);
+                D[i] = fmaf(rstd2, fmaf(-n2, c2, fh[i] * Q[u][i]), D[i]);
                 apre[u][i] = fmaf(fh[i], n2, apre[u][i]);
+                const float n1 = fb[i] * rstd1;
+                S[u][i] = fmaf(D[i], n1, S[u][i]);
+                const float w = RING_GATE ? W[u][i] * g[i] : W[u][i];
+                e[i] = rstd1 * fmaf(-n1, m1, D[i] * w);
             }
-            if (a.dr) st_v2(a.dr + at, make_uint2(cvt_bf16x2(D[0], D[1]), cvt_bf16x2(D[2], D[3])));
-            if (!a.b) continue;
-            if (a.post) load4(a.post + col, p);
-            if (a.gate) load_gate4(a.gate, a.gate_bf16, g0 + col, g);
+            if (on && a.dr) st_v4(a.dr + at, narrow8(D));
+            if (on && a.db) st_v4(a.db + at, narrow8(e));
+            if (flush && on) {
+                float p[8], f[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float n1 = fb[i] * rstd1, aD = a.alpha * D[i];
-                const float dy = aD * g[i];
-                apost[u][i] = fmaf(dy, n1, apost[u][i]);
-                agate[u][i] = fmaf(aD, n1 * p[i], agate[u][i]);
-                e[i] = rstd1 * fmaf(-n1, m1, dy * p[i]);
-            }
-            if (a.db) st_v2(a.db + at, make_uint2(cvt_bf16x2(e[0], e[1]), cvt_bf16x2(e[2], e[3])));
-            if (flush) {
+                for (int i = 0; i < 8; ++i) p[i] = 1.0f;
+                if (a.post) load8(a.post + col, p);
+                if (a.gate && !RING_GATE) load_gate8(a.gate, a.gate_bf16, group * a.H + col, g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    S[u][i] *= a.alpha;
+                    f[i] = a.gate ? S[u][i] * g[i] : S[u][i];
+                    p[i] *= S[u][i];
+                    S[u][i] = 0.0f;
+                }
+                float4 lo = post_sum[(2 * u) * 256], hi = post_sum[(2 * u + 1) * 256];
+                lo.x += f[0]; lo.y += f[1]; lo.z += f[2]; lo.w += f[3];
+                hi.x += f[4]; hi.y += f[5]; hi.z += f[6]; hi.w += f[7];
+                post_sum[(2 * u) * 256] = lo;
+                post_sum[(2 * u + 1) * 256] = hi;
                 if (a.dgate) {
                     // a group that lies in this strip whole goes straight out
-                    if (whole && (row + 1 == gend || row + 1 == a.rows)) {
-                        store_gate4(a.dgate, a.gate_bf16, g0 + col, agate[u]);
-                    } else {
-                        float* sp = a.space + (2 * a.strips + 2 * strip + (whole ? 1 : 0)) * a.H + col;
-                        *reinterpret_cast<float4*>(sp) = make_float4(agate[u][0], agate[u][1], agate[u][2], agate[u][3]);
-                    }
+                    if (whole && (row + 1 == gend || row + 1 == a.rows))
+                        store_gate8(a.dgate, a.gate_bf16, group * a.H + col, p);
+                    else
+                        store8(a.space + (2 * a.strips + 2 * strip + (whole ? 1 : 0)) * a.H + col, p);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) agate[u][i] = 0.0f;
             }
         }
+        // this stage has been used: the row after the next ones into it
+        fetch(it + kStages < a.per_strip ? row + kStages : row1, stage);
+        if (++stage == kStages) stage = 0;
         if (a.gate && row + 1 == gend) {
             ++group;
             gend += a.per;
             whole = true;
+            if (!RING_GATE && row + 1 < row1) {
+                weight(0);
+                weight(1);
+            }
         }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int col = c0 + (u * T + t) * 4;
-        if (strip >= a.strips || col >= c1) continue;
-        if (a.dpre)
-            *reinterpret_cast<float4*>(a.space + strip * a.H + col) = make_float4(apre[u][0], apre[u][1], apre[u][2], apre[u][3]);
-        if (a.dpost)
-            *reinterpret_cast<float4*>(a.space + (a.strips + strip) * a.H + col) =
-                make_float4(apost[u][0], apost[u][1], apost[u][2], apost[u][3]);
+    for (int u = 0; u < 2; ++u) {
+        const int col = c0 + (u * T + t) * 8;
+        if (strip < a.strips && col < c1) {
+            if (a.dpre) store8(a.space + strip * a.H + col, apre[u]);
+            if (a.dpost) {
+                float4* o = reinterpret_cast<float4*>(a.space + (a.strips + strip) * a.H + col);
+                o[0] = post_sum[(2 * u) * 256];
+                o[1] = post_sum[(2 * u + 1) * 256];
+            }
+        }
     }
+    copies_wait<0>();
     if (CLUSTER) cg::this_cluster().sync();  // nobody's `sums` goes away while another CTA may write it
 }
 
-// 32 columns a CTA, 32 strips at a time: blockIdx.y 0 adds dpre, 1 dpost, and
-// 2 + s the group of dgate that lies across the border behind strip s, if it
-// began in that strip.
+// 32 columns a CTA, 32 strips at a time: blockIdx.y 0 adds dpre, 1 dpost, and from
+// 2 on a row of dgate that lies in several strips: row blockIdx.y - 2, where gates
+// span strips, or else the one across the border behind strip blockIdx.y - 2.
 __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs a) {
     __shared__ float t[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -445,11 +643,10 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs
         if (col < a.H)
             for (int64_t s = w; s < a.strips; s += 32) v += a.space[(what * a.strips + s) * a.H + col];
     } else {
-        const int64_t s0 = what - 2, border = (s0 + 1) * a.per_strip;
-        group = border / a.per;
+        group = a.per >= a.per_strip ? what - 2 : (what - 1) * a.per_strip / a.per;
         const int64_t begin = group * a.per, end = min(begin + a.per, a.rows);
-        if (begin == border || begin < s0 * a.per_strip) return;
-        const int64_t s1 = (end - 1) / a.per_strip;
+        const int64_t s0 = begin / a.per_strip, s1 = (end - 1) / a.per_strip;
+        if (s0 == s1 || (a.per < a.per_strip && s0 != what - 2)) return;  // in one strip, or another border's
         const float* sp = a.space + 2 * a.strips * a.H;
         if (col < a.H) {
             // its first rows are the tail of strip s0, the rest the heads of those that follow
@@ -472,10 +669,47 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs
     }
 }
 
+template <bool CLUSTER, bool RING_GATE>
+fp8q_status launch_backward(const RnBwdArgs& a, unsigned ctas, unsigned slices, cudaStream_t s) {
+    static std::atomic<uint64_t> devices{0};
+    auto kern = residual_norm_backward_kernel<CLUSTER, RING_GATE>;
+    const size_t smem = ((RING_GATE ? 2 * 2 * (a.gate_bf16 ? 5 : 6) : 3 * 2 * 4) + 4) * 4096;
+    cudaError_t e = allow_smem(kern, 112 * 1024, devices);
+    if (e != cudaSuccess) return cuda_fail(e, "residual_norm_backward_kernel setup");
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = slices;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = CLUSTER ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "residual_norm_backward_kernel");
+}
+
 template <int FMT>
-fp8q_status launch_forward(const RnArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
-    auto kern = a.H > 16384 ? residual_norm_kernel<FMT, 8> : residual_norm_kernel<FMT, 4>;
-    return launch_kernel(kern, grid, block, 0, s, "residual_norm_kernel", a);
+fp8q_status launch_forward(RnArgs a, cudaStream_t s) {
+    const int U = a.H > 16384 ? 4 : 2;
+    a.T = 1024;
+    while (a.T > 32 && a.H <= a.T * 4 * U) a.T /= 2;
+    const int block = a.T < 256 ? 256 : a.T, per_cta = block / a.T;
+    // strips: two CTAs of 256 threads an SM, one of 512 or 1024
+    const int64_t most = (int64_t)(block == 256 ? 2 : 1) * 152 * per_cta;
+    a.per_strip = (a.rows + most - 1) / most;
+    const int64_t strips = (a.rows + a.per_strip - 1) / a.per_strip;
+    const int slots = 1 + (a.b != nullptr) + (a.T < 1024 && a.gate && a.per == 1 ? (a.gate_bf16 ? 1 : 2) : 0);
+    const size_t smem = (size_t)(U == 2 ? 3 : 1) * U * slots * block * 16;
+    const dim3 grid((unsigned)((strips + per_cta - 1) / per_cta));
+    static std::atomic<uint64_t> devices[3];
+    auto kern = U == 4 ? residual_norm_kernel<FMT, 4, false> : a.T == 1024 ? residual_norm_kernel<FMT, 2, false> : residual_norm_kernel<FMT, 2, true>;
+    // 3 stages of 4 slots of 512 threads, or of 2 slots of 1024
+    const cudaError_t e = allow_smem(kern, 192 * 1024, devices[U == 4 ? 2 : a.T == 1024 ? 1 : 0]);
+    if (e != cudaSuccess) return cuda_fail(e, "residual_norm_kernel setup");
+    return launch_kernel(kern, grid, dim3(block), smem, s, "residual_norm_kernel", a);
 }
 
 bool misaligned(std::initializer_list<const void*> ps, uintptr_t mask) {
@@ -525,17 +759,13 @@ fp8q_status fp8q_residual_norm_quantize_amax(const fp8q_residual_norm* n, void* 
     a.gate_bf16 = n->gate_is_bf16 != 0;
     a.alpha = n->alpha;
     a.eps = n->eps;
-    a.T = 1024;
-    while (a.T > 32 && a.H <= a.T * 8) a.T /= 2;
-    const int block = a.T < 256 ? 256 : a.T, per_cta = block / a.T;
-    const dim3 grid((unsigned)((a.rows + per_cta - 1) / per_cta));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!a.q) return launch_forward<kOutNone>(a, grid, dim3(block), s);
+    if (!a.q) return launch_forward<kOutNone>(a, s);
     switch (n->fmt) {
-        case FP8Q_E4M3FN: return launch_forward<FP8Q_E4M3FN>(a, grid, dim3(block), s);
-        case FP8Q_E5M2: return launch_forward<FP8Q_E5M2>(a, grid, dim3(block), s);
-        case FP8Q_MXFP4: return launch_forward<FP8Q_MXFP4>(a, grid, dim3(block), s);
-        default: return launch_forward<FP8Q_NVFP4>(a, grid, dim3(block), s);
+        case FP8Q_E4M3FN: return launch_forward<FP8Q_E4M3FN>(a, s);
+        case FP8Q_E5M2: return launch_forward<FP8Q_E5M2>(a, s);
+        case FP8Q_MXFP4: return launch_forward<FP8Q_MXFP4>(a, s);
+        default: return launch_forward<FP8Q_NVFP4>(a, s);
     }
 }
 
@@ -592,27 +822,16 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t per_cta = 256 / st.T;
     const unsigned ctas = (unsigned)((st.strips + per_cta - 1) / per_cta) * (unsigned)st.slices;
-    fp8q_status rc;
-    if (st.slices == 1) {
-        rc = launch_kernel(residual_norm_backward_kernel<false>, dim3(ctas), dim3(256), 0, s, "residual_norm_backward_kernel", a);
-    } else {
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)st.slices;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(ctas);
-        cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, residual_norm_backward_kernel<true>, a);
-        rc = e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "residual_norm_backward_kernel");
-    }
+    const bool ring_gate = a.gate && a.per == 1;
+    const unsigned slices = (unsigned)st.slices;
+    const fp8q_status rc = slices == 1 ? (ring_gate ? launch_backward<false, true>(a, ctas, 1, s) : launch_backward<false, false>(a, ctas, 1, s))
+                                       : (ring_gate ? launch_backward<true, true>(a, ctas, slices, s) : launch_backward<true, false>(a, ctas, slices, s));
     if (rc != FP8Q_OK || (!a.dpre && !a.dpost && !spread)) return rc;
-    // borders that a group lies across there are only where strips are not whole groups
-    const bool borders = spread && st.strips > 1 && st.per_strip % n->rows_per_gate != 0;
-    const dim3 grid((unsigned)((n->hidden + 31) / 32), 2u + (borders ? (unsigned)(st.strips - 1) : 0u));
+    // rows of dgate to add up: those of a gate that spans strips, or the ones across their borders
+    int64_t across = 0;
+    if (spread && st.strips > 1 && st.per_strip % a.per != 0)
+        across = a.per >= st.per_strip ? (a.rows + a.per - 1) / a.per : st.strips - 1;
+    const dim3 grid((unsigned)((n->hidden + 31) / 32), (unsigned)(2 + across));
     return launch_kernel(residual_norm_sum_kernel, grid, dim3(1024), 0, s, "residual_norm_sum_kernel", a);
 }
 
