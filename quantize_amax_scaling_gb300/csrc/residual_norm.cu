@@ -20,6 +20,7 @@
 // weights of its columns stay in registers.
 
 #include "fp4.cuh"
+#include "packed_f32.cuh"
 
 #include <cooperative_groups.h>
 
@@ -42,35 +43,49 @@ struct RnArgs {
     float alpha, eps;
 };
 
-__device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight columns of a thread, as four pairs: the arithmetic is two-lane binary32
+// (packed_f32.cuh), which halves the instructions that bound these kernels.
+struct Oct {
+    float2 v[4];
+};
+
+__device__ __forceinline__ Oct widen8(const uint4& w) {
+    Oct o;
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) o.v[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+    return o;
 }
 
-__device__ __forceinline__ uint4 narrow8(const float (&f)[8]) {
-    return make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 narrow8(const Oct& o) {
+    return make_uint4(cvt_bf16x2(o.v[0].x, o.v[0].y), cvt_bf16x2(o.v[1].x, o.v[1].y), cvt_bf16x2(o.v[2].x, o.v[2].y),
+                      cvt_bf16x2(o.v[3].x, o.v[3].y));
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p)), w = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-    f[4] = w.x; f[5] = w.y; f[6] = w.z; f[7] = w.w;
+__device__ __forceinline__ Oct pairs8(const float4& a, const float4& b) {
+    return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
-__device__ __forceinline__ void load_gate8(const void* g, int is_bf16, int64_t at, float (&f)[8]) {
-    if (is_bf16)
-        widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + at)), f);
-    else
-        load8(static_cast<const float*>(g) + at, f);
+__device__ __forceinline__ Oct splat8(float v) { return pairs8(make_float4(v, v, v, v), make_float4(v, v, v, v)); }
+
+__device__ __forceinline__ Oct load8(const float* p) {
+    return pairs8(__ldg(reinterpret_cast<const float4*>(p)), __ldg(reinterpret_cast<const float4*>(p) + 1));
 }
 
-// Sixteen bytes from global to shared memory, or zeros (then nothing is read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ Oct load_gate8(const void* g, int is_bf16, int64_t at) {
+    return is_bf16 ? widen8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + at)))
+                   : load8(static_cast<const float*>(g) + at);
+}
+
+__device__ __forceinline__ void mul8(Oct& a, const Oct& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a.v[i] = mul2_rn(a.v[i], b.v[i]);
+}
+
+__device__ __forceinline__ float sum2(const float2& a, const float2& b) { return (a.x + a.y) + (b.x + b.y); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {  // global to shared memory
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -82,16 +97,15 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 as_f4(const uint4& v) {
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
 // Eight gate values that lie in the ring: one 16-byte slot of bf16, or two of binary32.
-__device__ __forceinline__ void ring_gate8(uint32_t at, uint32_t step, int is_bf16, float (&f)[8]) {
-    const uint4 v = ld_shared(at);
-    if (is_bf16) {
-        widen8(v, f);
-    } else {
-        const uint4 w = ld_shared(at + step);
-        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
-        f[4] = __uint_as_float(w.x); f[5] = __uint_as_float(w.y); f[6] = __uint_as_float(w.z); f[7] = __uint_as_float(w.w);
-    }
+__device__ __forceinline__ Oct ring_gate8(uint32_t at, uint32_t step, int is_bf16) {
+    return is_bf16 ? widen8(ld_shared(at)) : pairs8(as_f4(ld_shared(at)), as_f4(ld_shared(at + step)));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -100,32 +114,33 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the T threads of a row (T a multiple of 32; every thread of the CTA
-// calls it).  `part` holds one float a warp and is not written again before the
-// next barrier but one.
+// Sum over the T threads of a row (T a power of two from 32 to 1024; every thread
+// of the CTA calls it).  `part` holds one float a warp and is not written again
+// before the next barrier but one.
 __device__ __forceinline__ float row_sum(float v, int T, float* part) {
     v = warp_sum(v);
     if (T == 32) return v;
-    const int warp = threadIdx.x >> 5, first = (threadIdx.x / T) * (T >> 5);
+    const int warp = threadIdx.x >> 5, warps = T >> 5;
     if ((threadIdx.x & 31) == 0) part[warp] = v;
     __syncthreads();
-    v = part[first];
-    for (int i = 1; i < (T >> 5); ++i) v += part[first + i];
+    v = part[(warp & ~(warps - 1)) + (threadIdx.x & (warps - 1))];
+    for (int o = warps >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
 // Codes of eight columns of h, a warp together, as fp8q_quantize_amax or
 // fp8q_fp4_quantize_amax give them.
 template <int FMT>
-__device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, const Fp4Scale& c4, int64_t row, int col, bool live,
-                                            const uint4& w) {
+__device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, const Fp4Scale& c4, int64_t row, int64_t at, int u, int T,
+                                            int t, bool live, const uint4& w) {
+    const int col = (u * T + t) * 8;
     if constexpr (FMT == FP8Q_E4M3FN || FMT == FP8Q_E5M2) {
         uint2 o;
         if (c8.fast)
             o = make_uint2(quant_quad<FMT, true>(w.x, w.y, c8), quant_quad<FMT, true>(w.z, w.w, c8));
         else
             o = make_uint2(quant_quad<FMT, false>(w.x, w.y, c8), quant_quad<FMT, false>(w.z, w.w, c8));
-        if (live && col < a.H) st_v2(a.q + row * a.H + col, o);
+        if (live && col < a.H) st_v2(a.q + at + u * T * 8, o);
     } else if constexpr (FMT == FP8Q_MXFP4 || FMT == FP8Q_NVFP4) {
         constexpr int kLanes = Fp4<FMT>::kBlock / 8;  // lanes a block
         const uint32_t m = bf16x2_absmax(bf16x2_absmax(w.x, w.y), bf16x2_absmax(w.z, w.w));
@@ -151,7 +166,7 @@ __device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, c
 // of up to 512 threads); longer rows, with 64 registers a thread, read them from
 // L1 for each row, and the longest have room for one row ahead in shared memory.
 template <int FMT, int U, bool WREG>
-__global__ void __launch_bounds__(WREG ? 512 : 1024) residual_norm_kernel(const RnArgs a) {
+__global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(const RnArgs a) {
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float part[4][32];
     __shared__ uint32_t red[32];
@@ -163,65 +178,69 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024) residual_norm_kernel(const 
     const uint32_t step = blockDim.x * 16;  // from one slot to the next
     const uint32_t slots = 1 + (a.b != nullptr) + (ring_gate ? (a.gate_bf16 ? 1 : 2) : 0);
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) + threadIdx.x * 16;
-
-    auto fetch = [&](int64_t row, uint32_t stage) {
-        const bool live = row < row1;
+    const int64_t first = row0 * a.H + t * 8;  // this thread's first element
+    const uint32_t next_u = T * 8;             // from one group of eight columns to the next
+    bool on[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int col = (u * T + t) * 8;
-            const bool on = live && col < a.H;
-            const int64_t at = on ? row * a.H + col : 0;
-            uint32_t dst = ring + (stage * U + u) * slots * step;
-            copy16(dst, a.r + at, on);
-            if (a.b) copy16(dst += step, a.b + at, on);
-            if (ring_gate) {
-                if (a.gate_bf16) {
-                    copy16(dst += step, static_cast<const uint16_t*>(a.gate) + at, on);
-                } else {
-                    copy16(dst += step, static_cast<const float*>(a.gate) + at, on);
-                    copy16(dst += step, static_cast<const float*>(a.gate) + at + (on ? 4 : 0), on);
+    for (int u = 0; u < U; ++u) on[u] = (u * T + t) * 8 < a.H;
+
+    // rows of a strip that are not there are not fetched: what the ring holds then is never used
+    const uint16_t *src_r = a.r + first, *src_b = a.b ? a.b + first : nullptr;
+    const uint8_t* src_g = ring_gate ? static_cast<const uint8_t*>(a.gate) + first * (a.gate_bf16 ? 2 : 4) : nullptr;
+    int64_t fetched = row0;
+    auto fetch = [&](uint32_t stage) {
+        if (fetched < row1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t dst = ring + (stage * U + u) * slots * step;
+                if (!on[u]) continue;
+                copy16(dst, src_r + u * next_u);
+                if (a.b) copy16(dst += step, src_b + u * next_u);
+                if (ring_gate) {
+                    if (a.gate_bf16) {
+                        copy16(dst += step, src_g + u * next_u * 2);
+                    } else {
+                        copy16(dst += step, src_g + u * next_u * 4);
+                        copy16(dst += step, src_g + u * next_u * 4 + 16);
+                    }
                 }
             }
+            src_r += a.H;
+            src_b += a.H;
+            if (ring_gate) src_g += a.H * (a.gate_bf16 ? 2 : 4);
+            ++fetched;
         }
         copies_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) fetch(i < a.per_strip ? row0 + i : row1, i);
+    for (int i = 0; i < kStages; ++i) fetch(i);
 
     QScale c8;
     Fp4Scale c4;
     if constexpr (FMT == FP8Q_E4M3FN || FMT == FP8Q_E5M2) c8 = make_qscale(a.scale);
     if constexpr (FMT == FP8Q_MXFP4 || FMT == FP8Q_NVFP4) c4 = make_fp4_scale(a.scale);
     // alpha * gate * post of a column, without the gate where it comes with the row
-    auto weight = [&](int u, int64_t group, float (&w)[8]) {
+    auto weight = [&](int u, int64_t group) {
         const int col = (u * T + t) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = a.alpha;
-        if (col >= a.H) return;
-        float f[8];
-        if (a.gate && !ring_gate) {
-            load_gate8(a.gate, a.gate_bf16, group * a.H + col, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= f[i];
-        }
-        if (a.post) {
-            load8(a.post + col, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] *= f[i];
-        }
+        Oct w = splat8(a.alpha);
+        if (a.gate && !ring_gate) mul8(w, load_gate8(a.gate, a.gate_bf16, group * a.H + col));
+        if (a.post) mul8(w, load8(a.post + col));
+        return w;
     };
-    float W[WREG ? U : 1][8], P[WREG ? U : 1][8];
+    Oct W[WREG ? U : 1], P[WREG ? U : 1];
     int64_t group = a.gate && !ring_gate ? row0 / a.per : 0, gend = a.gate && !ring_gate ? (group + 1) * a.per : a.rows;
     if constexpr (WREG) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (a.b && row0 < a.rows) weight(u, group, W[u]);
-            if (a.pre && (u * T + t) * 8 < a.H) load8(a.pre + (u * T + t) * 8, P[u]);
+            W[u] = P[u] = splat8(0.0f);
+            if (a.b && row0 < a.rows && on[u]) W[u] = weight(u, group);
+            if (a.pre && on[u]) P[u] = load8(a.pre + (u * T + t) * 8);
         }
     }
     const float inv_h = 1.0f / (float)a.H;
     uint32_t m2 = 0, stage = 0;
-    for (int64_t it = 0; it < a.per_strip; ++it) {
+    int64_t at = first;
+    for (int64_t it = 0; it < a.per_strip; ++it, at += a.H) {
         const int64_t row = row0 + it;
         const bool live = row < row1;
         if (row == gend) {
@@ -230,98 +249,74 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024) residual_norm_kernel(const 
             if constexpr (WREG) {
                 if (live)
 #pragma unroll
-                    for (int u = 0; u < U; ++u) weight(u, group, W[u]);
+                    for (int u = 0; u < U; ++u)
+                        if (on[u]) W[u] = weight(u, group);
             }
         }
         copies_wait<kStages - 1>();
-        uint4 r[U], b[U];
+        Oct x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t at = ring + (stage * U + u) * slots * step;
-            r[u] = ld_shared(at);
-            b[u] = a.b ? ld_shared(at + step) : make_uint4(0, 0, 0, 0);
-        }
+        for (int u = 0; u < U; ++u) x[u] = on[u] ? widen8(ld_shared(ring + (stage * U + u) * slots * step)) : splat8(0.0f);
         if (a.b) {
+            Oct b[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) b[u] = on[u] ? widen8(ld_shared(ring + ((stage * U + u) * slots + 1) * step)) : splat8(0.0f);
             float rstd = 1.0f;
             if (a.post) {
-                float s = 0.0f;
+                float2 s[2] = {};
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float f[8];
-                    widen8(b[u], f);
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
-                }
-                s = row_sum(s, T, part[(it & 1) * 2]);
-                rstd = __frcp_rn(__fsqrt_rn(fmaf(s, inv_h, a.eps)));
+                    for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(b[u].v[i], b[u].v[i], s[i & 1]);
+                rstd = __frcp_rn(__fsqrt_rn(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2]), inv_h, a.eps)));
                 if (a.rstd_post && live && t == 0) a.rstd_post[row] = rstd;
             }
+            const float2 rs = splat2(rstd);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float f[8], x[8], g[8], w[8];
-                widen8(b[u], f);
-                widen8(r[u], x);
-                if constexpr (WREG) {
+                if (!on[u]) continue;
+                Oct w;
+                if constexpr (WREG)
+                    w = W[u];
+                else
+                    w = weight(u, live ? group : 0);
+                if (ring_gate) mul8(w, ring_gate8(ring + ((stage * U + u) * slots + 2) * step, step, a.gate_bf16));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = W[u][i];
-                } else if (live) {
-                    weight(u, group, w);
-                }
-                if (ring_gate) {
-                    ring_gate8(ring + ((stage * U + u) * slots + 2) * step, step, a.gate_bf16, g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] *= g[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fmaf(w[i], f[i] * rstd, x[i]);
-                r[u] = narrow8(x);
+                for (int i = 0; i < 4; ++i) x[u].v[i] = fma2_rn(w.v[i], mul2_rn(b[u].v[i], rs), x[u].v[i]);
             }
-        }
-        float s = 0.0f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int col = (u * T + t) * 8;
-            if (!live || col >= a.H) r[u] = make_uint4(0, 0, 0, 0);
-            float f[8];
-            widen8(r[u], f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(f[i], f[i], s);
         }
         // everything of this stage has been used: the row after the next ones into it
-        fetch(it + kStages < a.per_strip ? row + kStages : row1, stage);
+        fetch(stage);
         if (++stage == kStages) stage = 0;
-        if (a.ro && live) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int col = (u * T + t) * 8;
-                if (col < a.H) st_v4(a.ro + row * a.H + col, r[u]);
-            }
-        }
-        if (!a.pre) continue;
-        s = row_sum(s, T, part[(it & 1) * 2 + 1]);
-        const float rstd = __frcp_rn(__fsqrt_rn(fmaf(s, inv_h, a.eps)));
-        if (a.rstd_pre && live && t == 0) a.rstd_pre[row] = rstd;
+        float2 s[2] = {};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int col = (u * T + t) * 8;
+            const uint4 o = narrow8(x[u]);
+            if (a.ro && live && on[u]) st_v4(a.ro + at + u * next_u, o);
+            x[u] = widen8(o);  // the norm before the next block is of what was stored
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(x[u].v[i], x[u].v[i], s[i & 1]);
+        }
+        if (!a.pre) continue;
+        const float rstd = __frcp_rn(__fsqrt_rn(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2 + 1]), inv_h, a.eps)));
+        if (a.rstd_pre && live && t == 0) a.rstd_pre[row] = rstd;
+        const float2 rs = splat2(rstd);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             uint4 o = make_uint4(0, 0, 0, 0);
-            if (live && col < a.H) {
-                float f[8];
-                widen8(r[u], f);
-                if constexpr (WREG) {
+            if (live && on[u]) {
+                Oct g;
+                if constexpr (WREG)
+                    g = P[u];
+                else
+                    g = load8(a.pre + (u * T + t) * 8);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * P[u][i];
-                } else {
-                    float g[8];
-                    load8(a.pre + col, g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
-                }
-                o = narrow8(f);
+                for (int i = 0; i < 4; ++i) x[u].v[i] = mul2_rn(mul2_rn(x[u].v[i], rs), g.v[i]);
+                o = narrow8(x[u]);
                 m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(o.x, o.y), bf16x2_absmax(o.z, o.w)));
-                if (a.h) st_v4(a.h + row * a.H + col, o);
+                if (a.h) st_v4(a.h + at + u * next_u, o);
             }
-            if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, col, live, o);
+            if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, at, u, T, t, live, o);
         }
     }
     if (a.amax) {
@@ -378,31 +373,49 @@ struct RnBwdArgs {
     float alpha;
 };
 
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float* p, const Oct& o) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(o.v[0].x, o.v[0].y, o.v[1].x, o.v[1].y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(o.v[2].x, o.v[2].y, o.v[3].x, o.v[3].y);
 }
 
-__device__ __forceinline__ void store_gate8(void* p, int is_bf16, int64_t at, const float (&f)[8]) {
+__device__ __forceinline__ void store_gate8(void* p, int is_bf16, int64_t at, const Oct& o) {
     if (is_bf16)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = narrow8(f);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = narrow8(o);
     else
-        store8(static_cast<float*>(p) + at, f);
+        store8(static_cast<float*>(p) + at, o);
+}
+
+// Sums of three values over the warp: lane 0 has the first, 8 the second, 16 the
+// third.  The lanes part the values between them as they add, so six exchanges
+// do for what would take fifteen.
+__device__ __forceinline__ float warp_sum3(float a, float b, float c) {
+    const int lane = threadIdx.x & 31;
+    // lanes below 16 keep a and b, the others c and nothing
+    const float give0 = lane & 16 ? a : c, give1 = lane & 16 ? b : 0.0f;
+    float k0 = lane & 16 ? c : a, k1 = lane & 16 ? 0.0f : b;
+    k0 += __shfl_xor_sync(0xFFFFFFFFu, give0, 16);
+    k1 += __shfl_xor_sync(0xFFFFFFFFu, give1, 16);
+    const float give = lane & 8 ? k0 : k1;
+    float k = lane & 8 ? k1 : k0;
+    k += __shfl_xor_sync(0xFFFFFFFFu, give, 8);
+#pragma unroll
+    for (int o = 4; o; o >>= 1) k += __shfl_xor_sync(0xFFFFFFFFu, k, o);
+    return k;
 }
 
 // Per row: one pass for the three sums, one for the gradients, both from shared
-// memory (kept in registers between them, a row would spill).  With X = D n1 and W = alpha gate g1 of a column, a row
-// adds X to the one sum S that dgate and dg1 share: a gate's row of dgate is
-// alpha g1 S, and dg1 takes alpha gate S whenever a gate's rows end.  RING_GATE:
-// each row has its own gate, which comes with it.
+// memory (kept in registers between them, a row would spill).  With X = D n1 and
+// W = alpha gate g1 of a column, a row adds X to the one sum S that dgate and dg1
+// share: a gate's row of dgate is alpha g1 S, and dg1 takes alpha gate S whenever
+// a gate's rows end.  RING_GATE: each row has its own gate, which comes with it.
 template <bool CLUSTER, bool RING_GATE>
 __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const RnBwdArgs a) {
     namespace cg = cooperative_groups;
     constexpr int kStages = RING_GATE ? 2 : 3;
     extern __shared__ __align__(16) uint8_t ring_raw[];
-    __shared__ float part[2][8][3];
+    __shared__ float part[2][3][8];
     __shared__ float sums[2][8][3];  // of each CTA of the cluster
-    const int T = a.T, t = threadIdx.x % T, warp = threadIdx.x >> 5;
+    const int T = a.T, t = threadIdx.x % T, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int slices = 1, slice = 0;
     if (CLUSTER) {
         slices = (int)cg::this_cluster().num_blocks();
@@ -411,122 +424,112 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
     const int64_t strip = (int64_t)(blockIdx.x / slices) * (256 / T) + threadIdx.x / T;
     const int64_t row0 = strip * a.per_strip, row1 = min(row0 + a.per_strip, a.rows);
     const int c0 = slice * a.width, c1 = min(c0 + a.width, a.H);  // this CTA's columns
+    const int col0 = c0 + t * 8;                                  // this thread's first, and
+    const int next_u = T * 8;                                     // from one group of eight to the next
+    const bool on[2] = {col0 < c1, col0 + next_u < c1};
     const float inv_h = 1.0f / (float)a.H;
     // ring: a stage holds, for each of two groups of eight columns, a slot of b, r', dr', dh and one
     // or two of the gate; behind it this thread's sums of dg1
     constexpr uint32_t kStep = 256 * 16;
     const uint32_t slots = RING_GATE ? (a.gate_bf16 ? 5 : 6) : 4;
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) + threadIdx.x * 16;
-    float4* const post_sum = reinterpret_cast<float4*>(ring_raw + kStages * 2 * slots * kStep) + threadIdx.x;
+    const uint32_t post_sum = ring + kStages * 2 * slots * kStep;
 
-    auto fetch = [&](int64_t row, uint32_t stage) {
-        const bool live = row < row1;
+    // what is not there stays zero in the ring (columns, whole tensors) or is never used (rows)
+    for (uint32_t i = 0; i < kStages * 2 * slots + 4; ++i) st_shared(ring + i * kStep, make_uint4(0, 0, 0, 0));
+    int64_t fetched = row0, src = row0 * a.H + col0;
+    auto fetch = [&](uint32_t stage) {
+        if (fetched < row1) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int col = c0 + (u * T + t) * 8;
-            const bool on = live && col < c1;
-            const int64_t at = on ? row * a.H + col : 0;
-            const uint32_t dst = ring + (stage * 2 + u) * slots * kStep;
-            if (a.b) copy16(dst, a.b + at, on);
-            if (a.dh) {
-                copy16(dst + kStep, a.ro + at, on);
-                copy16(dst + 3 * kStep, a.dh + at, on);
-            }
-            if (a.dro) copy16(dst + 2 * kStep, a.dro + at, on);
-            if (RING_GATE) {
-                if (a.gate_bf16) {
-                    copy16(dst + 4 * kStep, static_cast<const uint16_t*>(a.gate) + at, on);
-                } else {
-                    copy16(dst + 4 * kStep, static_cast<const float*>(a.gate) + at, on);
-                    copy16(dst + 5 * kStep, static_cast<const float*>(a.gate) + at + (on ? 4 : 0), on);
+            for (int u = 0; u < 2; ++u) {
+                if (!on[u]) continue;
+                const uint32_t dst = ring + (stage * 2 + u) * slots * kStep;
+                const int64_t at = src + u * next_u;
+                if (a.b) copy16(dst, a.b + at);
+                if (a.dh) {
+                    copy16(dst + kStep, a.ro + at);
+                    copy16(dst + 3 * kStep, a.dh + at);
+                }
+                if (a.dro) copy16(dst + 2 * kStep, a.dro + at);
+                if (RING_GATE) {
+                    if (a.gate_bf16) {
+                        copy16(dst + 4 * kStep, static_cast<const uint16_t*>(a.gate) + at);
+                    } else {
+                        copy16(dst + 4 * kStep, static_cast<const float*>(a.gate) + at);
+                        copy16(dst + 5 * kStep, static_cast<const float*>(a.gate) + at + 4);
+                    }
                 }
             }
+            src += a.H;
+            ++fetched;
         }
         copies_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) fetch(i < a.per_strip ? row0 + i : row1, i);
+    for (int i = 0; i < kStages; ++i) fetch(i);
 
     int64_t group = a.gate ? row0 / a.per : 0;
     int64_t gend = a.gate ? (group + 1) * a.per : a.rows;  // first row behind the group
     bool whole = a.gate && group * a.per >= row0;          // the group began in this strip
-    float Q[2][8], W[2][8], S[2][8] = {}, apre[2][8] = {};
+    Oct Q[2], W[2], S[2], apre[2];
     // alpha * gate * post of a column, without a gate that comes with the row
     auto weight = [&](int u) {
-        const int col = c0 + (u * T + t) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) W[u][i] = a.alpha;
-        if (col >= c1) return;
-        float f[8];
-        if (a.post) {
-            load8(a.post + col, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) W[u][i] *= f[i];
-        }
-        if (a.gate && !RING_GATE) {
-            load_gate8(a.gate, a.gate_bf16, group * a.H + col, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) W[u][i] *= f[i];
-        }
+        W[u] = splat8(a.alpha);
+        if (a.post) mul8(W[u], load8(a.post + col0 + u * next_u));
+        if (a.gate && !RING_GATE) mul8(W[u], load_gate8(a.gate, a.gate_bf16, group * a.H + col0 + u * next_u));
     };
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const int col = c0 + (u * T + t) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) Q[u][i] = 0.0f;
-        if (a.dh && col < c1) load8(a.pre + col, Q[u]);
-        if (row0 < a.rows) weight(u);
-        post_sum[(2 * u) * 256] = post_sum[(2 * u + 1) * 256] = make_float4(0, 0, 0, 0);
+        Q[u] = W[u] = S[u] = apre[u] = splat8(0.0f);
+        if (a.dh && on[u]) Q[u] = load8(a.pre + col0 + u * next_u);
+        if (row0 < a.rows && on[u]) weight(u);
     }
 
     uint32_t stage = 0;
-    for (int64_t it = 0; it < a.per_strip; ++it) {
+    int64_t at = row0 * a.H + col0;
+    for (int64_t it = 0; it < a.per_strip; ++it, at += a.H) {
         const int64_t row = row0 + it;
         const bool live = row < row1;
         const float rstd2 = a.dh && live ? __ldg(a.rstd_pre + row) : 0.0f;
         const float rstd1 = a.post && live ? __ldg(a.rstd_post + row) : 1.0f;
+        const float2 r2 = splat2(rstd2), r1 = splat2(rstd1);
         copies_wait<kStages - 1>();
         const uint32_t at_stage = ring + stage * 2 * slots * kStep;
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
+        float2 q0 = {}, q1 = {}, q2 = {};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint32_t at = at_stage + u * slots * kStep;
-            float fb[8], fo[8], fd[8], fh[8], g[8];
-            widen8(a.b ? ld_shared(at) : none, fb);
-            widen8(a.dh ? ld_shared(at + kStep) : none, fo);
-            widen8(a.dro ? ld_shared(at + 2 * kStep) : none, fd);
-            widen8(a.dh ? ld_shared(at + 3 * kStep) : none, fh);
-            if (RING_GATE) ring_gate8(at + 4 * kStep, kStep, a.gate_bf16, g);
+            const uint32_t from = at_stage + u * slots * kStep;
+            const Oct fb = widen8(ld_shared(from)), fo = widen8(ld_shared(from + kStep)), fd = widen8(ld_shared(from + 2 * kStep)),
+                      fh = widen8(ld_shared(from + 3 * kStep));
+            Oct w = W[u];
+            if (RING_GATE) mul8(w, ring_gate8(from + 4 * kStep, kStep, a.gate_bf16));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float n2 = fo[i] * rstd2, dn = fh[i] * Q[u][i];
-                float w = W[u][i] * (fb[i] * rstd1);
-                if (RING_GATE) w *= g[i];
-                s0 = fmaf(dn, n2, s0);
-                s1 = fmaf(w, fmaf(rstd2, dn, fd[i]), s1);
-                s2 = fmaf(w, n2, s2);
+            for (int i = 0; i < 4; ++i) {
+                const float2 n2 = mul2_rn(fo.v[i], r2), dn = mul2_rn(fh.v[i], Q[u].v[i]);
+                const float2 k = mul2_rn(w.v[i], mul2_rn(fb.v[i], r1));
+                q0 = fma2_rn(dn, n2, q0);
+                q1 = fma2_rn(k, fma2_rn(r2, dn, fd.v[i]), q1);
+                q2 = fma2_rn(k, n2, q2);
             }
         }
-        s0 = warp_sum(s0);
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (T > 32) {
-            float(*pt)[3] = part[it & 1];
-            if ((threadIdx.x & 31) == 0) {
-                pt[warp][0] = s0;
-                pt[warp][1] = s1;
-                pt[warp][2] = s2;
-            }
-            __syncthreads();
-            const int first = (threadIdx.x / T) * (T >> 5);
-            s0 = pt[first][0];
-            s1 = pt[first][1];
-            s2 = pt[first][2];
-            for (int i = 1; i < (T >> 5); ++i) {
-                s0 += pt[first + i][0];
-                s1 += pt[first + i][1];
-                s2 += pt[first + i][2];
+        float s0, s1, s2;
+        {
+            const float k = warp_sum3(q0.x + q0.y, q1.x + q1.y, q2.x + q2.y);
+            const int warps = T >> 5, from = warp & ~(warps - 1);
+            float(*pt)[8] = part[it & 1];
+            if ((lane & 7) == 0 && lane < 24) pt[lane >> 3][warp] = k;
+            if (T > 32)
+                __syncthreads();
+            else
+                __syncwarp();
+            const int i = from + (lane & (warps - 1));
+            s0 = pt[0][i];
+            s1 = pt[1][i];
+            s2 = pt[2][i];
+            for (int o = warps >> 1; o; o >>= 1) {
+                s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+                s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+                s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
             }
         }
         if (CLUSTER) {
@@ -547,49 +550,45 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
         }
         const float c2 = s0 * inv_h;
         const float m1 = a.post ? (s1 - rstd2 * c2 * s2) * inv_h : 0.0f;  // mean(w D); no term without g1
+        const float2 mc2 = splat2(-c2), mm1 = splat2(-m1);
         const bool flush = live && a.b && (row + 1 == gend || row + 1 == row1);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int col = c0 + (u * T + t) * 8;
-            const bool on = live && col < c1;
-            const int64_t at = row * a.H + col;
-            float fb[8], fo[8], D[8], fh[8], e[8], g[8];
             const uint32_t from = at_stage + u * slots * kStep;
-            widen8(a.b ? ld_shared(from) : none, fb);
-            widen8(a.dh ? ld_shared(from + kStep) : none, fo);
-            widen8(a.dro ? ld_shared(from + 2 * kStep) : none, D);
-            widen8(a.dh ? ld_shared(from + 3 * kStep) : none, fh);
-            if (RING_GATE) ring_gate8(from + 4 * kStep, kStep, a.gate_bf16, g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float n2 = fo[i] * rstd2;
-                D[i] = fmaf(rstd2, fmaf(-n2, c2, fh[i] * Q[u][i]), D[i]);
-                apre[u][i] = fmaf(fh[i], n2, apre[u][i]);
-                const float n1 = fb[i] * rstd1;
-                S[u][i] = fmaf(D[i], n1, S[u][i]);
-                const float w = RING_GATE ? W[u][i] * g[i] : W[u][i];
-                e[i] = rstd1 * fmaf(-n1, m1, D[i] * w);
+            const Oct fb = widen8(ld_shared(from)), fo = widen8(ld_shared(from + kStep)), fh = widen8(ld_shared(from + 3 * kStep));
+            Oct D = widen8(ld_shared(from + 2 * kStep)), w = W[u], e, g;
+            if (RING_GATE) {
+                g = ring_gate8(from + 4 * kStep, kStep, a.gate_bf16);
+                mul8(w, g);
             }
-            if (on && a.dr) st_v4(a.dr + at, narrow8(D));
-            if (on && a.db) st_v4(a.db + at, narrow8(e));
-            if (flush && on) {
-                float p[8], f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = 1.0f;
-                if (a.post) load8(a.post + col, p);
-                if (a.gate && !RING_GATE) load_gate8(a.gate, a.gate_bf16, group * a.H + col, g);
+            for (int i = 0; i < 4; ++i) {
+                const float2 n2 = mul2_rn(fo.v[i], r2), n1 = mul2_rn(fb.v[i], r1);
+                D.v[i] = fma2_rn(r2, fma2_rn(n2, mc2, mul2_rn(fh.v[i], Q[u].v[i])), D.v[i]);
+                apre[u].v[i] = fma2_rn(fh.v[i], n2, apre[u].v[i]);
+                S[u].v[i] = fma2_rn(D.v[i], n1, S[u].v[i]);
+                e.v[i] = mul2_rn(r1, fma2_rn(n1, mm1, mul2_rn(D.v[i], w.v[i])));
+            }
+            if (!live || !on[u]) continue;
+            if (a.dr) st_v4(a.dr + at + u * next_u, narrow8(D));
+            if (a.db) st_v4(a.db + at + u * next_u, narrow8(e));
+            if (flush) {
+                const int col = col0 + u * next_u;
+                Oct p = splat8(1.0f);
+                if (a.post) p = load8(a.post + col);
+                if (a.gate && !RING_GATE) g = load_gate8(a.gate, a.gate_bf16, group * a.H + col);
+                if (!a.gate) g = splat8(1.0f);
+                mul8(S[u], splat8(a.alpha));
+                mul8(p, S[u]);
+                float4 lo = as_f4(ld_shared(post_sum + 2 * u * kStep)), hi = as_f4(ld_shared(post_sum + (2 * u + 1) * kStep));
+                Oct sum = pairs8(lo, hi);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    S[u][i] *= a.alpha;
-                    f[i] = a.gate ? S[u][i] * g[i] : S[u][i];
-                    p[i] *= S[u][i];
-                    S[u][i] = 0.0f;
-                }
-                float4 lo = post_sum[(2 * u) * 256], hi = post_sum[(2 * u + 1) * 256];
-                lo.x += f[0]; lo.y += f[1]; lo.z += f[2]; lo.w += f[3];
-                hi.x += f[4]; hi.y += f[5]; hi.z += f[6]; hi.w += f[7];
-                post_sum[(2 * u) * 256] = lo;
-                post_sum[(2 * u + 1) * 256] = hi;
+                for (int i = 0; i < 4; ++i) sum.v[i] = fma2_rn(S[u].v[i], g.v[i], sum.v[i]);
+                st_shared(post_sum + 2 * u * kStep, make_uint4(__float_as_uint(sum.v[0].x), __float_as_uint(sum.v[0].y),
+                                                               __float_as_uint(sum.v[1].x), __float_as_uint(sum.v[1].y)));
+                st_shared(post_sum + (2 * u + 1) * kStep, make_uint4(__float_as_uint(sum.v[2].x), __float_as_uint(sum.v[2].y),
+                                                                     __float_as_uint(sum.v[3].x), __float_as_uint(sum.v[3].y)));
+                S[u] = splat8(0.0f);
                 if (a.dgate) {
                     // a group that lies in this strip whole goes straight out
                     if (whole && (row + 1 == gend || row + 1 == a.rows))
@@ -600,28 +599,26 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
             }
         }
         // this stage has been used: the row after the next ones into it
-        fetch(it + kStages < a.per_strip ? row + kStages : row1, stage);
+        fetch(stage);
         if (++stage == kStages) stage = 0;
         if (a.gate && row + 1 == gend) {
             ++group;
             gend += a.per;
             whole = true;
-            if (!RING_GATE && row + 1 < row1) {
-                weight(0);
-                weight(1);
-            }
+            if (!RING_GATE && row + 1 < row1)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (on[u]) weight(u);
         }
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const int col = c0 + (u * T + t) * 8;
-        if (strip < a.strips && col < c1) {
+        if (strip < a.strips && on[u]) {
+            const int col = col0 + u * next_u;
             if (a.dpre) store8(a.space + strip * a.H + col, apre[u]);
-            if (a.dpost) {
-                float4* o = reinterpret_cast<float4*>(a.space + (a.strips + strip) * a.H + col);
-                o[0] = post_sum[(2 * u) * 256];
-                o[1] = post_sum[(2 * u + 1) * 256];
-            }
+            if (a.dpost)
+                store8(a.space + (a.strips + strip) * a.H + col,
+                       pairs8(as_f4(ld_shared(post_sum + 2 * u * kStep)), as_f4(ld_shared(post_sum + (2 * u + 1) * kStep))));
         }
     }
     copies_wait<0>();
