@@ -16,6 +16,7 @@
 #pragma once
 
 #include "fp8q_common.cuh"
+#include "packed_f32.cuh"
 
 #include <atomic>
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ void st_v2(void* p, uint2 v) {
 
 // Four pairs of binary32 values -> eight e2m1 codes (nearest, ties to even,
 // held at +-6; the first value in the lowest four bits).
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&f)[8]) {
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float2 (&f)[4]) {
     uint32_t d;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -64,7 +65,7 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&f)[8]) {
         "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(d)
-        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+        : "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y));
     return d;
 }
 
@@ -92,11 +93,12 @@ __device__ __forceinline__ float sf_value(uint32_t code) {
 
 // What a CTA derives from the tensor scale of the 16-block format.
 struct Fp4Scale {
-    float s;     // the tensor scale
-    float s6;    // RN(6 s)
-    float r6;    // RN(1 / s6) where `fast`
-    bool good;   // s6 positive and finite
-    bool fast;   // s6 in [2^-60, 2^60]: the exact quotient without a divide
+    float s;      // the tensor scale
+    float s6;     // RN(6 s)
+    float r6;     // RN(1 / s6) where `fast`
+    float limit;  // the largest block maximum whose elements take the exact quotient without a divide
+    bool good;    // s6 positive and finite
+    bool fast;    // s in [2^-50, 2^50]: with block scales from 2^-9 to 448 everything stays in [2^-60, 2^60]
 };
 
 __device__ __forceinline__ Fp4Scale make_fp4_scale(const float* scale) {
@@ -104,8 +106,9 @@ __device__ __forceinline__ Fp4Scale make_fp4_scale(const float* scale) {
     c.s = scale ? __ldg(scale) : 1.0f;
     c.s6 = __fmul_rn(c.s, 6.0f);
     c.good = c.s6 > 0.0f && c.s6 <= 3.402823466e38f;
-    c.fast = c.s6 >= 0x1p-60f && c.s6 <= 0x1p60f;
+    c.fast = c.s >= 0x1p-50f && c.s <= 0x1p50f;
     c.r6 = c.fast ? __frcp_rn(c.s6) : 1.0f;
+    c.limit = c.fast ? c.s * (448.0f * 131072.0f) : -1.0f;
     return c;
 }
 
@@ -116,12 +119,18 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
     return __fmaf_rn(-__fmaf_rn(y0, s, -x), r, y0);
 }
 
+// The same for two, with mr = -r; a zero keeps its sign.
+__device__ __forceinline__ float2 quotient2(float2 x, float2 s, float2 r, float2 mr) {
+    const float2 y0 = mul2_rn(x, r);
+    return fma2_rn(fma2_rn(y0, s, mul2_rn(x, splat2(-1.0f))), mr, y0);
+}
+
 // A block's scale byte, and what its elements are divided by.
 struct BlockScale {
     uint32_t code;
-    float d;     // MX: the factor 2^-e; NV: RN(block scale * tensor scale)
-    float r;     // NV: RN(1 / d)
-    int mode;    // NV: 0 all codes zero, 1 exact quotient by r, 2 divide
+    float d;    // MX: the factor 2^-e; NV: RN(block scale * tensor scale), 1 where that is 0
+    float r;    // NV: RN(1 / d), 0 where all codes are zero
+    bool slow;  // NV: beyond the exact quotient's range
 };
 
 // a: the block's max|x| as bf16 bits (NaN above 0x7F80).
@@ -136,59 +145,63 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t a, const Fp4Scale& c)
         b.code = a > 0x7F80u ? 255u : code;
         b.d = __uint_as_float((254u - code) << 23);  // 2^(127 - code), normal for code <= 252
         b.r = 1.0f;
-        b.mode = 1;
+        b.slow = false;
         return b;
     }
     const float af = __uint_as_float(a << 16);
-    float v;
-    if (c.fast)  // beyond 2^17 s6 the scale is held at 448 anyway
-        v = quotient(fminf(af, c.s6 * 131072.0f), c.s6, c.r6);
-    else
-        v = __fdiv_rn(af, c.s6);
-    b.code = cvt_fp8x2<FP8Q_E4M3FN>(v, 0.0f) & 0xFFu;
-    if (!c.good && a != 0u) b.code = 0x7Fu;
-    if (a > 0x7F80u) b.code = 0x7Fu;
-    if (a == 0u) b.code = 0u;
-    b.d = __fmul_rn(sf_value<FMT>(b.code), c.s);
-    b.mode = 0;
-    b.r = 1.0f;
-    if (b.d > 0.0f) {
-        const bool q = b.d >= 0x1p-60f && b.d <= 0x1p60f && af <= b.d * 131072.0f;
-        b.mode = q ? 1 : 2;
-        if (q) b.r = __frcp_rn(b.d);
+    if (c.fast) {  // the same branch for every thread
+        // beyond 2^17 s6 the scale is held at 448 anyway
+        b.code = cvt_fp8x2<FP8Q_E4M3FN>(quotient(fminf(af, c.s6 * 131072.0f), c.s6, c.r6), 0.0f) & 0xFFu;
+        b.code = a > 0x7F80u ? 0x7Fu : b.code;
+        b.d = __fmul_rn(sf_value<FMT>(b.code), c.s);
+        // RN(1 / d): the approximation and one correction (packed_f32.cuh) for d 2^64, which
+        // lies where that is checked for every significand
+        const float e = b.d * 0x1p64f, y = rcp_approx_ftz(e);
+        b.r = fmaf(y, fmaf(-e, y, 1.0f), y) * 0x1p64f;
+        b.slow = af > c.limit;
+    } else {
+        b.code = cvt_fp8x2<FP8Q_E4M3FN>(__fdiv_rn(af, c.s6), 0.0f) & 0xFFu;
+        if (a > 0x7F80u || !c.good) b.code = 0x7Fu;
+        if (a == 0u) b.code = 0u;
+        b.d = __fmul_rn(sf_value<FMT>(b.code), c.s);
+        b.r = 1.0f;
+        b.slow = b.d > 0.0f;
     }
+    if (b.code == 0u || !(b.d > 0.0f)) b.r = 0.0f, b.d = 1.0f;  // quotient() of it: zero, with x's sign
     return b;
 }
 
-// Sixteen bf16 (eight words, the even column low) -> sixteen codes (two words).
+// Off the fast path: d may be infinite, and an infinity is +-6 all the same.
+__device__ __noinline__ float slow_quotient(float x, float d) {
+    return fabsf(x) > 3.402823466e38f ? x : __fdiv_rn(x, d);
+}
+
+// Eight bf16 of a block (four words, the even column low) -> eight codes.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], const BlockScale& b) {
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    if (FMT == FP8Q_MXFP4) {
+        const float2 d = splat2(b.d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2_rn(f[i], d);  // exact, or below half the smallest code
+    } else if (!b.slow) {  // quotient(), two at a time
+        const float2 r = splat2(b.r), mr = splat2(-b.r), d = splat2(b.d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = quotient2(f[i], d, r, mr);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(slow_quotient(f[i].x, b.d), slow_quotient(f[i].y, b.d));
+    }
+    return cvt_e2m1x8(f);
+}
+
+// Sixteen bf16 (eight words) -> sixteen codes (two words).
 template <int FMT>
 __device__ __forceinline__ uint2 block_codes(const uint32_t (&w)[8], const BlockScale& b) {
-    uint32_t o[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[4 * h + i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[4 * h + i] & 0xFFFF0000u);
-        }
-        if (FMT == FP8Q_MXFP4) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], b.d);  // exact, or below half the smallest code
-        } else if (b.mode == 1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = quotient(f[i], b.d, b.r);
-        } else if (b.mode == 2) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)  // d may be infinite: an infinity is +-6 all the same
-                f[i] = fabsf(f[i]) > 3.402823466e38f ? f[i] : __fdiv_rn(f[i], b.d);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = copysignf(0.0f, f[i]);
-        }
-        o[h] = cvt_e2m1x8(f);
-    }
-    return make_uint2(o[0], o[1]);
+    const uint32_t lo[4] = {w[0], w[1], w[2], w[3]}, hi[4] = {w[4], w[5], w[6], w[7]};
+    return make_uint2(codes8<FMT>(lo, b), codes8<FMT>(hi, b));
 }
 
 __device__ __forceinline__ uint32_t absmax16(const uint32_t (&w)[8]) {  // both halves, sign undefined

@@ -6,6 +6,8 @@
 // contiguous bytes) and, for the transpose, 64 contiguous bytes of each of its
 // 128 code rows.  A thread quantizes 16 columns of a row from registers; the
 // transpose reads the same tile back from shared memory by pairs of columns.
+// Matrices whose rows do not start on 32-byte boundaries pass through shared
+// memory by aligned 32-bit words, a warp a row.
 
 #include "fp4.cuh"
 
@@ -13,13 +15,93 @@ namespace {
 
 constexpr int kTile = 128;  // rows and columns of a CTA's tile
 
+constexpr int kRawWords = kTile / 2 + 1;  // a row of the tile in shared memory, from an odd place too
+
+// How a row's part of the tile, elements [c0, c0 + n) of the row, lies by 32-bit
+// words: `odd` first element alone, then whole words, then perhaps one more
+// element.  In shared memory element e is half-word e + odd, so that the words
+// stay words.
+struct RowWords {
+    int n, odd;
+};
+__device__ __forceinline__ RowWords row_words(const uint16_t* first, int64_t c0, int64_t cols) {
+    return {(int)min((int64_t)kTile, cols - c0), (int)(((uintptr_t)first >> 1) & 1)};
+}
+
+// Rows [r0, r0 + 128) of x, columns [c0, c0 + 128), into `raw`, zeros where there
+// are none; a warp takes a row, eight rows' loads at a time, a lane the words
+// `lane` and `lane` + 32 (lane 0 the odd last one too).
+__device__ __forceinline__ void load_rows(uint32_t* raw, const uint16_t* x, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int base = 0; base < kTile; base += 64) {
+        uint32_t v[8][2];
+        uint16_t edge[8][2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = base + j * 8 + warp;
+            const uint16_t* p = x + (r0 + row) * cols + c0;
+            RowWords k = row_words(p, c0, cols);
+            if (r0 + row >= rows) k.n = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = 2 * (lane + 32 * i) - k.odd;  // the word holds elements e and e + 1
+                v[j][i] = 0;
+                edge[j][i] = 0;
+                if (e >= 0 && e + 1 < k.n)
+                    v[j][i] = __ldg(reinterpret_cast<const unsigned int*>(p + e));
+                else if (e < k.n && e + 1 >= 0 && k.n > 0)  // one of them
+                    edge[j][i] = __ldg(p + (e < 0 ? 0 : e));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = base + j * 8 + warp;
+            const uint16_t* p = x + (r0 + row) * cols + c0;
+            const RowWords k = row_words(p, c0, cols);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int w = lane + 32 * i;
+                raw[row * kRawWords + w] = v[j][i] | (2 * w < k.odd ? (uint32_t)edge[j][i] << 16 : edge[j][i]);
+            }
+        }
+    }
+    if (threadIdx.x < kTile) {
+        const int row = threadIdx.x;
+        const uint16_t* p = x + (r0 + row) * cols + c0;
+        const RowWords k = row_words(p, c0, cols);
+        raw[row * kRawWords + kTile / 2] = k.odd && k.n == kTile && r0 + row < rows ? p[kTile - 1] : 0;
+    }
+}
+
+// The same way back.
+__device__ __forceinline__ void store_rows(const uint32_t* raw, uint16_t* y, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 4
+    for (int row = threadIdx.x >> 5; row < kTile; row += kThreads / 32) {
+        uint16_t* p = y + (r0 + row) * cols + c0;
+        RowWords k = row_words(p, c0, cols);
+        if (r0 + row >= rows) k.n = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int w = lane + 32 * i, e = 2 * w - k.odd;
+            if (w >= kRawWords) continue;
+            const uint32_t v = raw[row * kRawWords + w];
+            if (e >= 0 && e + 1 < k.n) {
+                *reinterpret_cast<uint32_t*>(p + e) = v;
+            } else {
+                if (e >= 0 && e < k.n) p[e] = (uint16_t)v;
+                if (e + 1 >= 0 && e + 1 < k.n) p[e + 1] = (uint16_t)(v >> 16);
+            }
+        }
+    }
+}
+
 struct Fp4QuantArgs {
     const uint16_t* x;
     uint8_t *q, *sf, *qt, *sft;
     const float* scale;
     float* amax;
     int64_t rows, cols, tile_cols;
-    int vec;  // rows start on 32-byte boundaries and hold whole 16-column chunks
 };
 
 // The 512-byte scale tiles gathered in `s` go out by 32-bit words (four blocks
@@ -39,37 +121,45 @@ __device__ __forceinline__ int sf_byte(int row, int block) {
     return (block >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4 + (block & 3);
 }
 
-template <int FMT, bool ROW, bool COL>
+template <int FMT, bool ROW, bool COL, bool VEC>
 __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantArgs a) {
     constexpr int kBlock = Fp4<FMT>::kBlock;
     __shared__ uint32_t red[kThreads / 32];
     __shared__ __align__(16) uint32_t sfs[2 * 128];
-    __shared__ __align__(16) uint32_t xs[COL ? kTile * kTile / 2 : 4];
+    __shared__ __align__(16) uint32_t xs[VEC ? (COL ? kTile * kTile / 2 : 4) : kTile * kRawWords];
     __shared__ __align__(16) uint2 qts[COL ? kTile * 9 : 1];  // 72 bytes a code row: 2-way conflicts at most
     const int tid = threadIdx.x;
     const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
     const int64_t r0 = tr * kTile, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kTile;
 
     uint32_t w[4][8];
+    if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int id = u * kThreads + tid;
-        const int64_t r = r0 + (id >> 3), c = c0 + (id & 7) * 16;
-        const uint16_t* p = a.x + r * a.cols + c;
-        if (a.vec) {
+        for (int u = 0; u < 4; ++u) {
+            const int id = u * kThreads + tid;
+            const int64_t r = r0 + (id >> 3), c = c0 + (id & 7) * 16;
             uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (r < a.rows && c < a.cols) ld_stream_v8(p, lo, hi);
+            if (r < a.rows && c < a.cols) ld_stream_v8(a.x + r * a.cols + c, lo, hi);
             w[u][0] = lo.x; w[u][1] = lo.y; w[u][2] = lo.z; w[u][3] = lo.w;
             w[u][4] = hi.x; w[u][5] = hi.y; w[u][6] = hi.z; w[u][7] = hi.w;
-        } else {
+        }
+    } else {
+        load_rows(xs, a.x, r0, a.rows, c0, a.cols);
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int id = u * kThreads + tid, row = id >> 3;
+            const int odd = row_words(a.x + (r0 + row) * a.cols + c0, c0, a.cols).odd;
+            const uint32_t* p = xs + row * kRawWords + (id & 7) * 8;
+            uint32_t v = p[0];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                uint32_t v = 0;
-                if (r < a.rows && c + 2 * i < a.cols) v = p[2 * i];
-                if (r < a.rows && c + 2 * i + 1 < a.cols) v |= (uint32_t)p[2 * i + 1] << 16;
-                w[u][i] = v;
+                const uint32_t next = odd || i < 7 ? p[i + 1] : 0u;
+                w[u][i] = odd ? __byte_perm(v, next, 0x5432) : v;
+                v = next;
             }
         }
+        if (COL) __syncthreads();  // xs is laid out again
     }
     const Fp4Scale sc = make_fp4_scale(a.scale);
 
@@ -143,13 +233,13 @@ struct Fp4DequantArgs {
     uint16_t* y;
     const float* scale;
     int64_t rows, cols, tile_cols;
-    int vec;
 };
 
-template <int FMT>
+template <int FMT, bool VEC>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4DequantArgs a) {
     constexpr int kBlock = Fp4<FMT>::kBlock, kTiles = kTile / Fp4<FMT>::kSfCols;
     __shared__ __align__(16) uint32_t sfs[2 * 128];
+    __shared__ __align__(16) uint32_t raw[VEC ? 4 : kTile * kRawWords];
     const int tid = threadIdx.x;
     const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
     const int64_t r0 = tr * kTile, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kTile;
@@ -173,30 +263,60 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
     for (int u = 0; u < 4; ++u) {
         const int id = u * kThreads + tid, row = id >> 3, ck = id & 7;
         const int64_t r = r0 + row, c = c0 + ck * 16;
-        if (r >= a.rows || c >= a.cols) continue;
-        const float b = sf_value<FMT>(reinterpret_cast<const uint8_t*>(sfs)[sf_byte(row, ck * 16 / kBlock)]);
+        const bool on = r < a.rows && c < a.cols;
+        if (!on && VEC) continue;
+        const uint32_t code = reinterpret_cast<const uint8_t*>(sfs)[sf_byte(row, ck * 16 / kBlock)];
         uint32_t h[8], o[8];
         e2m1x8_to_f16(w[u].x, *reinterpret_cast<uint32_t(*)[4]>(h));
         e2m1x8_to_f16(w[u].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+        if (FMT == FP8Q_MXFP4) {
+            const float2 b = splat2(sf_value<FMT>(code));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o[i] = cvt_bf16x2(__fmul_rn(__fmul_rn(f16_lo(h[i]), b), s), __fmul_rn(__fmul_rn(f16_hi(h[i]), b), s));
-        uint16_t* y = a.y + r * a.cols + c;
-        if (a.vec) {
+            for (int i = 0; i < 8; ++i) {
+                const float2 y = mul2_rn(make_float2(f16_lo(h[i]), f16_hi(h[i])), b);
+                o[i] = cvt_bf16x2(y.x, y.y);
+            }
+        } else {
+            // code times block scale is exact in binary16: six bits at most, from 2^-10 to 2688
+            const uint32_t b = fp8x2_to_f16x2<FP8Q_E4M3FN>(code | code << 8);
+            const float2 ss = splat2(s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t v;
+                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(h[i]), "r"(b));
+                const float2 y = mul2_rn(make_float2(f16_lo(v), f16_hi(v)), ss);
+                o[i] = cvt_bf16x2(y.x, y.y);
+            }
+        }
+        if constexpr (VEC) {
+            uint16_t* y = a.y + r * a.cols + c;
             st_v4(y, make_uint4(o[0], o[1], o[2], o[3]));
             st_v4(y + 8, make_uint4(o[4], o[5], o[6], o[7]));
         } else {
+            const int odd = row_words(a.y + r * a.cols + c0, c0, a.cols).odd;
+            uint32_t* p = raw + row * kRawWords + ck * 8;
+            if (odd) {  // half a word on: this chunk's first element is its neighbour's last half-word
+                uint16_t* q = reinterpret_cast<uint16_t*>(p);
+                q[1] = (uint16_t)o[0];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < a.cols) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+                for (int i = 1; i < 8; ++i) p[i] = __byte_perm(o[i - 1], o[i], 0x5432);
+                q[16] = (uint16_t)(o[7] >> 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = o[i];
+            }
         }
+    }
+    if constexpr (!VEC) {
+        __syncthreads();
+        store_rows(raw, a.y, r0, a.rows, c0, a.cols);
     }
 }
 
-template <int FMT>
+template <int FMT, bool VEC>
 fp8q_status launch_quantize(const Fp4QuantArgs& a, unsigned grid, cudaStream_t s) {
-    auto kern = a.q ? (a.qt ? fp4_quantize_kernel<FMT, true, true> : fp4_quantize_kernel<FMT, true, false>)
-                    : fp4_quantize_kernel<FMT, false, true>;
+    auto kern = a.q ? (a.qt ? fp4_quantize_kernel<FMT, true, true, VEC> : fp4_quantize_kernel<FMT, true, false, VEC>)
+                    : fp4_quantize_kernel<FMT, false, true, VEC>;
     return launch_kernel(kern, dim3(grid), dim3(kThreads), 0, s, "fp4_quantize_kernel", a);
 }
 
@@ -239,9 +359,11 @@ fp8q_status fp8q_fp4_quantize_amax(const void* x_bf16, int64_t rows, int64_t col
     a.rows = rows;
     a.cols = cols;
     a.tile_cols = (cols + kTile - 1) / kTile;
-    a.vec = cols % 16 == 0 && ((uintptr_t)x_bf16 & 31u) == 0;
+    // rows of whole 16-column chunks on 32-byte boundaries load straight into registers
+    const bool vec = cols % 16 == 0 && ((uintptr_t)x_bf16 & 31u) == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return fmt == FP8Q_MXFP4 ? launch_quantize<FP8Q_MXFP4>(a, grid, s) : launch_quantize<FP8Q_NVFP4>(a, grid, s);
+    if (fmt == FP8Q_MXFP4) return vec ? launch_quantize<FP8Q_MXFP4, true>(a, grid, s) : launch_quantize<FP8Q_MXFP4, false>(a, grid, s);
+    return vec ? launch_quantize<FP8Q_NVFP4, true>(a, grid, s) : launch_quantize<FP8Q_NVFP4, false>(a, grid, s);
 }
 
 fp8q_status fp8q_fp4_dequantize(const uint8_t* q, const uint8_t* sf, void* y_bf16, int64_t rows, int64_t cols,
@@ -262,9 +384,10 @@ fp8q_status fp8q_fp4_dequantize(const uint8_t* q, const uint8_t* sf, void* y_bf1
     a.rows = rows;
     a.cols = cols;
     a.tile_cols = (cols + kTile - 1) / kTile;
-    a.vec = cols % 16 == 0 && ((uintptr_t)y_bf16 & 15u) == 0;
+    const bool vec = cols % 16 == 0 && ((uintptr_t)y_bf16 & 15u) == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto kern = fmt == FP8Q_MXFP4 ? fp4_dequantize_kernel<FP8Q_MXFP4> : fp4_dequantize_kernel<FP8Q_NVFP4>;
+    auto kern = fmt == FP8Q_MXFP4 ? (vec ? fp4_dequantize_kernel<FP8Q_MXFP4, true> : fp4_dequantize_kernel<FP8Q_MXFP4, false>)
+                                  : (vec ? fp4_dequantize_kernel<FP8Q_NVFP4, true> : fp4_dequantize_kernel<FP8Q_NVFP4, false>);
     return launch_kernel(kern, dim3(grid), dim3(kThreads), 0, s, "fp4_dequantize_kernel", a);
 }
 

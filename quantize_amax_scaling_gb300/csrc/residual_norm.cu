@@ -124,34 +124,54 @@ __device__ __forceinline__ float row_sum(float v, int T, float* part) {
     if ((threadIdx.x & 31) == 0) part[warp] = v;
     __syncthreads();
     v = part[(warp & ~(warps - 1)) + (threadIdx.x & (warps - 1))];
-    for (int o = warps >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+        if (o < warps) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
+// 1 / sqrt(v): the hardware's approximation and one Newton step (a relative error
+// of 2^-22 goes to 1.5 times its square, so the roundings remain: 3 u at most).
+__device__ __forceinline__ float inv_sqrt(float v) {
+    float y;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(v));
+    const float z = fmaf(y, fmaf(-0.5f * v * y, y, 0.5f), y);
+    return v > 0x1p-126f && v < 3.4e38f ? z : __frcp_rn(__fsqrt_rn(v));
+}
+
 // Codes of eight columns of h, a warp together, as fp8q_quantize_amax or
-// fp8q_fp4_quantize_amax give them.
+// fp8q_fp4_quantize_amax give them.  `at` is the place of the first in [rows, H].
 template <int FMT>
-__device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, const Fp4Scale& c4, int64_t row, int64_t at, int u, int T,
-                                            int t, bool live, const uint4& w) {
-    const int col = (u * T + t) * 8;
+__device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, const Fp4Scale& c4, int64_t row, int64_t at, int col, bool live,
+                                            const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if constexpr (FMT == FP8Q_E4M3FN || FMT == FP8Q_E5M2) {
-        uint2 o;
-        if (c8.fast)
-            o = make_uint2(quant_quad<FMT, true>(w.x, w.y, c8), quant_quad<FMT, true>(w.z, w.w, c8));
-        else
-            o = make_uint2(quant_quad<FMT, false>(w.x, w.y, c8), quant_quad<FMT, false>(w.z, w.w, c8));
-        if (live && col < a.H) st_v2(a.q + at + u * T * 8, o);
+        uint32_t o[2];
+        if (c8.fast) {
+            const float2 r = splat2(c8.r), mr = splat2(-c8.r), d = splat2(c8.s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t x = bf16x2_clamp(w[i], c8.t2);
+                const float2 f = make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+                const float2 y = quotient2(f, d, r, mr);  // divide<true>, two at a time
+                const uint32_t q = cvt_fp8x2<FMT>(y.x, y.y);
+                o[i >> 1] = i & 1 ? o[i >> 1] | (q << 16) : q;
+            }
+        } else {
+            o[0] = quant_quad<FMT, false>(w[0], w[1], c8);
+            o[1] = quant_quad<FMT, false>(w[2], w[3], c8);
+        }
+        if (live && col < a.H) st_v2(a.q + at, make_uint2(o[0], o[1]));
     } else if constexpr (FMT == FP8Q_MXFP4 || FMT == FP8Q_NVFP4) {
         constexpr int kLanes = Fp4<FMT>::kBlock / 8;  // lanes a block
-        const uint32_t m = bf16x2_absmax(bf16x2_absmax(w.x, w.y), bf16x2_absmax(w.z, w.w));
+        const uint32_t m = bf16x2_absmax(bf16x2_absmax(w[0], w[1]), bf16x2_absmax(w[2], w[3]));
         uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
         const BlockScale b = block_scale<FMT>(am, c4);
-        const uint32_t full[8] = {w.x, w.y, w.z, w.w, 0, 0, 0, 0};
-        const uint32_t mine = block_codes<FMT>(full, b).x;
+        const uint32_t codes = codes8<FMT>(w, b);
         const int64_t ld = fp4_row_bytes(a.H);
-        if (live && col < 2 * ld) *reinterpret_cast<uint32_t*>(a.q + row * ld + col / 2) = mine;
+        if (live && col < 2 * ld) *reinterpret_cast<uint32_t*>(a.q + row * ld + col / 2) = codes;
         uint32_t s = b.code;
         s |= __shfl_down_sync(0xFFFFFFFFu, b.code, kLanes) << 8;
         s |= __shfl_down_sync(0xFFFFFFFFu, b.code, 2 * kLanes) << 16;
@@ -178,36 +198,34 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
     const uint32_t step = blockDim.x * 16;  // from one slot to the next
     const uint32_t slots = 1 + (a.b != nullptr) + (ring_gate ? (a.gate_bf16 ? 1 : 2) : 0);
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) + threadIdx.x * 16;
-    const int64_t first = row0 * a.H + t * 8;  // this thread's first element
-    const uint32_t next_u = T * 8;             // from one group of eight columns to the next
+    const int col0 = t * 8;  // this thread's first columns; groups lie side by side across the warp
+    auto off = [T](int u) { return u * T * 8; };
     bool on[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) on[u] = (u * T + t) * 8 < a.H;
+    for (int u = 0; u < U; ++u) on[u] = col0 + off(u) < a.H;
 
-    // rows of a strip that are not there are not fetched: what the ring holds then is never used
-    const uint16_t *src_r = a.r + first, *src_b = a.b ? a.b + first : nullptr;
-    const uint8_t* src_g = ring_gate ? static_cast<const uint8_t*>(a.gate) + first * (a.gate_bf16 ? 2 : 4) : nullptr;
-    int64_t fetched = row0;
+    // columns that are not there stay zero in the ring, as their weights are; rows are not fetched, and
+    // what the ring holds then goes nowhere
+    for (uint32_t i = 0; i < kStages * U * slots; ++i) st_shared(ring + i * step, make_uint4(0, 0, 0, 0));
+    int64_t fetched = row0, src = row0 * a.H + col0;
     auto fetch = [&](uint32_t stage) {
         if (fetched < row1) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 uint32_t dst = ring + (stage * U + u) * slots * step;
                 if (!on[u]) continue;
-                copy16(dst, src_r + u * next_u);
-                if (a.b) copy16(dst += step, src_b + u * next_u);
+                copy16(dst, a.r + src + off(u));
+                if (a.b) copy16(dst += step, a.b + src + off(u));
                 if (ring_gate) {
                     if (a.gate_bf16) {
-                        copy16(dst += step, src_g + u * next_u * 2);
+                        copy16(dst += step, static_cast<const uint16_t*>(a.gate) + src + off(u));
                     } else {
-                        copy16(dst += step, src_g + u * next_u * 4);
-                        copy16(dst += step, src_g + u * next_u * 4 + 16);
+                        copy16(dst += step, static_cast<const float*>(a.gate) + src + off(u));
+                        copy16(dst += step, static_cast<const float*>(a.gate) + src + off(u) + 4);
                     }
                 }
             }
-            src_r += a.H;
-            src_b += a.H;
-            if (ring_gate) src_g += a.H * (a.gate_bf16 ? 2 : 4);
+            src += a.H;
             ++fetched;
         }
         copies_commit();
@@ -221,10 +239,11 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
     if constexpr (FMT == FP8Q_MXFP4 || FMT == FP8Q_NVFP4) c4 = make_fp4_scale(a.scale);
     // alpha * gate * post of a column, without the gate where it comes with the row
     auto weight = [&](int u, int64_t group) {
-        const int col = (u * T + t) * 8;
-        Oct w = splat8(a.alpha);
-        if (a.gate && !ring_gate) mul8(w, load_gate8(a.gate, a.gate_bf16, group * a.H + col));
-        if (a.post) mul8(w, load8(a.post + col));
+        Oct w = splat8(0.0f);
+        if (!on[u]) return w;
+        w = splat8(a.alpha);
+        if (a.gate && !ring_gate) mul8(w, load_gate8(a.gate, a.gate_bf16, group * a.H + col0 + off(u)));
+        if (a.post) mul8(w, load8(a.post + col0 + off(u)));
         return w;
     };
     Oct W[WREG ? U : 1], P[WREG ? U : 1];
@@ -233,13 +252,13 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             W[u] = P[u] = splat8(0.0f);
-            if (a.b && row0 < a.rows && on[u]) W[u] = weight(u, group);
-            if (a.pre && on[u]) P[u] = load8(a.pre + (u * T + t) * 8);
+            if (a.b && row0 < a.rows) W[u] = weight(u, group);
+            if (a.pre && on[u]) P[u] = load8(a.pre + col0 + off(u));
         }
     }
     const float inv_h = 1.0f / (float)a.H;
     uint32_t m2 = 0, stage = 0;
-    int64_t at = first;
+    int64_t at = row0 * a.H + col0;
     for (int64_t it = 0; it < a.per_strip; ++it, at += a.H) {
         const int64_t row = row0 + it;
         const bool live = row < row1;
@@ -249,18 +268,18 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
             if constexpr (WREG) {
                 if (live)
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (on[u]) W[u] = weight(u, group);
+                    for (int u = 0; u < U; ++u) W[u] = weight(u, group);
             }
         }
         copies_wait<kStages - 1>();
+        const uint32_t from = ring + stage * U * slots * step;
         Oct x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = on[u] ? widen8(ld_shared(ring + (stage * U + u) * slots * step)) : splat8(0.0f);
+        for (int u = 0; u < U; ++u) x[u] = widen8(ld_shared(from + u * slots * step));
         if (a.b) {
             Oct b[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) b[u] = on[u] ? widen8(ld_shared(ring + ((stage * U + u) * slots + 1) * step)) : splat8(0.0f);
+            for (int u = 0; u < U; ++u) b[u] = widen8(ld_shared(from + (u * slots + 1) * step));
             float rstd = 1.0f;
             if (a.post) {
                 float2 s[2] = {};
@@ -268,19 +287,18 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(b[u].v[i], b[u].v[i], s[i & 1]);
-                rstd = __frcp_rn(__fsqrt_rn(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2]), inv_h, a.eps)));
+                rstd = inv_sqrt(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2]), inv_h, a.eps));
                 if (a.rstd_post && live && t == 0) a.rstd_post[row] = rstd;
             }
             const float2 rs = splat2(rstd);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (!on[u]) continue;
                 Oct w;
                 if constexpr (WREG)
                     w = W[u];
                 else
                     w = weight(u, live ? group : 0);
-                if (ring_gate) mul8(w, ring_gate8(ring + ((stage * U + u) * slots + 2) * step, step, a.gate_bf16));
+                if (ring_gate) mul8(w, ring_gate8(from + (u * slots + 2) * step, step, a.gate_bf16));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[u].v[i] = fma2_rn(w.v[i], mul2_rn(b[u].v[i], rs), x[u].v[i]);
             }
@@ -292,31 +310,32 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint4 o = narrow8(x[u]);
-            if (a.ro && live && on[u]) st_v4(a.ro + at + u * next_u, o);
+            if (a.ro && live && on[u]) st_v4(a.ro + at + off(u), o);
             x[u] = widen8(o);  // the norm before the next block is of what was stored
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(x[u].v[i], x[u].v[i], s[i & 1]);
         }
         if (!a.pre) continue;
-        const float rstd = __frcp_rn(__fsqrt_rn(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2 + 1]), inv_h, a.eps)));
+        const float rstd = inv_sqrt(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2 + 1]), inv_h, a.eps));
         if (a.rstd_pre && live && t == 0) a.rstd_pre[row] = rstd;
         const float2 rs = splat2(rstd);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            uint4 o = make_uint4(0, 0, 0, 0);
-            if (live && on[u]) {
-                Oct g;
-                if constexpr (WREG)
-                    g = P[u];
-                else
-                    g = load8(a.pre + (u * T + t) * 8);
+            Oct g = splat8(0.0f);
+            if constexpr (WREG)
+                g = P[u];
+            else if (on[u])
+                g = load8(a.pre + col0 + off(u));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[u].v[i] = mul2_rn(mul2_rn(x[u].v[i], rs), g.v[i]);
-                o = narrow8(x[u]);
+            for (int i = 0; i < 4; ++i) x[u].v[i] = mul2_rn(mul2_rn(x[u].v[i], rs), g.v[i]);
+            uint4 o = narrow8(x[u]);
+            if (live && on[u]) {
+                if (a.h) st_v4(a.h + at + off(u), o);
                 m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(o.x, o.y), bf16x2_absmax(o.z, o.w)));
-                if (a.h) st_v4(a.h + at + u * next_u, o);
+            } else {
+                o = make_uint4(0, 0, 0, 0);  // where there is no column: 0 * NaN is not zero
             }
-            if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, at, u, T, t, live, o);
+            if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, at + off(u), col0 + off(u), live, o);
         }
     }
     if (a.amax) {
@@ -605,10 +624,10 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
             ++group;
             gend += a.per;
             whole = true;
-            if (!RING_GATE && row + 1 < row1)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (on[u]) weight(u);
+            if (!RING_GATE && row + 1 < row1) {
+                if (on[0]) weight(0);
+                if (on[1]) weight(1);
+            }
         }
     }
 #pragma unroll
@@ -625,44 +644,53 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
     if (CLUSTER) cg::this_cluster().sync();  // nobody's `sums` goes away while another CTA may write it
 }
 
-// 32 columns a CTA, 32 strips at a time: blockIdx.y 0 adds dpre, 1 dpost, and from
-// 2 on a row of dgate that lies in several strips: row blockIdx.y - 2, where gates
-// span strips, or else the one across the border behind strip blockIdx.y - 2.
-__global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs a) {
-    __shared__ float t[32][33];
+// 128 columns a CTA, four a thread, 16 strips at a time: blockIdx.y 0 adds dpre, 1
+// dpost, and from 2 on a row of dgate that lies in several strips: row blockIdx.y -
+// 2, where gates span strips, or else the one across the border behind strip
+// blockIdx.y - 2.
+__global__ void __launch_bounds__(512) residual_norm_sum_kernel(const RnBwdArgs a) {
+    __shared__ float4 part[16][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
+    const int col = blockIdx.x * 128 + lane * 4;
     const int what = blockIdx.y;
-    float v = 0.0f;
-    int64_t group = 0;
+    int64_t group = 0, s0 = 0, s1 = a.strips - 1;
+    const float* from = a.space + what * a.strips * a.H + col;
+    int64_t step = a.H;
     if (what < 2) {
         if (what == 0 ? !a.dpre : !a.dpost) return;
-        if (col < a.H)
-            for (int64_t s = w; s < a.strips; s += 32) v += a.space[(what * a.strips + s) * a.H + col];
     } else {
         group = a.per >= a.per_strip ? what - 2 : (what - 1) * a.per_strip / a.per;
         const int64_t begin = group * a.per, end = min(begin + a.per, a.rows);
-        const int64_t s0 = begin / a.per_strip, s1 = (end - 1) / a.per_strip;
+        s0 = begin / a.per_strip, s1 = (end - 1) / a.per_strip;
         if (s0 == s1 || (a.per < a.per_strip && s0 != what - 2)) return;  // in one strip, or another border's
-        const float* sp = a.space + 2 * a.strips * a.H;
-        if (col < a.H) {
-            // its first rows are the tail of strip s0, the rest the heads of those that follow
-            for (int64_t s = s0 + w; s <= s1; s += 32) v += sp[(2 * s + (s == s0 ? 1 : 0)) * a.H + col];
+        from = a.space + 2 * a.strips * a.H + col;
+        step = 2 * a.H;
+    }
+    float4 v = make_float4(0, 0, 0, 0);
+    if (col < a.H) {
+#pragma unroll 8
+        for (int64_t s = s0 + w; s <= s1; s += 16) {
+            // a group's first rows are the tail of strip s0, the rest the heads of those that follow
+            const float4 x = *reinterpret_cast<const float4*>(from + s * step + (what >= 2 && s == s0 ? a.H : 0));
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
         }
     }
-    t[w][lane] = v;
+    part[w][lane] = v;
     __syncthreads();
     if (w == 0 && col < a.H) {
 #pragma unroll
-        for (int i = 1; i < 32; ++i) v += t[i][lane];
+        for (int i = 1; i < 16; ++i) {
+            const float4 x = part[i][lane];
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
         if (what == 0)
-            a.dpre[col] = v;
+            *reinterpret_cast<float4*>(a.dpre + col) = v;
         else if (what == 1)
-            a.dpost[col] = v;
+            *reinterpret_cast<float4*>(a.dpost + col) = v;
         else if (a.gate_bf16)
-            static_cast<uint16_t*>(a.dgate)[group * a.H + col] = (uint16_t)(cvt_bf16x2(v, 0.0f) & 0xFFFFu);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dgate) + group * a.H + col) = make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
         else
-            static_cast<float*>(a.dgate)[group * a.H + col] = v;
+            *reinterpret_cast<float4*>(static_cast<float*>(a.dgate) + group * a.H + col) = v;
     }
 }
 
@@ -828,8 +856,8 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     int64_t across = 0;
     if (spread && st.strips > 1 && st.per_strip % a.per != 0)
         across = a.per >= st.per_strip ? (a.rows + a.per - 1) / a.per : st.strips - 1;
-    const dim3 grid((unsigned)((n->hidden + 31) / 32), (unsigned)(2 + across));
-    return launch_kernel(residual_norm_sum_kernel, grid, dim3(1024), 0, s, "residual_norm_sum_kernel", a);
+    const dim3 grid((unsigned)((n->hidden + 127) / 128), (unsigned)(2 + across));
+    return launch_kernel(residual_norm_sum_kernel, grid, dim3(512), 0, s, "residual_norm_sum_kernel", a);
 }
 
 }  // extern "C"

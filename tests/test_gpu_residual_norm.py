@@ -154,6 +154,16 @@ def test_forward_h_alone_leaves_the_residual(dev):
     near_bf16(h, w, 44 * U * w.abs(), "h")
 
 
+@pytest.mark.parametrize("fmt", [0, 1, 2, 3])
+def test_forward_zeros_keep_their_sign(dev, fmt):
+    d = make(4, 256, 4, None, 21, dev)
+    d["residual"][:, ::3] = -0.0
+    d["residual"][:, 1::6] = 0.0
+    o = forward(d, 4, 256, 4, 1.0, 1e-6, fmt=fmt, block=False, dev=dev)
+    check_forward(d, o, 4, 256, 4, 1.0, 1e-6, fmt, block=False)
+    assert (bf16_bits_of(o["h"]) == 0x8000).any()
+
+
 @pytest.mark.parametrize("fmt", [0, 3])
 @pytest.mark.parametrize("H", [64, 4096])
 def test_forward_degenerate_rows(dev, H, fmt):
