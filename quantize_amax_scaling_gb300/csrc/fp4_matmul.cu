@@ -634,7 +634,7 @@ fp8q_status launch_tiles(const CUtensorMap& mp, const CUtensorMap& mq, const MmA
     cfg.dynamicSmemBytes = MmGeom<FMT, BN>::kSmem;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.split > 1 ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, kern, mp, mq, a);
     return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "fp4_matmul_kernel");
 }
