@@ -20,6 +20,9 @@ DEPS = SRCS + [os.path.join(CSRC, h) for h in ("fp8q_common.cuh", "packed_f32.cu
 LIB = os.path.join(PKG, "libfp8q.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-lineinfo", "-O3", "-std=c++17",
@@ -41,9 +44,11 @@ def nvcc_path() -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libfp8q.so if missing or older than its sources; return its path."""
-    if not force and os.path.exists(LIB):
-        if os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in DEPS):
+    """Build libfp8q.so and the binding's compiled part if missing or older than their sources;
+    return the library's path."""
+    deps = DEPS + [BINDING_SRC]
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
+        if min(os.path.getmtime(LIB), os.path.getmtime(BINDING)) >= max(os.path.getmtime(p) for p in deps):
             return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
     nvcc = nvcc_path()
@@ -57,14 +62,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.run(cmd, check=True)
         return obj
 
-    with ThreadPoolExecutor(len(SRCS)) as ex:
+    with ThreadPoolExecutor(len(SRCS) + 1) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, SRCS))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
     for o in objs:
         os.remove(o)
     return LIB
+
+
+def build_binding() -> str:
+    """Compile _binding.so (host code; g++, torch's headers) for the running Python and torch."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    libs = os.path.join(home, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc),
+                    "-o", tmp, BINDING_SRC, f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                    "-ltorch_python"], check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build_variant(lib_path: str, defines) -> str:

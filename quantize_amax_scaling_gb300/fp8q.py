@@ -114,6 +114,24 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_binding = None
+
+
+def _native():
+    """The compiled marshalling (csrc/binding.cpp) of the 4-bit and residual-norm calls, on libfp8q's entry points."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    L = lib()
+    import torch  # noqa: F401  the module's symbols come from torch's libraries
+    from . import _binding as b
+    b.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+             (L.fp8q_fp4_quantize_amax, L.fp8q_fp4_dequantize, L.fp8q_fp4_matmul, L.fp8q_residual_norm_quantize_amax,
+              L.fp8q_residual_norm_backward)))
+    _binding = b
+    return b
+
+
 def _check(status: int, where: str):
     if status != 0:
         detail = lib().fp8q_last_cuda_error().decode() if status == 3 else ""
@@ -381,38 +399,6 @@ def fp8q_amax_scale_update_ring_quantize(history, head_in, head_out, amax_new, s
         "fp8q_amax_scale_update_ring_quantize")
 
 
-_KINDS = None
-_raw_stream = None
-
-
-def _devs(*triples):
-    """_dev for (tensor, kind, name) triples, None passed over: the common case in one
-    expression a tensor, anything else gets _dev's message.  Returns the device."""
-    global _KINDS, _raw_stream
-    if _KINDS is None:
-        import torch
-        _dev(None, "bf16", "")
-        _KINDS = {"bf16": (torch.bfloat16,), "u8": _FP8_DTYPES, "f32": (torch.float32,),
-                  "gate": (torch.float32, torch.bfloat16), "current": torch.cuda.current_device}
-        _raw_stream = torch._C._cuda_getCurrentRawStream
-    cur = None
-    for t, kind, name in triples:
-        if t is None:
-            continue
-        if cur is None and t.is_cuda:
-            cur = _KINDS["current"]()
-        if t.dtype not in _KINDS[kind] or t.get_device() != cur or not t.is_contiguous():
-            if kind == "gate":
-                kind = "bf16" if t.dtype == _KINDS["bf16"][0] else "f32"
-            _dev(t, kind, name)
-    return cur
-
-
-def _on(stream, device):
-    """The stream's handle: the device's current stream where none is given."""
-    return _raw_stream(device) if stream is None else _stream(stream)
-
-
 def fp4_row_bytes(cols):
     """Bytes of a row's codes in a packed 4-bit operand: two codes a byte, rows of whole 32-column groups."""
     return (cols + 31) // 32 * 16
@@ -425,6 +411,8 @@ def fp4_scale_bytes(rows, cols, fmt):
 
 def fp4_empty(rows, cols, fmt, device="cuda"):
     """Room for a packed 4-bit operand of an [rows, cols] matrix: (codes [rows, row bytes], scales)."""
+    if device == "cuda":
+        return _native().fp4_empty(rows, cols, fmt)
     import torch
     if fmt not in (MXFP4, NVFP4):
         raise ValueError("fmt must be MXFP4 or NVFP4")
@@ -432,78 +420,26 @@ def fp4_empty(rows, cols, fmt, device="cuda"):
             torch.empty(fp4_scale_bytes(rows, cols, fmt), dtype=torch.uint8, device=device))
 
 
-def _packed(q, sf, rows, cols, fmt, name):
-    if q.numel() != rows * fp4_row_bytes(cols) or sf is None or sf.numel() != fp4_scale_bytes(rows, cols, fmt):
-        raise ValueError(f"{name} is not a packed operand of [{rows}, {cols}]: see fp4_empty")
-
-
-def _one(t, name):
-    if t is not None and t.numel() != 1:
-        raise ValueError(f"{name} must have one element")
-
-
 def fp8q_fp4_quantize_amax(x, q, sf, fmt, scale=None, amax=None, qt=None, sft=None, stream=None):
     """The packed 4-bit operand (q, sf) of x [rows, cols], and (qt, sft) of its transpose, either
     pair None, with amax = max(amax, max|x|), in one launch.  scale (NVFP4): the tensor scale, None for 1."""
-    if x.dim() != 2:
-        raise ValueError("x must be [rows, cols]")
-    rows, cols = x.shape
-    dev = _devs((x, "bf16", "x"), (q, "u8", "q"), (sf, "u8", "sf"), (qt, "u8", "qt"), (sft, "u8", "sft"),
-                (scale, "f32", "scale"), (amax, "f32", "amax"))
-    if q is not None:
-        _packed(q, sf, rows, cols, fmt, "(q, sf)")
-    if qt is not None:
-        _packed(qt, sft, cols, rows, fmt, "(qt, sft)")
-    _one(scale, "scale")
-    _one(amax, "amax")
-    st = lib().fp8q_fp4_quantize_amax(x.data_ptr(), rows, cols, _ptr(q), _ptr(sf), _ptr(qt), _ptr(sft), fmt, _ptr(scale),
-                                      _ptr(amax), _on(stream, dev))
+    st = _native().fp4_quantize_amax(x, q, sf, fmt, scale, amax, qt, sft, stream)
     if st:
         _check(st, "fp8q_fp4_quantize_amax")
 
 
 def fp8q_fp4_dequantize(q, sf, y, fmt, scale=None, stream=None):
     """y [rows, cols] = bf16 of what the packed 4-bit operand (q, sf) stands for."""
-    if y.dim() != 2:
-        raise ValueError("y must be [rows, cols]")
-    rows, cols = y.shape
-    dev = _devs((q, "u8", "q"), (sf, "u8", "sf"), (y, "bf16", "y"), (scale, "f32", "scale"))
-    _packed(q, sf, rows, cols, fmt, "(q, sf)")
-    _one(scale, "scale")
-    st = lib().fp8q_fp4_dequantize(q.data_ptr(), sf.data_ptr(), y.data_ptr(), rows, cols, fmt, _ptr(scale), _on(stream, dev))
+    st = _native().fp4_dequantize(q, sf, y, fmt, scale, stream)
     if st:
         _check(st, "fp8q_fp4_dequantize")
 
 
 def fp8q_fp4_matmul(a, a_sf, b, b_sf, d, k, fmt, a_scale=None, b_scale=None, stream=None):
     """d [m, n] (bf16 or float32) = A [m, k] times the transpose of B [n, k], both packed 4-bit operands."""
-    if d.dim() != 2:
-        raise ValueError("d must be [m, n]")
-    m, n = d.shape
-    dev = _devs((a, "u8", "a"), (a_sf, "u8", "a_sf"), (b, "u8", "b"), (b_sf, "u8", "b_sf"), (d, "gate", "d"),
-                (a_scale, "f32", "a_scale"), (b_scale, "f32", "b_scale"))
-    _packed(a, a_sf, m, k, fmt, "(a, a_sf)")
-    _packed(b, b_sf, n, k, fmt, "(b, b_sf)")
-    _one(a_scale, "a_scale")
-    _one(b_scale, "b_scale")
-    st = lib().fp8q_fp4_matmul(a.data_ptr(), a_sf.data_ptr(), b.data_ptr(), b_sf.data_ptr(), d.data_ptr(), m, n, k, fmt,
-                               d.element_size() == 4, _ptr(a_scale), _ptr(b_scale), _on(stream, dev))
+    st = _native().fp4_matmul(a, a_sf, b, b_sf, d, k, fmt, a_scale, b_scale, stream)
     if st:
         _check(st, "fp8q_fp4_matmul")
-
-
-def _gate_rows(gate, rows, hidden, rows_per_gate):
-    if rows_per_gate < 1:
-        raise ValueError("rows_per_gate must be at least 1")
-    groups = (rows + rows_per_gate - 1) // rows_per_gate
-    if gate.numel() != groups * hidden:
-        raise ValueError(f"gate must be [{groups}, {hidden}]")
-
-
-def _sizes(n, what, *pairs):
-    for t, name in pairs:
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name} must have {what}={n} elements")
 
 
 def fp8q_residual_norm_quantize_amax(residual, residual_out, block=None, post_weight=None, gate=None, rows_per_gate=0,
@@ -516,30 +452,8 @@ def fp8q_residual_norm_quantize_amax(residual, residual_out, block=None, post_we
     Parts left None are left out (no ``post_weight``: block is added as it is); ``residual_out`` may be
     ``residual``.  ``rstd_post`` and ``rstd_pre`` (float32 [rows]) keep what the backward pass needs.
     """
-    if residual.dim() != 2:
-        raise ValueError("residual must be [rows, hidden]")
-    rows, hidden = residual.shape
-    dev = _devs((residual, "bf16", "residual"), (residual_out, "bf16", "residual_out"), (block, "bf16", "block"),
-                (post_weight, "f32", "post_weight"), (gate, "gate", "gate"), (pre_weight, "f32", "pre_weight"),
-                (h, "bf16", "h"), (q, "u8", "q"), (sf, "u8", "sf"), (scale, "f32", "scale"), (amax, "f32", "amax"),
-                (rstd_post, "f32", "rstd_post"), (rstd_pre, "f32", "rstd_pre"))
-    n = rows * hidden
-    _sizes(n, "rows * hidden", (residual_out, "residual_out"), (block, "block"), (h, "h"))
-    _sizes(hidden, "hidden", (post_weight, "post_weight"), (pre_weight, "pre_weight"))
-    _sizes(rows, "rows", (rstd_post, "rstd_post"), (rstd_pre, "rstd_pre"))
-    if gate is not None:
-        _gate_rows(gate, rows, hidden, rows_per_gate)
-    if q is not None:
-        if fmt in (MXFP4, NVFP4):
-            _packed(q, sf, rows, hidden, fmt, "(q, sf)")
-        else:
-            _sizes(n, "rows * hidden", (q, "q"))
-    _one(scale, "scale")
-    _one(amax, "amax")
-    args = ResidualNorm(rows, hidden, fmt, residual.data_ptr(), _ptr(block), _ptr(post_weight), _ptr(gate), rows_per_gate,
-                        gate is not None and gate.element_size() == 2, alpha, eps, _ptr(pre_weight), _ptr(residual_out),
-                        _ptr(h), _ptr(q), _ptr(sf), _ptr(scale), _ptr(amax), _ptr(rstd_post), _ptr(rstd_pre))
-    st = lib().fp8q_residual_norm_quantize_amax(ctypes.byref(args), _on(stream, dev))
+    st = _native().residual_norm_quantize_amax(residual, residual_out, block, post_weight, gate, rows_per_gate, alpha,
+                                               pre_weight, h, q, sf, fmt, scale, amax, rstd_post, rstd_pre, eps, stream)
     if st:
         _check(st, "fp8q_residual_norm_quantize_amax")
 
@@ -556,29 +470,9 @@ def fp8q_residual_norm_backward(d_residual_out, d_h, residual_out, rstd_pre, pre
     rstd_pre and pre_weight) come from what follows, either may be None; gradients left None are not
     computed.  ``workspace``: residual_norm_backward_workspace bytes (uint8), for one call at a time.
     """
-    d = d_residual_out if d_residual_out is not None else d_h
-    if d is None or d.dim() != 2:
-        raise ValueError("d_residual_out or d_h must be [rows, hidden]")
-    rows, hidden = d.shape
-    dev = _devs((d_residual_out, "bf16", "d_residual_out"), (d_h, "bf16", "d_h"), (residual_out, "bf16", "residual_out"),
-                (rstd_pre, "f32", "rstd_pre"), (pre_weight, "f32", "pre_weight"), (d_residual, "bf16", "d_residual"),
-                (d_pre_weight, "f32", "d_pre_weight"), (block, "bf16", "block"), (rstd_post, "f32", "rstd_post"),
-                (post_weight, "f32", "post_weight"), (gate, "gate", "gate"), (d_block, "bf16", "d_block"),
-                (d_post_weight, "f32", "d_post_weight"), (d_gate, "gate", "d_gate"), (workspace, "u8", "workspace"))
-    _sizes(rows * hidden, "rows * hidden", (d_residual_out, "d_residual_out"), (d_h, "d_h"), (residual_out, "residual_out"),
-           (block, "block"), (d_residual, "d_residual"), (d_block, "d_block"))
-    _sizes(hidden, "hidden", (pre_weight, "pre_weight"), (post_weight, "post_weight"), (d_pre_weight, "d_pre_weight"),
-           (d_post_weight, "d_post_weight"))
-    _sizes(rows, "rows", (rstd_pre, "rstd_pre"), (rstd_post, "rstd_post"))
-    if gate is not None:
-        _gate_rows(gate, rows, hidden, rows_per_gate)
-        if d_gate is not None and (d_gate.numel() != gate.numel() or d_gate.dtype != gate.dtype):
-            raise ValueError("d_gate must have gate's shape and type")
-    args = ResidualNormGrad(rows, hidden, gate is not None and gate.element_size() == 2, _ptr(d_residual_out), _ptr(d_h),
-                            _ptr(residual_out), _ptr(rstd_pre), _ptr(pre_weight), _ptr(block), _ptr(rstd_post),
-                            _ptr(post_weight), _ptr(gate), rows_per_gate, alpha, _ptr(d_residual), _ptr(d_block),
-                            _ptr(d_pre_weight), _ptr(d_post_weight), _ptr(d_gate), _ptr(workspace), _numel(workspace))
-    st = lib().fp8q_residual_norm_backward(ctypes.byref(args), _on(stream, dev))
+    st = _native().residual_norm_backward(d_residual_out, d_h, residual_out, rstd_pre, pre_weight, d_residual,
+                                          d_pre_weight, block, rstd_post, post_weight, gate, rows_per_gate, alpha,
+                                          d_block, d_post_weight, d_gate, workspace, stream)
     if st:
         _check(st, "fp8q_residual_norm_backward")
 
