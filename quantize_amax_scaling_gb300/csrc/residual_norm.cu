@@ -114,15 +114,24 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the T threads of a row (T a power of two from 32 to 1024; every thread
-// of the CTA calls it).  `part` holds one float a warp and is not written again
+// A row's T threads wait for one another: the whole CTA where it has one row,
+// else by a barrier of their own.
+__device__ __forceinline__ void row_barrier(int T) {
+    if (T == (int)blockDim.x)
+        __syncthreads();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / T), "r"(T) : "memory");
+}
+
+// Sum over the T threads of a row (T a power of two from 32 to 1024; all of them
+// call it).  `part` holds one float a warp and is not written again
 // before the next barrier but one.
 __device__ __forceinline__ float row_sum(float v, int T, float* part) {
     v = warp_sum(v);
     if (T == 32) return v;
     const int warp = threadIdx.x >> 5, warps = T >> 5;
     if ((threadIdx.x & 31) == 0) part[warp] = v;
-    __syncthreads();
+    row_barrier(T);
     v = part[(warp & ~(warps - 1)) + (threadIdx.x & (warps - 1))];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -182,22 +191,30 @@ __device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, c
     }
 }
 
-// U groups of eight columns a thread.  WREG: the weights stay in registers (rows
-// of up to 512 threads); longer rows, with 64 registers a thread, read them from
-// L1 for each row, and the longest have room for one row ahead in shared memory.
-template <int FMT, int U, bool WREG>
-__global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(const RnArgs a) {
+// U groups of eight columns a thread, THREADS threads a CTA.  Nothing but the
+// packed sum stays in registers across the two reductions, and the weights lie in
+// shared memory beside the ring (each thread's own; rows of 1024 threads read them
+// from L1): with 16 columns' weights and values in registers 16 warps fit an SM and
+// issued 59% of the time, 53 us for 8192x4096; with 24 warps it takes 49.  ROW > 0:
+// the call that a block's edge makes (all parts there, a gate for several rows),
+// for rows of that many threads: 43 us.
+template <int FMT, int U, int THREADS, int ROW>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) residual_norm_kernel(const RnArgs a) {
+    constexpr bool kFull = ROW > 0, kHold = THREADS < 1024;  // weights in shared memory
+    constexpr int kStages = THREADS < 1024 ? 2 : U == 2 ? 3 : 1;  // rows under way
+    constexpr uint32_t kStep = THREADS * 16;                // from one slot to the next
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float part[4][32];
     __shared__ uint32_t red[32];
-    const int T = a.T, t = threadIdx.x % T;
-    const int64_t strip = (int64_t)blockIdx.x * (blockDim.x / T) + threadIdx.x / T;
-    const int64_t row0 = strip * a.per_strip, row1 = min(row0 + a.per_strip, a.rows);
-    constexpr int kStages = U == 2 ? 3 : 1;  // rows under way
-    const bool ring_gate = WREG && a.gate && a.per == 1;
-    const uint32_t step = blockDim.x * 16;  // from one slot to the next
-    const uint32_t slots = 1 + (a.b != nullptr) + (ring_gate ? (a.gate_bf16 ? 1 : 2) : 0);
+    const bool has_b = kFull || a.b, has_post = kFull || a.post, has_pre = kFull || a.pre, has_ro = kFull || a.ro;
+    const int T = kFull ? ROW : a.T, t = threadIdx.x % T;
+    const uint32_t strip = blockIdx.x * (THREADS / T) + threadIdx.x / T;
+    const uint32_t rows = (uint32_t)a.rows, per_strip = (uint32_t)a.per_strip;
+    const uint32_t row0 = strip * per_strip, row1 = min(row0 + per_strip, rows);
+    const bool ring_gate = !kFull && kHold && a.gate && a.per == 1;
+    const uint32_t slots = 1 + has_b + (ring_gate ? (a.gate_bf16 ? 1 : 2) : 0);
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) + threadIdx.x * 16;
+    const uint32_t weights = ring + kStages * U * slots * kStep;  // 2 U slots of alpha * gate * post, 2 U of pre
     const int col0 = t * 8;  // this thread's first columns; groups lie side by side across the warp
     auto off = [T](int u) { return u * T * 8; };
     bool on[U];
@@ -206,22 +223,23 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
 
     // columns that are not there stay zero in the ring, as their weights are; rows are not fetched, and
     // what the ring holds then goes nowhere
-    for (uint32_t i = 0; i < kStages * U * slots; ++i) st_shared(ring + i * step, make_uint4(0, 0, 0, 0));
-    int64_t fetched = row0, src = row0 * a.H + col0;
+    for (uint32_t i = 0; i < kStages * U * slots + (kHold ? 4 * U : 0); ++i) st_shared(ring + i * kStep, make_uint4(0, 0, 0, 0));
+    uint32_t fetched = row0;
+    int64_t src = (int64_t)row0 * a.H + col0;
     auto fetch = [&](uint32_t stage) {
         if (fetched < row1) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                uint32_t dst = ring + (stage * U + u) * slots * step;
+                uint32_t dst = ring + (stage * U + u) * slots * kStep;
                 if (!on[u]) continue;
                 copy16(dst, a.r + src + off(u));
-                if (a.b) copy16(dst += step, a.b + src + off(u));
+                if (has_b) copy16(dst += kStep, a.b + src + off(u));
                 if (ring_gate) {
                     if (a.gate_bf16) {
-                        copy16(dst += step, static_cast<const uint16_t*>(a.gate) + src + off(u));
+                        copy16(dst += kStep, static_cast<const uint16_t*>(a.gate) + src + off(u));
                     } else {
-                        copy16(dst += step, static_cast<const float*>(a.gate) + src + off(u));
-                        copy16(dst += step, static_cast<const float*>(a.gate) + src + off(u) + 4);
+                        copy16(dst += kStep, static_cast<const float*>(a.gate) + src + off(u));
+                        copy16(dst += kStep, static_cast<const float*>(a.gate) + src + off(u) + 4);
                     }
                 }
             }
@@ -243,99 +261,104 @@ __global__ void __launch_bounds__(WREG ? 512 : 1024, 1) residual_norm_kernel(con
         if (!on[u]) return w;
         w = splat8(a.alpha);
         if (a.gate && !ring_gate) mul8(w, load_gate8(a.gate, a.gate_bf16, group * a.H + col0 + off(u)));
-        if (a.post) mul8(w, load8(a.post + col0 + off(u)));
+        if (has_post) mul8(w, load8(a.post + col0 + off(u)));
         return w;
     };
-    Oct W[WREG ? U : 1], P[WREG ? U : 1];
-    int64_t group = a.gate && !ring_gate ? row0 / a.per : 0, gend = a.gate && !ring_gate ? (group + 1) * a.per : a.rows;
-    if constexpr (WREG) {
+    auto keep = [&](uint32_t at, const Oct& o) {
+        st_shared(at, make_uint4(__float_as_uint(o.v[0].x), __float_as_uint(o.v[0].y), __float_as_uint(o.v[1].x), __float_as_uint(o.v[1].y)));
+        st_shared(at + kStep, make_uint4(__float_as_uint(o.v[2].x), __float_as_uint(o.v[2].y), __float_as_uint(o.v[3].x), __float_as_uint(o.v[3].y)));
+    };
+    auto kept = [&](uint32_t at) { return pairs8(as_f4(ld_shared(at)), as_f4(ld_shared(at + kStep))); };
+    const uint32_t per = ring_gate || !a.gate ? rows : (uint32_t)min(a.per, (int64_t)rows);  // rows a gate's row
+    uint32_t group = row0 / per, gend = (group + 1) * per;
+    if (gend < row0) gend = rows;  // past 32 bits
+    if (kHold && row0 < rows) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            W[u] = P[u] = splat8(0.0f);
-            if (a.b && row0 < a.rows) W[u] = weight(u, group);
-            if (a.pre && on[u]) P[u] = load8(a.pre + col0 + off(u));
+            if (has_b) keep(weights + 2 * u * kStep, weight(u, group));
+            if (has_pre && on[u]) keep(weights + (2 * U + 2 * u) * kStep, load8(a.pre + col0 + off(u)));
         }
     }
     const float inv_h = 1.0f / (float)a.H;
     uint32_t m2 = 0, stage = 0;
-    int64_t at = row0 * a.H + col0;
-    for (int64_t it = 0; it < a.per_strip; ++it, at += a.H) {
-        const int64_t row = row0 + it;
+    int64_t at = (int64_t)row0 * a.H + col0;
+    for (uint32_t it = 0; it < per_strip; ++it, at += a.H) {
+        const uint32_t row = row0 + it;
         const bool live = row < row1;
-        if (row == gend) {
+        if (row == gend && live) {
             ++group;
-            gend += a.per;
-            if constexpr (WREG) {
-                if (live)
+            gend += per;
+            if (kHold && has_b)
 #pragma unroll
-                    for (int u = 0; u < U; ++u) W[u] = weight(u, group);
-            }
+                for (int u = 0; u < U; ++u) keep(weights + 2 * u * kStep, weight(u, group));
         }
         copies_wait<kStages - 1>();
-        const uint32_t from = ring + stage * U * slots * step;
-        Oct x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = widen8(ld_shared(from + u * slots * step));
-        if (a.b) {
-            Oct b[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) b[u] = widen8(ld_shared(from + (u * slots + 1) * step));
+        const uint32_t from = ring + stage * U * slots * kStep;
+        uint4 o[U];
+        float2 s[2] = {};
+        if (has_b) {
             float rstd = 1.0f;
-            if (a.post) {
-                float2 s[2] = {};
+            if (has_post) {
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u) {
+                    const Oct b = widen8(ld_shared(from + (u * slots + 1) * kStep));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(b[u].v[i], b[u].v[i], s[i & 1]);
+                    for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(b.v[i], b.v[i], s[i & 1]);
+                }
                 rstd = inv_sqrt(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2]), inv_h, a.eps));
                 if (a.rstd_post && live && t == 0) a.rstd_post[row] = rstd;
+                s[0] = s[1] = make_float2(0.0f, 0.0f);
             }
             const float2 rs = splat2(rstd);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                Oct w;
-                if constexpr (WREG)
-                    w = W[u];
-                else
-                    w = weight(u, live ? group : 0);
-                if (ring_gate) mul8(w, ring_gate8(from + (u * slots + 2) * step, step, a.gate_bf16));
+                Oct w = kHold ? kept(weights + 2 * u * kStep) : weight(u, live ? group : 0);
+                if (ring_gate) mul8(w, ring_gate8(from + (u * slots + 2) * kStep, kStep, a.gate_bf16));
+                Oct x = widen8(ld_shared(from + u * slots * kStep));
+                const Oct b = widen8(ld_shared(from + (u * slots + 1) * kStep));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[u].v[i] = fma2_rn(w.v[i], mul2_rn(b[u].v[i], rs), x[u].v[i]);
+                for (int i = 0; i < 4; ++i) x.v[i] = fma2_rn(w.v[i], mul2_rn(b.v[i], rs), x.v[i]);
+                o[u] = narrow8(x);
             }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) o[u] = ld_shared(from + u * slots * kStep);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (has_ro && live && on[u]) st_v4(a.ro + at + off(u), o[u]);
+            const Oct x = widen8(o[u]);  // the norm before the next block is of what was stored
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(x.v[i], x.v[i], s[i & 1]);
+        }
+        float rstd = 0.0f;
+        if (has_pre) {
+            rstd = inv_sqrt(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2 + 1]), inv_h, a.eps));
+            if (a.rstd_pre && live && t == 0) a.rstd_pre[row] = rstd;
         }
         // everything of this stage has been used: the row after the next ones into it
         fetch(stage);
         if (++stage == kStages) stage = 0;
-        float2 s[2] = {};
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint4 o = narrow8(x[u]);
-            if (a.ro && live && on[u]) st_v4(a.ro + at + off(u), o);
-            x[u] = widen8(o);  // the norm before the next block is of what was stored
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i & 1] = fma2_rn(x[u].v[i], x[u].v[i], s[i & 1]);
-        }
-        if (!a.pre) continue;
-        const float rstd = inv_sqrt(fmaf(row_sum(sum2(s[0], s[1]), T, part[(it & 1) * 2 + 1]), inv_h, a.eps));
-        if (a.rstd_pre && live && t == 0) a.rstd_pre[row] = rstd;
+        if (!has_pre) continue;
         const float2 rs = splat2(rstd);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             Oct g = splat8(0.0f);
-            if constexpr (WREG)
-                g = P[u];
+            if (kHold)
+                g = kept(weights + (2 * U + 2 * u) * kStep);
             else if (on[u])
                 g = load8(a.pre + col0 + off(u));
+            Oct x = widen8(o[u]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[u].v[i] = mul2_rn(mul2_rn(x[u].v[i], rs), g.v[i]);
-            uint4 o = narrow8(x[u]);
+            for (int i = 0; i < 4; ++i) x.v[i] = mul2_rn(mul2_rn(x.v[i], rs), g.v[i]);
+            uint4 h = narrow8(x);
             if (live && on[u]) {
-                if (a.h) st_v4(a.h + at + off(u), o);
-                m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(o.x, o.y), bf16x2_absmax(o.z, o.w)));
+                if (a.h) st_v4(a.h + at + off(u), h);
+                m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(h.x, h.y), bf16x2_absmax(h.z, h.w)));
             } else {
-                o = make_uint4(0, 0, 0, 0);  // where there is no column: 0 * NaN is not zero
+                h = make_uint4(0, 0, 0, 0);  // where there is no column: 0 * NaN is not zero
             }
-            if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, at + off(u), col0 + off(u), live, o);
+            if constexpr (FMT != kOutNone) store_codes<FMT>(a, c8, c4, row, at + off(u), col0 + off(u), live, h);
         }
     }
     if (a.amax) {
@@ -722,17 +745,32 @@ fp8q_status launch_forward(RnArgs a, cudaStream_t s) {
     a.T = 1024;
     while (a.T > 32 && a.H <= a.T * 4 * U) a.T /= 2;
     const int block = a.T < 256 ? 256 : a.T, per_cta = block / a.T;
-    // strips: two CTAs of 256 threads an SM, one of 512 or 1024
-    const int64_t most = (int64_t)(block == 256 ? 2 : 1) * 152 * per_cta;
+    const int slots = 1 + (a.b != nullptr) + (block < 1024 && a.gate && a.per == 1 ? (a.gate_bf16 ? 1 : 2) : 0);
+    const size_t smem = (size_t)((block < 1024 ? 2 : U == 2 ? 3 : 1) * U * slots + (block < 1024 ? 4 * U : 0)) * block * 16;
+    // strips: as many as CTAs are resident, three of 256 threads an SM (two with a gate in the ring), one of 512 or 1024
+    const int64_t most = (int64_t)(block > 256 ? 1 : smem <= 74 * 1024 ? 3 : 2) * 152 * per_cta;
     a.per_strip = (a.rows + most - 1) / most;
     const int64_t strips = (a.rows + a.per_strip - 1) / a.per_strip;
-    const int slots = 1 + (a.b != nullptr) + (a.T < 1024 && a.gate && a.per == 1 ? (a.gate_bf16 ? 1 : 2) : 0);
-    const size_t smem = (size_t)(U == 2 ? 3 : 1) * U * slots * block * 16;
     const dim3 grid((unsigned)((strips + per_cta - 1) / per_cta));
-    static std::atomic<uint64_t> devices[3];
-    auto kern = U == 4 ? residual_norm_kernel<FMT, 4, false> : a.T == 1024 ? residual_norm_kernel<FMT, 2, false> : residual_norm_kernel<FMT, 2, true>;
-    // 3 stages of 4 slots of 512 threads, or of 2 slots of 1024
-    const cudaError_t e = allow_smem(kern, 192 * 1024, devices[U == 4 ? 2 : a.T == 1024 ? 1 : 0]);
+    static std::atomic<uint64_t> devices[9];
+    const int which = block == 256 ? 0 : block == 512 ? 1 : U == 2 ? 2 : 3;
+    auto kern = which == 0   ? residual_norm_kernel<FMT, 2, 256, 0>
+                : which == 1 ? residual_norm_kernel<FMT, 2, 512, 0>
+                : which == 2 ? residual_norm_kernel<FMT, 2, 1024, 0>
+                             : residual_norm_kernel<FMT, 4, 1024, 0>;
+    int set = which;
+    if constexpr (FMT != kOutNone) {
+        if (a.b && a.post && a.pre && a.ro && !(a.gate && a.per == 1) && a.T <= 512) {
+            set = a.T == 32 ? 4 : a.T == 64 ? 5 : a.T == 128 ? 6 : a.T == 256 ? 7 : 8;
+            kern = set == 4   ? residual_norm_kernel<FMT, 2, 256, 32>
+                   : set == 5 ? residual_norm_kernel<FMT, 2, 256, 64>
+                   : set == 6 ? residual_norm_kernel<FMT, 2, 256, 128>
+                   : set == 7 ? residual_norm_kernel<FMT, 2, 256, 256>
+                              : residual_norm_kernel<FMT, 2, 512, 512>;
+        }
+    }
+    // at most 2 stages of 8 slots and 8 of weights of 512 threads, or 6 or 8 slots of 1024
+    const cudaError_t e = allow_smem(kern, 192 * 1024, devices[set]);
     if (e != cudaSuccess) return cuda_fail(e, "residual_norm_kernel setup");
     return launch_kernel(kern, grid, dim3(block), smem, s, "residual_norm_kernel", a);
 }
