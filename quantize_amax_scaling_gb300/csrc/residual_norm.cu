@@ -450,14 +450,17 @@ __device__ __forceinline__ float warp_sum3(float a, float b, float c) {
 // W = alpha gate g1 of a column, a row adds X to the one sum S that dgate and dg1
 // share: a gate's row of dgate is alpha g1 S, and dg1 takes alpha gate S whenever
 // a gate's rows end.  RING_GATE: each row has its own gate, which comes with it.
-template <bool CLUSTER, bool RING_GATE>
+template <bool CLUSTER, bool RING_GATE, int ROW>
 __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const RnBwdArgs a) {
     namespace cg = cooperative_groups;
     constexpr int kStages = RING_GATE ? 2 : 3;
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float part[2][3][8];
     __shared__ float sums[2][8][3];  // of each CTA of the cluster
-    const int T = a.T, t = threadIdx.x % T, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr bool kFull = ROW > 0;
+    const bool has_b = kFull || a.b, has_post = kFull || a.post, has_dh = kFull || a.dh, has_dro = kFull || a.dro;
+    const bool has_dr = kFull || a.dr, has_db = kFull || a.db;
+    const int T = kFull ? ROW : a.T, t = threadIdx.x % T, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int slices = 1, slice = 0;
     if (CLUSTER) {
         slices = (int)cg::this_cluster().num_blocks();
@@ -487,12 +490,12 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
                 if (!on[u]) continue;
                 const uint32_t dst = ring + (stage * 2 + u) * slots * kStep;
                 const int64_t at = src + u * next_u;
-                if (a.b) copy16(dst, a.b + at);
-                if (a.dh) {
+                if (has_b) copy16(dst, a.b + at);
+                if (has_dh) {
                     copy16(dst + kStep, a.ro + at);
                     copy16(dst + 3 * kStep, a.dh + at);
                 }
-                if (a.dro) copy16(dst + 2 * kStep, a.dro + at);
+                if (has_dro) copy16(dst + 2 * kStep, a.dro + at);
                 if (RING_GATE) {
                     if (a.gate_bf16) {
                         copy16(dst + 4 * kStep, static_cast<const uint16_t*>(a.gate) + at);
@@ -517,23 +520,29 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
     // alpha * gate * post of a column, without a gate that comes with the row
     auto weight = [&](int u) {
         W[u] = splat8(a.alpha);
-        if (a.post) mul8(W[u], load8(a.post + col0 + u * next_u));
+        if (has_post) mul8(W[u], load8(a.post + col0 + u * next_u));
         if (a.gate && !RING_GATE) mul8(W[u], load_gate8(a.gate, a.gate_bf16, group * a.H + col0 + u * next_u));
     };
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         Q[u] = W[u] = S[u] = apre[u] = splat8(0.0f);
-        if (a.dh && on[u]) Q[u] = load8(a.pre + col0 + u * next_u);
+        if (has_dh && on[u]) Q[u] = load8(a.pre + col0 + u * next_u);
         if (row0 < a.rows && on[u]) weight(u);
     }
 
     uint32_t stage = 0;
     int64_t at = row0 * a.H + col0;
+    // a row's two factors are on their way while the row before it is worked on
+    float next2 = has_dh && row0 < row1 ? __ldg(a.rstd_pre + row0) : 0.0f;
+    float next1 = has_post && row0 < row1 ? __ldg(a.rstd_post + row0) : 1.0f;
     for (int64_t it = 0; it < a.per_strip; ++it, at += a.H) {
         const int64_t row = row0 + it;
         const bool live = row < row1;
-        const float rstd2 = a.dh && live ? __ldg(a.rstd_pre + row) : 0.0f;
-        const float rstd1 = a.post && live ? __ldg(a.rstd_post + row) : 1.0f;
+        const float rstd2 = next2, rstd1 = next1;
+        if (row + 1 < row1) {
+            if (has_dh) next2 = __ldg(a.rstd_pre + row + 1);
+            if (has_post) next1 = __ldg(a.rstd_post + row + 1);
+        }
         const float2 r2 = splat2(rstd2), r1 = splat2(rstd1);
         copies_wait<kStages - 1>();
         const uint32_t at_stage = ring + stage * 2 * slots * kStep;
@@ -591,11 +600,12 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
             }
         }
         const float c2 = s0 * inv_h;
-        const float m1 = a.post ? (s1 - rstd2 * c2 * s2) * inv_h : 0.0f;  // mean(w D); no term without g1
+        const float m1 = has_post ? (s1 - rstd2 * c2 * s2) * inv_h : 0.0f;  // mean(w D); no term without g1
         const float2 mc2 = splat2(-c2), mm1 = splat2(-m1);
-        const bool flush = live && a.b && (row + 1 == gend || row + 1 == row1);
+        const bool flush = has_b && (row + 1 == gend || row + 1 == row1);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+            if (!live) continue;  // what the ring holds is another row's
             const uint32_t from = at_stage + u * slots * kStep;
             const Oct fb = widen8(ld_shared(from)), fo = widen8(ld_shared(from + kStep)), fh = widen8(ld_shared(from + 3 * kStep));
             Oct D = widen8(ld_shared(from + 2 * kStep)), w = W[u], e, g;
@@ -611,13 +621,13 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
                 S[u].v[i] = fma2_rn(D.v[i], n1, S[u].v[i]);
                 e.v[i] = mul2_rn(r1, fma2_rn(n1, mm1, mul2_rn(D.v[i], w.v[i])));
             }
-            if (!live || !on[u]) continue;
-            if (a.dr) st_v4(a.dr + at + u * next_u, narrow8(D));
-            if (a.db) st_v4(a.db + at + u * next_u, narrow8(e));
+            if (!on[u]) continue;
+            if (has_dr) st_v4(a.dr + at + u * next_u, narrow8(D));
+            if (has_db) st_v4(a.db + at + u * next_u, narrow8(e));
             if (flush) {
                 const int col = col0 + u * next_u;
                 Oct p = splat8(1.0f);
-                if (a.post) p = load8(a.post + col);
+                if (has_post) p = load8(a.post + col);
                 if (a.gate && !RING_GATE) g = load_gate8(a.gate, a.gate_bf16, group * a.H + col);
                 if (!a.gate) g = splat8(1.0f);
                 mul8(S[u], splat8(a.alpha));
@@ -717,10 +727,10 @@ __global__ void __launch_bounds__(512) residual_norm_sum_kernel(const RnBwdArgs 
     }
 }
 
-template <bool CLUSTER, bool RING_GATE>
+template <bool CLUSTER, bool RING_GATE, int ROW>
 fp8q_status launch_backward(const RnBwdArgs& a, unsigned ctas, unsigned slices, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};
-    auto kern = residual_norm_backward_kernel<CLUSTER, RING_GATE>;
+    auto kern = residual_norm_backward_kernel<CLUSTER, RING_GATE, ROW>;
     const size_t smem = ((RING_GATE ? 2 * 2 * (a.gate_bf16 ? 5 : 6) : 3 * 2 * 4) + 4) * 4096;
     cudaError_t e = allow_smem(kern, 112 * 1024, devices);
     if (e != cudaSuccess) return cuda_fail(e, "residual_norm_backward_kernel setup");
@@ -887,8 +897,20 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     const unsigned ctas = (unsigned)((st.strips + per_cta - 1) / per_cta) * (unsigned)st.slices;
     const bool ring_gate = a.gate && a.per == 1;
     const unsigned slices = (unsigned)st.slices;
-    const fp8q_status rc = slices == 1 ? (ring_gate ? launch_backward<false, true>(a, ctas, 1, s) : launch_backward<false, false>(a, ctas, 1, s))
-                                       : (ring_gate ? launch_backward<true, true>(a, ctas, slices, s) : launch_backward<true, false>(a, ctas, slices, s));
+    // the call that a block's edge makes: everything there
+    const bool full = a.b && a.post && a.dh && a.dro && a.dr && a.db;
+    fp8q_status rc;
+    if (ring_gate)
+        rc = slices == 1 ? launch_backward<false, true, 0>(a, ctas, 1, s) : launch_backward<true, true, 0>(a, ctas, slices, s);
+    else if (slices > 1)
+        rc = full ? launch_backward<true, false, 256>(a, ctas, slices, s) : launch_backward<true, false, 0>(a, ctas, slices, s);
+    else if (!full)
+        rc = launch_backward<false, false, 0>(a, ctas, 1, s);
+    else
+        rc = a.T == 32    ? launch_backward<false, false, 32>(a, ctas, 1, s)
+             : a.T == 64  ? launch_backward<false, false, 64>(a, ctas, 1, s)
+             : a.T == 128 ? launch_backward<false, false, 128>(a, ctas, 1, s)
+                          : launch_backward<false, false, 256>(a, ctas, 1, s);
     if (rc != FP8Q_OK || (!a.dpre && !a.dpost && !spread)) return rc;
     // rows of dgate to add up: those of a gate that spans strips, or the ones across their borders
     int64_t across = 0;
