@@ -677,12 +677,14 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
     if (CLUSTER) cg::this_cluster().sync();  // nobody's `sums` goes away while another CTA may write it
 }
 
-// 128 columns a CTA, four a thread, 16 strips at a time: blockIdx.y 0 adds dpre, 1
+// 128 columns a CTA, four a thread, 32 strips at a time: blockIdx.y 0 adds dpre, 1
 // dpost, and from 2 on a row of dgate that lies in several strips: row blockIdx.y -
 // 2, where gates span strips, or else the one across the border behind strip
 // blockIdx.y - 2.
-__global__ void __launch_bounds__(512) residual_norm_sum_kernel(const RnBwdArgs a) {
-    __shared__ float4 part[16][32];
+__global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs a) {
+    __shared__ float4 part[32][32];
+    // launched while the kernel that writes the strips still runs: nothing is read before it has ended
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int col = blockIdx.x * 128 + lane * 4;
     const int what = blockIdx.y;
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(512) residual_norm_sum_kernel(const RnBwdArgs 
     float4 v = make_float4(0, 0, 0, 0);
     if (col < a.H) {
 #pragma unroll 8
-        for (int64_t s = s0 + w; s <= s1; s += 16) {
+        for (int64_t s = s0 + w; s <= s1; s += 32) {
             // a group's first rows are the tail of strip s0, the rest the heads of those that follow
             const float4 x = *reinterpret_cast<const float4*>(from + s * step + (what >= 2 && s == s0 ? a.H : 0));
             v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(512) residual_norm_sum_kernel(const RnBwdArgs 
     __syncthreads();
     if (w == 0 && col < a.H) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) {
+        for (int i = 1; i < 32; ++i) {
             const float4 x = part[i][lane];
             v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
         }
@@ -917,7 +919,17 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     if (spread && st.strips > 1 && st.per_strip % a.per != 0)
         across = a.per >= st.per_strip ? (a.rows + a.per - 1) / a.per : st.strips - 1;
     const dim3 grid((unsigned)((n->hidden + 127) / 128), (unsigned)(2 + across));
-    return launch_kernel(residual_norm_sum_kernel, grid, dim3(512), 0, s, "residual_norm_sum_kernel", a);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, residual_norm_sum_kernel, a);
+    return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "residual_norm_sum_kernel");
 }
 
 }  // extern "C"
