@@ -176,12 +176,9 @@ __device__ __noinline__ float slow_quotient(float x, float d) {
     return fabsf(x) > 3.402823466e38f ? x : __fdiv_rn(x, d);
 }
 
-// Eight bf16 of a block (four words, the even column low) -> eight codes.
+// Eight values of a block -> eight codes.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], const BlockScale& b) {
-    float2 f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+__device__ __forceinline__ uint32_t codes8(float2 (&f)[4], const BlockScale& b) {
     if (FMT == FP8Q_MXFP4) {
         const float2 d = splat2(b.d);
 #pragma unroll
@@ -195,6 +192,15 @@ __device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], const BlockSc
         for (int i = 0; i < 4; ++i) f[i] = make_float2(slow_quotient(f[i].x, b.d), slow_quotient(f[i].y, b.d));
     }
     return cvt_e2m1x8(f);
+}
+
+// Eight bf16 of a block (four words, the even column low).
+template <int FMT>
+__device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], const BlockScale& b) {
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    return codes8<FMT>(f, b);
 }
 
 // Sixteen bf16 (eight words) -> sixteen codes (two words).
