@@ -56,16 +56,16 @@ __device__ __forceinline__ void st_v2(void* p, uint2 v) {
 
 // Four pairs of binary32 values -> eight e2m1 codes (nearest, ties to even,
 // held at +-6; the first value in the lowest four bits).
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float2 (&f)[4]) {
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const unsigned long long (&f)[4]) {
     uint32_t d;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .f32 x, y;\n\t"
+        "mov.b64 {x, y}, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 a, y, x;\n\t"
+        "mov.b64 {x, y}, %2;\n\tcvt.rn.satfinite.e2m1x2.f32 b, y, x;\n\t"
+        "mov.b64 {x, y}, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, y, x;\n\t"
+        "mov.b64 {x, y}, %4;\n\tcvt.rn.satfinite.e2m1x2.f32 d, y, x;\n\t"
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(d)
-        : "f"(f[0].x), "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y));
+        : "l"(f[0]), "l"(f[1]), "l"(f[2]), "l"(f[3]));
     return d;
 }
 
@@ -96,6 +96,8 @@ struct Fp4Scale {
     float s;      // the tensor scale
     float s6;     // RN(6 s)
     float r6;     // RN(1 / s6) where `fast`
+    float s64;    // s 2^64
+    float cap;    // s6 2^17
     float limit;  // the largest block maximum whose elements take the exact quotient without a divide
     bool good;    // s6 positive and finite
     bool fast;    // s in [2^-50, 2^50]: with block scales from 2^-9 to 448 everything stays in [2^-60, 2^60]
@@ -108,6 +110,8 @@ __device__ __forceinline__ Fp4Scale make_fp4_scale(const float* scale) {
     c.good = c.s6 > 0.0f && c.s6 <= 3.402823466e38f;
     c.fast = c.s >= 0x1p-50f && c.s <= 0x1p50f;
     c.r6 = c.fast ? __frcp_rn(c.s6) : 1.0f;
+    c.s64 = c.fast ? c.s * 0x1p64f : 1.0f;
+    c.cap = c.s6 * 131072.0f;
     c.limit = c.fast ? c.s * (448.0f * 131072.0f) : -1.0f;
     return c;
 }
@@ -119,7 +123,34 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
     return __fmaf_rn(-__fmaf_rn(y0, s, -x), r, y0);
 }
 
-// The same for two, with mr = -r; a zero keeps its sign.
+// Two binary32 values in one 64-bit register, as the two-lane instructions take
+// them.  Kept whole between operations: as two floats they cost moves.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(uint32_t lo, uint32_t hi) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ Two two(float v) { return two(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ Two widen2(uint32_t w) { return two(w << 16, w & 0xFFFF0000u); }  // two bf16
+__device__ __forceinline__ Two mul_two(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two fma_two(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// quotient() for two, with mr = -r; a zero keeps its sign.
+__device__ __forceinline__ Two quotient_two(Two x, Two s, Two r, Two mr) {
+    const Two y0 = mul_two(x, r);
+    return fma_two(fma_two(y0, s, mul_two(x, two(-1.0f))), mr, y0);
+}
+
+// The same on pairs of floats.
 __device__ __forceinline__ float2 quotient2(float2 x, float2 s, float2 r, float2 mr) {
     const float2 y0 = mul2_rn(x, r);
     return fma2_rn(fma2_rn(y0, s, mul2_rn(x, splat2(-1.0f))), mr, y0);
@@ -133,8 +164,8 @@ struct BlockScale {
     bool slow;  // NV: beyond the exact quotient's range
 };
 
-// a: the block's max|x| as bf16 bits (NaN above 0x7F80).
-template <int FMT>
+// a: the block's max|x| as bf16 bits (NaN above 0x7F80).  FAST: c.fast.
+template <int FMT, bool FAST>
 __device__ __forceinline__ BlockScale block_scale(uint32_t a, const Fp4Scale& c) {
     BlockScale b;
     if (FMT == FP8Q_MXFP4) {
@@ -149,14 +180,16 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t a, const Fp4Scale& c)
         return b;
     }
     const float af = __uint_as_float(a << 16);
-    if (c.fast) {  // the same branch for every thread
-        // beyond 2^17 s6 the scale is held at 448 anyway
-        b.code = cvt_fp8x2<FP8Q_E4M3FN>(quotient(fminf(af, c.s6 * 131072.0f), c.s6, c.r6), 0.0f) & 0xFFu;
-        b.code = a > 0x7F80u ? 0x7Fu : b.code;
-        b.d = __fmul_rn(sf_value<FMT>(b.code), c.s);
+    if (FAST) {
+        // beyond 2^17 s6 the scale is held at 448 anyway; a NaN stays one
+        float v;
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(af), "f"(c.cap));
+        b.code = cvt_fp8x2<FP8Q_E4M3FN>(quotient(v, c.s6, c.r6), 0.0f);
+        const float f = f16_lo(fp8x2_to_f16x2<FP8Q_E4M3FN>(b.code));
+        b.d = __fmul_rn(f, c.s);
         // RN(1 / d): the approximation and one correction (packed_f32.cuh) for d 2^64, which
         // lies where that is checked for every significand
-        const float e = b.d * 0x1p64f, y = rcp_approx_ftz(e);
+        const float e = __fmul_rn(f, c.s64), y = rcp_approx_ftz(e);
         b.r = fmaf(y, fmaf(-e, y, 1.0f), y) * 0x1p64f;
         b.slow = af > c.limit;
     } else {
@@ -167,7 +200,7 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t a, const Fp4Scale& c)
         b.r = 1.0f;
         b.slow = b.d > 0.0f;
     }
-    if (b.code == 0u || !(b.d > 0.0f)) b.r = 0.0f, b.d = 1.0f;  // quotient() of it: zero, with x's sign
+    if (!(b.d > 0.0f)) b.r = 0.0f, b.d = 1.0f;  // quotient() of it: zero, with x's sign
     return b;
 }
 
@@ -178,18 +211,20 @@ __device__ __noinline__ float slow_quotient(float x, float d) {
 
 // Eight values of a block -> eight codes.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes8(float2 (&f)[4], const BlockScale& b) {
+__device__ __forceinline__ uint32_t codes8(Two (&f)[4], const BlockScale& b) {
     if (FMT == FP8Q_MXFP4) {
-        const float2 d = splat2(b.d);
+        const Two d = two(b.d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = mul2_rn(f[i], d);  // exact, or below half the smallest code
-    } else if (!b.slow) {  // quotient(), two at a time
-        const float2 r = splat2(b.r), mr = splat2(-b.r), d = splat2(b.d);
+        for (int i = 0; i < 4; ++i) f[i] = mul_two(f[i], d);  // exact, or below half the smallest code
+    } else if (!b.slow) {
+        const Two r = two(b.r), mr = two(-b.r), d = two(b.d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = quotient2(f[i], d, r, mr);
+        for (int i = 0; i < 4; ++i) f[i] = quotient_two(f[i], d, r, mr);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = make_float2(slow_quotient(f[i].x, b.d), slow_quotient(f[i].y, b.d));
+        for (int i = 0; i < 4; ++i)
+            f[i] = two(__float_as_uint(slow_quotient(__uint_as_float((uint32_t)f[i]), b.d)),
+                       __float_as_uint(slow_quotient(__uint_as_float((uint32_t)(f[i] >> 32)), b.d)));
     }
     return cvt_e2m1x8(f);
 }
@@ -197,9 +232,9 @@ __device__ __forceinline__ uint32_t codes8(float2 (&f)[4], const BlockScale& b) 
 // Eight bf16 of a block (four words, the even column low).
 template <int FMT>
 __device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[4], const BlockScale& b) {
-    float2 f[4];
+    Two f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    for (int i = 0; i < 4; ++i) f[i] = widen2(w[i]);
     return codes8<FMT>(f, b);
 }
 

@@ -8,8 +8,16 @@
 // transpose reads the same tile back from shared memory by pairs of columns.
 // Matrices whose rows do not start on 32-byte boundaries pass through shared
 // memory by aligned 32-bit words, a warp a row.
+//
+// Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 16.6 us
+// (27.9), MXFP4 16.2 us (20.5), back 16.4 and 14.3 us, 5.1 to 6.0 TB/s; 1187 x 2731
+// both ways, where rows start anywhere, 8.3 and 7.2 us.  NVFP4 both ways issues
+// 64 % of its cycles' instructions: a scale of every 16 elements costs a
+// conversion there and back, two products and a reciprocal, twice over.
 
 #include "fp4.cuh"
+
+#include <type_traits>
 
 namespace {
 
@@ -129,17 +137,20 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantAr
     __shared__ __align__(16) uint32_t xs[VEC ? kTile * kTile / 2 : kTile * kRawWords];
     __shared__ __align__(16) uint2 qts[COL ? kTile * 9 : 1];  // 72 bytes a code row: 2-way conflicts at most
     const int tid = threadIdx.x;
-    const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
-    const int64_t r0 = tr * kTile, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kTile;
+    const uint32_t tr = blockIdx.x / (uint32_t)a.tile_cols;
+    const int64_t r0 = (int64_t)tr * kTile, c0 = (int64_t)(blockIdx.x - tr * (uint32_t)a.tile_cols) * kTile;
 
     uint32_t w[4][8];
+    // a thread's four chunks lie 32 rows apart
+    const int ck = tid & 7, left = (int)min(a.rows - r0, (int64_t)kTile) - (tid >> 3);
     if constexpr (VEC) {
+        const bool in = c0 + ck * 16 < a.cols;
+        const uint16_t* x = a.x + (r0 + (tid >> 3)) * a.cols + c0 + ck * 16;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int id = u * kThreads + tid;
-            const int64_t r = r0 + (id >> 3), c = c0 + (id & 7) * 16;
             uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (r < a.rows && c < a.cols) ld_stream_v8(a.x + r * a.cols + c, lo, hi);
+            if (in && u * 32 < left) ld_stream_v8(x, lo, hi);
+            x += 32 * a.cols;
             w[u][0] = lo.x; w[u][1] = lo.y; w[u][2] = lo.z; w[u][3] = lo.w;
             w[u][4] = hi.x; w[u][5] = hi.y; w[u][6] = hi.z; w[u][7] = hi.w;
         }
@@ -164,81 +175,97 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantAr
     const Fp4Scale sc = make_fp4_scale(a.scale);
 
     uint32_t m2 = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int id = u * kThreads + tid, row = id >> 3, ck = id & 7;
-        const uint32_t m = absmax16(w[u]);
-        m2 = bf16x2_absmax(m2, m);
-        if (ROW) {
-            uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
-            if (FMT == FP8Q_MXFP4) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-            const BlockScale b = block_scale<FMT>(am, sc);
-            const uint2 o = block_codes<FMT>(w[u], b);
-            const int64_t c = c0 + ck * 16;
-            if (r0 + row < a.rows && c < 2 * fp4_row_bytes(a.cols))
-                *reinterpret_cast<uint2*>(a.q + (r0 + row) * fp4_row_bytes(a.cols) + c / 2) = o;
-            if (FMT == FP8Q_NVFP4 || (ck & 1) == 0)
-                reinterpret_cast<uint8_t*>(sfs)[sf_byte(row, ck * 16 / kBlock)] = (uint8_t)b.code;
-        }
-        if (COL) {
-            uint4* d = reinterpret_cast<uint4*>(xs + row * (kTile / 2) + ck * 8);
-            d[0] = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
-            d[1] = make_uint4(w[u][4], w[u][5], w[u][6], w[u][7]);
-        }
-    }
-    __syncthreads();
-    if (ROW) store_sf<FMT>(a.sf, sfs, r0, a.rows, c0, a.cols);
-    if (COL) {
-        if (ROW) __syncthreads();  // sfs is used again
-        constexpr int kHalves = kBlock / 16, kUnits = kTile / kBlock;  // blocks down a column
-#pragma unroll 1
-        for (int id = tid; id < kUnits * (kTile / 2); id += kThreads) {
-            const int p = id & 63, rb = id >> 6;  // column pair, block of rows
-            uint32_t v[kHalves * 16];  // a row's two neighbours each
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < kHalves * 16; ++i) v[i] = xs[(rb * kBlock + i) * (kTile / 2) + p];
-#pragma unroll
-            for (int i = 0; i < kHalves * 16; i += 2) m = bf16x2_absmax(m, bf16x2_absmax(v[i], v[i + 1]));
-            const BlockScale bl = block_scale<FMT>(m & 0x7FFFu, sc), bh = block_scale<FMT>((m >> 16) & 0x7FFFu, sc);
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-                uint32_t lo[2], hi[2];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float2 f[4], e[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t v0 = v[h * 16 + g * 8 + 2 * i], v1 = v[h * 16 + g * 8 + 2 * i + 1];
-                        f[i] = make_float2(__uint_as_float(v0 << 16), __uint_as_float(v1 << 16));
-                        e[i] = make_float2(__uint_as_float(v0 & 0xFFFF0000u), __uint_as_float(v1 & 0xFFFF0000u));
-                    }
-                    lo[g] = codes8<FMT>(f, bl);
-                    hi[g] = codes8<FMT>(e, bh);
-                }
-                qts[(2 * p) * 9 + rb * kHalves + h] = make_uint2(lo[0], lo[1]);
-                qts[(2 * p + 1) * 9 + rb * kHalves + h] = make_uint2(hi[0], hi[1]);
-            }
-            reinterpret_cast<uint8_t*>(sfs)[sf_byte(2 * p, rb)] = (uint8_t)bl.code;
-            reinterpret_cast<uint8_t*>(sfs)[sf_byte(2 * p + 1, rb)] = (uint8_t)bh.code;
-        }
-        __syncthreads();
-        store_sf<FMT>(a.sft, sfs, c0, a.cols, r0, a.rows);
-        const int64_t ldt = fp4_row_bytes(a.rows);
+    auto run = [&](auto fast) {
+        const int64_t ld = fp4_row_bytes(a.cols);
+        uint8_t* q = a.q + (r0 + (tid >> 3)) * ld + c0 / 2 + ck * 8;
+        const bool out = c0 + ck * 16 < 2 * ld;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int id = u * kThreads + tid, col = id >> 3, k = id & 7;
-            if (c0 + col < a.cols && r0 / 2 + k * 8 < ldt)
-                *reinterpret_cast<uint2*>(a.qt + (c0 + col) * ldt + r0 / 2 + k * 8) = qts[col * 9 + k];
+            const int row = u * 32 + (tid >> 3);
+            const uint32_t m = absmax16(w[u]);
+            m2 = bf16x2_absmax(m2, m);
+            if (ROW) {
+                uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
+                if (FMT == FP8Q_MXFP4) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+                const BlockScale b = block_scale<FMT, decltype(fast)::value>(am, sc);
+                const uint2 o = block_codes<FMT>(w[u], b);
+                // the address anew for each row with MXFP4, 32 rows on with NVFP4: either is the better
+                // for its format's registers (8192x4096 both directions, MXFP4 20.5 and 24.6 us,
+                // NVFP4 28.6 and 27.9)
+                if (FMT == FP8Q_MXFP4) q = a.q + (r0 + row) * fp4_row_bytes(a.cols) + c0 / 2 + ck * 8;
+                if (out && u * 32 < left) *reinterpret_cast<uint2*>(q) = o;
+                if (FMT == FP8Q_NVFP4) q += 32 * ld;
+                if (FMT == FP8Q_NVFP4 || (ck & 1) == 0)
+                    reinterpret_cast<uint8_t*>(sfs)[sf_byte(row, ck * 16 / kBlock)] = (uint8_t)b.code;
+            }
+            if (COL) {
+                uint4* d = reinterpret_cast<uint4*>(xs + row * (kTile / 2) + ck * 8);
+                d[0] = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
+                d[1] = make_uint4(w[u][4], w[u][5], w[u][6], w[u][7]);
+            }
         }
-    }
+        __syncthreads();
+        if (ROW) store_sf<FMT>(a.sf, sfs, r0, a.rows, c0, a.cols);
+        if (COL) {
+            if (ROW) __syncthreads();  // sfs is used again
+            constexpr int kHalves = kBlock / 16, kUnits = kTile / kBlock;  // blocks down a column
+#pragma unroll 1
+            for (int id = tid; id < kUnits * (kTile / 2); id += kThreads) {
+                const int p = id & 63, rb = id >> 6;  // column pair, block of rows
+                uint32_t v[kHalves * 16];  // a row's two neighbours each
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < kHalves * 16; ++i) v[i] = xs[(rb * kBlock + i) * (kTile / 2) + p];
+#pragma unroll
+                for (int i = 0; i < kHalves * 16; i += 2) m = bf16x2_absmax(m, bf16x2_absmax(v[i], v[i + 1]));
+                const BlockScale bl = block_scale<FMT, decltype(fast)::value>(m & 0x7FFFu, sc);
+                const BlockScale bh = block_scale<FMT, decltype(fast)::value>((m >> 16) & 0x7FFFu, sc);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    uint32_t lo[2], hi[2];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        Two f[4], e[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t v0 = v[h * 16 + g * 8 + 2 * i], v1 = v[h * 16 + g * 8 + 2 * i + 1];
+                            f[i] = two(v0 << 16, v1 << 16);
+                            e[i] = two(v0 & 0xFFFF0000u, v1 & 0xFFFF0000u);
+                        }
+                        lo[g] = codes8<FMT>(f, bl);
+                        hi[g] = codes8<FMT>(e, bh);
+                    }
+                    qts[(2 * p) * 9 + rb * kHalves + h] = make_uint2(lo[0], lo[1]);
+                    qts[(2 * p + 1) * 9 + rb * kHalves + h] = make_uint2(hi[0], hi[1]);
+                }
+                reinterpret_cast<uint8_t*>(sfs)[sf_byte(2 * p, rb)] = (uint8_t)bl.code;
+                reinterpret_cast<uint8_t*>(sfs)[sf_byte(2 * p + 1, rb)] = (uint8_t)bh.code;
+            }
+            __syncthreads();
+            store_sf<FMT>(a.sft, sfs, c0, a.cols, r0, a.rows);
+            const int64_t ldt = fp4_row_bytes(a.rows);
+            const int cols_left = (int)min(a.cols - c0, (int64_t)kTile) - (tid >> 3);
+            uint8_t* qt = a.qt + (c0 + (tid >> 3)) * ldt + r0 / 2 + ck * 8;
+            const bool in_t = r0 / 2 + ck * 8 < ldt;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (in_t && u * 32 < cols_left) *reinterpret_cast<uint2*>(qt) = qts[((tid >> 3) + u * 32) * 9 + ck];
+                qt += 32 * ldt;
+            }
+        }
+    };
+    if (FMT == FP8Q_MXFP4 || sc.fast)  // the same for every thread
+        run(std::true_type());
+    else
+        run(std::false_type());
     if (a.amax) flush_amax(m2, 0u, a.amax, red);
 }
 
 // One direction of rows that start on 32-byte boundaries: the same work on tiles
 // of kWideRows x kWide columns, from registers alone, so that a CTA reads longer
 // stretches of memory; scales go out by words of four blocks.  (8192x4096, NVFP4:
-// 18.6 us, 19.1 on tiles of 128 x 128; 1024 columns measure the same.)
+// 16.6 us; 18.6, and 19.1 on tiles of 128 x 128, with every address worked out
+// anew; 1024 columns measure the same.)
 constexpr int kWide = 512, kWideRows = kTile * kTile / kWide;
 
 template <int FMT>
@@ -246,34 +273,45 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_rows_kernel(const Fp4Qu
     constexpr int kBlock = Fp4<FMT>::kBlock, kSf = Fp4<FMT>::kSfCols;
     __shared__ uint32_t red[kThreads / 32];
     __shared__ uint32_t sfs[kWideRows * kWide / kSf];
-    const int tid = threadIdx.x;
-    const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
-    const int64_t r0 = tr * kWideRows, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kWide;
-    const uint16_t* x = a.x + r0 * a.cols + c0;
+    // a warp takes a row of the tile, every eighth: addresses advance by eight rows
+    static_assert(kWide == 512 && kThreads == 256, "a warp a row");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t tr = blockIdx.x / (uint32_t)a.tile_cols;
+    const int64_t r0 = (int64_t)tr * kWideRows, c0 = (int64_t)(blockIdx.x - tr * (uint32_t)a.tile_cols) * kWide;
     const int64_t ld = fp4_row_bytes(a.cols);
+    const int left = (int)min(a.rows - r0, (int64_t)kWideRows) - warp;  // rows from this warp's first on
+    const bool in = c0 + lane * 16 < a.cols, out = c0 + lane * 16 < 2 * ld;
+    const uint16_t* x = a.x + (r0 + warp) * a.cols + c0 + lane * 16;
+    uint8_t* q = a.q + (r0 + warp) * ld + c0 / 2 + lane * 8;
     uint4 lo[4], hi[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        const int id = u * kThreads + tid, row = id / (kWide / 16), c = id % (kWide / 16) * 16;
         lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-        if (r0 + row < a.rows && c0 + c < a.cols) ld_stream_v8(x + row * a.cols + c, lo[u], hi[u]);
+        if (in && u * 8 < left) ld_stream_v8(x, lo[u], hi[u]);
+        x += 8 * a.cols;
     }
     const Fp4Scale sc = make_fp4_scale(a.scale);
     uint32_t m2 = 0;
+    auto run = [&](auto fast) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int id = u * kThreads + tid, row = id / (kWide / 16), ck = id % (kWide / 16);
-        const uint32_t w[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
-        const uint32_t m = absmax16(w);
-        m2 = bf16x2_absmax(m2, m);
-        uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
-        if (FMT == FP8Q_MXFP4) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-        const BlockScale b = block_scale<FMT>(am, sc);
-        const uint2 o = block_codes<FMT>(w, b);
-        if (r0 + row < a.rows && c0 + ck * 16 < 2 * ld) st_v2(a.q + (r0 + row) * ld + (c0 + ck * 16) / 2, o);
-        if (FMT == FP8Q_NVFP4 || (ck & 1) == 0)
-            reinterpret_cast<uint8_t*>(sfs)[row * (kWide / kBlock) + ck * 16 / kBlock] = (uint8_t)b.code;
-    }
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t w[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+            const uint32_t m = absmax16(w);
+            m2 = bf16x2_absmax(m2, m);
+            uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
+            if (FMT == FP8Q_MXFP4) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+            const BlockScale b = block_scale<FMT, decltype(fast)::value>(am, sc);
+            const uint2 o = block_codes<FMT>(w, b);
+            if (out && u * 8 < left) st_v2(q, o);
+            q += 8 * ld;
+            if (FMT == FP8Q_NVFP4 || (lane & 1) == 0)
+                reinterpret_cast<uint8_t*>(sfs)[(warp + u * 8) * (kWide / kBlock) + lane * 16 / kBlock] = (uint8_t)b.code;
+        }
+    };
+    if (FMT == FP8Q_MXFP4 || sc.fast)  // the same for every thread
+        run(std::true_type());
+    else
+        run(std::false_type());
     __syncthreads();
     const int64_t across = fp4_sf_tiles<FMT>(a.cols);
     if (tid < kWideRows * kWide / kSf) {
@@ -324,8 +362,8 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
     __shared__ __align__(16) uint32_t sfs[2 * 128];
     __shared__ __align__(16) uint32_t raw[kTile * kRawWords];
     const int tid = threadIdx.x;
-    const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
-    const int64_t r0 = tr * kTile, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kTile;
+    const uint32_t tr = blockIdx.x / (uint32_t)a.tile_cols;
+    const int64_t r0 = (int64_t)tr * kTile, c0 = (int64_t)(blockIdx.x - tr * (uint32_t)a.tile_cols) * kTile;
     const int64_t ld = fp4_row_bytes(a.cols), across = fp4_sf_tiles<FMT>(a.cols), t0 = c0 / Fp4<FMT>::kSfCols;
     uint2 w[4];
 #pragma unroll
@@ -370,37 +408,42 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
 
 // Rows that start on 16-byte boundaries: tiles of kOutRows x kOut columns, eight
 // columns a thread at a time, so that a warp's stores are one stretch (8192x4096,
-// NVFP4: 16.1 us; 17.0 with two chunks a thread, 18.9 with sixteen columns at a time).
+// NVFP4: 16.4 us; 17.0 with two chunks a thread, 18.9 with sixteen columns at a time).
 constexpr int kOut = 1024, kOutChunks = 4, kOutRows = kThreads * kOutChunks * 8 / kOut;
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_rows_kernel(const Fp4DequantArgs a) {
     constexpr int kBlock = Fp4<FMT>::kBlock, kSf = Fp4<FMT>::kSfCols;
     __shared__ uint32_t sfs[kOutRows * kOut / kSf];
-    const int tid = threadIdx.x;
-    const int64_t tr = (int64_t)blockIdx.x / a.tile_cols;
-    const int64_t r0 = tr * kOutRows, c0 = ((int64_t)blockIdx.x - tr * a.tile_cols) * kOut;
+    // half a CTA takes a row of the tile, every second: addresses advance by two rows
+    static_assert(kOut == 1024 && kThreads == 256, "128 threads a row");
+    const int tid = threadIdx.x, t = tid & 127, row0 = tid >> 7;
+    const uint32_t tr = blockIdx.x / (uint32_t)a.tile_cols;
+    const int64_t r0 = (int64_t)tr * kOutRows, c0 = (int64_t)(blockIdx.x - tr * (uint32_t)a.tile_cols) * kOut;
     const int64_t ld = fp4_row_bytes(a.cols), across = fp4_sf_tiles<FMT>(a.cols);
+    const int left = (int)min(a.rows - r0, (int64_t)kOutRows) - row0;
+    const bool in = c0 + t * 8 < a.cols;
+    const uint8_t* q = a.q + (r0 + row0) * ld + c0 / 2 + t * 4;
+    uint16_t* y = a.y + (r0 + row0) * a.cols + c0 + t * 8;
     uint32_t w[kOutChunks];
 #pragma unroll
     for (int u = 0; u < kOutChunks; ++u) {
-        const int id = u * kThreads + tid, row = id / (kOut / 8), c = id % (kOut / 8) * 8;
         w[u] = 0;
-        if (r0 + row < a.rows && c0 + c < a.cols) w[u] = __ldg(reinterpret_cast<const unsigned int*>(a.q + (r0 + row) * ld + (c0 + c) / 2));
+        if (in && u * 2 < left) w[u] = __ldg(reinterpret_cast<const unsigned int*>(q));
+        q += 2 * ld;
     }
     for (int i = tid; i < kOutRows * kOut / kSf; i += kThreads) {
-        const int64_t r = r0 + i / (kOut / kSf), t = c0 / kSf + i % (kOut / kSf);
-        if (r < a.rows && t < across)
-            sfs[i] = __ldg(reinterpret_cast<const unsigned int*>(a.sf + ((r / 128) * across + t) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4));
+        const int64_t r = r0 + i / (kOut / kSf), k = c0 / kSf + i % (kOut / kSf);
+        if (r < a.rows && k < across)
+            sfs[i] = __ldg(reinterpret_cast<const unsigned int*>(a.sf + ((r / 128) * across + k) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4));
     }
     const float s = a.scale ? __ldg(a.scale) : 1.0f;
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kOutChunks; ++u) {
-        const int id = u * kThreads + tid, row = id / (kOut / 8), c = id % (kOut / 8) * 8;
-        if (r0 + row < a.rows && c0 + c < a.cols)
-            st_v4(a.y + (r0 + row) * a.cols + c0 + c,
-                  values8<FMT>(w[u], reinterpret_cast<const uint8_t*>(sfs)[row * (kOut / kBlock) + c / kBlock], s));
+        if (in && u * 2 < left)
+            st_v4(y, values8<FMT>(w[u], reinterpret_cast<const uint8_t*>(sfs)[(row0 + u * 2) * (kOut / kBlock) + t * 8 / kBlock], s));
+        y += 2 * a.cols;
     }
 }
 

@@ -177,7 +177,7 @@ __device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, c
         uint32_t am = max(m & 0x7FFFu, (m >> 16) & 0x7FFFu);
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-        const BlockScale b = block_scale<FMT>(am, c4);
+        const BlockScale b = FMT == FP8Q_MXFP4 || c4.fast ? block_scale<FMT, true>(am, c4) : block_scale<FMT, false>(am, c4);
         const uint32_t codes = codes8<FMT>(w, b);
         const int64_t ld = fp4_row_bytes(a.H);
         if (live && col < 2 * ld) *reinterpret_cast<uint32_t*>(a.q + row * ld + col / 2) = codes;
