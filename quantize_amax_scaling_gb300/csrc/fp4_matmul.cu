@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    start_behind();
 
     if (warp == 4) {
         const uint8_t* psf = a.p_sf + (int64_t)(p0 / 128) * a.sf_across * 512;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     __syncwarp();
     __syncthreads();
     tc_fence_after();
-    const float alpha = __fmul_rn(a.sa ? __ldg(a.sa) : 1.0f, a.sb ? __ldg(a.sb) : 1.0f);
+    const float alpha = __fmul_rn(a.sa ? *a.sa : 1.0f, a.sb ? *a.sb : 1.0f);
     // A wait that ran out (correct operation never gets there) shows as NaN in the whole tile.
     const float nan = __uint_as_float(0x7FFFFFFFu);
     const int bad = gave_up;
@@ -349,6 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     cluster_sync_all();  // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    start_behind();
 
     if (warp == 8) {
         uint32_t st = 0, round = 0, n = 0;
@@ -481,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         }
         if (!ok) gave_up = 1;
     } else {
-        const float alpha = __fmul_rn(a.sa ? __ldg(a.sa) : 1.0f, a.sb ? __ldg(a.sb) : 1.0f);
+        const float alpha = __fmul_rn(a.sa ? *a.sa : 1.0f, a.sb ? *a.sb : 1.0f);
         const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * 128;
         const uint32_t bar = in_cluster(smem_addr(&drained), 0);
         bool ok = true;
@@ -624,19 +626,7 @@ fp8q_status launch_tiles(const CUtensorMap& mp, const CUtensorMap& mq, const MmA
     auto kern = fp4_matmul_kernel<FMT, BN, F32>;
     cudaError_t e = allow_smem(kern, MmGeom<FMT, BN>::kSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp4_matmul_kernel setup");
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(192);
-    cfg.dynamicSmemBytes = MmGeom<FMT, BN>::kSmem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = a.split > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kern, mp, mq, a);
-    return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "fp4_matmul_kernel");
+    return launch_behind(kern, dim3(grid), dim3(192), MmGeom<FMT, BN>::kSmem, (unsigned)a.split, s, "fp4_matmul_kernel", mp, mq, a);
 }
 
 int sm_count() {
@@ -669,7 +659,7 @@ fp8q_status launch_pairs(const uint8_t* p, const uint8_t* q, int64_t k, MmArgs g
     if (tiles > 0x3FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
     const int64_t pairs = sm_count() / 2;
     const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-    return launch_kernel(kern, dim3(grid), dim3(kPairThreads), G::kSmem, s, "fp4_matmul_pair_kernel", mp, mq, ms, mt, md, g);
+    return launch_behind(kern, dim3(grid), dim3(kPairThreads), G::kSmem, 1, s, "fp4_matmul_pair_kernel", mp, mq, ms, mt, md, g);
 }
 
 template <int FMT, bool F32>
