@@ -302,6 +302,33 @@ struct PairGeom {
     static constexpr int kSfCols = 3 * kSfTiles * 4;
 };
 
+// Rows of D that start anywhere: 32 swizzled lines of 128 bytes in shared memory go out a line at a time, a lane a
+// 32-bit word, the words as they are aligned in D.  `rows` and `n` elements of a row are there, from `first` on.
+// (8192 x 16383 x 4096: 243 us; 362 by single elements, whose half-filled sectors cost the memory a read each.)
+template <bool F32>
+__device__ __forceinline__ void store_rows(void* d, int64_t first, int64_t ld, int rows, int n, uint32_t lines) {
+    const int lane = threadIdx.x & 31;
+    rows = min(rows, 32);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r, first += ld) {
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(lines + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) : "memory");
+        if constexpr (F32) {
+            if (lane < n) static_cast<uint32_t*>(d)[first + lane] = w;
+        } else {
+            uint16_t* row = static_cast<uint16_t*>(d) + first;
+            const int odd = (int)(((uintptr_t)row >> 1) & 1), e = 2 * lane - odd;  // the word in D holds elements e and e + 1
+            const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w, 1);
+            const uint32_t v = odd ? __byte_perm(before, w, 0x5432) : w;
+            if (e >= 0 && e + 1 < n)
+                *reinterpret_cast<uint32_t*>(row + e) = v;
+            else if (max(e, 0) < n)  // one of the two
+                row[max(e, 0)] = (uint16_t)(e < 0 ? w : v);
+            if (odd && lane == 31 && n >= 64) row[63] = (uint16_t)(w >> 16);
+        }
+    }
+}
+
 // Tiles go in bands of eight along P, along Q within a band, so that the tiles
 // under way at one time share rows of both operands in L2.
 struct PairTile {
@@ -492,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         const uint32_t out = base + kPairStages * G::kStageBytes + warp * 4096, line = out + lane * 128;
         for (int tile = blockIdx.x / 2; tile < tiles; tile += stride, ++it) {
             const PairTile t = pair_tile(tile, p_tiles, a.q_tiles);
-            const int p_first = t.p + (int)rank * 128 + (warp & 3) * 32, p = p_first + lane;
+            const int p_first = t.p + (int)rank * 128 + (warp & 3) * 32;
             const int q = t.q + (warp >> 2) * 128, left = a.q_rows - q;
             ok = ok && mbar_wait_warp(&done, it & 1, 32);
             if (!ok) gave_up = 1;
@@ -519,29 +546,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                     tc_fence_before();
                     if (lane == 0) arrive_cluster(bar);
                 }
-                if (a.p_is_m && a.vec) {
-                    // through shared memory (128-byte swizzle), out by a tensor-map store
-                    if (lane == 0) store_read_wait();
-                    __syncwarp();
+                // through shared memory (128-byte swizzle)
+                if (a.vec && lane == 0) store_read_wait();
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((j ^ (lane & 7)) << 4)), "r"(o[4 * j]),
-                                     "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
-                                     : "memory");
+                for (int j = 0; j < 8; ++j)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((j ^ (lane & 7)) << 4)), "r"(o[4 * j]),
+                                 "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
+                                 : "memory");
+                if (a.vec) {  // out by a tensor-map store
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0 && left > c && p_first < a.p_rows) tile_store(&map_d, q + c, p_first, out);
-                } else if (p < a.p_rows) {
-                    const int64_t step = a.p_is_m ? 1 : a.ld;
-                    const int64_t first = a.p_is_m ? (int64_t)p * a.ld + q + c : (int64_t)(q + c) * a.ld + p;
-#pragma unroll
-                    for (int i = 0; i < kLine; ++i)
-                        if (c + i < left) {
-                            if constexpr (F32)
-                                static_cast<uint32_t*>(a.d)[first + i * step] = o[i];
-                            else
-                                static_cast<uint16_t*>(a.d)[first + i * step] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
-                        }
+                } else {
+                    __syncwarp();
+                    store_rows<F32>(a.d, (int64_t)p_first * a.ld + q + c, a.ld, a.p_rows - p_first, left - c, out);
                 }
                 __syncwarp();
             }
@@ -652,7 +671,7 @@ fp8q_status launch_pairs(const uint8_t* p, const uint8_t* q, int64_t k, MmArgs g
     if (!codes_map(&mp, p, g.p_rows, k, 128) || !codes_map(&mq, q, g.q_rows, k, 128) ||
         !scales_map(&ms, g.p_sf, g.p_rows, g.sf_across, G::kSfTiles, 1) || !scales_map(&mt, g.q_sf, g.q_rows, g.sf_across, G::kSfTiles, 2))
         return cuda_fail(cudaErrorInvalidValue, "fp4_matmul_pair_kernel tensor map");
-    if (g.p_is_m && g.vec && !result_map<F32>(&md, g.d, g.p_rows, g.q_rows))
+    if (g.vec && !result_map<F32>(&md, g.d, g.p_rows, g.q_rows))
         return cuda_fail(cudaErrorInvalidValue, "fp4_matmul_pair_kernel tensor map");
     g.q_tiles = (g.q_rows + 255) / 256;
     const int64_t tiles = (int64_t)((g.p_rows + 255) / 256) * g.q_tiles;
@@ -687,9 +706,9 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     }
     g.split = split;
     // P, whose rows are the accumulators' 128 lanes, is A, and a thread holds part of a row of D, where
-    // D's rows hold whole vectors; otherwise the lanes run along D's rows, so that a warp's stores are
-    // contiguous, as they are where few rows of A leave the lanes to B.
-    g.p_is_m = g.vec && split == 1 && (pairs || m >= n);
+    // pairs write it through shared memory and where D's rows hold whole vectors; otherwise the lanes run along
+    // D's rows, so that a warp's stores are contiguous, as they are where few rows of A leave the lanes to B.
+    g.p_is_m = pairs || (g.vec && split == 1 && m >= n);
     const uint8_t *p = g.p_is_m ? a : b, *q = g.p_is_m ? b : a;
     g.p_sf = g.p_is_m ? a_sf : b_sf;
     g.q_sf = g.p_is_m ? b_sf : a_sf;
