@@ -372,7 +372,7 @@ int64_t fp8q_fp4_scale_bytes(int64_t rows, int64_t cols, fp8q_format fmt);
  * Errors: INVALID_ARG for another fmt, rows or cols < 0, a NULL x_bf16, no
  *         output or half a pair, a scale with FP8Q_MXFP4, or a misaligned
  *         x_bf16, scale or amax; UNSUPPORTED for q, sf, qt or sft off a
- *         16-byte boundary, or rows or cols above 2^31 - 128.
+ *         16-byte boundary, or rows or cols above 2^31 - 1024.
  */
 fp8q_status fp8q_fp4_quantize_amax(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q, uint8_t* sf,
                                    uint8_t* qt, uint8_t* sft, fp8q_format fmt, const float* scale, float* amax,
@@ -398,10 +398,14 @@ fp8q_status fp8q_fp4_dequantize(const uint8_t* q, const uint8_t* sf, void* y_bf1
  * transposes.  Products are exact; sums are held in binary32.
  * a_scale, b_scale: the tensor scales, one float each (device), or NULL for 1;
  * NULL for FP8Q_MXFP4.  Calls with the same arguments give the same bits.
- * Errors: INVALID_ARG for another fmt or out, m, n or k < 0, k == 0 with m and
- *         n > 0, a NULL operand or d, a scale with FP8Q_MXFP4, or a misaligned
- *         d or scale; UNSUPPORTED for an operand off a 16-byte boundary or
- *         m, n or k above 2^31 - 128.  m == 0 or n == 0 launches nothing.
+ * With k == 0, d is zeros (the operands may be NULL).
+ * A wait inside the kernel that runs out, which only a fault elsewhere could
+ * cause, ends the kernel and shows as NaN in d, with all the bits behind the
+ * sign set.
+ * Errors: INVALID_ARG for another fmt or out, m, n or k < 0, a NULL operand or
+ *         d, a scale with FP8Q_MXFP4, or a misaligned d or scale; UNSUPPORTED
+ *         for an operand off a 16-byte boundary or m, n or k above 2^31 -
+ *         1024.  m == 0 or n == 0 launches nothing.
  */
 fp8q_status fp8q_fp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, void* d,
                             int64_t m, int64_t n, int64_t k, fp8q_format fmt, fp8q_out_type out,
@@ -449,7 +453,7 @@ typedef struct {
  * Errors: INVALID_ARG for a NULL args, another fmt, rows < 0, hidden < 16 or
  *         not a multiple of 16, rows_per_gate < 1 with gate, parts missing or
  *         left over as listed above, or a misaligned scale, amax or rstd;
- *         UNSUPPORTED for hidden > 32768, rows above 2^31 - 128 or another
+ *         UNSUPPORTED for hidden > 32768, rows above 2^31 - 1024 or another
  *         pointer off a 16-byte boundary.  rows == 0 launches nothing.
  */
 fp8q_status fp8q_residual_norm_quantize_amax(const fp8q_residual_norm* args, void* stream);
@@ -502,8 +506,9 @@ int64_t fp8q_residual_norm_backward_workspace(int64_t rows, int32_t hidden, int6
  * Errors: INVALID_ARG for a NULL args, rows < 0, hidden < 16 or not a multiple
  *         of 16, neither gradient given, parts missing or left over, too small
  *         a workspace, or a misaligned rstd; UNSUPPORTED for hidden > 32768,
- *         rows above 2^31 - 128 or another pointer off a 16-byte boundary.
- *         rows == 0 launches nothing (and writes no sums).
+ *         rows above 2^31 - 1024 or another pointer off a 16-byte boundary.
+ *         With rows == 0 d_pre_weight and d_post_weight are zeros; nothing else
+ *         is read or written.
  */
 fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* args, void* stream);
 

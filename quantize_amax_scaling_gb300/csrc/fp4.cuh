@@ -36,7 +36,7 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& devices) {
 
 inline bool valid_fp4(int fmt) { return fmt == FP8Q_MXFP4 || fmt == FP8Q_NVFP4; }
 
-constexpr int64_t kFp4MaxDim = 0x7FFFFF80;  // rows and columns of an operand: tile coordinates are 32-bit
+constexpr int64_t kFp4MaxDim = 0x7FFFFC00;  // rows and columns of an operand: coordinates within a tile beyond the last stay in 32 bits
 
 template <int FMT>
 struct Fp4 {

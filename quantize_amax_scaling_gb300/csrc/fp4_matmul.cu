@@ -741,14 +741,17 @@ fp8q_status fp8q_fp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t
     if (!valid_fp4(fmt) || m < 0 || n < 0 || k < 0) return FP8Q_ERR_INVALID_ARG;
     if (out != FP8Q_OUT_BF16 && out != FP8Q_OUT_F32) return FP8Q_ERR_INVALID_ARG;
     if (m == 0 || n == 0) return FP8Q_OK;
-    if (k == 0) return FP8Q_ERR_INVALID_ARG;
     if (m > kFp4MaxDim || n > kFp4MaxDim || k > kFp4MaxDim) return FP8Q_ERR_UNSUPPORTED;
-    if (!a || !a_sf || !b || !b_sf || !d) return FP8Q_ERR_INVALID_ARG;
+    if (!d || (k > 0 && (!a || !a_sf || !b || !b_sf))) return FP8Q_ERR_INVALID_ARG;
     if (fmt == FP8Q_MXFP4 && (a_scale || b_scale)) return FP8Q_ERR_INVALID_ARG;
     if (((uintptr_t)d & (out == FP8Q_OUT_F32 ? 3u : 1u)) || ((uintptr_t)a_scale & 3u) || ((uintptr_t)b_scale & 3u))
         return FP8Q_ERR_INVALID_ARG;
     if (((uintptr_t)a | (uintptr_t)a_sf | (uintptr_t)b | (uintptr_t)b_sf) & 15u) return FP8Q_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k == 0) {  // an empty sum
+        const cudaError_t e = cudaMemsetAsync(d, 0, (size_t)(m * n) * (out == FP8Q_OUT_F32 ? 4 : 2), s);
+        return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "fp8q_fp4_matmul");
+    }
     if (fmt == FP8Q_MXFP4)
         return out == FP8Q_OUT_F32 ? matmul<FP8Q_MXFP4, true>(a, a_sf, b, b_sf, d, m, n, k, a_scale, b_scale, s)
                                    : matmul<FP8Q_MXFP4, false>(a, a_sf, b, b_sf, d, m, n, k, a_scale, b_scale, s);

@@ -855,7 +855,17 @@ int64_t fp8q_residual_norm_backward_workspace(int64_t rows, int32_t hidden, int6
 fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* stream) {
     if (!n || n->rows < 0 || n->hidden < 16 || n->hidden % 16 != 0) return FP8Q_ERR_INVALID_ARG;
     if (n->hidden > kRnMaxH || n->rows > kFp4MaxDim) return FP8Q_ERR_UNSUPPORTED;
-    if (n->rows == 0) return FP8Q_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (n->rows == 0) {  // the sums over no rows
+        if (misaligned({n->d_pre_weight, n->d_post_weight}, 15)) return FP8Q_ERR_UNSUPPORTED;
+        if (!n->d_pre_weight && !n->d_post_weight) return FP8Q_OK;
+        RnBwdArgs none = {};
+        none.dpre = n->d_pre_weight;
+        none.dpost = n->d_post_weight;
+        none.H = n->hidden;
+        return launch_behind(residual_norm_sum_kernel, dim3((unsigned)((n->hidden + 127) / 128), 2), dim3(1024), 0, 1, s,
+                             "residual_norm_sum_kernel", none);
+    }
     if (!n->d_residual_out && !n->d_h) return FP8Q_ERR_INVALID_ARG;
     if (n->d_h ? (!n->residual_out || !n->rstd_pre || !n->pre_weight) : (n->pre_weight || n->d_pre_weight != nullptr))
         return FP8Q_ERR_INVALID_ARG;
@@ -896,7 +906,6 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     a.alpha = n->alpha;
     // slices of equal width, whole groups of four columns a thread
     a.width = ((n->hidden + st.slices - 1) / st.slices + 15) / 16 * 16;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t per_cta = 256 / st.T;
     const unsigned ctas = (unsigned)((st.strips + per_cta - 1) / per_cta) * (unsigned)st.slices;
     const bool ring_gate = a.gate && a.per == 1;

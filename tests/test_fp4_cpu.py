@@ -132,7 +132,7 @@ def test_dequantize_and_matmul_refusals(L):
         return m(*a)
 
     assert call((5, 0)) == OK and call((6, 0)) == OK and call((5, 0), (7, 0)) == OK
-    assert call((7, 0)) == INVALID
+    assert call((7, 0), (4, None)) == INVALID               # k == 0 writes zeros: d has to be there
     for i in (5, 6, 7):
         assert call((i, -1)) == INVALID and call((i, 2 ** 31)) == UNSUPPORTED
     assert call((8, 1)) == INVALID and call((9, 2)) == INVALID and call((8, 2)) == INVALID
@@ -182,7 +182,8 @@ def test_residual_norm_backward_refusals(L):
         return L.fp8q_residual_norm_backward(ctypes.byref(fp8q.ResidualNormGrad(**a)), None)
 
     assert L.fp8q_residual_norm_backward(None, None) == INVALID
-    assert call(rows=0) == OK
+    assert call(rows=0, d_pre_weight=None, d_post_weight=None) == OK
+    assert call(rows=0, d_post_weight=p + 4) == UNSUPPORTED
     for c in (dict(rows=-1), dict(hidden=24), dict(d_residual_out=None, d_h=None), dict(residual_out=None), dict(rstd_pre=None),
               dict(pre_weight=None), dict(d_h=None), dict(block=None), dict(rstd_post=None), dict(post_weight=None),
               dict(rows_per_gate=0), dict(gate=None), dict(workspace=None), dict(workspace_bytes=16), dict(rstd_pre=p + 1)):
