@@ -304,27 +304,33 @@ struct PairGeom {
 
 // Rows of D that start anywhere: 32 swizzled lines of 128 bytes in shared memory go out a line at a time, a lane a
 // 32-bit word, the words as they are aligned in D.  `rows` and `n` elements of a row are there, from `first` on.
-// (8192 x 16383 x 4096: 243 us; 362 by single elements, whose half-filled sectors cost the memory a read each.)
+// (8192 x 16383 x 4096: 240 us; 362 by single elements, whose half-filled sectors cost the memory a read each.)
 template <bool F32>
 __device__ __forceinline__ void store_rows(void* d, int64_t first, int64_t ld, int rows, int n, uint32_t lines) {
     const int lane = threadIdx.x & 31;
-    rows = min(rows, 32);
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r, first += ld) {
-        uint32_t w;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(lines + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) : "memory");
-        if constexpr (F32) {
-            if (lane < n) static_cast<uint32_t*>(d)[first + lane] = w;
-        } else {
-            uint16_t* row = static_cast<uint16_t*>(d) + first;
-            const int odd = (int)(((uintptr_t)row >> 1) & 1), e = 2 * lane - odd;  // the word in D holds elements e and e + 1
-            const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w, 1);
-            const uint32_t v = odd ? __byte_perm(before, w, 0x5432) : w;
-            if (e >= 0 && e + 1 < n)
-                *reinterpret_cast<uint32_t*>(row + e) = v;
-            else if (max(e, 0) < n)  // one of the two
-                row[max(e, 0)] = (uint16_t)(e < 0 ? w : v);
-            if (odd && lane == 31 && n >= 64) row[63] = (uint16_t)(w >> 16);
+    uint8_t* row = static_cast<uint8_t*>(d) + first * (F32 ? 4 : 2);
+    for (int r0 = 0; r0 < min(rows, 32); r0 += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[j]) : "r"(lines + (r0 + j) * 128 + ((((uint32_t)lane >> 2) ^ j) << 4) + (lane & 3) * 4) : "memory");
+#pragma unroll
+        for (int j = 0; j < 8; ++j, row += ld * (F32 ? 4 : 2)) {
+            if (r0 + j >= rows) break;
+            uint16_t* h = reinterpret_cast<uint16_t*>(row);
+            if (F32) {
+                if (lane < n) reinterpret_cast<uint32_t*>(row)[lane] = w[j];
+            } else if (n < 64) {  // elements 2 lane and 2 lane + 1
+                if (2 * lane < n) h[2 * lane] = (uint16_t)w[j];
+                if (2 * lane + 1 < n) h[2 * lane + 1] = (uint16_t)(w[j] >> 16);
+            } else if ((uintptr_t)row & 2) {  // the same for the warp: a word in D holds elements 2 lane - 1 and 2 lane
+                const uint32_t v = __byte_perm(__shfl_up_sync(0xFFFFFFFFu, w[j], 1), w[j], 0x5432);
+                if (lane) reinterpret_cast<uint32_t*>(h - 1)[lane] = v;
+                if (lane == 0) h[0] = (uint16_t)w[j];
+                if (lane == 31) h[63] = (uint16_t)(w[j] >> 16);
+            } else {
+                reinterpret_cast<uint32_t*>(row)[lane] = w[j];
+            }
         }
     }
 }
