@@ -1,5 +1,6 @@
 /*
- * fp8q.h -- C ABI of libfp8q: FP8 delayed-scaling quantization on one GPU.
+ * fp8q.h -- C ABI of libfp8q: FP8 delayed-scaling quantization, microscaled
+ * 4-bit operands and residual norms on one GPU.
  *
  * Fourteen operations, each one kernel launch on the caller's stream (the last,
  * where it sums gradients over rows, two):
@@ -47,7 +48,9 @@
  *     (as allocators return them) take the vectorised path.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
  *     return once the kernel is enqueued; results are ready when the stream
- *     reaches that point.
+ *     reaches that point.  The fp8q_fp4_* and fp8q_residual_norm_* kernels are
+ *     launched so that their start overlaps the end of the kernel before them
+ *     in the stream; they touch memory only when that has ended.
  *   - Errors are returned as fp8q_status, never raised or aborted.  Argument
  *     errors are detected before anything is launched.  FP8Q_ERR_CUDA means
  *     the launch itself failed; fp8q_last_cuda_error() (per thread) then
@@ -55,7 +58,8 @@
  *     per-thread last error (cudaGetLastError) so that it is reported once.
  *     Each call checks only its own launch: a runtime error that an earlier,
  *     unrelated call left pending is neither reported nor cleared.
- *     A zero-sized call succeeds and launches nothing.
+ *     A zero-sized call succeeds and launches nothing (but an output that is a
+ *     sum over nothing is zeros, where a call says so).
  */
 #ifndef FP8Q_H
 #define FP8Q_H

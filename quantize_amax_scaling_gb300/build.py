@@ -1,7 +1,8 @@
 """Compile libfp8q.so (the CUDA kernels and their C ABI) for sm_103a, in tree.
 
-Four translation units compiled in parallel with one -gencode each, then
-linked; no cmake.  The library and its objects are written next to this file
+Translation units compiled in parallel with one -gencode each, then linked; no
+cmake.  Beside it the compiled part of the Python binding (csrc/binding.cpp, g++
+against torch's headers).  Both and their objects are written next to this file
 and git-ignored.
 """
 import os

@@ -9,9 +9,9 @@
 // Matrices whose rows do not start on 32-byte boundaries pass through shared
 // memory by aligned 32-bit words, a warp a row.
 //
-// Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 16.6 us
-// (27.9), MXFP4 16.2 us (20.5), back 16.4 and 14.3 us, 5.1 to 6.0 TB/s; 1187 x 2731
-// both ways, where rows start anywhere, 8.3 and 7.2 us.  NVFP4 both ways issues
+// Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 17.0 us
+// (28.0), MXFP4 14.4 us (19.8), back 14.2 and 13.9 us, 5.0 to 6.1 TB/s; 1187 x 2731
+// both ways, where rows start anywhere, 8.5 and 7.1 us.  NVFP4 both ways issues
 // 64 % of its cycles' instructions: a scale of every 16 elements costs a
 // conversion there and back, two products and a reciprocal, twice over.
 
@@ -191,12 +191,8 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantAr
                 if (FMT == FP8Q_MXFP4) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
                 const BlockScale b = block_scale<FMT, decltype(fast)::value>(am, sc);
                 const uint2 o = block_codes<FMT>(w[u], b);
-                // the address anew for each row with MXFP4, 32 rows on with NVFP4: either is the better
-                // for its format's registers (8192x4096 both directions, MXFP4 20.5 and 24.6 us,
-                // NVFP4 28.6 and 27.9)
-                if (FMT == FP8Q_MXFP4) q = a.q + (r0 + row) * fp4_row_bytes(a.cols) + c0 / 2 + ck * 8;
                 if (out && u * 32 < left) *reinterpret_cast<uint2*>(q) = o;
-                if (FMT == FP8Q_NVFP4) q += 32 * ld;
+                q += 32 * ld;
                 if (FMT == FP8Q_NVFP4 || (ck & 1) == 0)
                     reinterpret_cast<uint8_t*>(sfs)[sf_byte(row, ck * 16 / kBlock)] = (uint8_t)b.code;
             }

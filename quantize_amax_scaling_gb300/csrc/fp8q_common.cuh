@@ -1,8 +1,8 @@
 // fp8q_common.cuh -- what the kernels of libfp8q share: launch geometry,
 // bf16/FP8 conversions, the exact division by the scale, the CTA-wide amax
 // flush, and host-side error reporting.  The kernels and their C ABI entry
-// points live in quantize.cu, producers.cu and scale_update.cu; abi.cu holds
-// the status strings.
+// points live in quantize.cu, producers.cu, scale_update.cu, fp4_quantize.cu,
+// fp4_matmul.cu and residual_norm.cu; abi.cu holds the status strings.
 //
 // Sources (web pages, by title and section):
 //   "User Guide on Native XLA-FP8" (NVIDIA JAX-Toolbox), section "JAX":
@@ -13,8 +13,9 @@
 //   "Implement fused kernel for FP8 scale update" (TransformerEngine PR):
 //     the whole amax_and_scale_update in one in-place kernel, all layers.
 //
-// Every kernel here streams HBM; none is a contraction, so there are no
-// tensor-core instructions.  Design points:
+// Every kernel but the 4-bit product (fp4_matmul.cu) streams HBM; that one runs
+// on the tensor cores.  Design points of quantize.cu, producers.cu and
+// scale_update.cu (the others state their own):
 //   * quantize+amax reads each bf16 once (32-byte vector loads), writes each
 //     FP8 byte once (16-byte stores), and reduces |x| with packed
 //     NaN-propagating bf16x2 max, then one warp redux and one atomic per CTA
