@@ -516,8 +516,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                         store_scales4(to + 8, sf + 1024, 1024);
                     } else {
                         store_scales4(to, sf, 512);
-                        store_scales4(to + 16, sf + 2048, 2048);
-                        store_scales4(to + 32, sf + 3072, 2048);
+                        store_scales4(to + 16, sf + 4 * 512, 4 * 512);
+                        store_scales4(to + 32, sf + 6 * 512, 4 * 512);
                     }
                     scales_stored();
                     if (lane == 0) arrive_cluster(bars + st * 8);

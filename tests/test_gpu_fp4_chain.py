@@ -3,11 +3,15 @@ norms uses them: norm -> codes -> product -> norm, and back through the second n
 transposed operands and the first norm.  Each stage is compared with its formula in float64 on what the stage
 was given; and the same step on another stream, replayed from a graph, beside itself on two streams, and call
 behind call without a wait between them gives the same bits."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
 
 import fp4_reference as R
+from conftest import ROOT
 from gpu_helpers import bf16_bits_of
 from quantize_amax_scaling_gb300 import fp8q
 from test_gpu_fp4 import product_bound
@@ -198,3 +202,13 @@ def test_step_anywhere(dev, rows, H, fmt):
         y = torch.empty_like(two[1]["h"])
         fp8q.fp8q_fp4_dequantize(w["xq"], w["xs"], y, fmt, None if d["scales"] is None else d["scales"][:1])
         assert torch.equal(y, two[1]["h"])
+
+
+def test_readme_example(dev):
+    """The readme's second example, which goes on from its first."""
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(ROOT, "README.md")).read(), re.S)
+    ns = {}
+    for b in blocks:
+        exec(compile(b, "readme example", "exec"), ns)
+    torch.cuda.synchronize()
+    assert float(ns["amax"]) > 1 and torch.isfinite(ns["y"]).all() and ns["y"].float().std() > 1
