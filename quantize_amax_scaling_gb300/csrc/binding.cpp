@@ -324,8 +324,17 @@ PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return nullptr;
         }
         const auto o = at::TensorOptions().dtype(at::kByte).device(at::kCUDA, c10::cuda::current_device());
-        PyObject* q = THPVariable_Wrap(at::empty({v[0], row_bytes(v[1])}, o));
-        PyObject* sf = q ? THPVariable_Wrap(at::empty({scale_bytes(v[0], v[1], v[2])}, o)) : nullptr;
+        // one allocation for both, the scales behind the codes (a multiple of 16 bytes)
+        const int64_t codes = v[0] * row_bytes(v[1]), scales = scale_bytes(v[0], v[1], v[2]);
+        const at::Tensor all = at::empty({codes + scales}, o);
+        const auto part = [&](at::IntArrayRef sizes, int64_t from) {
+            at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+            t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+            t.unsafeGetTensorImpl()->set_storage_offset(from);
+            return t;
+        };
+        PyObject* q = THPVariable_Wrap(part({v[0], row_bytes(v[1])}, 0));
+        PyObject* sf = q ? THPVariable_Wrap(part({scales}, codes)) : nullptr;
         PyObject* both = sf ? PyTuple_Pack(2, q, sf) : nullptr;
         Py_XDECREF(q);
         Py_XDECREF(sf);

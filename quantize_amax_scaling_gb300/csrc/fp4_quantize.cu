@@ -9,9 +9,9 @@
 // Matrices whose rows do not start on 32-byte boundaries pass through shared
 // memory by aligned 32-bit words, a warp a row.
 //
-// Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 17.0 us
-// (28.0), MXFP4 14.4 us (19.8), back 14.2 and 13.9 us, 5.0 to 6.1 TB/s; 1187 x 2731
-// both ways, where rows start anywhere, 8.5 and 7.1 us.  NVFP4 both ways issues
+// Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 15.9 us
+// (26.7), MXFP4 14.4 us (19.8), back 14.2 and 13.9 us, 3.9 to 6.1 TB/s; 1187 x 2731
+// both ways, where rows start anywhere, 8.3 and 7.1 us.  NVFP4 both ways issues
 // 64 % of its cycles' instructions: a scale of every 16 elements costs a
 // conversion there and back, two products and a reciprocal, twice over.
 
