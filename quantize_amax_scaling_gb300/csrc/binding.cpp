@@ -27,6 +27,7 @@ decltype(&fp8q_fp4_dequantize) g_dequantize;
 decltype(&fp8q_fp4_matmul) g_matmul;
 decltype(&fp8q_residual_norm_quantize_amax) g_norm;
 decltype(&fp8q_residual_norm_backward) g_norm_backward;
+decltype(&fp8q_residual_norm_backward_workspace) g_workspace;
 
 struct Refused {};  // a Python exception has been set
 
@@ -311,6 +312,13 @@ PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
+// (rows, hidden, rows_per_gate)
+int64_t workspace(PyObject* const* v, Py_ssize_t n) {
+    Args a("residual_norm_backward_workspace", v, n, 3);
+    const int64_t rows = a.integer(), hidden = a.integer(), per = a.integer();
+    return g_workspace(rows, (int32_t)(hidden > INT32_MAX ? INT32_MAX : hidden < 0 ? 0 : hidden), per);
+}
+
 // (rows, cols, fmt): room for a packed operand on the current CUDA device
 PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
@@ -347,11 +355,11 @@ PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // Addresses of the entry points, in the order of the calls below.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* p[5] = {};
-    for (Py_ssize_t i = 0; i < 5; ++i) {
+    void* p[6] = {};
+    for (Py_ssize_t i = 0; i < 6; ++i) {
         if (i < n) p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind takes five addresses");
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind takes six addresses");
             return nullptr;
         }
     }
@@ -360,6 +368,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_matmul = reinterpret_cast<decltype(g_matmul)>(p[2]);
     g_norm = reinterpret_cast<decltype(g_norm)>(p[3]);
     g_norm_backward = reinterpret_cast<decltype(g_norm_backward)>(p[4]);
+    g_workspace = reinterpret_cast<decltype(g_workspace)>(p[5]);
     Py_RETURN_NONE;
 }
 
@@ -371,6 +380,7 @@ PyMethodDef g_methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                            {"fp4_matmul", FAST(call<matmul>), METH_FASTCALL, nullptr},
                            {"residual_norm_quantize_amax", FAST(call<norm>), METH_FASTCALL, nullptr},
                            {"residual_norm_backward", FAST(call<norm_backward>), METH_FASTCALL, nullptr},
+                           {"residual_norm_backward_workspace", FAST(call<workspace>), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -129,7 +129,7 @@ def _native():
     from . import _binding as b
     b.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
              (L.fp8q_fp4_quantize_amax, L.fp8q_fp4_dequantize, L.fp8q_fp4_matmul, L.fp8q_residual_norm_quantize_amax,
-              L.fp8q_residual_norm_backward)))
+              L.fp8q_residual_norm_backward, L.fp8q_residual_norm_backward_workspace)))
     _binding = b
     return b
 
@@ -462,7 +462,7 @@ def fp8q_residual_norm_quantize_amax(residual, residual_out, block=None, post_we
 
 def residual_norm_backward_workspace(rows, hidden, rows_per_gate=0):
     """Bytes of workspace of fp8q_residual_norm_backward (rows_per_gate 0: no gate)."""
-    return lib().fp8q_residual_norm_backward_workspace(rows, hidden, rows_per_gate)
+    return _native().residual_norm_backward_workspace(rows, hidden, rows_per_gate)
 
 
 def fp8q_residual_norm_backward(d_residual_out, d_h, residual_out, rstd_pre, pre_weight, d_residual, d_pre_weight,
