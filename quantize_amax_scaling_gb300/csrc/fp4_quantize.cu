@@ -7,11 +7,11 @@
 // 128 code rows.  A thread quantizes 16 columns of a row from registers; the
 // transpose reads the same tile back from shared memory by pairs of columns.
 // Matrices whose rows do not start on 32-byte boundaries pass through shared
-// memory by aligned 32-bit words, a warp a row.
+// memory by 16 aligned bytes.
 //
 // Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 15.9 us
 // (26.7), MXFP4 14.4 us (19.8), back 14.2 and 13.9 us, 3.9 to 6.1 TB/s; 1187 x 2731
-// both ways, where rows start anywhere, 8.3 and 7.1 us.  NVFP4 both ways issues
+// both ways, where rows start anywhere, 7.1 and 5.6 us.  NVFP4 both ways issues
 // 64 % of its cycles' instructions: a scale of every 16 elements costs a
 // conversion there and back, two products and a reciprocal, twice over.
 
@@ -23,85 +23,53 @@ namespace {
 
 constexpr int kTile = 128;  // rows and columns of a CTA's tile
 
-constexpr int kRawWords = kTile / 2 + 1;  // a row of the tile in shared memory, from an odd place too
+// Rows that start anywhere pass through shared memory as they lie in memory, by
+// groups of 16 aligned bytes: element e of a row's part of the tile is half-word
+// e + shift there, `shift` the part's place within its 16 bytes.
+constexpr int kGroups = kTile / 8 + 1;  // a row's
+__device__ __forceinline__ int shift_of(const uint16_t* first) { return (int)(((uintptr_t)first >> 1) & 7); }
 
-// How a row's part of the tile, elements [c0, c0 + n) of the row, lies by 32-bit
-// words: `odd` first element alone, then whole words, then perhaps one more
-// element.  In shared memory element e is half-word e + odd, so that the words
-// stay words.
-struct RowWords {
-    int n, odd;
-};
-__device__ __forceinline__ RowWords row_words(const uint16_t* first, int64_t c0, int64_t cols) {
-    return {(int)min((int64_t)kTile, cols - c0), (int)(((uintptr_t)first >> 1) & 1)};
-}
-
-// Rows [r0, r0 + 128) of x, columns [c0, c0 + 128), into `raw`, zeros where there
-// are none; a warp takes a row, eight rows' loads at a time, a lane the words
-// `lane` and `lane` + 32 (lane 0 the odd last one too).
-__device__ __forceinline__ void load_rows(uint32_t* raw, const uint16_t* x, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int base = 0; base < kTile; base += 64) {
-        uint32_t v[8][2];
-        uint16_t edge[8][2];
+// Rows [r0, r0 + 128) of x, columns [c0, c0 + 128), into `raw`, zeros where there are none; nine groups a thread,
+// all on their way at once.  A group takes its neighbours' elements along, where they belong to x.
+// (8192x4095, NVFP4: 27.9 us, both ways 38.8; 31.7 and 47.7 by 32-bit words.)
+__device__ __forceinline__ void load_rows(uint4* raw, const uint16_t* x, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+    constexpr int kLoads = (kTile * kGroups + kThreads - 1) / kThreads;
+    const int n = (int)min((int64_t)kTile, cols - c0);
+    const uint16_t* end = x + rows * cols;
+    uint4 v[kLoads];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = base + j * 8 + warp;
-            const uint16_t* p = x + (r0 + row) * cols + c0;
-            RowWords k = row_words(p, c0, cols);
-            if (r0 + row >= rows) k.n = 0;
+    for (int j = 0; j < kLoads; ++j) {
+        const int i = j * kThreads + threadIdx.x, k = i / kGroups;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (k < kTile && r0 + k < rows) {
+            const uint16_t* first = x + (r0 + k) * cols + c0;
+            const int e = (i - k * kGroups) * 8 - shift_of(first);
+            const uint16_t* at = first + e;
+            if (e < n) {
+                if (at >= x && at + 8 <= end) {
+                    v[j] = *reinterpret_cast<const uint4*>(at);
+                } else {  // x's first or last
+                    uint32_t u[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int e = 2 * (lane + 32 * i) - k.odd;  // the word holds elements e and e + 1
-                v[j][i] = 0;
-                edge[j][i] = 0;
-                if (e >= 0 && e + 1 < k.n)
-                    v[j][i] = *reinterpret_cast<const unsigned int*>(p + e);
-                else if (e < k.n && e + 1 >= 0 && k.n > 0)  // one of them
-                    edge[j][i] = p[e < 0 ? 0 : e];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = base + j * 8 + warp;
-            const uint16_t* p = x + (r0 + row) * cols + c0;
-            const RowWords k = row_words(p, c0, cols);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int w = lane + 32 * i;
-                raw[row * kRawWords + w] = v[j][i] | (2 * w < k.odd ? (uint32_t)edge[j][i] << 16 : edge[j][i]);
+                    for (int h = 0; h < 4; ++h)
+                        u[h] = (at + 2 * h >= x && at + 2 * h < end ? (uint32_t)at[2 * h] : 0u) |
+                               (at + 2 * h + 1 >= x && at + 2 * h + 1 < end ? (uint32_t)at[2 * h + 1] << 16 : 0u);
+                    v[j] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
             }
         }
     }
-    if (threadIdx.x < kTile) {
-        const int row = threadIdx.x;
-        const uint16_t* p = x + (r0 + row) * cols + c0;
-        const RowWords k = row_words(p, c0, cols);
-        raw[row * kRawWords + kTile / 2] = k.odd && k.n == kTile && r0 + row < rows ? p[kTile - 1] : 0;
-    }
-}
-
-// The same way back, ROWS rows.
-template <int ROWS>
-__device__ __forceinline__ void store_rows(const uint32_t* raw, uint16_t* y, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll 4
-    for (int row = threadIdx.x >> 5; row < ROWS; row += kThreads / 32) {
-        uint16_t* p = y + (r0 + row) * cols + c0;
-        RowWords k = row_words(p, c0, cols);
-        if (r0 + row >= rows) k.n = 0;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const int w = lane + 32 * i, e = 2 * w - k.odd;
-            if (w >= kRawWords) continue;
-            const uint32_t v = raw[row * kRawWords + w];
-            if (e >= 0 && e + 1 < k.n) {
-                *reinterpret_cast<uint32_t*>(p + e) = v;
-            } else {
-                if (e >= 0 && e < k.n) p[e] = (uint16_t)v;
-                if (e + 1 >= 0 && e + 1 < k.n) p[e + 1] = (uint16_t)(v >> 16);
-            }
+    for (int j = 0; j < kLoads; ++j) {
+        const int i = j * kThreads + threadIdx.x, k = i / kGroups;
+        if (n < kTile && r0 + k < rows) {  // columns past the last
+            const int keep = n - ((i - k * kGroups) * 8 - shift_of(x + (r0 + k) * cols + c0));  // elements of the group
+            uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) u[h] &= (keep > 2 * h ? 0xFFFFu : 0u) | (keep > 2 * h + 1 ? 0xFFFF0000u : 0u);
+            v[j] = make_uint4(u[0], u[1], u[2], u[3]);
         }
+        if (k < kTile) raw[i] = v[j];
     }
 }
 
@@ -135,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantAr
     constexpr int kBlock = Fp4<FMT>::kBlock;
     __shared__ uint32_t red[kThreads / 32];
     __shared__ __align__(16) uint32_t sfs[2 * 128];
-    __shared__ __align__(16) uint32_t xs[VEC ? kTile * kTile / 2 : kTile * kRawWords];
+    __shared__ __align__(16) uint32_t xs[VEC ? kTile * kTile / 2 : kTile * kGroups * 4];
     __shared__ __align__(16) uint2 qts[COL ? kTile * 9 : 1];  // 72 bytes a code row: 2-way conflicts at most
     const int tid = threadIdx.x;
     const uint32_t tr = blockIdx.x / (uint32_t)a.tile_cols;
@@ -143,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantAr
 
     start_behind();
     Fp4Scale sc;
-    if (!VEC) sc = make_fp4_scale(a.scale);  // on its way before the barriers of load_rows() (1187x2731, NVFP4: 8.5 us, 9.5 behind them)
+    if (!VEC) sc = make_fp4_scale(a.scale);  // on its way before the barriers of load_rows() (1187x2731, NVFP4: 7.1 us; 1 us more behind them)
     uint32_t w[4][8];
     // a thread's four chunks lie 32 rows apart
     const int ck = tid & 7, left = (int)min(a.rows - r0, (int64_t)kTile) - (tid >> 3);
@@ -159,13 +127,13 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantAr
             w[u][4] = hi.x; w[u][5] = hi.y; w[u][6] = hi.z; w[u][7] = hi.w;
         }
     } else {
-        load_rows(xs, a.x, r0, a.rows, c0, a.cols);
+        load_rows(reinterpret_cast<uint4*>(xs), a.x, r0, a.rows, c0, a.cols);
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int id = u * kThreads + tid, row = id >> 3;
-            const int odd = row_words(a.x + (r0 + row) * a.cols + c0, c0, a.cols).odd;
-            const uint32_t* p = xs + row * kRawWords + (id & 7) * 8;
+            const int shift = shift_of(a.x + (r0 + row) * a.cols + c0), odd = shift & 1;
+            const uint32_t* p = xs + row * kGroups * 4 + (id & 7) * 8 + (shift >> 1);
             uint32_t v = p[0];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -356,40 +324,74 @@ __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t code, float s) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Rows that start anywhere: tiles of kOddRows x kTile columns, a chunk of 16 a thread, through shared memory.
-// (1187x2731: XX us; 6.1 on tiles of 128 rows, too few CTAs to hide a CTA's way.)
-constexpr int kOddRows = kThreads * 16 / kTile;
+// Rows that start anywhere: tiles of kOddRows x kTile columns, kOddChunks of 16 a thread, through shared memory.
+// (1187x2731, 8192x4095: 4.7 and 25.9 us; 5.3 and 27.5 with one chunk, 6.3 and 27.0 with four.)
+constexpr int kOddChunks = 2, kOddRows = kThreads * kOddChunks * 16 / kTile;
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4DequantArgs a) {
-    __shared__ __align__(16) uint32_t raw[kOddRows * kRawWords];
-    const int row = threadIdx.x >> 3, ck = threadIdx.x & 7;
+    __shared__ uint4 raw[kOddRows * kGroups];
+    const int ck = threadIdx.x & 7;
     const uint32_t tr = blockIdx.x / (uint32_t)a.tile_cols;
     const int64_t r0 = (int64_t)tr * kOddRows, c0 = (int64_t)(blockIdx.x - tr * (uint32_t)a.tile_cols) * kTile;
-    const int64_t r = r0 + row, c = c0 + ck * 16, block = c / Fp4<FMT>::kBlock;
+    const int64_t c = c0 + ck * 16, block = c / Fp4<FMT>::kBlock;
     start_behind();
     const float s = a.scale ? *a.scale : 1.0f;
-    uint2 w = make_uint2(0, 0);
-    uint32_t code = 0;
-    if (r < a.rows && c < a.cols) {
-        w = ld_once_v2(a.q + r * fp4_row_bytes(a.cols) + c / 2);
-        code = a.sf[(r / 128 * fp4_sf_tiles<FMT>(a.cols) + block / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + block % 4];
+    uint2 w[kOddChunks];
+    uint32_t code[kOddChunks];
+#pragma unroll
+    for (int u = 0; u < kOddChunks; ++u) {
+        const int64_t r = r0 + u * (kThreads / 8) + (threadIdx.x >> 3);
+        w[u] = make_uint2(0, 0);
+        code[u] = 0;
+        if (r < a.rows && c < a.cols) {
+            w[u] = ld_once_v2(a.q + r * fp4_row_bytes(a.cols) + c / 2);
+            code[u] = a.sf[(r / 128 * fp4_sf_tiles<FMT>(a.cols) + block / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + block % 4];
+        }
     }
-    const uint4 v0 = values8<FMT>(w.x, code, s), v1 = values8<FMT>(w.y, code, s);
-    const uint32_t o[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    uint32_t* p = raw + row * kRawWords + ck * 8;
-    if (row_words(a.y + r * a.cols + c0, c0, a.cols).odd) {  // half a word on: this chunk's first element is its neighbour's last half-word
-        uint16_t* h = reinterpret_cast<uint16_t*>(p);
-        h[1] = (uint16_t)o[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) p[i] = __byte_perm(o[i - 1], o[i], 0x5432);
-        h[16] = (uint16_t)(o[7] >> 16);
-    } else {
+    for (int u = 0; u < kOddChunks; ++u) {
+        const int row = u * (kThreads / 8) + (threadIdx.x >> 3);
+        const uint4 v0 = values8<FMT>(w[u].x, code[u], s), v1 = values8<FMT>(w[u].y, code[u], s);
+        const uint32_t o[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        const int shift = shift_of(a.y + (r0 + row) * a.cols + c0);
+        uint32_t* p = reinterpret_cast<uint32_t*>(raw + row * kGroups) + ck * 8 + (shift >> 1);
+        if (shift & 1) {  // half a word on: this chunk's first element is its neighbour's last half-word
+            uint16_t* h = reinterpret_cast<uint16_t*>(p);
+            h[1] = (uint16_t)o[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = o[i];
+            for (int i = 1; i < 8; ++i) p[i] = __byte_perm(o[i - 1], o[i], 0x5432);
+            h[16] = (uint16_t)(o[7] >> 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = o[i];
+        }
     }
     __syncthreads();
-    store_rows<kOddRows>(raw, a.y, r0, a.rows, c0, a.cols);
+    const int n = (int)min(a.cols - c0, (int64_t)kTile);
+#pragma unroll
+    for (int i = threadIdx.x; i < kOddRows * kGroups; i += kThreads) {
+        const int k = i / kGroups;
+        if (r0 + k >= a.rows) break;
+        uint16_t* first = a.y + (r0 + k) * a.cols + c0;
+        const int e = (i - k * kGroups) * 8 - shift_of(first);  // the group's first element
+        const uint4 v = raw[i];
+        if (e >= 0 && e + 8 <= n) {
+            st_v4(first + e, v);
+        } else {
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int f = e + 2 * j;
+                if (f >= 0 && f + 1 < n) {
+                    *reinterpret_cast<uint32_t*>(first + f) = u[j];
+                } else {
+                    if (f >= 0 && f < n) first[f] = (uint16_t)u[j];
+                    if (f + 1 >= 0 && f + 1 < n) first[f + 1] = (uint16_t)(u[j] >> 16);
+                }
+            }
+        }
+    }
 }
 
 // Rows that start on 16-byte boundaries: tiles of kOutRows x kOut columns, eight
