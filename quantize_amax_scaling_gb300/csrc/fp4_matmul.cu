@@ -13,7 +13,7 @@
 // Two kernels.  Few tiles: 128 rows of P by 16 to 128 of Q a CTA, k split over a
 // cluster while every CTA is resident; what bounds them is the operands' way from
 // HBM, and at these sizes the time until it flows: 1 x 16384 x 4096 (37.7 MB)
-// 9.5 us, 4.0 TB/s; 1 x 4096 x 4096 4.7 us; each megabyte more costs 0.17 us, 6 TB/s.
+// 9.5 us, 4.0 TB/s; 1 x 4096 x 4096 4.7 us; each megabyte more costs 0.15 us, 6.5 TB/s.
 // Many tiles: pairs of CTAs with 256 x 256 (below), bound by the tensor cores,
 // between tiles by the accumulators' way out, and in a loop by the power limit:
 // 8192 x 16384 x 4096 172 us (MXFP4 165), 6.4 PFLOP/s; seconds long 198 us at 1400 W
@@ -377,6 +377,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 
     if (warp == 9) tmem_alloc<2>(&tmem_slot, 512);
     if (threadIdx.x == 0) {
+        prefetch_map(&map_p);
+        prefetch_map(&map_q);
+        prefetch_map(&map_psf);
+        prefetch_map(&map_qsf);
         for (int i = 0; i < kPairStages; ++i) {
             mbar_init_count(&full[i], 1 + 8);
             mbar_init(&sf_full[i]);
@@ -713,13 +717,17 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     const int sms = sm_count();
     const bool pairs = m > 128 && n > 128 && (m + 127) / 128 * ((n + 127) / 128) > sms;
     // Otherwise few tiles share out their sums over clusters, while every CTA is resident (two an SM up to 32
-    // rows of Q; clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and keeps four steps or more: 1x4096x4096 takes 7.4 us
-    // on 32 CTAs, 5.8 on clusters of 4; 128x4096x4096 9.6 and 8.2.
+    // rows of Q; clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and keeps four steps or more: 1x4096x4096 takes
+    // 6.6 us on 32 CTAs, 4.7 on clusters of 4; 128x4096x4096 8.3 and 7.5.  A cluster and its sums cost 1 us or two, so
+    // the more of the GPU the tiles take anyway, the longer k has to be: 24x16384x2048 takes 6.7 us, 7.8 on clusters of
+    // 2; 1000x1040x2072 6.8 and 8.6; 1x12288x8192 12.5 on clusters of 2, 13.9 without.
     const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, steps = (g.ksteps + 3) / 4;
     int split = 1;
     if (!pairs) {
         const int64_t tiles = (n + 127) / 128 * ((m + bn - 1) / bn), room = (bn <= 32 ? 2 : 1) * sms;
-        while (split < 8 && tiles * split * 2 <= room * (split == 1 ? 20 : split == 2 ? 19 : 16) / 20 && steps >= split * 8) split *= 2;
+        while (split < 8 && tiles * split * 2 <= room * (split == 1 ? 20 : split == 2 ? 19 : 16) / 20 &&
+               steps >= (split > 1 ? split * 8 : tiles * 3 > sms * 2 ? 32 : tiles * 5 > sms * 2 ? 16 : 8))
+            split *= 2;
     }
     g.split = split;
     // P, whose rows are the accumulators' 128 lanes, is A, and a thread holds part of a row of D, where

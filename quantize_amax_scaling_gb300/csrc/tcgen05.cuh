@@ -270,6 +270,10 @@ __device__ __forceinline__ void tile_store(const CUtensorMap* map, int x, int y,
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// A tensor map on its way before its first copy.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
