@@ -716,18 +716,18 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     // Pairs of CTAs where 128-row tiles of one CTA each would not all be resident at once.
     const int sms = sm_count();
     const bool pairs = m > 128 && n > 128 && (m + 127) / 128 * ((n + 127) / 128) > sms;
-    // Otherwise few tiles share out their sums over clusters, while every CTA is resident (two an SM up to 32
-    // rows of Q; clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and keeps four steps or more: 1x4096x4096 takes
-    // 6.6 us on 32 CTAs, 4.7 on clusters of 4; 128x4096x4096 8.3 and 7.5.  A cluster and its sums cost 1 us or two, so
-    // the more of the GPU the tiles take anyway, the longer k has to be: 24x16384x2048 takes 6.7 us, 7.8 on clusters of
-    // 2; 1000x1040x2072 6.8 and 8.6; 1x12288x8192 12.5 on clusters of 2, 13.9 without.
+    // Otherwise the CTAs of a cluster share a tile's sums, as many as are resident at once (two an SM up to 32 rows of Q;
+    // clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and have two steps or more, where the steps that a CTA
+    // saves are worth the cluster and its sums, 1 us for 16 rows of Q to 3 for 128, a step 0.3: 1x4096x4096
+    // takes 4.7 us on clusters of 4, 6.6 without; 128x4096x4096 7.5 and 8.5, 128x4096x2048 6.5 and 5.7.  The more of the
+    // GPU the tiles take anyway, the longer k has to be: 24x16384x2048 takes 6.7 us, 7.8 on clusters of 2.
     const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, steps = (g.ksteps + 3) / 4;
     int split = 1;
     if (!pairs) {
         const int64_t tiles = (n + 127) / 128 * ((m + bn - 1) / bn), room = (bn <= 32 ? 2 : 1) * sms;
-        while (split < 8 && tiles * split * 2 <= room * (split == 1 ? 20 : split == 2 ? 19 : 16) / 20 &&
-               steps >= (split > 1 ? split * 8 : tiles * 3 > sms * 2 ? 32 : tiles * 5 > sms * 2 ? 16 : 8))
-            split *= 2;
+        int most = 1;
+        while (most < 8 && tiles * most * 2 <= room * (most == 1 ? 20 : most == 2 ? 19 : 16) / 20 && steps >= most * 4) most *= 2;
+        if (steps - steps / most > 5 + bn / 20 && steps >= (tiles * 3 > sms * 2 ? 32 : tiles * 5 > sms * 2 ? 16 : 0)) split = most;
     }
     g.split = split;
     // P, whose rows are the accumulators' 128 lanes, is A, and a thread holds part of a row of D, where
