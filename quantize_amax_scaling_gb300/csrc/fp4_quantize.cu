@@ -11,7 +11,7 @@
 //
 // Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 15.9 us
 // (26.7), MXFP4 14.4 us (19.8), back 14.2 and 13.9 us, 3.9 to 6.1 TB/s; 1187 x 2731
-// both ways, where rows start anywhere, 7.1 and 5.6 us.  NVFP4 both ways issues
+// both ways, where rows start anywhere, 7.0 and 5.5 us.  NVFP4 both ways issues
 // 64 % of its cycles' instructions: a scale of every 16 elements costs a
 // conversion there and back, two products and a reciprocal, twice over.
 
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const Fp4QuantAr
 // One direction of rows that start on 32-byte boundaries: the same work on tiles
 // of kWideRows x kWide columns, from registers alone, so that a CTA reads longer
 // stretches of memory; scales go out by words of four blocks.  (8192x4096, NVFP4:
-// 16.6 us; 18.6, and 19.1 on tiles of 128 x 128, with every address worked out
+// 15.9 us; 2 us more, and 2.5 on tiles of 128 x 128, with every address worked out
 // anew; 1024 columns measure the same.)
 constexpr int kWide = 512, kWideRows = kTile * kTile / kWide;
 
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const Fp4Dequa
 
 // Rows that start on 16-byte boundaries: tiles of kOutRows x kOut columns, eight
 // columns a thread at a time, so that a warp's stores are one stretch (8192x4096,
-// NVFP4: 16.4 us; 17.0 with two chunks a thread, 18.9 with sixteen columns at a time).
+// NVFP4: 14.0 us; half a us more with two chunks a thread, 2.5 with sixteen columns at a time).
 constexpr int kOut = 1024, kOutChunks = 4, kOutRows = kThreads * kOutChunks * 8 / kOut;
 
 template <int FMT>
