@@ -94,6 +94,43 @@ __device__ __forceinline__ void store_row16(void* d, int64_t at, const float (&v
     }
 }
 
+// This CTA's share of a tile's sums, added over the SPLIT CTAs of the cluster in rank order, four rows a thread, BATCH such
+// groups on their way at a time: a read of another CTA's memory takes hundreds of cycles (256x4096x8192 11.1 us,
+// 12.7 with one group at a time).
+template <bool F32, int SPLIT, int BATCH>
+__device__ __forceinline__ void add_shares(const MmArgs& a, uint32_t part, int bn, int rank, int p0, int q0, float alpha) {
+    const int share = bn * 32 / SPLIT, end = (rank + 1) * share;
+    for (int i0 = rank * share + (int)threadIdx.x; i0 < end; i0 += 192 * BATCH) {
+        float4 v[BATCH][SPLIT];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+            if (i0 + 192 * b < end)
+#pragma unroll
+                for (int r = 0; r < SPLIT; ++r) v[b][r] = ld_cluster_f32x4(in_cluster(part + (i0 + 192 * b) * 16, r));
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int i = i0 + 192 * b, q = q0 + (i >> 5), p = p0 + (i & 31) * 4;
+            if (i >= end) break;
+            float f[4] = {v[b][0].x, v[b][0].y, v[b][0].z, v[b][0].w};
+#pragma unroll
+            for (int r = 1; r < SPLIT; ++r) f[0] += v[b][r].x, f[1] += v[b][r].y, f[2] += v[b][r].z, f[3] += v[b][r].w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = __fmul_rn(f[k], alpha);
+            const int64_t at = (int64_t)q * a.ld + p;  // split tiles have D's rows along P
+            if (q < a.q_rows && a.vec && p < a.p_rows) {
+                if (F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.d) + at) = make_float4(f[0], f[1], f[2], f[3]);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.d) + at) = make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
+            } else if (q < a.q_rows) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (p + k < a.p_rows) store_one<F32>(a.d, at + k, f[k]);
+            }
+        }
+    }
+}
+
 template <int FMT, int BN, bool F32>
 __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                                                          const MmArgs a) {
@@ -258,30 +295,10 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
             }
         }
         cluster_sync_all();
-        const int share = BN * 32 / a.split;
-        for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += 192) {
-            const int q = q0 + (i >> 5), p = p0 + (i & 31) * 4;
-            float4 v[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < a.split) v[r] = ld_cluster_f32x4(in_cluster(base + i * 16, r));
-            float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-            for (int r = 1; r < 8; ++r)
-                if (r < a.split) f[0] += v[r].x, f[1] += v[r].y, f[2] += v[r].z, f[3] += v[r].w;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = __fmul_rn(f[k], alpha);
-            const int64_t at = (int64_t)q * a.ld + p;  // split tiles have D's rows along P
-            if (q < a.q_rows && a.vec && p < a.p_rows) {
-                if (F32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(a.d) + at) = make_float4(f[0], f[1], f[2], f[3]);
-                else
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.d) + at) = make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
-            } else if (q < a.q_rows) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (p + k < a.p_rows) store_one<F32>(a.d, at + k, f[k]);
-            }
+        switch (a.split) {
+            case 2: add_shares<F32, 2, 4>(a, base, BN, rank, p0, q0, alpha); break;
+            case 4: add_shares<F32, 4, 2>(a, base, BN, rank, p0, q0, alpha); break;
+            default: add_shares<F32, 8, 2>(a, base, BN, rank, p0, q0, alpha);
         }
         cluster_sync_all();  // no CTA's sums go away while another reads them
     }
@@ -718,16 +735,16 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     const bool pairs = m > 128 && n > 128 && (m + 127) / 128 * ((n + 127) / 128) > sms;
     // Otherwise the CTAs of a cluster share a tile's sums, as many as are resident at once (two an SM up to 32 rows of Q;
     // clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and have two steps or more, where the steps that a CTA
-    // saves are worth the cluster and its sums, 1 us for 16 rows of Q to 3 for 128, a step 0.3: 1x4096x4096
-    // takes 4.7 us on clusters of 4, 6.6 without; 128x4096x4096 7.5 and 8.5, 128x4096x2048 6.5 and 5.7.  The more of the
-    // GPU the tiles take anyway, the longer k has to be: 24x16384x2048 takes 6.7 us, 7.8 on clusters of 2.
+    // saves are worth the cluster and its sums, 1 us for 16 rows of Q to 2.5 for 128, a step 0.3: 1x4096x4096
+    // takes 4.7 us on clusters of 4, 6.6 without; 128x4096x4096 7.0 and 8.5, 128x8192x4096 9.0 and 9.6, but 128x4096x2048 6.3 and 5.7.
+    // The more of the GPU the tiles take anyway, the longer k has to be: 24x16384x2048 takes 6.7 us, 7.8 on clusters of 2.
     const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, steps = (g.ksteps + 3) / 4;
     int split = 1;
     if (!pairs) {
         const int64_t tiles = (n + 127) / 128 * ((m + bn - 1) / bn), room = (bn <= 32 ? 2 : 1) * sms;
         int most = 1;
         while (most < 8 && tiles * most * 2 <= room * (most == 1 ? 20 : most == 2 ? 19 : 16) / 20 && steps >= most * 4) most *= 2;
-        if (steps - steps / most > 5 + bn / 20 && steps >= (tiles * 3 > sms * 2 ? 32 : tiles * 5 > sms * 2 ? 16 : 0)) split = most;
+        if (steps - steps / most > 3 + bn / 32 && steps >= (tiles * 3 > sms * 2 ? 32 : tiles * 5 > sms * 2 ? 16 : 0)) split = most;
     }
     g.split = split;
     // P, whose rows are the accumulators' 128 lanes, is A, and a thread holds part of a row of D, where

@@ -412,7 +412,8 @@ def fp4_scale_bytes(rows, cols, fmt):
 
 
 def fp4_empty(rows, cols, fmt, device="cuda"):
-    """Room for a packed 4-bit operand of an [rows, cols] matrix: (codes [rows, row bytes], scales)."""
+    """Room for a packed 4-bit operand of an [rows, cols] matrix: (codes [rows, row bytes], scales); on the
+    current CUDA device one allocation holds both."""
     if device == "cuda":
         return _native().fp4_empty(rows, cols, fmt)
     import torch
