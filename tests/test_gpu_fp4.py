@@ -228,6 +228,15 @@ def test_matmul_exact_sums(dev, m, n, k, fmt):
     assert torch.equal(d.double(), a @ b.t())
 
 
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.NVFP4])
+@pytest.mark.parametrize("m,n,k", [(2, 9800, 8192), (16, 4097, 2048), (9, 300, 4100), (24, 9800, 8200), (24, 6000, 4097), (30, 335, 16384),
+                                   (64, 8200, 4200), (64, 4097, 3000), (60, 1001, 8200), (256, 4096, 8192), (128, 4097, 4096),
+                                   (300, 1000, 4096), (128, 1024, 8192), (100, 333, 4100)])
+def test_matmul_sums_shared_by_clusters(dev, m, n, k, fmt):
+    """Clusters of 2, 4 and 8 for each width of tile, rows of D that hold whole vectors and odd ones, exact sums."""
+    test_matmul_exact_sums(dev, m, n, k, fmt)
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 64, 96), (300, 520, 320)])
 def test_matmul_nan_block_reaches_its_row_only(dev, m, n, k):
     qa, sa, ca, fa = random_operand(m, k, R.MXFP4, 1, dev)
