@@ -129,7 +129,13 @@ __device__ __forceinline__ void row_barrier(int T) {
         asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / T), "r"(T) : "memory");
 }
 
-// Sum over the T threads of a row (T a power of two from 32 to 1024; all of them
+// This lane's of the sums that a row's warps left in `part`: lane by lane, zeros up to the next power of two.
+__device__ __forceinline__ float part_of(const float* part, int T) {
+    const int warps = T >> 5, j = threadIdx.x & ((2 << (31 - __clz(warps - 1))) - 1);
+    return j < warps ? part[threadIdx.x / T * warps + j] : 0.0f;
+}
+
+// Sum over the T threads of a row (T a multiple of 32 up to 1024; all of them
 // call it).  `part` holds one float a warp and is not written again
 // before the next barrier but one.
 __device__ __forceinline__ float row_sum(float v, int T, float* part) {
@@ -138,7 +144,7 @@ __device__ __forceinline__ float row_sum(float v, int T, float* part) {
     const int warp = threadIdx.x >> 5, warps = T >> 5;
     if ((threadIdx.x & 31) == 0) part[warp] = v;
     row_barrier(T);
-    v = part[(warp & ~(warps - 1)) + (threadIdx.x & (warps - 1))];
+    v = part_of(part, T);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
         if (o < warps) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -203,18 +209,18 @@ __device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, c
 // from L1): with 16 columns' weights and values in registers 16 warps fit an SM and
 // issued 59% of the time, 53 us for 8192x4096; with 24 warps it takes 49.  ROW > 0:
 // the call that a block's edge makes (all parts there, a gate for several rows),
-// for rows of that many threads: 42.6 us.
+// for rows of that many threads: 42.6 us; ROW < 0: for any number of warps a row.
 template <int FMT, int U, int THREADS, int ROW>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) residual_norm_kernel(const RnArgs a) {
-    constexpr bool kFull = ROW > 0, kHold = THREADS < 1024;  // weights in shared memory
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : THREADS == 320 ? 2 : 1) residual_norm_kernel(const RnArgs a) {
+    constexpr bool kFull = ROW != 0, kFixed = ROW > 0, kHold = THREADS < 1024;  // weights in shared memory
     constexpr int kStages = THREADS < 1024 ? 2 : U == 2 ? 3 : 1;  // rows under way
-    constexpr uint32_t kStep = THREADS * 16;                // from one slot to the next
+    const uint32_t kStep = (kFixed ? THREADS : blockDim.x) * 16;   // from one slot to the next
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float part[4][32];
     __shared__ uint32_t red[32];
     const bool has_b = kFull || a.b, has_post = kFull || a.post, has_pre = kFull || a.pre, has_ro = kFull || a.ro;
-    const int T = kFull ? ROW : a.T, t = threadIdx.x % T;
-    const uint32_t strip = blockIdx.x * (THREADS / T) + threadIdx.x / T;
+    const int T = kFixed ? ROW : a.T, t = threadIdx.x % T;
+    const uint32_t strip = blockIdx.x * ((kFixed ? THREADS : blockDim.x) / T) + threadIdx.x / T;
     const uint32_t rows = (uint32_t)a.rows, per_strip = (uint32_t)a.per_strip;
     const uint32_t row0 = strip * per_strip, row1 = min(row0 + per_strip, rows);
     const bool ring_gate = !kFull && kHold && a.gate && a.per == 1;
@@ -762,31 +768,41 @@ fp8q_status launch_backward(const RnBwdArgs& a, unsigned ctas, unsigned slices, 
 template <int FMT>
 fp8q_status launch_forward(RnArgs a, cudaStream_t s) {
     const int U = a.H > 16384 ? 4 : 2;
-    a.T = 1024;
-    while (a.T > 32 && a.H <= a.T * 4 * U) a.T /= 2;
-    const int block = a.T < 256 ? 256 : a.T, per_cta = block / a.T;
-    const int slots = 1 + (a.b != nullptr) + (block < 1024 && a.gate && a.per == 1 ? (a.gate_bf16 ? 1 : 2) : 0);
-    const size_t smem = (size_t)((block < 1024 ? 2 : U == 2 ? 3 : 1) * U * slots + (block < 1024 ? 4 * U : 0)) * block * 16;
-    // strips: as many as CTAs are resident, three of 256 threads an SM (two with a gate in the ring), one of 512 or 1024
-    const int64_t most = (int64_t)(block > 256 ? 1 : smem <= 74 * 1024 ? 3 : 2) * 152 * per_cta;
+    // As many threads a row as its columns want, whole warps: a power of two leaves up to half of them idle (6553x5120, e4m3:
+    // 46.5 us, 68 with 512 threads; 8160x4112 53.7 and 82).  Where it leaves less than a quarter, or two such rows
+    // would not fit an SM, the power of two is as good or better (5242x6400 57 us, 61 with 416).
+    a.T = (a.H + U * 256 - 1) / (U * 256) * 32;
+    if (a.T > 192 && a.T < 256) a.T = 256;
+    if (a.T > 320 && a.T < 512) a.T = 512;
+    const int per_cta = a.T < 256 ? 256 / a.T : 1, block = a.T * per_cta;
+    const bool hold = block <= 512;  // weights in shared memory, two rows under way
+    const int slots = 1 + (a.b != nullptr) + (hold && a.gate && a.per == 1 ? (a.gate_bf16 ? 1 : 2) : 0);
+    const size_t smem = (size_t)((hold ? 2 : U == 2 ? 3 : 1) * U * slots + (hold ? 4 * U : 0)) * block * 16;
+    // strips: as many as CTAs are resident, by registers (80 a thread, 24 warps; 96 in CTAs of up to 320, 20; 128 of 512, 16;
+    // 64 above, 32) and shared memory
+    const int64_t by_regs = (block <= 256 ? 24 : block <= 320 ? 20 : hold ? 16 : 32) / (block / 32), by_smem = (int64_t)(224 * 1024 / (smem + 2048));
+    const int64_t most = (by_regs < by_smem ? by_regs : by_smem) * 152 * per_cta;
     a.per_strip = (a.rows + most - 1) / most;
     const int64_t strips = (a.rows + a.per_strip - 1) / a.per_strip;
     const dim3 grid((unsigned)((strips + per_cta - 1) / per_cta));
-    static std::atomic<uint64_t> devices[9];
-    const int which = block == 256 ? 0 : block == 512 ? 1 : U == 2 ? 2 : 3;
+    static std::atomic<uint64_t> devices[12];
+    const int which = block <= 256 ? 0 : block == 512 ? 1 : U == 4 ? 3 : hold ? 11 : 2;
     auto kern = which == 0   ? residual_norm_kernel<FMT, 2, 256, 0>
                 : which == 1 ? residual_norm_kernel<FMT, 2, 512, 0>
                 : which == 2 ? residual_norm_kernel<FMT, 2, 1024, 0>
+                : which == 11 ? residual_norm_kernel<FMT, 2, 320, 0>
                              : residual_norm_kernel<FMT, 4, 1024, 0>;
     int set = which;
     if constexpr (FMT != kOutNone) {
-        if (a.b && a.post && a.pre && a.ro && !(a.gate && a.per == 1) && a.T <= 512) {
-            set = a.T == 32 ? 4 : a.T == 64 ? 5 : a.T == 128 ? 6 : a.T == 256 ? 7 : 8;
+        if (a.b && a.post && a.pre && a.ro && !(a.gate && a.per == 1) && hold) {
+            set = a.T == 32 ? 4 : a.T == 64 ? 5 : a.T == 128 ? 6 : a.T == 256 ? 7 : a.T == 512 ? 8 : block <= 256 ? 9 : 10;
             kern = set == 4   ? residual_norm_kernel<FMT, 2, 256, 32>
                    : set == 5 ? residual_norm_kernel<FMT, 2, 256, 64>
                    : set == 6 ? residual_norm_kernel<FMT, 2, 256, 128>
                    : set == 7 ? residual_norm_kernel<FMT, 2, 256, 256>
-                              : residual_norm_kernel<FMT, 2, 512, 512>;
+                   : set == 8 ? residual_norm_kernel<FMT, 2, 512, 512>
+                   : set == 9 ? residual_norm_kernel<FMT, 2, 256, -1>
+                              : residual_norm_kernel<FMT, 2, 320, -1>;
         }
     }
     // at most 2 stages of 8 slots and 8 of weights of 512 threads, or 6 or 8 slots of 1024
