@@ -205,15 +205,15 @@ __device__ __forceinline__ void store_codes(const RnArgs& a, const QScale& c8, c
 
 // U groups of eight columns a thread, THREADS threads a CTA.  Nothing but the
 // packed sum stays in registers across the two reductions, and the weights lie in
-// shared memory beside the ring (each thread's own; rows of 1024 threads read them
-// from L1): with 16 columns' weights and values in registers 16 warps fit an SM and
+// shared memory beside the ring (each thread's own; rows of more than 8192 columns
+// read them from L1): with 16 columns' weights and values in registers 16 warps fit an SM and
 // issued 59% of the time, 53 us for 8192x4096; with 24 warps it takes 49.  ROW > 0:
 // the call that a block's edge makes (all parts there, a gate for several rows),
 // for rows of that many threads: 42.6 us; ROW < 0: for any number of warps a row.
 template <int FMT, int U, int THREADS, int ROW>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : THREADS == 320 ? 2 : 1) residual_norm_kernel(const RnArgs a) {
     constexpr bool kFull = ROW != 0, kFixed = ROW > 0, kHold = THREADS < 1024;  // weights in shared memory
-    constexpr int kStages = THREADS < 1024 ? 2 : U == 2 ? 3 : 1;  // rows under way
+    constexpr int kStages = kHold ? 2 : 1;  // rows under way
     const uint32_t kStep = (kFixed ? THREADS : blockDim.x) * 16;   // from one slot to the next
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float part[4][32];
@@ -767,30 +767,31 @@ fp8q_status launch_backward(const RnBwdArgs& a, unsigned ctas, unsigned slices, 
 
 template <int FMT>
 fp8q_status launch_forward(RnArgs a, cudaStream_t s) {
-    const int U = a.H > 16384 ? 4 : 2;
+    // rows of more than 8192 columns: 32 columns a thread, the row after next not on its way and the weights from L1, so that
+    // two or three rows are under way on an SM and not one (2048x16384, e4m3: 68 us, 79; 4088x8208 70 and 108)
+    const int U = a.H > 8192 ? 4 : 2;
     // As many threads a row as its columns want, whole warps: a power of two leaves up to half of them idle (6553x5120, e4m3:
     // 46.5 us, 68 with 512 threads; 8160x4112 53.7 and 82).  Where it leaves less than a quarter, or two such rows
     // would not fit an SM, the power of two is as good or better (5242x6400 57 us, 61 with 416).
     a.T = (a.H + U * 256 - 1) / (U * 256) * 32;
     if (a.T > 192 && a.T < 256) a.T = 256;
-    if (a.T > 320 && a.T < 512) a.T = 512;
+    if (U == 2 && a.T > 320 && a.T < 512) a.T = 512;
     const int per_cta = a.T < 256 ? 256 / a.T : 1, block = a.T * per_cta;
-    const bool hold = block <= 512;  // weights in shared memory, two rows under way
+    const bool hold = U == 2;  // weights in shared memory, two rows under way
     const int slots = 1 + (a.b != nullptr) + (hold && a.gate && a.per == 1 ? (a.gate_bf16 ? 1 : 2) : 0);
-    const size_t smem = (size_t)((hold ? 2 : U == 2 ? 3 : 1) * U * slots + (hold ? 4 * U : 0)) * block * 16;
+    const size_t smem = (size_t)((hold ? 2 : 1) * U * slots + (hold ? 4 * U : 0)) * block * 16;
     // strips: as many as CTAs are resident, by registers (80 a thread, 24 warps; 96 in CTAs of up to 320, 20; 128 of 512, 16;
-    // 64 above, 32) and shared memory
-    const int64_t by_regs = (block <= 256 ? 24 : block <= 320 ? 20 : hold ? 16 : 32) / (block / 32), by_smem = (int64_t)(224 * 1024 / (smem + 2048));
+    // 64 with 32 columns a thread, 32) and shared memory
+    const int64_t by_regs = (!hold ? 32 : block <= 256 ? 24 : block <= 320 ? 20 : 16) / (block / 32), by_smem = (int64_t)(224 * 1024 / (smem + 2048));
     const int64_t most = (by_regs < by_smem ? by_regs : by_smem) * 152 * per_cta;
     a.per_strip = (a.rows + most - 1) / most;
     const int64_t strips = (a.rows + a.per_strip - 1) / a.per_strip;
     const dim3 grid((unsigned)((strips + per_cta - 1) / per_cta));
-    static std::atomic<uint64_t> devices[12];
-    const int which = block <= 256 ? 0 : block == 512 ? 1 : U == 4 ? 3 : hold ? 11 : 2;
+    static std::atomic<uint64_t> devices[11];
+    const int which = !hold ? 3 : block <= 256 ? 0 : block <= 320 ? 2 : 1;
     auto kern = which == 0   ? residual_norm_kernel<FMT, 2, 256, 0>
                 : which == 1 ? residual_norm_kernel<FMT, 2, 512, 0>
-                : which == 2 ? residual_norm_kernel<FMT, 2, 1024, 0>
-                : which == 11 ? residual_norm_kernel<FMT, 2, 320, 0>
+                : which == 2 ? residual_norm_kernel<FMT, 2, 320, 0>
                              : residual_norm_kernel<FMT, 4, 1024, 0>;
     int set = which;
     if constexpr (FMT != kOutNone) {
@@ -805,7 +806,7 @@ fp8q_status launch_forward(RnArgs a, cudaStream_t s) {
                               : residual_norm_kernel<FMT, 2, 320, -1>;
         }
     }
-    // at most 2 stages of 8 slots and 8 of weights of 512 threads, or 6 or 8 slots of 1024
+    // at most 2 stages of 8 slots and 8 of weights of 512 threads, or 8 slots of 1024
     const cudaError_t e = allow_smem(kern, 192 * 1024, devices[set]);
     if (e != cudaSuccess) return cuda_fail(e, "residual_norm_kernel setup");
     return launch_behind(kern, grid, dim3(block), smem, 1, s, "residual_norm_kernel", a);
