@@ -131,7 +131,7 @@ __device__ __forceinline__ void row_barrier(int T) {
 
 // This lane's of the sums that a row's warps left in `part`: lane by lane, zeros up to the next power of two.
 __device__ __forceinline__ float part_of(const float* part, int T) {
-    const int warps = T >> 5, j = threadIdx.x & ((2 << (31 - __clz(warps - 1))) - 1);
+    const int warps = T >> 5, j = warps == 1 ? 0 : threadIdx.x & ((2 << (31 - __clz(warps - 1))) - 1);
     return j < warps ? part[threadIdx.x / T * warps + j] : 0.0f;
 }
 
@@ -411,16 +411,21 @@ constexpr int kRnCtas = 304;       // two CTAs on each of 152 SMs
 constexpr int kRnSlice = 4096;     // columns a CTA
 
 struct RnStrips {
-    int32_t T, slices;
+    int32_t T, slices, width, block;  // threads a strip, CTAs a row, columns and threads a CTA
     int64_t per_strip, strips;
 };
 
 RnStrips rn_strips(int64_t rows, int32_t H) {
     RnStrips s;
     s.slices = (H + kRnSlice - 1) / kRnSlice;
+    s.width = ((H + s.slices - 1) / s.slices + 15) / 16 * 16;
     s.T = 256;
-    while (s.T > 32 && H <= s.T * 8) s.T /= 2;
-    const int64_t most = (int64_t)(kRnCtas / s.slices) * (256 / s.T);
+    while (s.T > 32 && s.width <= s.T * 8) s.T /= 2;
+    // three CTAs of 160 threads an SM where 256 would leave every third idle and more (16256x2064: 76 us, 91; 6553x5120, two CTAs a row,
+    // 86 and 109)
+    if (s.T == 256 && s.width <= 160 * 16) s.T = 160;
+    s.block = s.T == 160 ? 160 : 256;
+    const int64_t most = (int64_t)((s.T == 160 ? kRnCtas / 2 * 3 : kRnCtas) / s.slices) * (s.block / s.T);
     s.per_strip = (rows + most - 1) / most;
     s.strips = s.per_strip ? (rows + s.per_strip - 1) / s.per_strip : 0;
     return s;
@@ -475,23 +480,24 @@ __device__ __forceinline__ float warp_sum3(float a, float b, float c) {
 // W = alpha gate g1 of a column, a row adds X to the one sum S that dgate and dg1
 // share: a gate's row of dgate is alpha g1 S, and dg1 takes alpha gate S whenever
 // a gate's rows end.  RING_GATE: each row has its own gate, which comes with it.
-template <bool CLUSTER, bool RING_GATE, int ROW>
-__global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const RnBwdArgs a) {
+// FULL: every part is there.  ROW > 0: strips of that many threads, in CTAs of 160 or 256.
+template <bool CLUSTER, bool RING_GATE, bool FULL, int ROW>
+__global__ void __launch_bounds__(ROW == 160 ? 160 : 256, ROW == 160 ? 3 : 2) residual_norm_backward_kernel(const RnBwdArgs a) {
     namespace cg = cooperative_groups;
     constexpr int kStages = RING_GATE ? 2 : 3;
     extern __shared__ __align__(16) uint8_t ring_raw[];
     __shared__ float part[2][3][8];
     __shared__ float sums[2][8][3];  // of each CTA of the cluster
-    constexpr bool kFull = ROW > 0;
-    const bool has_b = kFull || a.b, has_post = kFull || a.post, has_dh = kFull || a.dh, has_dro = kFull || a.dro;
-    const bool has_dr = kFull || a.dr, has_db = kFull || a.db;
-    const int T = kFull ? ROW : a.T, t = threadIdx.x % T, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kBlock = ROW == 160 ? 160 : 256;
+    const bool has_b = FULL || a.b, has_post = FULL || a.post, has_dh = FULL || a.dh, has_dro = FULL || a.dro;
+    const bool has_dr = FULL || a.dr, has_db = FULL || a.db;
+    const int T = ROW > 0 ? ROW : a.T, t = threadIdx.x % T, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int slices = 1, slice = 0;
     if (CLUSTER) {
         slices = (int)cg::this_cluster().num_blocks();
         slice = (int)cg::this_cluster().block_rank();
     }
-    const int64_t strip = (int64_t)(blockIdx.x / slices) * (256 / T) + threadIdx.x / T;
+    const int64_t strip = (int64_t)(blockIdx.x / slices) * (kBlock / T) + threadIdx.x / T;
     const int64_t row0 = strip * a.per_strip, row1 = min(row0 + a.per_strip, a.rows);
     const int c0 = slice * a.width, c1 = min(c0 + a.width, a.H);  // this CTA's columns
     const int col0 = c0 + t * 8;                                  // this thread's first, and
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
     const float inv_h = 1.0f / (float)a.H;
     // ring: a stage holds, for each of two groups of eight columns, a slot of b, r', dr', dh and one
     // or two of the gate; behind it this thread's sums of dg1
-    constexpr uint32_t kStep = 256 * 16;
+    constexpr uint32_t kStep = kBlock * 16;
     const uint32_t slots = RING_GATE ? (a.gate_bf16 ? 5 : 6) : 4;
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_raw)) + threadIdx.x * 16;
     const uint32_t post_sum = ring + kStages * 2 * slots * kStep;
@@ -592,18 +598,23 @@ __global__ void __launch_bounds__(256, 2) residual_norm_backward_kernel(const Rn
         float s0, s1, s2;
         {
             const float k = warp_sum3(q0.x + q0.y, q1.x + q1.y, q2.x + q2.y);
-            const int warps = T >> 5, from = warp & ~(warps - 1);
             float(*pt)[8] = part[it & 1];
             if ((lane & 7) == 0 && lane < 24) pt[lane >> 3][warp] = k;
             if (T > 32)
                 __syncthreads();
             else
                 __syncwarp();
-            const int i = from + (lane & (warps - 1));
-            s0 = pt[0][i];
-            s1 = pt[1][i];
-            s2 = pt[2][i];
-            for (int o = warps >> 1; o; o >>= 1) {
+            if constexpr (ROW == 160) {
+                s0 = part_of(pt[0], T);
+                s1 = part_of(pt[1], T);
+                s2 = part_of(pt[2], T);
+            } else {  // a power of two
+                const int i = (warp & ~((T >> 5) - 1)) + (lane & ((T >> 5) - 1));
+                s0 = pt[0][i];
+                s1 = pt[1][i];
+                s2 = pt[2][i];
+            }
+            for (int o = ROW == 160 ? 4 : T >> 6; o; o >>= 1) {
                 s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
                 s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
                 s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
@@ -755,14 +766,15 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs
     }
 }
 
-template <bool CLUSTER, bool RING_GATE, int ROW>
+template <bool CLUSTER, bool RING_GATE, bool FULL, int ROW>
 fp8q_status launch_backward(const RnBwdArgs& a, unsigned ctas, unsigned slices, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};
-    auto kern = residual_norm_backward_kernel<CLUSTER, RING_GATE, ROW>;
-    const size_t smem = ((RING_GATE ? 2 * 2 * (a.gate_bf16 ? 5 : 6) : 3 * 2 * 4) + 4) * 4096;
+    constexpr int block = ROW == 160 ? 160 : 256;
+    auto kern = residual_norm_backward_kernel<CLUSTER, RING_GATE, FULL, ROW>;
+    const size_t smem = ((RING_GATE ? 2 * 2 * (a.gate_bf16 ? 5 : 6) : 3 * 2 * 4) + 4) * block * 16;
     cudaError_t e = allow_smem(kern, 112 * 1024, devices);
     if (e != cudaSuccess) return cuda_fail(e, "residual_norm_backward_kernel setup");
-    return launch_behind(kern, dim3(ctas), dim3(256), smem, CLUSTER ? slices : 1, s, "residual_norm_backward_kernel", a);
+    return launch_behind(kern, dim3(ctas), dim3(block), smem, CLUSTER ? slices : 1, s, "residual_norm_backward_kernel", a);
 }
 
 template <int FMT>
@@ -927,26 +939,30 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     a.T = st.T;
     a.gate_bf16 = n->gate_is_bf16 != 0;
     a.alpha = n->alpha;
-    // slices of equal width, whole groups of four columns a thread
-    a.width = ((n->hidden + st.slices - 1) / st.slices + 15) / 16 * 16;
-    const int64_t per_cta = 256 / st.T;
+    a.width = st.width;
+    const int64_t per_cta = st.block / st.T;
     const unsigned ctas = (unsigned)((st.strips + per_cta - 1) / per_cta) * (unsigned)st.slices;
     const bool ring_gate = a.gate && a.per == 1;
     const unsigned slices = (unsigned)st.slices;
     // the call that a block's edge makes: everything there
     const bool full = a.b && a.post && a.dh && a.dro && a.dr && a.db;
     fp8q_status rc;
-    if (ring_gate)
-        rc = slices == 1 ? launch_backward<false, true, 0>(a, ctas, 1, s) : launch_backward<true, true, 0>(a, ctas, slices, s);
+    if (a.T == 160)
+        rc = ring_gate ? (slices == 1 ? launch_backward<false, true, false, 160>(a, ctas, 1, s) : launch_backward<true, true, false, 160>(a, ctas, slices, s))
+             : full    ? (slices == 1 ? launch_backward<false, false, true, 160>(a, ctas, 1, s) : launch_backward<true, false, true, 160>(a, ctas, slices, s))
+             : slices == 1 ? launch_backward<false, false, false, 160>(a, ctas, 1, s)
+                           : launch_backward<true, false, false, 160>(a, ctas, slices, s);
+    else if (ring_gate)
+        rc = slices == 1 ? launch_backward<false, true, false, 0>(a, ctas, 1, s) : launch_backward<true, true, false, 0>(a, ctas, slices, s);
     else if (slices > 1)
-        rc = full ? launch_backward<true, false, 256>(a, ctas, slices, s) : launch_backward<true, false, 0>(a, ctas, slices, s);
+        rc = full ? launch_backward<true, false, true, 256>(a, ctas, slices, s) : launch_backward<true, false, false, 0>(a, ctas, slices, s);
     else if (!full)
-        rc = launch_backward<false, false, 0>(a, ctas, 1, s);
+        rc = launch_backward<false, false, false, 0>(a, ctas, 1, s);
     else
-        rc = a.T == 32    ? launch_backward<false, false, 32>(a, ctas, 1, s)
-             : a.T == 64  ? launch_backward<false, false, 64>(a, ctas, 1, s)
-             : a.T == 128 ? launch_backward<false, false, 128>(a, ctas, 1, s)
-                          : launch_backward<false, false, 256>(a, ctas, 1, s);
+        rc = a.T == 32    ? launch_backward<false, false, true, 32>(a, ctas, 1, s)
+             : a.T == 64  ? launch_backward<false, false, true, 64>(a, ctas, 1, s)
+             : a.T == 128 ? launch_backward<false, false, true, 128>(a, ctas, 1, s)
+                          : launch_backward<false, false, true, 256>(a, ctas, 1, s);
     if (rc != FP8Q_OK || (!a.dpre && !a.dpost && !spread)) return rc;
     // rows of dgate to add up: those of a gate that spans strips, or the ones across their borders
     int64_t across = 0;

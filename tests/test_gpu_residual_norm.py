@@ -301,6 +301,29 @@ def test_backward_parts(dev, rows, H, parts):
         check_backward(dev, rows, H, 4, None, **parts)
 
 
+PARTS = [dict(), dict(block=False), dict(post=False), dict(pre=False)]
+
+
+@pytest.mark.parametrize("parts", PARTS)
+@pytest.mark.parametrize("rows,H", [(700, 1040), (1900, 2064), (1300, 2560), (900, 4624), (700, 5120), (500, 8208), (350, 10256)])
+def test_forward_rows_of_any_number_of_warps(dev, rows, H, parts):
+    """Rows that take other numbers of threads than a power of two, several rows a strip, and the call's parts."""
+    for fmt in (0, 3):
+        for per in (1, 100):
+            if parts.get("pre") is False and fmt:
+                continue
+            d = make(rows, H, per, None if parts.get("block") is False else "bf16", rows + per, dev)
+            o = forward(d, rows, H, per, 0.9, 1e-6, fmt=fmt, dev=dev, **parts)
+            check_forward(d, o, rows, H, per, 0.9, 1e-6, fmt, block=parts.get("block", True), post=parts.get("post", True))
+
+
+@pytest.mark.parametrize("parts", [dict(), dict(dh=False), dict(dro=False), dict(block=False), dict(post=False)])
+@pytest.mark.parametrize("rows,H", [(1000, 2064), (470, 2560), (300, 5120)])
+def test_backward_rows_of_five_warps(dev, rows, H, parts):
+    for per in (1, 3, 90):
+        check_backward(dev, rows, H, per, None if parts.get("block") is False else "f32", alpha=-0.8, **parts)
+
+
 def test_backward_against_differences(dev):
     """The formula's own check: central differences of the float64 forward along random directions."""
     rows, H, per, alpha, eps = 6, 64, 2, 0.7, 1e-6
