@@ -14,8 +14,8 @@
 //   dg2 = sum dh n2, dg1 = sum alpha gate D n1, dgate = sum alpha D n1 g1.
 //
 // Both kernels stream HBM.  Rows are dealt out in strips of consecutive rows, a
-// strip to each T threads; a thread has 16 (or 32) columns of a row, in groups of
-// eight, and brings the next rows of its strip into shared memory by asynchronous
+// strip to each T threads, whole warps; a thread has 16 (or 32) columns of a row,
+// in groups of eight, and brings the next rows of its strip into shared memory by asynchronous
 // copies of its own (it alone reads them, so they need no barrier), while the
 // weights of its columns stay in shared memory (forward) or registers (backward).
 //
