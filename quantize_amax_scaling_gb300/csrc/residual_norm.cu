@@ -714,16 +714,18 @@ __global__ void __launch_bounds__(ROW == 160 ? 160 : 256, ROW == 160 ? 3 : 2) re
     if (CLUSTER) cg::this_cluster().sync();  // nobody's `sums` goes away while another CTA may write it
 }
 
-// 128 columns a CTA, four a thread, 32 strips at a time: blockIdx.y 0 adds dpre, 1
-// dpost, and from 2 on a row of dgate that lies in several strips: row blockIdx.y -
-// 2, where gates span strips, or else the one across the border behind strip
-// blockIdx.y - 2.
+// COLS columns a CTA, four a lane, 32 warps of 128 / COLS strips at a time: blockIdx.y 0 adds dpre, 1 dpost, and from 2
+// on a row of dgate that lies in several strips: row blockIdx.y - 2, where gates span strips, or else the one across the
+// border behind strip blockIdx.y - 2.  (32 columns a CTA where 128 would leave most SMs idle: 777x1552 13.1 us for the
+// call, 15.1 by 128; 8192x1024 29.6 and 33.7; wider rows and many gates by 128: 8192x4096 77.2 us, 80 by 32.)
+template <int COLS>
 __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs a) {
-    __shared__ float4 part[32][32];
+    constexpr int kLanes = COLS / 4, kStrips = 32 / kLanes;  // a warp's
+    __shared__ float4 part[32][kLanes];
     // launched while the kernel that writes the strips still runs: nothing is read before it has ended
     wait_behind();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int col = blockIdx.x * 128 + lane * 4;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = lane % kLanes, sub = lane / kLanes;
+    const int col = blockIdx.x * COLS + c * 4;
     const int what = blockIdx.y;
     int64_t group = 0, s0 = 0, s1 = a.strips - 1;
     const float* from = a.space + what * a.strips * a.H + col;
@@ -739,22 +741,28 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs
         step = 2 * a.H;
     }
     float4 v = make_float4(0, 0, 0, 0);
+    auto add = [&v](const float4& x) { v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w; };
+    auto across = [&] {  // the lanes of one column
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1)
+            add(make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o),
+                            __shfl_xor_sync(0xFFFFFFFFu, v.z, o), __shfl_xor_sync(0xFFFFFFFFu, v.w, o)));
+    };
     if (col < a.H) {
 #pragma unroll 8
-        for (int64_t s = s0 + w; s <= s1; s += 32) {
+        for (int64_t s = s0 + w * kStrips + sub; s <= s1; s += 32 * kStrips)
             // a group's first rows are the tail of strip s0, the rest the heads of those that follow
-            const float4 x = *reinterpret_cast<const float4*>(from + s * step + (what >= 2 && s == s0 ? a.H : 0));
-            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-        }
+            add(*reinterpret_cast<const float4*>(from + s * step + (what >= 2 && s == s0 ? a.H : 0)));
     }
-    part[w][lane] = v;
+    across();
+    if (sub == 0) part[w][c] = v;
     __syncthreads();
-    if (w == 0 && col < a.H) {
+    if (w > 0) return;
+    v = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 1; i < 32; ++i) {
-            const float4 x = part[i][lane];
-            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-        }
+    for (int i = 0; i < kLanes; ++i) add(part[sub * kLanes + i][c]);
+    across();
+    if (sub == 0 && col < a.H) {
         if (what == 0)
             *reinterpret_cast<float4*>(a.dpre + col) = v;
         else if (what == 1)
@@ -764,6 +772,14 @@ __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs
         else
             *reinterpret_cast<float4*>(static_cast<float*>(a.dgate) + group * a.H + col) = v;
     }
+}
+
+// The strips' sums, with `across` rows of dgate.
+fp8q_status launch_sums(const RnBwdArgs& a, int64_t across, cudaStream_t s) {
+    const int cols = a.H <= 2048 && across <= 4 ? 32 : 128;
+    return launch_behind(cols == 32 ? residual_norm_sum_kernel<32> : residual_norm_sum_kernel<128>,
+                         dim3((unsigned)((a.H + cols - 1) / cols), (unsigned)(2 + across)), dim3(1024), 0, 1, s,
+                         "residual_norm_sum_kernel", a);
 }
 
 template <bool CLUSTER, bool RING_GATE, bool FULL, int ROW>
@@ -898,8 +914,7 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
         none.dpre = n->d_pre_weight;
         none.dpost = n->d_post_weight;
         none.H = n->hidden;
-        return launch_behind(residual_norm_sum_kernel, dim3((unsigned)((n->hidden + 127) / 128), 2), dim3(1024), 0, 1, s,
-                             "residual_norm_sum_kernel", none);
+        return launch_sums(none, 0, s);
     }
     if (!n->d_residual_out && !n->d_h) return FP8Q_ERR_INVALID_ARG;
     if (n->d_h ? (!n->residual_out || !n->rstd_pre || !n->pre_weight) : (n->pre_weight || n->d_pre_weight != nullptr))
@@ -968,8 +983,7 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     int64_t across = 0;
     if (spread && st.strips > 1 && st.per_strip % a.per != 0)
         across = a.per >= st.per_strip ? (a.rows + a.per - 1) / a.per : st.strips - 1;
-    const dim3 grid((unsigned)((n->hidden + 127) / 128), (unsigned)(2 + across));
-    return launch_behind(residual_norm_sum_kernel, grid, dim3(1024), 0, 1, s, "residual_norm_sum_kernel", a);
+    return launch_sums(a, across, s);
 }
 
 }  // extern "C"
