@@ -732,7 +732,10 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     g.vec = ((uintptr_t)d & 15u) == 0 && n % (F32 ? 4 : 8) == 0;
     // Pairs of CTAs where 128-row tiles of one CTA each would not all be resident at once.
     const int sms = sm_count();
-    const bool pairs = m > 128 && n > 128 && (m + 127) / 128 * ((n + 127) / 128) > sms;
+    // (Odd rows of bf16, which a pair stores slowly at the end, stay with single CTAs where both tiles and steps are few:
+    // 1033x2071x1000 7.5 us, 10.2 on pairs; 2560x2561x1000 14.4 and 16.7, but 2560x2561x4096 25.5 and 22.6.)
+    const int64_t blocks = (m + 127) / 128 * ((n + 127) / 128);
+    const bool pairs = m > 128 && n > 128 && blocks > sms && (F32 || n % 2 == 0 || blocks > 3 * sms || g.ksteps >= 32);
     // Otherwise the CTAs of a cluster share a tile's sums, as many as are resident at once (two an SM up to 32 rows of Q;
     // clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and have two steps or more, where the steps that a CTA
     // saves are worth the cluster and its sums, 1 us for 16 rows of Q to 2.5 for 128, a step 0.3: 1x4096x4096

@@ -229,6 +229,13 @@ def test_matmul_exact_sums(dev, m, n, k, fmt):
 
 
 @pytest.mark.parametrize("fmt", [R.MXFP4, R.NVFP4])
+@pytest.mark.parametrize("m,n,k", [(1100, 2305, 2100), (2600, 2571, 100), (2600, 2701, 100), (2600, 2574, 100)])
+def test_matmul_odd_rows(dev, m, n, k, fmt):
+    """Rows of D that start anywhere, on single CTAs and on pairs."""
+    test_matmul(dev, m, n, k, fmt)
+
+
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.NVFP4])
 @pytest.mark.parametrize("m,n,k", [(2, 9800, 8192), (16, 4097, 2048), (9, 300, 4100), (24, 9800, 8200), (24, 6000, 4097), (30, 335, 16384),
                                    (64, 8200, 4200), (64, 4097, 3000), (60, 1001, 8200), (256, 4096, 8192), (128, 4097, 4096),
                                    (300, 1000, 4096), (128, 1024, 8192), (100, 333, 4100)])
