@@ -44,7 +44,24 @@ struct MmArgs {
     int32_t split;       // CTAs (of one cluster) that share a tile's k
     int32_t p_is_m;      // P's rows are D's rows
     int32_t vec;         // D's rows hold 16-byte groups
+#ifdef FP8Q_TEST_HOOKS
+    int32_t fail_role, fail_at, fail_cta;  // the wait that reports failure although what it waits for has come
+#endif
 };
+
+// The waits, by who waits for what; a test makes one of them run out.
+enum MmWait { kNoWait, kCopyEmpty, kSumFull, kSumScaled, kScaleFull, kOutDone, kScaleCopyEmpty, kSumDrained };
+__device__ __forceinline__ bool made_to_fail(const MmArgs& a, MmWait role, uint32_t at) {
+#ifdef FP8Q_TEST_HOOKS
+    return a.fail_role == role && a.fail_at == (int)at && (a.fail_cta < 0 || a.fail_cta == (int)blockIdx.x);
+#else
+    return false;
+#endif
+}
+// One wait of a whole warp, with one verdict.
+__device__ __forceinline__ bool wait_of(const MmArgs& a, MmWait role, uint32_t at, uint64_t* bar, uint32_t parity) {
+    return mbar_wait_all(bar, parity, made_to_fail(a, role, at) && (threadIdx.x & 31) == 5);
+}
 
 template <int FMT, int BN>
 struct MmGeom {
@@ -174,7 +191,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
         uint32_t st = 0, round = 0, n = 0;
         bool ok = true;
         for (int s = s0; s < s1; ++s, ++n) {
-            if (!mbar_wait(&empty[st], (round & 1) ^ 1)) {
+            if (!wait_of(a, kCopyEmpty, n, &empty[st], (round & 1) ^ 1)) {
                 ok = false;
                 break;
             }
@@ -191,7 +208,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
             if (++st == kStages) st = 0, ++round;
         }
         // the tensor core's last arrivals land before the CTA may go
-        for (uint32_t i = n > kStages ? n - kStages : 0; i < n && ok; ++i) ok = mbar_wait(&empty[i % kStages], (i / kStages) & 1);
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n && ok; ++i) ok = mbar_wait_all(&empty[i % kStages], (i / kStages) & 1);
         if (lane == 0) {
             if (!ok) gave_up = 1;
             loads = n;
@@ -200,7 +217,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
         uint32_t st = 0, round = 0;
         bool ok = true;
         for (int s = s0; s < s1; ++s) {
-            if (!mbar_wait(&full[st], round & 1) || !mbar_wait(&scaled[st], round & 1)) {
+            if (!wait_of(a, kSumFull, s - s0, &full[st], round & 1) || !wait_of(a, kSumScaled, s - s0, &scaled[st], round & 1)) {
                 ok = false;
                 break;
             }
@@ -232,7 +249,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
         uint32_t st = 0, round = 0;
         bool ok = true;
         for (int s = s0; s < s1; ++s) {
-            if (!mbar_wait(&full[st], round & 1)) {
+            if (!wait_of(a, kScaleFull, s - s0, &full[st], round & 1)) {
                 ok = false;
                 break;
             }
@@ -248,7 +265,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
             if (lane == 0) arrive_local(&scaled[st]);
             if (++st == kStages) st = 0, ++round;
         }
-        if (!mbar_wait_warp(&done, 0, 0) || !ok) gave_up = 1;
+        if (!mbar_wait_warp(&done, 0, 0) || made_to_fail(a, kOutDone, 0) || !ok) gave_up = 1;
     }
     __syncwarp();
     __syncthreads();
@@ -425,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
             const PairTile t = pair_tile(tile, p_tiles, a.q_tiles);
             const int p0 = t.p + (int)rank * 128, q0 = t.q + (int)rank * 128;
             for (int s = 0; s < steps; ++s, ++n) {
-                if (!mbar_wait(&empty[st], (round & 1) ^ 1)) {
+                if (!wait_of(a, kCopyEmpty, n, &empty[st], (round & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
@@ -442,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         // The tensor cores' last arrivals land before this CTA may go.
         for (uint32_t i = 0; i < kPairStages && i < n && ok; ++i) {
             st = st ? st - 1 : kPairStages - 1;
-            ok = mbar_wait(&empty[st], ((n - 1 - i) / kPairStages) & 1);
+            ok = mbar_wait_all(&empty[st], ((n - 1 - i) / kPairStages) & 1);
         }
         if (lane == 0) {
             if (!ok) gave_up = 1;
@@ -454,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride) {
             const PairTile t = pair_tile(tile, p_tiles, a.q_tiles);
             for (int s = 0; s < steps; ++s, ++n) {
-                if (!mbar_wait(&empty[st], (round & 1) ^ 1)) {
+                if (!wait_of(a, kScaleCopyEmpty, n, &empty[st], (round & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
@@ -477,12 +494,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
             uint32_t st = 0, round = 0, it = 0;
             bool ok = true;
             for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += stride, ++it) {
-                if (it > 0 && !mbar_wait(&drained, (it - 1) & 1)) {
+                if (it > 0 && !wait_of(a, kSumDrained, it, &drained, (it - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 for (int s = 0; s < steps; ++s) {
-                    if (!mbar_wait(&full[st], round & 1)) {
+                    if (!wait_of(a, kSumFull, it * steps + s, &full[st], round & 1)) {
                         ok = false;
                         break;
                     }
@@ -508,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                 }
             }
             // The other CTA's last arrivals land before this one may go.
-            if (ok && it > 0) ok = mbar_wait(&drained, (it - 1) & 1);
+            if (ok && it > 0) ok = mbar_wait_all(&drained, (it - 1) & 1);
             if (!ok && elect_lane()) {
                 tc_commit_pair(&done, 3);
                 gave_up = 1;
@@ -526,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                 if ((n & 1) == group) {
                     // The stage's last round went to the other group; its use has to be over before a
                     // parity tells this round's scales from the last but one's.
-                    if (!mbar_wait(&empty[st], (round & 1) ^ 1) || !mbar_wait(&sf_full[st], round & 1)) {
+                    if (!mbar_wait_all(&empty[st], (round & 1) ^ 1) || !wait_of(a, kScaleFull, n, &sf_full[st], round & 1)) {
                         ok = false;
                         break;
                     }
@@ -559,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
             const PairTile t = pair_tile(tile, p_tiles, a.q_tiles);
             const int p_first = t.p + (int)rank * 128 + (warp & 3) * 32;
             const int q = t.q + (warp >> 2) * 128, left = a.q_rows - q;
-            ok = ok && mbar_wait_warp(&done, it & 1, 32);
+            ok = ok && mbar_wait_warp(&done, it & 1, 32) && !made_to_fail(a, kOutDone, it);
             if (!ok) gave_up = 1;
             tc_fence_after();
 #pragma unroll
@@ -719,10 +736,19 @@ fp8q_status launch_pairs(const uint8_t* p, const uint8_t* q, int64_t k, MmArgs g
     return launch_behind(kern, dim3(grid), dim3(kPairThreads), G::kSmem, 1, s, "fp4_matmul_pair_kernel", mp, mq, ms, mt, md, g);
 }
 
+#ifdef FP8Q_TEST_HOOKS
+int g_fail_role = 0, g_fail_at = 0, g_fail_cta = -1;
+#endif
+
 template <int FMT, bool F32>
 fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, void* d, int64_t m, int64_t n, int64_t k,
                    const float* sa, const float* sb, cudaStream_t s) {
     MmArgs g;
+#ifdef FP8Q_TEST_HOOKS
+    g.fail_role = g_fail_role;
+    g.fail_at = g_fail_at;
+    g.fail_cta = g_fail_cta;
+#endif
     g.sa = sa;
     g.sb = sb;
     g.d = d;
@@ -779,6 +805,14 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
 }  // namespace
 
 extern "C" {
+
+#ifdef FP8Q_TEST_HOOKS  // the wait of that role (MmWait) at that step or tile reports failure, in one CTA or (cta < 0) in all
+void fp8q_test_set_matmul_give_up(int role, int at, int cta) {
+    g_fail_role = role;
+    g_fail_at = at;
+    g_fail_cta = cta;
+}
+#endif
 
 fp8q_status fp8q_fp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf, void* d,
                             int64_t m, int64_t n, int64_t k, fp8q_format fmt, fp8q_out_type out, const float* a_scale,

@@ -17,24 +17,21 @@ namespace {
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t pause) {
     uint32_t ok = 0;
     if ((threadIdx.x & 31) == 0) {
-        const uint32_t at = smem_addr(bar);
-        uint64_t t0 = 0;
-        for (;;) {
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(ok)
-                : "r"(at), "r"(parity)
-                : "memory");
-            if (ok) break;
+        WaitClock clock;
+        while (!(ok = mbar_try(bar, parity))) {
+            if (!clock.more()) break;
             if (pause) __nanosleep(pause);
-            const uint64_t t = global_ns();
-            if (t0 == 0) t0 = t;
-            else if (t - t0 > kWaitLimitNs) break;
         }
     }
     return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
+// mbar_wait() where each lane looks, with one verdict for the warp: every lane's
+// clock runs out for itself, and a warp of which some lanes went on and some
+// left would never come together again at the warp-wide instructions behind
+// the wait (elect, the .aligned ones of tensor memory).
+__device__ __forceinline__ bool mbar_wait_all(uint64_t* bar, uint32_t parity, bool fail_lane = false) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity) && !fail_lane);
 }
 
 // One lane of a converged warp.  The warps that issue copies and multiply-adds
@@ -208,6 +205,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
+    __syncwarp();  // the barrier is a warp's instruction: its lanes may come from loops of unlike lengths
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
