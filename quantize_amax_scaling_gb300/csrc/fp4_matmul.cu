@@ -399,8 +399,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     using G = PairGeom<FMT>;
     extern __shared__ uint8_t raw[];
     // full: the codes of a stage are there in both CTAs and its scales in both tensor memories (the first CTA's counts);
-    // sf_full: this CTA's scales are in shared memory; empty: the stage has been used
-    __shared__ uint64_t full[kPairStages], sf_full[kPairStages], empty[kPairStages], done, drained;
+    // sf_full: this CTA's scales are in shared memory; empty: the stage has been used; done: a tile's sums are
+    // complete; stopped: the multiply-adds of an issuer that gave up have ended
+    __shared__ uint64_t full[kPairStages], sf_full[kPairStages], empty[kPairStages], done, drained, stopped;
     __shared__ uint32_t tmem_slot, loads, sf_loads;
     __shared__ int gave_up;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -421,6 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
             mbar_init(&empty[i]);
         }
         mbar_init(&done);
+        mbar_init(&stopped);
         mbar_init_count(&drained, 16);
         loads = sf_loads = 0;
         gave_up = 0;
@@ -526,9 +528,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
             }
             // The other CTA's last arrivals land before this one may go.
             if (ok && it > 0) ok = mbar_wait_all(&drained, (it - 1) & 1);
-            if (!ok && elect_lane()) {
-                tc_commit_pair(&done, 3);
-                gave_up = 1;
+            // An unfinished tile is never announced as done: those who carry results out run out of time in their
+            // turn, in both CTAs, and write NaN.
+            if (!ok) {
+                if (elect_lane()) {
+                    tc_commit_pair(&stopped, 1);
+                    gave_up = 1;
+                }
+                __syncwarp();
+                mbar_wait_all(&stopped, 0);
             }
         }
     } else if (warp >= 10) {

@@ -74,3 +74,20 @@ def test_single_ctas(hooked, dev, m, n, k, role, at, fmt):
     assert check(hooked, dev, m, n, k, fmt, torch.bfloat16, role, at, -1).all()
     lost = check(hooked, dev, m, n, k, fmt, torch.float32, role, at, 1)  # one CTA of them: its tile
     assert lost.any() and int(lost.sum()) <= 128 * 128
+
+
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.NVFP4])
+@pytest.mark.parametrize("role,at", [(COPY_EMPTY, 0), (COPY_EMPTY, 7), (SCALE_COPY_EMPTY, 0), (SCALE_COPY_EMPTY, 3), (SUM_FULL, 0), (SUM_FULL, 1),
+                                     (SUM_FULL, 6), (SUM_FULL, 9), (SCALE_FULL, 0), (SCALE_FULL, 5), (SUM_DRAINED, 1), (OUT_DONE, 0),
+                                     (OUT_DONE, 1)])
+@pytest.mark.parametrize("m,n,k", [(2560, 2304, 1100), (2700, 2751, 1100)])
+def test_pairs(hooked, dev, m, n, k, role, at, fmt):
+    """Pairs of CTAs, the first of which take two tiles of 256 x 256, 5 steps each: what a pair had not
+    finished when it gave up is NaN, also where sums of a part of k were there."""
+    for dtype, cta in ((torch.bfloat16, -1), (torch.float32, 0), (torch.bfloat16, 1)):
+        if cta == 1 and role in (SUM_FULL, SUM_DRAINED):
+            continue  # the first CTA of a pair issues for both
+        lost = check(hooked, dev, m, n, k, fmt, dtype, role, at, cta)
+        assert lost.any() and (cta < 0 or int(lost.sum()) <= 2 * 256 * 256)
+        if role == SUM_FULL and cta == 0 and at < k // 256:  # in the pair's first tile
+            assert lost[:256, :256].all()
