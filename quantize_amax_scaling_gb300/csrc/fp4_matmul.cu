@@ -274,6 +274,11 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     // A wait that ran out (correct operation never gets there) shows as NaN in the whole tile.
     const float nan = __uint_as_float(0x7FFFFFFFu);
     const int bad = gave_up;
+    if (bad) {  // copies still under way end before the CTA does, and before sums (and NaN) lie where they go
+        if (threadIdx.x == 0)
+            for (uint32_t n = loads > kStages ? loads - kStages : 0; n < loads; ++n) mbar_wait(&full[n % kStages], (n / kStages) & 1);
+        __syncthreads();
+    }
     if (a.split == 1) {
         if (warp < 4) {
             const int p = p0 + warp * 32 + lane;
@@ -319,8 +324,6 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
         }
         cluster_sync_all();  // no CTA's sums go away while another reads them
     }
-    if (bad && threadIdx.x == 0)  // copies still under way end before the CTA does
-        for (uint32_t n = loads > kStages ? loads - kStages : 0; n < loads; ++n) mbar_wait(&full[n % kStages], (n / kStages) & 1);
     tc_fence_before();
     __syncthreads();
     if (warp == 5) tmem_free<1>(tmem, G::kCols);
