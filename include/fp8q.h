@@ -424,7 +424,9 @@ fp8q_status fp8q_fp4_matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t
  *   h  = bf16(r' / sqrt(mean(r'^2) + eps) * pre_weight)    of the rounded r'
  *   q  = the codes of h in fmt, exactly those of fp8q_quantize_amax or
  *        fp8q_fp4_quantize_amax;  *amax = max(*amax, max|h|)
- * A NaN, or an infinity where it is normalised, makes its row NaN.  Any part
+ * A norm of a row that holds a NaN or an infinity, or whose sum of squares is
+ * beyond binary32 (an element of 2^64 is enough), is NaN in every column: y, and
+ * so r', for such a row of block (with post_weight); h for one of r'.  Any part
  * may be left out by NULL: block (then no post_weight and gate), post_weight,
  * gate (1), residual_out (without block only), pre_weight (then no h, q and
  * amax), h or q (one of them with pre_weight), sf (FP8 formats), scale (NULL

@@ -153,11 +153,13 @@ __device__ __forceinline__ float row_sum(float v, int T, float* part) {
 
 // 1 / sqrt(v): the hardware's approximation and one Newton step (a relative error
 // of 2^-22 goes to 1.5 times its square, so the roundings remain: 3 u at most).
+// NaN for an infinite mean (an infinity in the row, or squares beyond binary32):
+// a factor of 0 would pass off every finite element of such a row as a zero.
 __device__ __forceinline__ float inv_sqrt(float v) {
     float y;
     asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(v));
     const float z = fmaf(y, fmaf(-0.5f * v * y, y, 0.5f), y);
-    return v > 0x1p-126f && v < 3.4e38f ? z : __frcp_rn(__fsqrt_rn(v));
+    return v > 0x1p-126f && v < 3.4e38f ? z : __frcp_rn(__fsqrt_rn(v)) + (v - v);
 }
 
 // Codes of eight columns of h, a warp together, as fp8q_quantize_amax or
