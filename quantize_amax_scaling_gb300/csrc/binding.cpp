@@ -149,7 +149,7 @@ void packed(const at::Tensor* q, const at::Tensor* sf, int64_t rows, int64_t col
 void gate_rows(const at::Tensor* gate, int64_t rows, int64_t hidden, int64_t per) {
     if (!gate) return;
     if (per < 1) Args::refuse("%s must be at least 1", "rows_per_gate");
-    const int64_t groups = (rows + per - 1) / per;
+    const int64_t groups = rows > 0 ? (rows - 1) / per + 1 : 0;
     if (gate->numel() == groups * hidden) return;
     PyErr_Format(PyExc_ValueError, "gate must be [%lld, %lld]", (long long)groups, (long long)hidden);
     throw Refused();

@@ -35,6 +35,7 @@
 namespace {
 
 constexpr int kRnMaxH = 32768;
+constexpr int64_t kAllRows = 1ll << 32;  // more rows than there may be: rows a gate's row, held there, add up within 64 bits
 constexpr int kOutNone = -1;  // no codes wanted
 
 struct RnArgs {
@@ -949,7 +950,7 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     a.dgate = n->d_gate;
     a.space = static_cast<float*>(n->workspace);
     a.rows = n->rows;
-    a.per = n->rows_per_gate;
+    a.per = n->rows_per_gate < kAllRows ? n->rows_per_gate : kAllRows;
     a.per_strip = st.per_strip;
     a.strips = st.strips;
     a.H = n->hidden;
@@ -984,7 +985,7 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     // rows of dgate to add up: those of a gate that spans strips, or the ones across their borders
     int64_t across = 0;
     if (spread && st.strips > 1 && st.per_strip % a.per != 0)
-        across = a.per >= st.per_strip ? (a.rows + a.per - 1) / a.per : st.strips - 1;
+        across = a.per >= st.per_strip ? (a.rows - 1) / a.per + 1 : st.strips - 1;
     return launch_sums(a, across, s);
 }
 
