@@ -348,7 +348,8 @@ fp8q_status fp8q_amax_scale_update_ring_quantize(float* amax_history, const int3
  *           block % 4.  A row's blocks are filled up to a multiple of 4 with
  *           zero scales; rows that fill up the last tile are neither written
  *           nor used.
- * Both arrays start on 16-byte boundaries.
+ * Both arrays start on 16-byte boundaries.  The two functions give 0 for sizes
+ * that the calls refuse.
  */
 int64_t fp8q_fp4_row_bytes(int64_t cols);
 int64_t fp8q_fp4_scale_bytes(int64_t rows, int64_t cols, fp8q_format fmt);
@@ -505,7 +506,7 @@ typedef struct {
 
 /* Bytes of workspace (16-byte aligned, contents irrelevant) for the gradients
  * of weights and of a gate that rows share; one call at a time may use it.
- * rows_per_gate: 0 without gate. */
+ * rows_per_gate: 0 without gate.  0 for sizes that the call refuses. */
 int64_t fp8q_residual_norm_backward_workspace(int64_t rows, int32_t hidden, int64_t rows_per_gate);
 
 /*

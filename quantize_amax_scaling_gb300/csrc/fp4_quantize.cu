@@ -457,10 +457,10 @@ unsigned tile_grid(int64_t rows, int64_t cols, int64_t tile_rows = kTile) {
 
 extern "C" {
 
-int64_t fp8q_fp4_row_bytes(int64_t cols) { return cols > 0 ? fp4_row_bytes(cols) : 0; }
+int64_t fp8q_fp4_row_bytes(int64_t cols) { return cols > 0 && cols <= kFp4MaxDim ? fp4_row_bytes(cols) : 0; }
 
 int64_t fp8q_fp4_scale_bytes(int64_t rows, int64_t cols, fp8q_format fmt) {
-    if (rows <= 0 || cols <= 0 || !valid_fp4(fmt)) return 0;
+    if (rows <= 0 || cols <= 0 || rows > kFp4MaxDim || cols > kFp4MaxDim || !valid_fp4(fmt)) return 0;
     return (rows + 127) / 128 * (fmt == FP8Q_MXFP4 ? fp4_sf_tiles<FP8Q_MXFP4>(cols) : fp4_sf_tiles<FP8Q_NVFP4>(cols)) * 512;
 }
 

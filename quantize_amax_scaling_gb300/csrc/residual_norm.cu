@@ -901,7 +901,7 @@ fp8q_status fp8q_residual_norm_quantize_amax(const fp8q_residual_norm* n, void* 
 }
 
 int64_t fp8q_residual_norm_backward_workspace(int64_t rows, int32_t hidden, int64_t rows_per_gate) {
-    if (rows <= 0 || hidden <= 0) return 0;
+    if (rows <= 0 || hidden <= 0 || rows > kFp4MaxDim || hidden > kRnMaxH) return 0;
     const RnStrips st = rn_strips(rows, hidden);
     return (rows_per_gate > 1 ? 4 : 2) * st.strips * hidden * (int64_t)sizeof(float);
 }
