@@ -327,8 +327,10 @@ PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
             v[i] = n == 3 ? PyLong_AsLongLong(a[i]) : -1;
             if (v[i] == -1 && PyErr_Occurred()) return nullptr;
         }
-        if (n != 3 || v[0] < 0 || v[1] < 0 || !four_bits(v[2])) {
-            PyErr_SetString(PyExc_ValueError, "fp4_empty takes rows, cols >= 0 and MXFP4 or NVFP4");
+        // beyond what the calls take, the bytes of both arrays could pass 64 bits and come out as few
+        constexpr int64_t kMax = 0x7FFFFC00;
+        if (n != 3 || v[0] < 0 || v[1] < 0 || v[0] > kMax || v[1] > kMax || !four_bits(v[2])) {
+            PyErr_SetString(PyExc_ValueError, "fp4_empty takes rows and cols from 0 to 2^31 - 1024 and MXFP4 or NVFP4");
             return nullptr;
         }
         const auto o = at::TensorOptions().dtype(at::kByte).device(at::kCUDA, c10::cuda::current_device());

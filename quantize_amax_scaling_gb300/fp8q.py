@@ -401,6 +401,9 @@ def fp8q_amax_scale_update_ring_quantize(history, head_in, head_out, amax_new, s
         "fp8q_amax_scale_update_ring_quantize")
 
 
+_FP4_MAX_DIM = 2 ** 31 - 1024  # rows and columns of a packed operand
+
+
 def fp4_row_bytes(cols):
     """Bytes of a row's codes in a packed 4-bit operand: two codes a byte, rows of whole 32-column groups."""
     return (cols + 31) // 32 * 16
@@ -417,8 +420,8 @@ def fp4_empty(rows, cols, fmt, device="cuda"):
     if device == "cuda":
         return _native().fp4_empty(rows, cols, fmt)
     import torch
-    if fmt not in (MXFP4, NVFP4):
-        raise ValueError("fmt must be MXFP4 or NVFP4")
+    if not (0 <= rows <= _FP4_MAX_DIM and 0 <= cols <= _FP4_MAX_DIM) or fmt not in (MXFP4, NVFP4):
+        raise ValueError("fp4_empty takes rows and cols from 0 to 2^31 - 1024 and MXFP4 or NVFP4")
     return (torch.empty((rows, fp4_row_bytes(cols)), dtype=torch.uint8, device=device),
             torch.empty(fp4_scale_bytes(rows, cols, fmt), dtype=torch.uint8, device=device))
 

@@ -4,6 +4,8 @@ import ctypes
 import subprocess
 import sys
 
+import pytest
+
 from conftest import ROOT
 
 TOP = 2 ** 31 - 1024  # the most rows and columns of an operand, the most rows of a norm
@@ -38,3 +40,16 @@ print("OK")
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.endswith("OK\n"), (r.returncode, r.stdout + r.stderr)
+
+
+def test_room_of_refused_sizes():
+    """fp4_empty says no before it asks for memory: of 2^53 rows of 2^15 columns both arrays' bytes are 0 modulo 2^64."""
+    from quantize_amax_scaling_gb300 import build, fp8q
+    build.build()
+    for device in ("cuda", "cpu"):
+        for rows, cols in ((2 ** 53, 2 ** 15), (TOP + 1, 16), (16, TOP + 1), (-1, 16), (16, -1)):
+            for fmt in (fp8q.MXFP4, fp8q.NVFP4):
+                with pytest.raises(ValueError, match="rows and cols"):
+                    fp8q.fp4_empty(rows, cols, fmt, device=device)
+        with pytest.raises(ValueError):
+            fp8q.fp4_empty(4, 64, fp8q.E4M3FN, device=device)
