@@ -1,9 +1,10 @@
 """Compile libfp8q.so (the CUDA kernels and their C ABI) for sm_103a, in tree.
 
 Translation units compiled in parallel with one -gencode each, then linked; no
-cmake.  Beside it the compiled part of the Python binding (csrc/binding.cpp, g++
-against torch's headers).  Both and their objects are written next to this file
-and git-ignored.
+cmake.  The library needs nothing else.  Beside it, where torch is there, the
+compiled part of the Python binding (csrc/binding.cpp, g++ against torch's
+headers).  Both and their objects are written next to this file and
+git-ignored.
 """
 import os
 import shutil
@@ -22,6 +23,7 @@ LIB = os.path.join(PKG, "libfp8q.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_DEPS = [BINDING_SRC, os.path.join(ROOT, "include", "fp8q.h")]
 BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,12 +47,24 @@ def nvcc_path() -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build libfp8q.so and the binding's compiled part if missing or older than their sources;
-    return the library's path."""
-    deps = DEPS + [BINDING_SRC]
-    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
-        if min(os.path.getmtime(LIB), os.path.getmtime(BINDING)) >= max(os.path.getmtime(p) for p in deps):
-            return LIB
+    """Build what is missing or older than its sources: libfp8q.so, and the binding's compiled part
+    where torch can be imported.  Return the library's path.  The library is made whatever becomes of the binding."""
+    with ThreadPoolExecutor(1) as ex:
+        binding = None
+        if force or not _current(BINDING, BINDING_DEPS):
+            binding = ex.submit(build_binding)
+        if force or not _current(LIB, DEPS):
+            _build_library(verbose)
+        if binding is not None:
+            binding.result()
+    return LIB
+
+
+def _current(path, deps) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= max(os.path.getmtime(p) for p in deps)
+
+
+def _build_library(verbose: bool) -> None:
     os.makedirs(OBJ_DIR, exist_ok=True)
     nvcc = nvcc_path()
     tag = f".{os.getpid()}"
@@ -63,23 +77,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.run(cmd, check=True)
         return obj
 
-    with ThreadPoolExecutor(len(SRCS) + 1) as ex:
-        binding = ex.submit(build_binding)
+    with ThreadPoolExecutor(len(SRCS)) as ex:
         objs = list(ex.map(compile_one, SRCS))
-        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
     for o in objs:
         os.remove(o)
-    return LIB
 
 
-def build_binding() -> str:
-    """Compile _binding.so (host code; g++, torch's headers) for the running Python and torch."""
+def build_binding():
+    """Compile _binding.so (host code; g++, torch's headers) for the running Python and torch; None without torch."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     home = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
