@@ -7,6 +7,7 @@ headers).  Both and their objects are written next to this file and
 git-ignored.
 """
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -23,6 +24,7 @@ LIB = os.path.join(PKG, "libfp8q.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_FOR = os.path.join(OBJ_DIR, "binding_for.txt")  # the Python and torch that _binding.so was made for
 BINDING_DEPS = [BINDING_SRC, os.path.join(ROOT, "include", "fp8q.h")]
 BINDING = os.path.join(PKG, "_binding.so")
 
@@ -51,13 +53,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
     where torch can be imported.  Return the library's path.  The library is made whatever becomes of the binding."""
     with ThreadPoolExecutor(1) as ex:
         binding = None
-        if force or not _current(BINDING, BINDING_DEPS):
+        if force or not _current(BINDING, BINDING_DEPS) or binding_for() not in (None, binding_made_for()):
             binding = ex.submit(build_binding)
         if force or not _current(LIB, DEPS):
             _build_library(verbose)
         if binding is not None:
             binding.result()
     return LIB
+
+
+def binding_for():
+    """The running Python and torch, whose compiled interfaces the binding uses; None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"{sys.implementation.cache_tag} ({platform.machine()}), torch {torch.__version__}"
+
+
+def binding_made_for():
+    """What binding_for() was when the binding was made; None if there is none."""
+    try:
+        with open(BINDING_FOR) as f:
+            return f.read() if os.path.exists(BINDING) else None
+    except OSError:
+        return None
 
 
 def _current(path, deps) -> bool:
@@ -90,10 +110,11 @@ def build_binding():
     """Compile _binding.so (host code; g++, torch's headers) for the running Python and torch; None without torch."""
     import sysconfig
 
-    try:
-        import torch
-    except ImportError:
+    made_for = binding_for()
+    if made_for is None:
         return None
+    import torch
+    os.makedirs(OBJ_DIR, exist_ok=True)
     home = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
@@ -104,7 +125,13 @@ def build_binding():
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc),
                     "-o", tmp, BINDING_SRC, f"-L{libs}", f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
                     "-ltorch_python"], check=True)
+    if os.path.exists(BINDING_FOR):  # never beside a binding that it is not true of
+        os.remove(BINDING_FOR)
     os.replace(tmp, BINDING)
+    tmp = BINDING_FOR + f".tmp{os.getpid()}"
+    with open(tmp, "w") as f:
+        f.write(made_for)
+    os.replace(tmp, BINDING_FOR)
     return BINDING
 
 

@@ -125,7 +125,11 @@ def _native():
     if _binding is not None:
         return _binding
     L = lib()
-    import torch  # noqa: F401  the module's symbols come from torch's libraries
+    from . import build
+    made_for, runs = build.binding_made_for(), build.binding_for()  # the import of torch also loads the libraries the module needs
+    if made_for != runs:
+        raise RuntimeError(f"_binding.so was made for {made_for or 'nothing yet'}, this is {runs or 'a Python without torch'}: "
+                           "run python -m quantize_amax_scaling_gb300.build")
     from . import _binding as b
     b.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
              (L.fp8q_fp4_quantize_amax, L.fp8q_fp4_dequantize, L.fp8q_fp4_matmul, L.fp8q_residual_norm_quantize_amax,

@@ -78,3 +78,25 @@ def test_each_is_made_again_for_its_own_sources(copy):
         os.utime(copy.root / so, (later, later))
     os.utime(copy.root / "csrc" / "tcgen05.cuh", (later + 10, later + 10))
     assert copy(BUILD)[1] == ["nvcc"] * (UNITS + 1)
+
+
+def test_a_binding_of_another_torch_is_refused_and_made_again(copy):
+    r, tools = copy(BUILD)
+    assert r.returncode == 0 and tools == ["g++"] + ["nvcc"] * (UNITS + 1), r.stdout + r.stderr
+    load = f"""
+import types
+from {PKG} import fp8q
+fp8q.lib = types.SimpleNamespace
+fp8q._native()
+"""
+    other = "import torch; torch.__version__ = '1.2.3'\n"
+    r, _ = copy(other + load)  # before it is loaded: its symbols or layouts may be other ones
+    assert r.returncode != 0 and "made for" in r.stderr and "torch 1.2.3" in r.stderr and "build" in r.stderr, r.stderr
+    assert copy(other + BUILD)[1] == ["g++"]
+    assert copy(other + BUILD)[1] == []
+    r, _ = copy(load)
+    assert r.returncode != 0 and "made for" in r.stderr and "torch 1.2.3" in r.stderr
+    assert copy(BUILD)[1] == ["g++"]
+    os.remove(copy.root / "_binding.so")
+    r, _ = copy(load)
+    assert r.returncode != 0 and "made for nothing yet" in r.stderr
