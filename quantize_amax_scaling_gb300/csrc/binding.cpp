@@ -155,6 +155,16 @@ void gate_rows(const at::Tensor* gate, int64_t rows, int64_t hidden, int64_t per
     throw Refused();
 }
 
+// The call of an entry point.  A launch waits where its stream's queue is full, and other Python threads go on meanwhile:
+// every argument has been read by then, and the caller's references keep the tensors.
+template <typename F, typename... A>
+int64_t launch(F f, A... args) {
+    PyThreadState* const state = PyEval_SaveThread();
+    const int64_t status = f(args...);
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 bool four_bits(int64_t fmt) { return fmt == FP8Q_MXFP4 || fmt == FP8Q_NVFP4; }
 
 // (x, q, sf, fmt, scale, amax, qt, sft, stream)
@@ -169,7 +179,8 @@ int64_t quantize(PyObject* const* v, Py_ssize_t n) {
     if (qt) packed(qt, sft, cols, rows, fmt, "(qt, sft)");
     one(scale, "scale");
     one(amax, "amax");
-    return g_quantize(ptr(x), rows, cols, bytes(q), bytes(sf), bytes(qt), bytes(sft), (fp8q_format)fmt, floats(scale), floats(amax), a.stream());
+    return launch(g_quantize, ptr(x), rows, cols, bytes(q), bytes(sf), bytes(qt), bytes(sft), (fp8q_format)fmt, floats(scale), floats(amax),
+                  a.stream());
 }
 
 // (q, sf, y, fmt, scale, stream)
@@ -180,7 +191,7 @@ int64_t dequantize(PyObject* const* v, Py_ssize_t n) {
     const at::Tensor* scale = a.tensor(kF32, "scale");
     packed(q, sf, rows, cols, fmt, "(q, sf)");
     one(scale, "scale");
-    return g_dequantize(bytes(q), bytes(sf), ptr(y), rows, cols, (fp8q_format)fmt, floats(scale), a.stream());
+    return launch(g_dequantize, bytes(q), bytes(sf), ptr(y), rows, cols, (fp8q_format)fmt, floats(scale), a.stream());
 }
 
 // (a, a_sf, b, b_sf, d, k, fmt, a_scale, b_scale, stream)
@@ -194,8 +205,8 @@ int64_t matmul(PyObject* const* v, Py_ssize_t n) {
     packed(q, qsf, cols, k, fmt, "(b, b_sf)");
     one(sa, "a_scale");
     one(sb, "b_scale");
-    return g_matmul(bytes(p), bytes(psf), bytes(q), bytes(qsf), ptr(d), rows, cols, k, (fp8q_format)fmt,
-                    d->scalar_type() == at::kFloat ? FP8Q_OUT_F32 : FP8Q_OUT_BF16, floats(sa), floats(sb), a.stream());
+    return launch(g_matmul, bytes(p), bytes(psf), bytes(q), bytes(qsf), ptr(d), rows, cols, k, (fp8q_format)fmt,
+                  d->scalar_type() == at::kFloat ? FP8Q_OUT_F32 : FP8Q_OUT_BF16, floats(sa), floats(sb), a.stream());
 }
 
 // (residual, residual_out, block, post_weight, gate, rows_per_gate, alpha, pre_weight, h, q, sf, fmt, scale, amax, rstd_post,
@@ -246,7 +257,7 @@ int64_t norm(PyObject* const* v, Py_ssize_t n) {
     g.amax = floats(amax);
     g.rstd_post = floats(rpost);
     g.rstd_pre = floats(rpre);
-    return g_norm(&g, a.stream());
+    return launch(g_norm, &g, a.stream());
 }
 
 // (d_residual_out, d_h, residual_out, rstd_pre, pre_weight, d_residual, d_pre_weight, block, rstd_post, post_weight, gate,
@@ -297,7 +308,7 @@ int64_t norm_backward(PyObject* const* v, Py_ssize_t n) {
     g.d_gate = ptr(dgate);
     g.workspace = ptr(space);
     g.workspace_bytes = space ? space->numel() : 0;
-    return g_norm_backward(&g, a.stream());
+    return launch(g_norm_backward, &g, a.stream());
 }
 
 template <int64_t (*F)(PyObject* const*, Py_ssize_t)>
