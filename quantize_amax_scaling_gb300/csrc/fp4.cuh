@@ -77,9 +77,10 @@ __device__ __forceinline__ void wait_behind() { asm volatile("griddepcontrol.wai
 // waits in its turn, so two kernels of a stream are under way at most.
 // (Quantize and multiply, NVFP4, 1 x 16384 x 4096: 12.5 us, 16.6 with launches in
 // order; residual norm and product, 1555 x 11264 x 4096: 49 and 55 us.)
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void start_behind() {
     wait_behind();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
 }
 
 // launch_kernel() for them; clusters of `cluster` CTAs.

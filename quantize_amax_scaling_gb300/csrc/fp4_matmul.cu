@@ -81,6 +81,12 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
     return v;
 }
 
+// A barrier of THREADS of the CTA's threads, whole warps.
+template <int THREADS>
+__device__ __forceinline__ void some_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
 template <bool F32>
 __device__ __forceinline__ void store_one(void* d, int64_t at, float v) {
     if (F32)
@@ -165,9 +171,7 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
     const int steps = (a.ksteps + 3) / 4;
     const int s0 = (int)((int64_t)steps * rank / a.split), s1 = (int)((int64_t)steps * (rank + 1) / a.split);
 
-    if (warp == 5) {
-        tmem_alloc<1>(&tmem_slot, G::kCols);
-    } else if (threadIdx.x == 128) {
+    if (threadIdx.x == 128) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i]);
             mbar_init_count(&scaled[i], 4);
@@ -179,11 +183,19 @@ __global__ void __launch_bounds__(192) fp4_matmul_kernel(const __grid_constant__
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    start_behind();
+    wait_behind();
+    if (warp == 5) {
+        tmem_alloc<1>(&tmem_slot, G::kCols);
+        let_next_start();
+    }
+    uint32_t tmem = 0;
+    if (warp != 4) {  // copies start without it
+        tc_fence_before();
+        some_sync<5 * 32>();
+        tc_fence_after();
+        tmem = tmem_slot;
+    }
 
     if (warp == 4) {
         const uint8_t* psf = a.p_sf + (int64_t)(p0 / 128) * a.sf_across * 512;
@@ -413,7 +425,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     const int p_tiles = (a.p_rows + 255) / 256, tiles = p_tiles * a.q_tiles, stride = gridDim.x / 2;
     const int steps = (a.ksteps + 3) / 4;
 
-    if (warp == 9) tmem_alloc<2>(&tmem_slot, 512);
     if (threadIdx.x == 0) {
         prefetch_map(&map_p);
         prefetch_map(&map_q);
@@ -432,12 +443,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers are there
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    start_behind();
+    wait_behind();
+    if (warp == 9) {
+        tmem_alloc<2>(&tmem_slot, 512);
+        let_next_start();
+    }
+    uint32_t tmem = 0;
+    if (warp != 8 && warp != 18) {  // copies start without it; no multiply-add starts before both CTAs' scale warps come from here
+        tc_fence_before();
+        some_sync<kPairThreads - 2 * 32>();
+        tc_fence_after();
+        tmem = tmem_slot;
+    }
 
     if (warp == 8) {
         uint32_t st = 0, round = 0, n = 0;

@@ -48,6 +48,10 @@ __device__ __forceinline__ bool elect_lane() {
 // Tensor memory
 
 // A whole warp.  The only allocation of its CTA: others on the SM may go on at once.
+// Behind wait_behind() and before let_next_start(): a kernel that held tensor memory
+// while it waits for the kernel ahead could keep that one's CTAs from theirs, and
+// both would wait for ever; and so could the next kernel, if it took tensor memory
+// at its start, before this one's CTAs all had theirs.
 template <int PAIR>
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
     if (PAIR == 2) {
