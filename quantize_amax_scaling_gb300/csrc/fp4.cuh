@@ -19,6 +19,7 @@
 #include "packed_f32.cuh"
 
 #include <atomic>
+#include <cstdlib>
 
 namespace {
 
@@ -32,6 +33,22 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& devices) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && dev < 64) devices.fetch_or(1ull << dev, std::memory_order_release);
     return e;
+}
+
+// The SMs of the current device, or of the part of it that this process has.
+inline int sm_count() {
+#ifdef FP8Q_TEST_HOOKS
+    if (const char* n = getenv("FP8Q_TEST_SM_COUNT")) return atoi(n);
+#endif
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 152;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) n = 152;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 inline bool valid_fp4(int fmt) { return fmt == FP8Q_MXFP4 || fmt == FP8Q_NVFP4; }

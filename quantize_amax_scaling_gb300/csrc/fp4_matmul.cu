@@ -733,18 +733,6 @@ fp8q_status launch_tiles(const CUtensorMap& mp, const CUtensorMap& mq, const MmA
     return launch_behind(kern, dim3(grid), dim3(192), MmGeom<FMT, BN>::kSmem, (unsigned)a.split, s, "fp4_matmul_kernel", mp, mq, a);
 }
 
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 152;
-    int n = known[dev].load(std::memory_order_relaxed);
-    if (!n) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) n = 152;
-        known[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 template <int FMT, bool F32>
 fp8q_status launch_pairs(const uint8_t* p, const uint8_t* q, int64_t k, MmArgs g, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};

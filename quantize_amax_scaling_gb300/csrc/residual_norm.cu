@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : THREADS == 320 ?
 // strip keeps its columns' sums of dg1, dg2 and dgate in registers and writes
 // them once; residual_norm_sum_kernel adds the strips in order, so a call gives
 // the same bits every time.
-constexpr int kRnCtas = 304;       // two CTAs on each of 152 SMs
+constexpr int kRnSms = 152;        // no more SMs' worth of strips than this, for which the workspace is sized: on fewer
+                                   // SMs a strip is longer and there are no more of them
 constexpr int kRnSlice = 4096;     // columns a CTA
 
 struct RnStrips {
@@ -418,7 +419,7 @@ struct RnStrips {
     int64_t per_strip, strips;
 };
 
-RnStrips rn_strips(int64_t rows, int32_t H) {
+RnStrips rn_strips(int64_t rows, int32_t H, int sms) {
     RnStrips s;
     s.slices = (H + kRnSlice - 1) / kRnSlice;
     s.width = ((H + s.slices - 1) / s.slices + 15) / 16 * 16;
@@ -428,7 +429,8 @@ RnStrips rn_strips(int64_t rows, int32_t H) {
     // 86 and 109)
     if (s.T == 256 && s.width <= 160 * 16) s.T = 160;
     s.block = s.T == 160 ? 160 : 256;
-    const int64_t most = (int64_t)((s.T == 160 ? kRnCtas / 2 * 3 : kRnCtas) / s.slices) * (s.block / s.T);
+    const int ctas = (sms < kRnSms ? sms : kRnSms) * (s.T == 160 ? 3 : 2), rows_at_once = ctas < s.slices ? 1 : ctas / s.slices;
+    const int64_t most = (int64_t)rows_at_once * (s.block / s.T);
     s.per_strip = (rows + most - 1) / most;
     s.strips = s.per_strip ? (rows + s.per_strip - 1) / s.per_strip : 0;
     return s;
@@ -814,7 +816,7 @@ fp8q_status launch_forward(RnArgs a, cudaStream_t s) {
     // strips: as many as CTAs are resident, by registers (80 a thread, 24 warps; 96 in CTAs of up to 320, 20; 128 of 512, 16;
     // 64 with 32 columns a thread, 32) and shared memory
     const int64_t by_regs = (!hold ? 32 : block <= 256 ? 24 : block <= 320 ? 20 : 16) / (block / 32), by_smem = (int64_t)(224 * 1024 / (smem + 2048));
-    const int64_t most = (by_regs < by_smem ? by_regs : by_smem) * 152 * per_cta;
+    const int64_t most = (by_regs < by_smem ? by_regs : by_smem) * sm_count() * per_cta;
     a.per_strip = (a.rows + most - 1) / most;
     const int64_t strips = (a.rows + a.per_strip - 1) / a.per_strip;
     const dim3 grid((unsigned)((strips + per_cta - 1) / per_cta));
@@ -902,7 +904,7 @@ fp8q_status fp8q_residual_norm_quantize_amax(const fp8q_residual_norm* n, void* 
 
 int64_t fp8q_residual_norm_backward_workspace(int64_t rows, int32_t hidden, int64_t rows_per_gate) {
     if (rows <= 0 || hidden <= 0 || rows > kFp4MaxDim || hidden > kRnMaxH) return 0;
-    const RnStrips st = rn_strips(rows, hidden);
+    const RnStrips st = rn_strips(rows, hidden, kRnSms);
     return (rows_per_gate > 1 ? 4 : 2) * st.strips * hidden * (int64_t)sizeof(float);
 }
 
@@ -925,7 +927,7 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* n, void* 
     if (!n->block && (n->post_weight || n->gate || n->d_block)) return FP8Q_ERR_INVALID_ARG;
     if (n->post_weight ? !n->rstd_post : n->d_post_weight != nullptr) return FP8Q_ERR_INVALID_ARG;
     if (n->gate ? n->rows_per_gate < 1 : n->d_gate != nullptr) return FP8Q_ERR_INVALID_ARG;
-    const RnStrips st = rn_strips(n->rows, n->hidden);
+    const RnStrips st = rn_strips(n->rows, n->hidden, sm_count());
     const int64_t need = fp8q_residual_norm_backward_workspace(n->rows, n->hidden, n->gate ? n->rows_per_gate : 0);
     const bool spread = n->d_gate && n->rows_per_gate > 1;  // groups that may lie across strips
     if ((n->d_pre_weight || n->d_post_weight || spread) && (!n->workspace || n->workspace_bytes < need)) return FP8Q_ERR_INVALID_ARG;
