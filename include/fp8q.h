@@ -3,7 +3,7 @@
  * 4-bit operands and residual norms on one GPU.
  *
  * Fourteen operations, each one kernel launch on the caller's stream (the last,
- * where it sums gradients over rows, two):
+ * where it sums gradients over rows, two; a product with an empty k is a fill):
  *   fp8q_quantize_amax        bf16 -> FP8 bytes, fused with amax = max|x|
  *   fp8q_multi_quantize_amax  the same over a ragged list of tensors
  *   fp8q_dequantize           FP8 bytes -> bf16

@@ -12,14 +12,16 @@
 //
 // Two kernels.  Few tiles: 128 rows of P by 16 to 128 of Q a CTA, k split over a
 // cluster while every CTA is resident; what bounds them is the operands' way from
-// HBM, and at these sizes the time until it flows: 1 x 16384 x 4096 (37.7 MB)
-// 9.5 us, 4.0 TB/s; 1 x 4096 x 4096 4.7 us; each megabyte more costs 0.15 us, 6.5 TB/s.
-// Many tiles: pairs of CTAs with 256 x 256 (below), bound by the tensor cores,
-// between tiles by the accumulators' way out, and in a loop by the power limit:
-// 8192 x 16384 x 4096 172 us (MXFP4 165), 6.4 PFLOP/s; seconds long 198 us at 1400 W
-// and 1690 MHz; the multiply-adds alone, 128 cycles for 256 x 256 x 64, 113 us at
-// 2 GHz.  Single CTAs take 507 us of it; pairs from more 128 x 128 tiles than SMs
+// HBM, and at these sizes the time until it flows: 1 x 16384 x 4096 (37.7 MB) 9.5 us,
+// 4.0 TB/s; 1 x 4096 x 4096 (9.4 MB) 4.6 us; each megabyte more costs 0.17 us, 5.8 TB/s.
+// Many tiles: pairs of CTAs with 256 x 256 (below).  8192 x 16384 x 4096 takes 173 us
+// (MXFP4 166), 6.4 PFLOP/s, of which the multiply-adds alone, 128 cycles for
+// 256 x 256 x 64, are 107 us at 2070 MHz: a step of 256 codes takes 0.29 us where they
+// take 0.25, and between tiles the tensor cores wait 0.9 to 1.4 us for the accumulators'
+// way out.  In a loop seconds long the power limit comes on top: 198 us at 1400 W and 1690 MHz.
+// Single CTAs take 507 us of it; pairs from more 128 x 128 tiles than SMs
 // on, 2560 x 1280 x 4096 10.5 us (17.1 on single CTAs), 2560 x 2560 x 4096 16.5 (26.7).
+// (All with operands in rotation beyond L2, replayed from a graph.)
 
 #include "tcgen05.cuh"
 

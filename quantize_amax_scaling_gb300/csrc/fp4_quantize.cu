@@ -1,19 +1,27 @@
 // fp4_quantize.cu -- bf16 -> microscaled 4-bit operands, of a matrix and of its
 // transpose in one pass, and back.
 //
-// Both kernels stream HBM.  A CTA takes a tile of 128 rows x 128 columns: 128
-// rows are what a scale tile spans, so a CTA writes whole scale tiles (512
-// contiguous bytes) and, for the transpose, 64 contiguous bytes of each of its
-// 128 code rows.  A thread quantizes 16 columns of a row from registers; the
-// transpose reads the same tile back from shared memory by pairs of columns.
-// Matrices whose rows do not start on 32-byte boundaries pass through shared
-// memory by 16 aligned bytes.
+// Four kernels, which stream HBM.
+//   fp4_quantize_kernel         with the transpose, or of rows that start anywhere:
+//       tiles of 128 x 128.  128 rows are what a scale tile spans, so a CTA writes
+//       whole scale tiles (512 contiguous bytes) and, for the transpose, 64
+//       contiguous bytes of each of its 128 code rows.  A thread quantizes 16
+//       columns of a row from registers; the transpose reads the same tile back
+//       from shared memory by pairs of columns.  Rows that do not start on
+//       32-byte boundaries pass through shared memory by 16 aligned bytes.
+//   fp4_quantize_rows_kernel    one direction of rows on 32-byte boundaries: tiles of
+//       32 x 512, from registers alone.
+//   fp4_dequantize_rows_kernel  rows on 16-byte boundaries: tiles of 8 x 1024.
+//   fp4_dequantize_kernel       rows that start anywhere: tiles of 64 x 128, out
+//       through shared memory by 16 aligned bytes.
 //
 // Measured, 8192 x 4096, 86 MB for one direction (105 MB for both): NVFP4 15.9 us
-// (26.7), MXFP4 14.4 us (19.8), back 14.2 and 13.9 us, 3.9 to 6.1 TB/s; 1187 x 2731
-// both ways, where rows start anywhere, 7.0 and 5.5 us.  NVFP4 both ways issues
-// 64 % of its cycles' instructions: a scale of every 16 elements costs a
-// conversion there and back, two products and a reciprocal, twice over.
+// (26.9), MXFP4 14.3 us (19.9), back 14.2 and 13.9 us, 3.9 to 6.1 TB/s; 1187 x 2731
+// both ways, where rows start anywhere, 7.1 and 5.5 us, back 4.7.  NVFP4 both ways
+// issues in 64 % of its cycles, with 24 warps an SM that load, compute and store in
+// turn (DRAM 33 %): a scale of every 16 elements costs a conversion there and back,
+// two products and a reciprocal, twice over.  (Inputs in rotation beyond L2,
+// replayed from a graph.)
 
 #include "fp4.cuh"
 

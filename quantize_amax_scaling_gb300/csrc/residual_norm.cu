@@ -19,11 +19,13 @@
 // copies of its own (it alone reads them, so they need no barrier), while the
 // weights of its columns stay in shared memory (forward) or registers (backward).
 //
-// Measured, 8192 x 4096: e4m3 codes 42.6 us for 235 MB (5.5 TB/s), NVFP4 48.6 us,
-// a gate row a token 57 us for 302 MB; gradients 77 us for 403 MB (5.2 TB/s), 95 with
-// a gate row a token.  One token of 4096 4.2 us, its gradients 7.2.  Both issue
-// instructions 50 to 65% of the time beside HBM at 55 to 67%: some 30 an element
-// forward, over two reductions a row that every warp of the row waits for.
+// Measured, 8192 x 4096: e4m3 codes 42.5 us for 235 MB (5.5 TB/s), e5m2 42.3, MXFP4 43.6,
+// NVFP4 48.5 us, a gate row a token 57.6 us for 302 MB; gradients 78 us for 403 MB
+// (5.2 TB/s), 95 with a gate row a token.  One token of 4096 4.0 us, its gradients 6.9.
+// Both issue instructions 48 to 65% of the time beside HBM at 44 to 67%: some 30 an
+// element forward (NVFP4 36: a scale of every 16 elements), over two reductions a
+// row that every warp of the row waits for.  (Inputs in rotation beyond L2, replayed
+// from a graph.)
 
 #include "fp4.cuh"
 #include "packed_f32.cuh"

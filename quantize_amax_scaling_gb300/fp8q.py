@@ -4,9 +4,10 @@ Argument marshalling only: every step of the path runs in the CUDA kernels of
 libfp8q.so.  Tensors are torch CUDA tensors (torch supplies device memory and
 streams); the functions keep the C names and raise Fp8qError on a non-OK
 status.  The 8-bit calls go through ctypes, the 4-bit and residual-norm calls
-through a compiled module (csrc/binding.cpp), which takes 2 us a call where a
-single token's kernel takes 2 to 5.  If the library has not been built,
-loading fails loudly -- there is no fallback.
+through a compiled module (csrc/binding.cpp), which takes 2 to 3 us a call where
+a single token's kernel takes 2 to 5; either lets other Python threads run
+meanwhile.  If the library has not been built, loading fails loudly -- there is
+no fallback.
 """
 from __future__ import annotations
 
