@@ -786,7 +786,9 @@ fp8q_status matmul(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, cons
     // clusters of 4 and 8 reach 144 and 120 of the 152 SMs) and have two steps or more, where the steps that a CTA
     // saves are worth the cluster and its sums, 1 us for 16 rows of Q to 2.5 for 128, a step 0.3: 1x4096x4096
     // takes 4.7 us on clusters of 4, 6.6 without; 128x4096x4096 7.0 and 8.5, 128x8192x4096 9.0 and 9.6, but 128x4096x2048 6.3 and 5.7.
-    // The more of the GPU the tiles take anyway, the longer k has to be: 24x16384x2048 takes 6.7 us, 7.8 on clusters of 2.
+    // The more of the GPU the tiles take anyway, the longer k has to be.  Above two fifths of the SMs, 16 steps: 128x8192x2048 (8)
+    // takes 6.3 us, 6.9 on clusters of 2; 128x8192x4096 9.7 and 9.2.  Above two thirds, 32: 24x16384x2048 6.9 and 7.4,
+    // 24x16384x4096 10.3 and 10.2, 24x16384x8192 16.9 and 15.6.
     const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, steps = (g.ksteps + 3) / 4;
     int split = 1;
     if (!pairs) {

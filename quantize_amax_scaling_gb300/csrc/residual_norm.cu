@@ -427,8 +427,8 @@ RnStrips rn_strips(int64_t rows, int32_t H, int sms) {
     s.width = ((H + s.slices - 1) / s.slices + 15) / 16 * 16;
     s.T = 256;
     while (s.T > 32 && s.width <= s.T * 8) s.T /= 2;
-    // three CTAs of 160 threads an SM where 256 would leave every third idle and more (16256x2064: 76 us, 91; 6553x5120, two CTAs a row,
-    // 86 and 109)
+    // three CTAs of 160 threads an SM where 256 would leave every third idle and more (16256x2064: 76 us, 92; 6553x5120, two CTAs a row,
+    // 88 and 111; a bf16 gate row a token 108 and 140, 125 and 150; few rows about the same: 777x2064 15.8 and 14.9, 15.5 and 15.6)
     if (s.T == 256 && s.width <= 160 * 16) s.T = 160;
     s.block = s.T == 160 ? 160 : 256;
     const int ctas = (sms < kRnSms ? sms : kRnSms) * (s.T == 160 ? 3 : 2), rows_at_once = ctas < s.slices ? 1 : ctas / s.slices;
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(ROW == 160 ? 160 : 256, ROW == 160 ? 3 : 2) re
 
 // COLS columns a CTA, four a lane, 32 warps of 128 / COLS strips at a time: blockIdx.y 0 adds dpre, 1 dpost, and from 2
 // on a row of dgate that lies in several strips: row blockIdx.y - 2, where gates span strips, or else the one across the
-// border behind strip blockIdx.y - 2.  (32 columns a CTA where 128 would leave most SMs idle: 777x1552 13.1 us for the
+// border behind strip blockIdx.y - 2.  (32 columns a CTA where 128 would leave most SMs idle: 777x1552 13.2 us for the
 // call, 15.1 by 128; 8192x1024 29.6 and 33.7; wider rows and many gates by 128: 8192x4096 77.2 us, 80 by 32.)
 template <int COLS>
 __global__ void __launch_bounds__(1024) residual_norm_sum_kernel(const RnBwdArgs a) {
