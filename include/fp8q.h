@@ -1,9 +1,9 @@
 /*
  * fp8q.h -- C ABI of libfp8q: FP8 delayed-scaling quantization, microscaled
- * 4-bit operands and residual norms on one GPU.
+ * 4-bit operands, residual norms, FP8 products and 8-bit checkpoints on one GPU.
  *
- * Fourteen operations, each one kernel launch on the caller's stream (the last,
- * where it sums gradients over rows, two; a product with an empty k is a fill):
+ * Twenty operations, each one kernel launch on the caller's stream (those that
+ * sum gradients over rows two; a 4-bit product with an empty k is a fill):
  *   fp8q_quantize_amax        bf16 -> FP8 bytes, fused with amax = max|x|
  *   fp8q_multi_quantize_amax  the same over a ragged list of tensors
  *   fp8q_dequantize           FP8 bytes -> bf16
@@ -22,6 +22,14 @@
  *   fp8q_residual_norm_quantize_amax  RMS norm after a block, gate, residual
  *                             add, RMS norm before the next block, quantize
  *   fp8q_residual_norm_backward  its gradients
+ *   fp8q_matmul               the product of two FP8 operands, with bias, GELU,
+ *                             residual, FP8 codes and a checkpoint in its epilogue
+ *   fp8q_grouped_matmul       the same over rows grouped by expert
+ *   fp8q_grouped_weight_gradient  the gradients of the experts' weights
+ *   fp8q_checkpoint_quantize  bf16 -> an 8-bit checkpoint
+ *   fp8q_checkpoint_dequantize  8-bit checkpoint -> bf16
+ *   fp8q_gelu_backward_quantize_amax  back through a GELU from the checkpoint of
+ *                             its input, quantize, the bias's gradient
  *
  * Sources (web pages, by title and section):
  *   "User Guide on Native XLA-FP8" (NVIDIA JAX-Toolbox): opening section
@@ -48,9 +56,10 @@
  *     (as allocators return them) take the vectorised path.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
  *     return once the kernel is enqueued; results are ready when the stream
- *     reaches that point.  The fp8q_fp4_* and fp8q_residual_norm_* kernels are
- *     launched so that their start overlaps the end of the kernel before them
- *     in the stream; they touch memory only when that has ended.
+ *     reaches that point.  The kernels of fp8q_fp4_* and of the calls behind it
+ *     in the list above are launched so that their start overlaps the end of
+ *     the kernel before them in the stream; they touch memory only when that
+ *     has ended.
  *   - Errors are returned as fp8q_status, never raised or aborted.  Argument
  *     errors are detected before anything is launched.  FP8Q_ERR_CUDA means
  *     the launch itself failed; fp8q_last_cuda_error() (per thread) then
@@ -518,6 +527,149 @@ int64_t fp8q_residual_norm_backward_workspace(int64_t rows, int32_t hidden, int6
  *         is read or written.
  */
 fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* args, void* stream);
+
+/*
+ * The product of two FP8 operands with what follows a linear layer:
+ *   z = RN(a_scale * b_scale) * (sum_k a[i][k] b[j][k]) + bias[j]
+ *   y = act(z) + residual[i][j]
+ *   d = RN_out(y);   q = FP8(bf16(y) / *q_scale), exactly fp8q_quantize_amax of
+ *   bf16(y);   *amax = max(*amax, max|bf16(y)|)
+ *   (h, h_sf) = fp8q_checkpoint_quantize of bf16(z)
+ * Parts may be left out by NULL: bias, residual, and of d, q, amax and h any but
+ * the last one.  A is [m, k], or with a_trans stored as its transpose, [k, m]; B
+ * is [n, k], or with b_trans [k, n]; each row starts lda (ldb) bytes behind the
+ * one before.  So with x [m, k], w [n, k] and the gradient dy [m, n], a layer's
+ * output is (x, w), its input's gradient (dy, w with b_trans) and its weight's
+ * gradient (dy with a_trans, x with b_trans); no transposed copies are needed.
+ * d, q, residual and h are contiguous [m, n].  residual has d's type (bf16
+ * without d) and may be d.  Products are exact, sums are held in binary32, the
+ * rest is binary32 with the GELU (tanh form) within 2^-18 of its value (beyond
+ * |z| = 10 within 2^-100 where it is near 0).  Calls with the same arguments
+ * give the same bits.  With k == 0 the sums are zeros and a and b may be NULL.
+ * A wait inside the kernel that runs out, which only a fault elsewhere could
+ * cause, ends the kernel and shows as NaN in what it had not finished.
+ */
+typedef enum {
+    FP8Q_ACT_NONE = 0,
+    FP8Q_ACT_GELU = 1
+} fp8q_activation;
+
+typedef struct {
+    int64_t m, n, k;
+    const uint8_t* a;     /* codes */
+    const uint8_t* b;
+    int64_t lda, ldb;     /* bytes from row to row as stored; multiples of 16 */
+    fp8q_format a_fmt, b_fmt;
+    int32_t a_trans, b_trans;
+    const float* a_scale; /* tensor scales, one float each, or NULL for 1 */
+    const float* b_scale;
+    const void* bias;     /* [n] binary32 or bf16 */
+    int32_t bias_is_bf16;
+    fp8q_activation act;
+    const void* residual; /* [m, n] */
+    void* d;              /* [m, n] */
+    fp8q_out_type out;    /* of d; FP8Q_OUT_BF16 with q or amax, or without d */
+    fp8q_format q_fmt;
+    uint8_t* q;           /* [m, n] */
+    const float* q_scale; /* one float (with q) */
+    float* amax;          /* one float, max-accumulated */
+    uint8_t* h;           /* [m, n] */
+    uint8_t* h_sf;        /* [m, ceil(n / 32)] (with h) */
+} fp8q_product;
+
+/*
+ * Errors: INVALID_ARG for a NULL args, an unknown format, type or act, m, n or
+ *         k < 0, parts missing or left over as said above, a row shorter than
+ *         its elements, or a pointer that its elements' size does not divide;
+ *         UNSUPPORTED for a, b, lda or ldb off 16 bytes, lda or ldb from 2^31
+ *         on, or m, n or k above 2^31 - 1024.  m == 0 or n == 0 launches
+ *         nothing.
+ */
+fp8q_status fp8q_matmul(const fp8q_product* args, void* stream);
+
+/*
+ * fp8q_matmul over rows grouped by expert: row i of A, of group g, is multiplied
+ * by B's g-th matrix.  Group g is the rows offsets[g] to offsets[g + 1] - 1; it
+ * may be empty.  args: A is [m, k] (never transposed), m the rows of all groups;
+ * B is [groups, n, k] ([groups, k, n] with b_trans), the matrices one behind the
+ * other; bias is [groups, n].  All groups share a_scale, b_scale and q_scale.
+ * Rows before the first group and behind the last are not written and count for
+ * nothing.
+ * offsets: int32[groups + 1] (device), read by the kernel: they must not
+ * decrease.  Any values are safe: one outside [0, m] counts as the bound, and a
+ * group that would end before it starts is empty; rows that two groups hold
+ * then get either's result.
+ * Errors: as for fp8q_matmul, and INVALID_ARG for groups < 0, NULL offsets or
+ *         a_trans; UNSUPPORTED for groups > 512.  groups == 0 launches nothing.
+ */
+fp8q_status fp8q_grouped_matmul(const fp8q_product* args, const int32_t* offsets, int32_t groups, void* stream);
+
+/*
+ * The gradients of the experts' weights: for every group g
+ *   d[g] = RN_out( RN(a_scale * b_scale) * sum over the group's rows t of a[t][i] b[t][j] + residual[g][i][j] )
+ * args: a is [k, m] and b is [k, n], k the rows of all groups (a_trans and
+ * b_trans are set); d and residual are [groups, m, n]; no bias, act, q, amax or
+ * h.  An empty group's sums are zeros.  Codes of other groups' rows, NaN among
+ * them, do not reach a group's sums.  offsets, groups, errors: as for
+ * fp8q_grouped_matmul.
+ */
+fp8q_status fp8q_grouped_weight_gradient(const fp8q_product* args, const int32_t* offsets, int32_t groups, void* stream);
+
+/*
+ * The 8-bit checkpoint of an activation, for a backward pass: e4m3 codes under
+ * a power of two for each block of 32 columns of a row.  With a = max|x| of the
+ * block, its scale is 2^e with the least e >= -127 for which a <= 448 * 2^e, kept
+ * as the byte e + 127; code = e4m3(x / 2^e), the quotient exact.  So a value is
+ * off by at most 2^-4 of itself, or 2^(e - 10) where that is more.  An infinity
+ * counts as the largest finite bf16 in a and comes back as an infinity; a NaN in
+ * the block makes its scale NaN (0xFF).
+ * q: [rows, cols] bytes, sf: fp8q_checkpoint_scale_bytes, [rows, ceil(cols / 32)]
+ * bytes, both contiguous, from any address; on 16-byte and 4-byte boundaries, with
+ * x_bf16 on a 32-byte one and whole blocks a row, they take the vectorised path.
+ * Back: y = bf16(code * 2^e), the product exact.
+ * Errors: INVALID_ARG for rows or cols < 0, a NULL or an odd bf16 pointer;
+ *         UNSUPPORTED for rows or cols above 2^31 - 1024.
+ */
+int64_t fp8q_checkpoint_scale_bytes(int64_t rows, int64_t cols);
+fp8q_status fp8q_checkpoint_quantize(const void* x_bf16, uint8_t* q, uint8_t* sf, int64_t rows, int64_t cols, void* stream);
+fp8q_status fp8q_checkpoint_dequantize(const uint8_t* q, const uint8_t* sf, void* y_bf16, int64_t rows, int64_t cols, void* stream);
+
+/*
+ * Back through a GELU (tanh form), from the checkpoint (h, h_sf) of its input:
+ *   D      = d_y * GELU'(h)                       in binary32 (d_y without h)
+ *   d_x    = bf16(D),  q = FP8(d_x / *scale) exactly as fp8q_quantize_amax,
+ *   *amax  = max(*amax, max|d_x|),  d_bias = sum over rows of D
+ * h and h_sf may be NULL together (a layer without activation), and of q (with
+ * scale), d_x, d_bias and amax any but the last one.  GELU' is within 2^-19 (1 +
+ * |h|) of its value; a NaN in h or d_y gives NaN.  Sums are taken in binary32 in
+ * a fixed order.
+ */
+typedef struct {
+    int64_t rows, cols;
+    fp8q_format fmt;      /* of q */
+    const void* d_y;      /* [rows, cols] bf16 */
+    const uint8_t* h;     /* [rows, cols] */
+    const uint8_t* h_sf;  /* [rows, ceil(cols / 32)] */
+    void* d_x;            /* [rows, cols] bf16 */
+    uint8_t* q;           /* [rows, cols] */
+    const float* scale;   /* one float */
+    float* amax;          /* one float, max-accumulated */
+    float* d_bias;        /* [cols] */
+    void* workspace;      /* fp8q_gelu_backward_workspace bytes, with d_bias */
+    int64_t workspace_bytes;
+} fp8q_gelu_grad;
+
+/* Bytes of workspace (4-byte aligned, contents irrelevant) for d_bias; one call
+ * at a time may use it.  0 for sizes that the call refuses. */
+int64_t fp8q_gelu_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * Errors: INVALID_ARG for a NULL args or d_y, an unknown fmt, rows or cols < 0,
+ *         parts missing or left over, too small a workspace, or a misaligned
+ *         pointer; UNSUPPORTED for rows or cols above 2^31 - 1024.  With rows ==
+ *         0 d_bias is zeros and nothing else is read or written.
+ */
+fp8q_status fp8q_gelu_backward_quantize_amax(const fp8q_gelu_grad* args, void* stream);
 
 /* Static, human-readable name of a status. */
 const char* fp8q_status_string(fp8q_status status);

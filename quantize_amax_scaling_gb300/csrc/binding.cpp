@@ -1,4 +1,4 @@
-// binding.cpp -- the 4-bit and residual-norm calls of the Python binding: torch
+// binding.cpp -- the calls of the Python binding from the 4-bit ones on: torch
 // tensors checked and marshalled into the C ABI of libfp8q (fp8q.h).
 //
 // A call of one token spends more time in Python's checks of a dozen tensors than
@@ -28,10 +28,17 @@ decltype(&fp8q_fp4_matmul) g_matmul;
 decltype(&fp8q_residual_norm_quantize_amax) g_norm;
 decltype(&fp8q_residual_norm_backward) g_norm_backward;
 decltype(&fp8q_residual_norm_backward_workspace) g_workspace;
+decltype(&fp8q_matmul) g_product;
+decltype(&fp8q_grouped_matmul) g_grouped;
+decltype(&fp8q_grouped_weight_gradient) g_grouped_gradient;
+decltype(&fp8q_checkpoint_quantize) g_checkpoint;
+decltype(&fp8q_checkpoint_dequantize) g_checkpoint_back;
+decltype(&fp8q_gelu_backward_quantize_amax) g_gelu_backward;
+decltype(&fp8q_gelu_backward_workspace) g_gelu_workspace;
 
 struct Refused {};  // a Python exception has been set
 
-enum Kind { kBf16, kByte, kF32, kGate };  // kByte: uint8 or a float8 type; kGate: binary32 or bf16
+enum Kind { kBf16, kByte, kF32, kGate, kI32 };  // kByte: uint8 or a float8 type; kGate: binary32 or bf16
 
 int64_t row_bytes(int64_t cols) { return (cols + 31) / 32 * 16; }
 int64_t scale_bytes(int64_t rows, int64_t cols, int64_t fmt) {
@@ -54,27 +61,30 @@ public:
     }
 
     // The next tensor, or nullptr for None; with `shape`, one of two dimensions.
-    const at::Tensor* tensor(Kind kind, const char* name, const char* shape = nullptr) {
+    // whole: contiguous; otherwise the caller looks at the strides.
+    const at::Tensor* tensor(Kind kind, const char* name, const char* shape = nullptr, bool whole = true) {
         PyObject* o = a_[i_++];
         if (o == Py_None && !shape) return nullptr;
         if (!THPVariable_Check(o)) refuse("%s must be a tensor", name);
         const at::Tensor& t = THPVariable_Unpack(o);
-        if (shape) matrix(&t, name, shape);
+        if (shape && whole) matrix(&t, name, shape);
         if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
         const at::ScalarType s = t.scalar_type();
         const bool ok = kind == kBf16   ? s == at::kBFloat16
                         : kind == kF32  ? s == at::kFloat
                         : kind == kGate ? s == at::kFloat || s == at::kBFloat16
+                        : kind == kI32  ? s == at::kInt
                                         : s == at::kByte || s == at::kFloat8_e4m3fn || s == at::kFloat8_e5m2;
         if (!ok) {
             PyErr_Format(PyExc_ValueError, "%s has dtype %s, expected %s", name, c10::toString(s),
                          kind == kBf16   ? "bfloat16"
                          : kind == kF32  ? "float32"
                          : kind == kGate ? "float32 or bfloat16"
+                         : kind == kI32  ? "int32"
                                          : "uint8 or a float8 type");
             throw Refused();
         }
-        if (!t.is_contiguous()) refuse("%s must be contiguous", name);
+        if (whole && !t.is_contiguous()) refuse("%s must be contiguous", name);
         if (device_ < 0) device_ = c10::cuda::current_device();
         if (t.device().index() != device_) {
             PyErr_Format(PyExc_ValueError,
@@ -84,6 +94,26 @@ public:
             throw Refused();
         }
         return &t;
+    }
+
+    // A matrix of FP8 codes, or with `groups` a stack of them: elements of a row side by side, rows a multiple of 16 bytes
+    // apart (or one row), the matrices one behind the other.  Its row length in bytes as `ld`.
+    const at::Tensor* codes(const char* name, bool groups, int64_t* ld) {
+        const at::Tensor* t = tensor(kByte, name, groups ? "[groups, rows, cols]" : "[rows, cols]", false);
+        const int64_t dims = groups ? 3 : 2;
+        if (t->dim() != dims) {
+            PyErr_Format(PyExc_ValueError, "%s must be %s", name, groups ? "[groups, rows, cols]" : "[rows, cols]");
+            throw Refused();
+        }
+        const int64_t rows = t->size(dims - 2), cols = t->size(dims - 1);
+        *ld = rows > 1 && cols > 0 ? t->stride(dims - 2) : (cols + 15) / 16 * 16;
+        if (cols > 1 && t->stride(dims - 1) != 1) refuse("%s must have the elements of a row side by side", name);
+        if (t->numel() > 0 && rows > 1 && (*ld < cols || *ld % 16)) refuse("%s must have rows a multiple of 16 bytes apart", name);
+        if (groups && t->numel() > 0 && t->size(0) > 1) {
+            if (rows == 1) *ld = t->stride(0);
+            if (t->stride(0) != rows * *ld || *ld < cols || *ld % 16) refuse("%s must have its matrices one behind the other, rows a multiple of 16 bytes apart", name);
+        }
+        return t;
     }
 
     int64_t integer() {
@@ -311,6 +341,152 @@ int64_t norm_backward(PyObject* const* v, Py_ssize_t n) {
     return launch(g_norm_backward, &g, a.stream());
 }
 
+void shaped(const at::Tensor* t, int64_t n, const char* name, const char* shape) {
+    if (!t || t->numel() == n) return;
+    PyErr_Format(PyExc_ValueError, "%s must be %s (%lld elements)", name, shape, (long long)n);
+    throw Refused();
+}
+
+// (a, b, d, a_fmt, b_fmt, a_scale, b_scale, a_trans, b_trans, bias, act, residual, q, q_fmt, q_scale, amax, h, h_sf[, offsets], stream)
+template <bool GROUPED>
+int64_t product(PyObject* const* v, Py_ssize_t n) {
+    Args a(GROUPED ? "grouped_matmul" : "matmul", v, n, GROUPED ? 20 : 19);
+    fp8q_product p = {};
+    const at::Tensor *x = a.codes("a", false, &p.lda), *w = a.codes("b", GROUPED, &p.ldb), *d = a.tensor(kGate, "d");
+    p.a_fmt = (fp8q_format)a.integer();
+    p.b_fmt = (fp8q_format)a.integer();
+    const at::Tensor *sa = a.tensor(kF32, "a_scale"), *sb = a.tensor(kF32, "b_scale");
+    p.a_trans = a.integer() != 0;
+    p.b_trans = a.integer() != 0;
+    const at::Tensor* bias = a.tensor(kGate, "bias");
+    p.act = (fp8q_activation)a.integer();
+    const at::Tensor *residual = a.tensor(kGate, "residual"), *q = a.tensor(kByte, "q");
+    p.q_fmt = (fp8q_format)a.integer();
+    const at::Tensor *qs = a.tensor(kF32, "q_scale"), *amax = a.tensor(kF32, "amax"), *h = a.tensor(kByte, "h"), *hs = a.tensor(kByte, "h_sf");
+    const at::Tensor* offsets = GROUPED ? a.tensor(kI32, "offsets") : nullptr;
+    const int64_t groups = GROUPED ? w->size(0) : 1, off = GROUPED ? 1 : 0;
+    p.m = x->size(p.a_trans ? 1 : 0);
+    p.k = x->size(p.a_trans ? 0 : 1);
+    p.n = w->size(off + (p.b_trans ? 1 : 0));
+    if (w->size(off + (p.b_trans ? 0 : 1)) != p.k) {
+        PyErr_Format(PyExc_ValueError, "a and b must have the same k, not %lld and %lld", (long long)p.k,
+                     (long long)w->size(off + (p.b_trans ? 0 : 1)));
+        throw Refused();
+    }
+    if (GROUPED && (!offsets || offsets->numel() != groups + 1)) Args::refuse("%s must have one element more than b has matrices", "offsets");
+    shaped(d, p.m * p.n, "d", "[m, n]");
+    shaped(residual, p.m * p.n, "residual", "[m, n]");
+    shaped(q, p.m * p.n, "q", "[m, n]");
+    shaped(h, p.m * p.n, "h", "[m, n]");
+    shaped(hs, p.m * ((p.n + 31) / 32), "h_sf", "[m, ceil(n / 32)]");
+    shaped(bias, groups * p.n, "bias", GROUPED ? "[groups, n]" : "[n]");
+    one(sa, "a_scale");
+    one(sb, "b_scale");
+    one(qs, "q_scale");
+    one(amax, "amax");
+    if (residual && residual->scalar_type() != (d ? d->scalar_type() : at::kBFloat16)) Args::refuse("%s must have d's type", "residual");
+    p.a = bytes(x);
+    p.b = bytes(w);
+    p.a_scale = floats(sa);
+    p.b_scale = floats(sb);
+    p.bias = ptr(bias);
+    p.bias_is_bf16 = bias && bias->scalar_type() == at::kBFloat16;
+    p.residual = ptr(residual);
+    p.d = ptr(d);
+    p.out = d && d->scalar_type() == at::kFloat ? FP8Q_OUT_F32 : FP8Q_OUT_BF16;
+    p.q = bytes(q);
+    p.q_scale = floats(qs);
+    p.amax = floats(amax);
+    p.h = bytes(h);
+    p.h_sf = bytes(hs);
+    if (!GROUPED) return launch(g_product, &p, a.stream());
+    return launch(g_grouped, &p, static_cast<int32_t*>(ptr(offsets)), (int32_t)(groups > INT32_MAX ? INT32_MAX : groups), a.stream());
+}
+
+// (a, b, offsets, d, a_fmt, b_fmt, a_scale, b_scale, residual, stream)
+int64_t grouped_gradient(PyObject* const* v, Py_ssize_t n) {
+    Args a("grouped_weight_gradient", v, n, 10);
+    fp8q_product p = {};
+    const at::Tensor *x = a.codes("a", false, &p.lda), *w = a.codes("b", false, &p.ldb), *offsets = a.tensor(kI32, "offsets"),
+                     *d = a.tensor(kGate, "d");
+    if (!d || d->dim() != 3) Args::refuse("%s must be [groups, m, n]", "d");
+    p.a_fmt = (fp8q_format)a.integer();
+    p.b_fmt = (fp8q_format)a.integer();
+    const at::Tensor *sa = a.tensor(kF32, "a_scale"), *sb = a.tensor(kF32, "b_scale"), *residual = a.tensor(kGate, "residual");
+    const int64_t groups = d->size(0);
+    p.k = x->size(0);
+    p.m = x->size(1);
+    p.n = w->size(1);
+    if (w->size(0) != p.k) Args::refuse("%s must have as many rows as a", "b");
+    if (d->size(1) != p.m || d->size(2) != p.n) Args::refuse("%s must be [groups, m, n]", "d");
+    if (!offsets || offsets->numel() != groups + 1) Args::refuse("%s must have one element more than d has matrices", "offsets");
+    shaped(residual, groups * p.m * p.n, "residual", "[groups, m, n]");
+    if (residual && residual->scalar_type() != d->scalar_type()) Args::refuse("%s must have d's type", "residual");
+    one(sa, "a_scale");
+    one(sb, "b_scale");
+    p.a = bytes(x);
+    p.b = bytes(w);
+    p.a_trans = p.b_trans = 1;
+    p.a_scale = floats(sa);
+    p.b_scale = floats(sb);
+    p.residual = ptr(residual);
+    p.d = ptr(d);
+    p.out = d->scalar_type() == at::kFloat ? FP8Q_OUT_F32 : FP8Q_OUT_BF16;
+    return launch(g_grouped_gradient, &p, static_cast<int32_t*>(ptr(offsets)), (int32_t)(groups > INT32_MAX ? INT32_MAX : groups), a.stream());
+}
+
+// (x, q, sf, stream) and (q, sf, y, stream)
+template <bool BACK>
+int64_t checkpoint(PyObject* const* v, Py_ssize_t n) {
+    Args a(BACK ? "checkpoint_dequantize" : "checkpoint_quantize", v, n, 4);
+    const at::Tensor* x = BACK ? nullptr : a.tensor(kBf16, "x", "[rows, cols]");
+    const at::Tensor *q = a.tensor(kByte, "q"), *sf = a.tensor(kByte, "sf");
+    if (BACK) x = a.tensor(kBf16, "y", "[rows, cols]");
+    const int64_t rows = x->size(0), cols = x->size(1);
+    if (!q || !sf) Args::refuse("%s must be a checkpoint: see checkpoint_empty", "(q, sf)");
+    shaped(q, rows * cols, "q", "[rows, cols]");
+    shaped(sf, rows * ((cols + 31) / 32), "sf", "[rows, ceil(cols / 32)]");
+    return BACK ? launch(g_checkpoint_back, bytes(q), bytes(sf), ptr(x), rows, cols, a.stream())
+                : launch(g_checkpoint, ptr(x), bytes(q), bytes(sf), rows, cols, a.stream());
+}
+
+// (d_y, h, h_sf, q, fmt, scale, amax, d_x, d_bias, workspace, stream)
+int64_t gelu_backward(PyObject* const* v, Py_ssize_t n) {
+    Args a("gelu_backward_quantize_amax", v, n, 11);
+    fp8q_gelu_grad g = {};
+    const at::Tensor *dy = a.tensor(kBf16, "d_y", "[rows, cols]"), *h = a.tensor(kByte, "h"), *hs = a.tensor(kByte, "h_sf"), *q = a.tensor(kByte, "q");
+    g.fmt = (fp8q_format)a.integer();
+    const at::Tensor *scale = a.tensor(kF32, "scale"), *amax = a.tensor(kF32, "amax"), *dx = a.tensor(kBf16, "d_x"),
+                     *db = a.tensor(kF32, "d_bias"), *space = a.tensor(kByte, "workspace");
+    g.rows = dy->size(0);
+    g.cols = dy->size(1);
+    shaped(h, g.rows * g.cols, "h", "[rows, cols]");
+    shaped(hs, g.rows * ((g.cols + 31) / 32), "h_sf", "[rows, ceil(cols / 32)]");
+    shaped(q, g.rows * g.cols, "q", "[rows, cols]");
+    shaped(dx, g.rows * g.cols, "d_x", "[rows, cols]");
+    shaped(db, g.cols, "d_bias", "[cols]");
+    one(scale, "scale");
+    one(amax, "amax");
+    g.d_y = ptr(dy);
+    g.h = bytes(h);
+    g.h_sf = bytes(hs);
+    g.d_x = ptr(dx);
+    g.q = bytes(q);
+    g.scale = floats(scale);
+    g.amax = floats(amax);
+    g.d_bias = floats(db);
+    g.workspace = ptr(space);
+    g.workspace_bytes = space ? space->numel() : 0;
+    return launch(g_gelu_backward, &g, a.stream());
+}
+
+// (rows, cols)
+int64_t gelu_workspace(PyObject* const* v, Py_ssize_t n) {
+    Args a("gelu_backward_workspace", v, n, 2);
+    const int64_t rows = a.integer(), cols = a.integer();
+    return g_gelu_workspace(rows, cols);
+}
+
 template <int64_t (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
@@ -368,11 +544,12 @@ PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // Addresses of the entry points, in the order of the calls below.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* p[6] = {};
-    for (Py_ssize_t i = 0; i < 6; ++i) {
+    constexpr int kEntries = 13;
+    void* p[kEntries] = {};
+    for (Py_ssize_t i = 0; i < kEntries; ++i) {
         if (i < n) p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind takes six addresses");
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind takes thirteen addresses");
             return nullptr;
         }
     }
@@ -382,6 +559,13 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_norm = reinterpret_cast<decltype(g_norm)>(p[3]);
     g_norm_backward = reinterpret_cast<decltype(g_norm_backward)>(p[4]);
     g_workspace = reinterpret_cast<decltype(g_workspace)>(p[5]);
+    g_product = reinterpret_cast<decltype(g_product)>(p[6]);
+    g_grouped = reinterpret_cast<decltype(g_grouped)>(p[7]);
+    g_grouped_gradient = reinterpret_cast<decltype(g_grouped_gradient)>(p[8]);
+    g_checkpoint = reinterpret_cast<decltype(g_checkpoint)>(p[9]);
+    g_checkpoint_back = reinterpret_cast<decltype(g_checkpoint_back)>(p[10]);
+    g_gelu_backward = reinterpret_cast<decltype(g_gelu_backward)>(p[11]);
+    g_gelu_workspace = reinterpret_cast<decltype(g_gelu_workspace)>(p[12]);
     Py_RETURN_NONE;
 }
 
@@ -394,6 +578,13 @@ PyMethodDef g_methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                            {"residual_norm_quantize_amax", FAST(call<norm>), METH_FASTCALL, nullptr},
                            {"residual_norm_backward", FAST(call<norm_backward>), METH_FASTCALL, nullptr},
                            {"residual_norm_backward_workspace", FAST(call<workspace>), METH_FASTCALL, nullptr},
+                           {"matmul", FAST(call<product<false>>), METH_FASTCALL, nullptr},
+                           {"grouped_matmul", FAST(call<product<true>>), METH_FASTCALL, nullptr},
+                           {"grouped_weight_gradient", FAST(call<grouped_gradient>), METH_FASTCALL, nullptr},
+                           {"checkpoint_quantize", FAST(call<checkpoint<false>>), METH_FASTCALL, nullptr},
+                           {"checkpoint_dequantize", FAST(call<checkpoint<true>>), METH_FASTCALL, nullptr},
+                           {"gelu_backward_quantize_amax", FAST(call<gelu_backward>), METH_FASTCALL, nullptr},
+                           {"gelu_backward_workspace", FAST(call<gelu_workspace>), METH_FASTCALL, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

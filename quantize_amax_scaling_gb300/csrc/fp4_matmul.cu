@@ -25,8 +25,6 @@
 
 #include "tcgen05.cuh"
 
-#include <atomic>
-
 namespace {
 
 constexpr int kStepBytes = 128;  // bytes of codes a row and step
@@ -76,18 +74,6 @@ struct MmGeom {
     static constexpr int kNeed = kAccCols + kStages * kSfCols;
     static constexpr int kCols = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
 };
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
-}
-
-// A barrier of THREADS of the CTA's threads, whole warps.
-template <int THREADS>
-__device__ __forceinline__ void some_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
-}
 
 template <bool F32>
 __device__ __forceinline__ void store_one(void* d, int64_t at, float v) {
@@ -397,17 +383,6 @@ __device__ __forceinline__ void store_rows(void* d, int64_t first, int64_t ld, i
     }
 }
 
-// Tiles go in bands of eight along P, along Q within a band, so that the tiles
-// under way at one time share rows of both operands in L2.
-struct PairTile {
-    int p, q;
-};
-__device__ __forceinline__ PairTile pair_tile(int tile, int p_tiles, int q_tiles) {
-    const int band = tile / (8 * q_tiles), in = tile - band * 8 * q_tiles;
-    const int high = min(8, p_tiles - band * 8);
-    return {(band * 8 + in % high) * 256, in / high * 256};
-}
-
 template <int FMT, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
@@ -671,26 +646,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 
 // ----------------------------------------------------------------------------
 // Host
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static std::atomic<EncodeTiled> known{nullptr};
-    EncodeTiled f = known.load(std::memory_order_acquire);
-    if (!f) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess) {
-            (void)cudaGetLastError();
-            return nullptr;
-        }
-        f = reinterpret_cast<EncodeTiled>(p);
-        known.store(f, std::memory_order_release);
-    }
-    return f;
-}
 
 // Codes [rows, cols]: boxes of 128 bytes x box_rows rows, zeros beyond the edges.
 bool codes_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t cols, int box_rows) {

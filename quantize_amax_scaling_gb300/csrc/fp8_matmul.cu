@@ -1,0 +1,929 @@
+// fp8_matmul.cu -- the product of two FP8 operands on the tensor cores, with what
+// follows a linear layer in its epilogue; over rows grouped by expert; and the
+// experts' weight gradients.
+//
+//   z = RN(sa sb) sum_k A[m][k] B[n][k] + bias[n],  D = RN(act(z) + residual),
+//   q = FP8(bf16(D) / scale) with amax,  (h, h_sf) = the 8-bit checkpoint of bf16(z)
+//
+// Codes come into shared memory by tensor-map copies of 128 x 128 bytes (128-byte
+// swizzle, zeros beyond the edges).  An operand may lie either way: where its rows
+// are not along k, a box holds 128 of its rows for each of 128 k, and the tensor
+// core reads it across, so the products of a backward pass need no transposed copy.
+//
+// Two kernels.  Few tiles: 128 rows of B by 16 to 128 of A a CTA, k split over a
+// cluster while every CTA is resident.  Many tiles: pairs of CTAs with 256 x 256.
+// Both hand their sums to the same epilogue, four consecutive columns of a row a
+// lane: a row's stores are whole sectors wherever rows start, and any rows and
+// columns may be left out at a group's or the matrix's edge.
+
+#include "checkpoint_calls.cuh"
+#include "tcgen05.cuh"
+
+namespace {
+
+constexpr int kStepK = 128;       // codes of k a step
+constexpr int kBoxBytes = 16384;  // of 128 x 128 codes
+constexpr int kMaxGroups = 512;
+
+struct Epilogue {
+    const float *sa, *sb;
+    const void *bias, *residual;
+    void* d;
+    uint8_t* q;
+    const float* q_scale;
+    float* amax;
+    uint8_t *h, *h_sf;
+    int32_t n;       // columns of D
+    int32_t blocks;  // of 32, a row
+    bool f32, bias_bf16, gelu, e5m2, vec;
+};
+
+// P is the operand whose rows are the accumulator's lanes, Q the one whose rows are its columns.
+struct ProductArgs {
+    Epilogue e;
+    const int32_t* offsets;  // [groups + 1]: group g is rows offsets[g] to offsets[g + 1] of A and D, or of k
+    int32_t groups;
+    int32_t rows;            // A's rows, of all groups; of ragged k: k's
+    int32_t m;               // D's rows, in one group where k is ragged
+    int32_t k;
+    uint32_t idesc;
+    int32_t p_across, q_across;  // P's, Q's rows do not lie along k
+    int32_t p_tiles, q_tiles;    // tiles of a group where all have the same
+    int32_t split;               // CTAs of a cluster that share a tile's k
+#ifdef FP8Q_TEST_HOOKS
+    int32_t fail_role, fail_at, fail_cta;  // the wait that reports failure although what it waits for has come
+#endif
+};
+
+enum PrWait { kPrNone, kPrCopyEmpty, kPrSumFull, kPrSumDrained, kPrMaskFull, kPrOutDone };
+__device__ __forceinline__ bool pr_made_to_fail(const ProductArgs& a, PrWait role, uint32_t at) {
+#ifdef FP8Q_TEST_HOOKS
+    return a.fail_role == role && a.fail_at == (int)at && (a.fail_cta < 0 || a.fail_cta == (int)blockIdx.x);
+#else
+    return false;
+#endif
+}
+// One wait of a whole warp, with one verdict.
+__device__ __forceinline__ bool pr_wait(const ProductArgs& a, PrWait role, uint32_t at, uint64_t* bar, uint32_t parity) {
+    return mbar_wait_all(bar, parity, pr_made_to_fail(a, role, at) && (threadIdx.x & 31) == 5);
+}
+
+// A group's rows; offsets that decrease or leave the tensor make it empty or end at the tensor's end.
+__device__ __forceinline__ int2 group_rows(const ProductArgs& a, int g) {
+    const int lo = min(max(a.offsets[g], 0), a.rows);
+    return make_int2(lo, max(lo, min(a.offsets[g + 1], a.rows)));
+}
+
+// ----------------------------------------------------------------------------
+// Epilogue
+
+// exp and the reciprocal by the hardware's approximations, 2 and 1 units in the last place of binary32: the sum of both is
+// 2^-21 of y beside a rounding to bf16 of 2^-9.  At -infinity the formula is NaN.
+__device__ __forceinline__ float gelu_fast(float x) {
+    // -2 sqrt(2 / pi) log2(e) (x + 0.044715 x^3)
+    const float u = x * fmaf(x * x, -0.102943239f, -2.302208198f);
+    float t, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(u));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    return x * r;
+}
+
+// Four consecutive elements of a row, `left` of them there.
+__device__ __forceinline__ void read4(const void* p, int64_t at, int left, bool f32, bool vec, float (&v)[4]) {
+    if (vec) {
+        if (f32) {
+            const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+            v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
+            v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left)
+                v[i] = f32 ? static_cast<const float*>(p)[at + i] : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[at + i] << 16);
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, const QScale& c) {
+    return c.fast ? quant_quad<FMT, true>(w0, w1, c) : quant_quad<FMT, false>(w0, w1, c);
+}
+
+// What a lane keeps over its columns.
+struct Lane {
+    QScale c;
+    float alpha;
+    uint32_t m2;  // the largest |bf16(D)|
+};
+
+__device__ __forceinline__ Lane make_lane(const Epilogue& e) {
+    Lane l;
+    l.alpha = __fmul_rn(e.sa ? *e.sa : 1.0f, e.sb ? *e.sb : 1.0f);
+    l.c = make_qscale_value(e.q ? *e.q_scale : 1.0f);
+    l.m2 = 0;
+    return l;
+}
+
+// Columns col to col + 3 of a row of D; eight lanes side by side hold a block of 32 columns.  `on`: the row is there.
+// r: the residual.  All lanes of a warp come here.
+__device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, int col, bool on, const float (&sum)[4], const float (&b)[4],
+                                      const float (&r)[4]) {
+    const int left = e.n - col;
+    on = on && left > 0;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaf(sum[i], l.alpha, b[i]);
+    if (e.h) {
+        uint32_t w0 = cvt_bf16x2(v[0], v[1]), w1 = cvt_bf16x2(v[2], v[3]);
+        if (left < 4) {  // beyond the row's end
+            w0 = left < 1 ? 0u : left < 2 ? w0 & 0xFFFFu : w0;
+            w1 = left < 3 ? 0u : w1 & 0xFFFFu;
+        }
+        const uint32_t m = bf16x2_absmax(w0, w1);
+        uint32_t a = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        const uint32_t code = ckpt_scale(a), four = ckpt_codes4(w0, w1, ckpt_factor(code));
+        if (on) {
+            uint8_t* h = e.h + row * e.n + col;
+            if (e.vec)
+                *reinterpret_cast<uint32_t*>(h) = four;
+            else
+                for (int i = 0; i < min(left, 4); ++i) h[i] = (uint8_t)(four >> 8 * i);
+            if ((threadIdx.x & 7) == 0) e.h_sf[row * e.blocks + (col >> 5)] = (uint8_t)code;
+        }
+    }
+    if (!on || !(e.d || e.q || e.amax)) return;
+    if (e.gelu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = gelu_fast(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += r[i];
+    const int64_t at = row * e.n + col;
+    if (e.f32) {
+        float* d = static_cast<float*>(e.d) + at;
+        if (e.vec) {
+            *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) d[i] = v[i];
+        }
+        return;
+    }
+    uint32_t w0 = cvt_bf16x2(v[0], v[1]), w1 = cvt_bf16x2(v[2], v[3]);
+    if (left < 4) w0 = left < 2 ? w0 & 0xFFFFu : w0, w1 = left < 3 ? 0u : w1 & 0xFFFFu;
+    if (e.amax) l.m2 = bf16x2_absmax(l.m2, bf16x2_absmax(w0, w1));
+    if (e.d) {
+        uint16_t* d = static_cast<uint16_t*>(e.d) + at;
+        if (e.vec)
+            *reinterpret_cast<uint2*>(d) = make_uint2(w0, w1);
+        else
+            for (int i = 0; i < min(left, 4); ++i) d[i] = (uint16_t)((i < 2 ? w0 : w1) >> 16 * (i & 1));
+    }
+    if (e.q) {
+        const uint32_t four = e.e5m2 ? codes4<FP8Q_E5M2>(w0, w1, l.c) : codes4<FP8Q_E4M3FN>(w0, w1, l.c);
+        if (e.vec)
+            *reinterpret_cast<uint32_t*>(e.q + at) = four;
+        else
+            for (int i = 0; i < min(left, 4); ++i) e.q[at + i] = (uint8_t)(four >> 8 * i);
+    }
+}
+
+// A warp's largest, once it is through.
+__device__ __forceinline__ void flush_lane(const Epilogue& e, const Lane& l) {
+    if (!e.amax) return;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(l.m2 & 0x7FFFu, l.m2 >> 16 & 0x7FFFu));
+    if ((threadIdx.x & 31) == 0 && m) atomicMax(reinterpret_cast<int*>(e.amax), (int)(m << 16));
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t at, const float* v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t at, float (&v)[4]) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(at) : "memory");
+}
+
+// A box of codes: 128 bytes along k by 128 rows, or 128 rows by 128 lines of k.  The multiply-adds of a step read 32 of k at
+// a time, 32 bytes on in a line or 32 lines on.
+__device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 : 2; }
+
+// ----------------------------------------------------------------------------
+// Few tiles: one CTA a tile, 128 rows of B by BN of A
+
+template <int BN>
+struct PrGeom {
+    static constexpr int kQBytes = BN * kStepK;
+    static constexpr int kStageBytes = kBoxBytes + kQBytes;
+    static constexpr int kStages = BN <= 32 ? 5 : 4;
+    static constexpr int kSmem = kStages * kStageBytes + 1024;  // and room to start on 1024 bytes
+    static constexpr int kCols = BN < 32 ? 32 : BN;             // of tensor memory
+};
+
+// This CTA's share of the tile's rows of A, over the SPLIT CTAs of the cluster whose sums are added in rank order.  A
+// warp takes a row of 128 columns at a time.
+template <int SPLIT, int BN>
+__device__ __forceinline__ void emit_tile(const ProductArgs& a, uint32_t part, int rank, int64_t group, int p0, int q0, int q_end) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = p0 + lane * 4;
+    const Epilogue& e = a.e;
+    Lane l = make_lane(e);
+    float b[4] = {};
+    if (e.bias && col < e.n) read4(e.bias, group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
+    constexpr int kShare = BN / SPLIT;
+#pragma unroll 1
+    for (int t = rank * kShare + warp; t < (rank + 1) * kShare; t += 6) {
+        const int row = q0 + t;
+        if (row >= q_end) break;
+        float r[4] = {}, v[4] = {};
+        if (e.residual && col < e.n) read4(e.residual, (int64_t)row * e.n + col, e.n - col, e.f32, e.vec, r);
+        const uint32_t at = part + t * 512 + lane * 16;
+        if (SPLIT == 1) {
+            ld_shared_v4(at, v);
+        } else {
+            float4 x[SPLIT];
+#pragma unroll
+            for (int i = 0; i < SPLIT; ++i) x[i] = ld_cluster_f32x4(in_cluster(at, i));
+#pragma unroll
+            for (int i = 0; i < SPLIT; ++i) v[0] += x[i].x, v[1] += x[i].y, v[2] += x[i].z, v[3] += x[i].w;
+        }
+        emit4(e, l, row, col, true, v, b, r);
+    }
+    flush_lane(e, l);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                                                         const ProductArgs a) {
+    using G = PrGeom<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[G::kStages], empty[G::kStages], done;
+    __shared__ uint32_t tmem_slot, loads;
+    __shared__ int gave_up;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
+    const int tile = blockIdx.x / a.split;
+
+    if (threadIdx.x == 128) {
+        for (int i = 0; i < G::kStages; ++i) {
+            mbar_init(&full[i]);
+            mbar_init(&empty[i]);
+        }
+        mbar_init(&done);
+        loads = 0;
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    wait_behind();
+    int p0, q0, q_end = a.m, group = 0;
+    if (a.offsets) {
+        // this tile's group: tiles of B fastest, so that the tiles of a group's rows share its weights in L2
+        const int t = tile / a.p_tiles;
+        p0 = tile % a.p_tiles * 128;
+        int before = 0, g0 = 0;
+        bool found = false;
+        for (; g0 < a.groups; g0 += 32) {
+            int2 r = make_int2(0, 0);
+            if (g0 + lane < a.groups) r = group_rows(a, g0 + lane);
+            const int here = (r.y - r.x + BN - 1) / BN;
+            int upto = here;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > t);
+            if (past) {
+                const int i = __ffs(past) - 1;
+                group = g0 + i;
+                q0 = __shfl_sync(0xFFFFFFFFu, r.x, i) + (t - before - __shfl_sync(0xFFFFFFFFu, upto - here, i)) * BN;
+                q_end = __shfl_sync(0xFFFFFFFFu, r.y, i);
+                found = true;
+                break;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        }
+        if (!found) {  // the grid has room for a part of a tile in every group; the whole cluster ends here
+            let_next_start();
+            return;
+        }
+    } else {
+        p0 = tile / a.q_tiles * 128;
+        q0 = tile % a.q_tiles * BN;
+    }
+    // this CTA's steps
+    const int steps = (a.k + kStepK - 1) / kStepK;
+    const int s0 = (int)((int64_t)steps * rank / a.split), s1 = (int)((int64_t)steps * (rank + 1) / a.split);
+    if (warp == 5) {
+        tmem_alloc<1>(&tmem_slot, G::kCols);
+        let_next_start();
+    }
+    uint32_t tmem = 0;
+    if (warp != 4) {  // copies start without it
+        tc_fence_before();
+        some_sync<5 * 32>();
+        tc_fence_after();
+        tmem = tmem_slot;
+    }
+
+    if (warp == 4) {
+        uint32_t st = 0, round = 0, n = 0;
+        bool ok = true;
+        for (int s = s0; s < s1; ++s, ++n) {
+            if (!pr_wait(a, kPrCopyEmpty, n, &empty[st], (round & 1) ^ 1)) {
+                ok = false;
+                break;
+            }
+            const uint32_t at = base + st * G::kStageBytes;
+            if (elect_lane()) {
+                expect_bytes(&full[st], G::kStageBytes);
+                if (a.p_across)
+                    tile_load3(at, &map_p, p0, s * kStepK, group, &full[st]);
+                else
+                    tile_load3(at, &map_p, s * kStepK, p0, group, &full[st]);
+                if (a.q_across)
+                    tile_load3(at + kBoxBytes, &map_q, q0, s * kStepK, 0, &full[st]);
+                else
+                    tile_load3(at + kBoxBytes, &map_q, s * kStepK, q0, 0, &full[st]);
+            }
+            __syncwarp();
+            if (++st == G::kStages) st = 0, ++round;
+        }
+        // the tensor core's last arrivals land before the CTA may go
+        for (uint32_t i = n > G::kStages ? n - G::kStages : 0; i < n && ok; ++i) ok = mbar_wait_all(&empty[i % G::kStages], (i / G::kStages) & 1);
+        if (lane == 0) {
+            if (!ok) gave_up = 1;
+            loads = n;
+        }
+    } else if (warp == 5) {
+        uint32_t st = 0, round = 0;
+        bool ok = true;
+        const uint64_t next_p = k_advance(a.p_across), next_q = k_advance(a.q_across);
+        for (int s = s0; s < s1; ++s) {
+            if (!pr_wait(a, kPrSumFull, s - s0, &full[st], round & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int nk = min(4, (a.k - s * kStepK + 31) / 32);
+            const uint32_t at = base + st * G::kStageBytes;
+            const uint64_t dp = desc_codes(at), dq = desc_codes(at + kBoxBytes);
+            if (elect_lane()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < nk) tc_mma_fp8<1>(tmem, dp + k * next_p, dq + k * next_q, a.idesc, (s - s0) | k);
+                tc_commit(&empty[st]);
+            }
+            __syncwarp();
+            if (++st == G::kStages) st = 0, ++round;
+        }
+        if (elect_lane()) {
+            tc_commit(&done);
+            if (!ok) gave_up = 1;
+        }
+    } else {
+        if (!mbar_wait_warp(&done, 0, 0) || pr_made_to_fail(a, kPrOutDone, 0)) gave_up = 1;
+    }
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    const int bad = gave_up;
+    if (bad) {  // copies still under way end before the CTA does, and before sums (and NaN) lie where they go
+        if (threadIdx.x == 0)
+            for (uint32_t n = loads > G::kStages ? loads - G::kStages : 0; n < loads; ++n) mbar_wait(&full[n % G::kStages], (n / G::kStages) & 1);
+        __syncthreads();
+    }
+    // the sums in shared memory, a row of A's 128 columns side by side; a wait that ran out (correct operation never gets there)
+    // shows as NaN in the whole tile
+    if (warp < 4) {
+        float* part = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
+        const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 16) {
+            float v[16] = {};
+            if (s0 < s1) tmem_load16(row + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(c + i) * 128 + warp * 32 + lane] = bad ? __uint_as_float(0x7FFFFFFFu) : v[i];
+        }
+    }
+    tc_fence_before();
+    if (a.split == 1) {
+        __syncthreads();
+        emit_tile<1, BN>(a, base, 0, group, p0, q0, q_end);
+    } else {
+        cluster_sync_all();
+        switch (a.split) {
+            case 2: emit_tile<2, BN>(a, base, rank, group, p0, q0, q_end); break;
+            case 4: emit_tile<4, BN>(a, base, rank, group, p0, q0, q_end); break;
+            default: emit_tile<8, BN>(a, base, rank, group, p0, q0, q_end);
+        }
+        cluster_sync_all();  // no CTA's sums go away while another reads them
+    }
+    if (warp == 5) tmem_free<1>(tmem, G::kCols);
+}
+
+// ----------------------------------------------------------------------------
+// Pairs: two CTAs of a cluster share tiles of 256 x 256.  Each holds 128 rows of
+// P and of Q and the accumulators of its own rows of P; the first issues the
+// multiply-adds for both, so a row of Q is read from shared memory once for 256
+// rows of P.  Persistent, with two sets of accumulators: the tensor cores go on
+// with the next tile while this one's sums go out.  Here P is A and Q is B.
+//
+// RAGGED_K: k is cut into groups that start and end anywhere, and a group's last
+// step reads rows of the next one.  A warp of each CTA sees every step's codes
+// arrive and, in the last, puts zeros over the lines that are not the group's (both
+// operands': zero times a NaN is none) before it tells the issuer.
+
+constexpr int kPrPairStages = 6;
+constexpr int kPrPairThreads = 352;  // warps 0-7 carry results out, 8 copies codes, 9 multiplies, 10 puts zeros (RAGGED_K)
+constexpr int kPrOut = kPrPairStages * 2 * kBoxBytes;  // 32 rows of 32 sums for each of eight warps
+constexpr int kPrState = kPrOut + 8 * 4096;
+
+// Behind them in shared memory, which starts on 1024 bytes.  full: a stage's codes are there in both CTAs (the first
+// CTA's counts); landed: they are in this one; empty: the stage has been used; done, drained: a set of accumulators is
+// complete, is in registers; stopped: the multiply-adds of an issuer that gave up have ended.
+struct PairState {
+    uint64_t full[kPrPairStages], landed[kPrPairStages], empty[kPrPairStages], done[2], drained[2], stopped;
+    uint32_t tmem_slot, loads;
+    int gave_up;
+    int cum[kMaxGroups + 1];  // row tiles before each group
+};
+constexpr int kPrPairSmem = kPrState + (int)sizeof(PairState);
+static_assert(kPrPairSmem <= 227 * 1024, "");
+
+struct PairWhere {
+    int p0, p_end, q0;  // rows of A (of this CTA's pair's tile, absolute) and of B
+    int group, k0, k;   // codes of k from k0
+};
+template <bool RAGGED_K>
+__device__ __forceinline__ PairWhere pair_where(const ProductArgs& a, const int* cum, int tile) {
+    PairWhere w;
+    w.k0 = 0, w.k = a.k, w.group = 0;
+    if (RAGGED_K) {
+        const int each = a.p_tiles * a.q_tiles;
+        w.group = tile / each;
+        const PairTile t = pair_tile(tile - w.group * each, a.p_tiles, a.q_tiles);
+        const int2 r = group_rows(a, w.group);
+        w.p0 = t.p, w.q0 = t.q, w.p_end = a.m;
+        w.k0 = r.x, w.k = r.y - r.x;
+        return w;
+    }
+    if (!a.offsets) {
+        const PairTile t = pair_tile(tile, a.p_tiles, a.q_tiles);
+        w.p0 = t.p, w.q0 = t.q, w.p_end = a.m;
+        return w;
+    }
+    const int at = tile / a.q_tiles;
+    int lo = 0, hi = a.groups;  // cum[lo] <= at < cum[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= at) lo = mid; else hi = mid;
+    }
+    const PairTile t = pair_tile(tile - cum[lo] * a.q_tiles, cum[lo + 1] - cum[lo], a.q_tiles);
+    const int2 r = group_rows(a, lo);
+    w.group = lo, w.p0 = r.x + t.p, w.p_end = r.y, w.q0 = t.q;
+    return w;
+}
+
+template <bool RAGGED_K>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
+    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const ProductArgs a) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    PairState& sh = *reinterpret_cast<PairState*>(raw + kPrState);
+    uint64_t *full = sh.full, *landed = sh.landed, *empty = sh.empty, *done = sh.done, *drained = sh.drained, &stopped = sh.stopped;
+    uint32_t &tmem_slot = sh.tmem_slot, &loads = sh.loads;
+    volatile int& gave_up = sh.gave_up;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t base = smem_addr(raw);
+    int* cum = sh.cum;
+    const uint32_t rank = cluster_rank();
+    const int stride = gridDim.x / 2, first = blockIdx.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPrPairStages; ++i) {
+            mbar_init_count(&full[i], RAGGED_K ? 2 : 1);
+            mbar_init(&landed[i]);
+            mbar_init(&empty[i]);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i]);
+            mbar_init_count(&drained[i], 16);
+        }
+        mbar_init(&stopped);
+        loads = 0;
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are there
+    wait_behind();
+    if (!RAGGED_K && a.offsets) {
+        if (warp == 0) {
+            int before = 0;
+            for (int g0 = 0; g0 <= a.groups; g0 += 32) {
+                int here = 0;
+                if (g0 + lane < a.groups) {
+                    const int2 r = group_rows(a, g0 + lane);
+                    here = (r.y - r.x + 255) / 256;
+                }
+                int upto = here;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                if (g0 + lane <= a.groups) cum[g0 + lane] = before + upto - here;
+                before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            }
+        }
+        __syncthreads();
+    }
+    const int tiles = RAGGED_K ? a.groups * a.p_tiles * a.q_tiles : a.offsets ? cum[a.groups] * a.q_tiles : a.p_tiles * a.q_tiles;
+    if (warp == 9) {
+        tmem_alloc<2>(&tmem_slot, 512);
+        let_next_start();
+    }
+    uint32_t tmem = 0;
+    if (warp != 8) {  // copies start without it
+        tc_fence_before();
+        some_sync<kPrPairThreads - 32>();
+        tc_fence_after();
+        tmem = *(volatile uint32_t*)&tmem_slot;
+    }
+    cluster_sync_all();  // both CTAs have tensor memory before the first multiplies into it
+
+    if (warp == 8) {
+        uint32_t st = 0, round = 0, n = 0;
+        bool ok = true;
+        const uint32_t bars = in_cluster(smem_addr(&full[0]), 0);
+        for (int tile = first; tile < tiles && ok; tile += stride) {
+            const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
+            const int p0 = w.p0 + (int)rank * 128, q0 = w.q0 + (int)rank * 128;
+            const int bg = RAGGED_K ? 0 : w.group;
+            for (int k = 0; k < w.k; k += kStepK, ++n) {
+                if (!pr_wait(a, kPrCopyEmpty, n, &empty[st], (round & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = base + st * 2 * kBoxBytes, bar = bars + st * 8;
+                const int px = a.p_across ? p0 : k, py = a.p_across ? w.k0 + k : p0;
+                const int qx = a.q_across ? q0 : k, qy = a.q_across ? w.k0 + k : q0;
+                if (elect_lane()) {
+                    if constexpr (RAGGED_K) {
+                        expect_bytes(&landed[st], 2 * kBoxBytes);
+                        tile_load3(at, &map_p, px, py, 0, &landed[st]);
+                        tile_load3(at + kBoxBytes, &map_q, qx, qy, bg, &landed[st]);
+                    } else {
+                        if (rank == 0) expect_bytes(&full[st], 4 * kBoxBytes);
+                        tile_load3_pair(at, &map_p, px, py, 0, bar);
+                        tile_load3_pair(at + kBoxBytes, &map_q, qx, qy, bg, bar);
+                    }
+                }
+                __syncwarp();
+                if (++st == kPrPairStages) st = 0, ++round;
+            }
+        }
+        // The tensor cores' last arrivals land before this CTA may go.
+        for (uint32_t i = 0; i < kPrPairStages && i < n && ok; ++i) {
+            st = st ? st - 1 : kPrPairStages - 1;
+            ok = mbar_wait_all(&empty[st], ((n - 1 - i) / kPrPairStages) & 1);
+        }
+        if (lane == 0) {
+            if (!ok) gave_up = 1;
+            loads = n;
+        }
+    } else if (warp == 9) {
+        if (rank == 0) {
+            uint32_t st = 0, round = 0, it = 0, n = 0;
+            bool ok = true;
+            const uint64_t next_p = k_advance(a.p_across), next_q = k_advance(a.q_across);
+            for (int tile = first; tile < tiles && ok; tile += stride, ++it) {
+                const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
+                const uint32_t set = it & 1, to = tmem + set * 256;
+                if (it > 1 && !pr_wait(a, kPrSumDrained, it, &drained[set], ((it >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int k = 0; k < w.k; k += kStepK, ++n) {
+                    if (!pr_wait(a, kPrSumFull, n, &full[st], round & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int nk = min(4, (w.k - k + 31) / 32);
+                    const uint32_t at = base + st * 2 * kBoxBytes;
+                    const uint64_t dp = desc_codes(at), dq = desc_codes(at + kBoxBytes);
+                    if (elect_lane()) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < nk) tc_mma_fp8<2>(to, dp + i * next_p, dq + i * next_q, a.idesc, k | i);
+                        tc_commit_pair(&empty[st], 3);
+                    }
+                    __syncwarp();
+                    if (++st == kPrPairStages) st = 0, ++round;
+                }
+                // An unfinished tile is never announced as done: those who carry results out run out of time in their
+                // turn, in both CTAs, and write NaN.
+                if (ok && elect_lane()) tc_commit_pair(&done[set], 3);
+                __syncwarp();
+            }
+            // The other CTA's last arrivals land before this one may go.
+            for (uint32_t i = it > 2 ? it - 2 : 0; i < it && ok; ++i) ok = mbar_wait_all(&drained[i & 1], (i >> 1) & 1);
+            if (!ok) {
+                if (elect_lane()) {
+                    tc_commit_pair(&stopped, 1);
+                    gave_up = 1;
+                }
+                __syncwarp();
+                mbar_wait_all(&stopped, 0);
+            }
+        }
+    } else if (warp == 10) {
+        if constexpr (RAGGED_K) {
+            uint32_t st = 0, round = 0, n = 0;
+            bool ok = true;
+            const uint32_t bars = in_cluster(smem_addr(&full[0]), 0);
+            for (int tile = first; tile < tiles && ok; tile += stride) {
+                const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
+                for (int k = 0; k < w.k; k += kStepK, ++n) {
+                    if (!pr_wait(a, kPrMaskFull, n, &landed[st], round & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int there = w.k - k, upto = (there + 31) & ~31;  // lines of the group, and those that are multiplied
+                    if (there < kStepK && there < upto) {
+                        const uint32_t at = base + st * 2 * kBoxBytes;
+                        const float zero[4] = {};
+                        for (int i = there * 8 + lane; i < upto * 8; i += 32) {
+                            st_shared_v4(at + i * 16, zero);
+                            st_shared_v4(at + kBoxBytes + i * 16, zero);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster_release(bars + st * 8);
+                    } else if (lane == 0) {
+                        arrive_cluster(bars + st * 8);
+                    }
+                    __syncwarp();
+                    if (++st == kPrPairStages) st = 0, ++round;
+                }
+            }
+            if (!ok && lane == 0) gave_up = 1;
+        }
+    } else {
+        const Epilogue& e = a.e;
+        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * 128;
+        const uint32_t room = base + kPrOut + warp * 4096;
+        const int sub = lane >> 3, c4 = (lane & 7) * 4;
+        Lane l = make_lane(e);
+        bool ok = true;
+        uint32_t it = 0;
+        for (int tile = first; tile < tiles; tile += stride, ++it) {
+            const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
+            const uint32_t set = it & 1;
+            const uint32_t bar = in_cluster(smem_addr(&drained[set]), 0);
+            const int p_first = w.p0 + (int)rank * 128 + (warp & 3) * 32;
+            const int64_t d_first = (int64_t)p_first + (RAGGED_K ? (int64_t)w.group * a.m : 0);
+            ok = ok && mbar_wait_warp(&done[set], (it >> 1) & 1, 32) && !pr_made_to_fail(a, kPrOutDone, it);
+            if (!ok) gave_up = 1;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                const int q = w.q0 + (warp >> 2) * 128 + c, col = q + c4;
+                float v[32];
+                if (w.k > 0) {
+                    tmem_load32(from + set * 256 + c, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                }
+                if (c == 96) {  // the accumulators are in registers
+                    tc_fence_before();
+                    if (lane == 0) arrive_cluster(bar);
+                }
+                if (q >= e.n || p_first >= w.p_end) continue;
+                // through shared memory: a thread has a row's sums, and four of eight rows go out
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) st_shared_v4(room + lane * 128 + ((j ^ (lane & 7)) << 4), v + 4 * j);
+                __syncwarp();
+                float b[4] = {}, r[8][4] = {};
+                if (e.bias && col < e.n) read4(e.bias, (int64_t)w.group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
+                if (e.residual) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (col < e.n && p_first + i * 4 + sub < w.p_end)
+                            read4(e.residual, (d_first + i * 4 + sub) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = i * 4 + sub;
+                    float x[4];
+                    ld_shared_v4(room + row * 128 + (((lane & 7) ^ (row & 7)) << 4), x);
+                    if (!ok) x[0] = x[1] = x[2] = x[3] = __uint_as_float(0x7FFFFFFFu);  // a wait that ran out shows as NaN
+                    emit4(e, l, d_first + row, col, p_first + row < w.p_end, x, b, r[i]);
+                }
+            }
+        }
+        flush_lane(e, l);
+    }
+    __syncwarp();
+    __syncthreads();
+    if (gave_up && threadIdx.x == 0) {  // copies still under way end before their CTAs do
+        uint64_t* bars = RAGGED_K ? landed : full;
+        for (uint32_t n = loads > kPrPairStages ? loads - kPrPairStages : 0; n < loads && (RAGGED_K || rank == 0); ++n)
+            mbar_wait(&bars[n % kPrPairStages], (n / kPrPairStages) & 1);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 9) tmem_free<2>(tmem, 512);
+    cluster_sync_all();
+}
+
+// ----------------------------------------------------------------------------
+// Host
+
+// Codes: `lines` of `inner` bytes, `groups` times; boxes of 128 bytes x box_lines, zeros beyond the edges.
+bool fp8_map(CUtensorMap* map, const uint8_t* q, int64_t inner, int64_t lines, int64_t ld, int64_t groups, int box_lines) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)inner, (cuuint64_t)lines, (cuuint64_t)groups}, stride[2] = {(cuuint64_t)ld, (cuuint64_t)(ld * lines)};
+    const cuuint32_t box[3] = {kStepK, (cuuint32_t)box_lines, 1}, one[3] = {1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(q), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand of `rows` rows; across: they do not lie along k.
+bool operand_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t k, int64_t ld, int64_t groups, bool across, int box_rows) {
+    return fp8_map(map, q, across ? rows : k, across ? k : rows, ld, groups, across ? kStepK : box_rows);
+}
+
+template <int BN>
+fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, const ProductArgs& a, unsigned grid, cudaStream_t s) {
+    static std::atomic<uint64_t> devices{0};
+    auto kern = fp8_matmul_kernel<BN>;
+    const cudaError_t e = allow_smem(kern, PrGeom<BN>::kSmem, devices);
+    if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_kernel setup");
+    return launch_behind(kern, dim3(grid), dim3(192), PrGeom<BN>::kSmem, (unsigned)a.split, s, "fp8_matmul_kernel", mp, mq, a);
+}
+
+template <bool RAGGED_K>
+fp8q_status launch_product_pairs(const CUtensorMap& mp, const CUtensorMap& mq, const ProductArgs& a, int64_t tiles, cudaStream_t s) {
+    static std::atomic<uint64_t> devices{0};
+    auto kern = fp8_matmul_pair_kernel<RAGGED_K>;
+    const cudaError_t e = allow_smem(kern, kPrPairSmem, devices);
+    if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_pair_kernel setup");
+    const int64_t pairs = sm_count() / 2;
+    const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+    return launch_behind(kern, dim3(grid), dim3(kPrPairThreads), kPrPairSmem, 1, s, "fp8_matmul_pair_kernel", mp, mq, a);
+}
+
+#ifdef FP8Q_TEST_HOOKS
+int g_pr_fail_role = 0, g_pr_fail_at = 0, g_pr_fail_cta = -1;
+#endif
+
+enum Grouping { kWhole, kGroupedRows, kGroupedK };
+
+fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t groups, Grouping how, void* stream) {
+    if (!p || p->m < 0 || p->n < 0 || p->k < 0 || (how != kWhole && groups < 0)) return FP8Q_ERR_INVALID_ARG;
+    if (!valid_fmt(p->a_fmt) || !valid_fmt(p->b_fmt) || (p->out != FP8Q_OUT_BF16 && p->out != FP8Q_OUT_F32)) return FP8Q_ERR_INVALID_ARG;
+    if (p->act != FP8Q_ACT_NONE && p->act != FP8Q_ACT_GELU) return FP8Q_ERR_INVALID_ARG;
+    if (p->m > kFp4MaxDim || p->n > kFp4MaxDim || p->k > kFp4MaxDim || (how != kWhole && groups > kMaxGroups)) return FP8Q_ERR_UNSUPPORTED;
+    if (p->m == 0 || p->n == 0 || (how != kWhole && groups == 0)) return FP8Q_OK;
+    if (!p->d && !p->q && !p->h && !p->amax) return FP8Q_ERR_INVALID_ARG;
+    if (p->q ? (!valid_fmt(p->q_fmt) || !p->q_scale) : p->q_scale != nullptr) return FP8Q_ERR_INVALID_ARG;
+    if (p->out == FP8Q_OUT_F32 && (!p->d || p->q || p->amax)) return FP8Q_ERR_INVALID_ARG;
+    if ((p->h != nullptr) != (p->h_sf != nullptr)) return FP8Q_ERR_INVALID_ARG;
+    if (how == kGroupedK && (p->bias || p->act != FP8Q_ACT_NONE || p->q || p->amax || p->h || !p->a_trans || !p->b_trans))
+        return FP8Q_ERR_INVALID_ARG;
+    if ((how == kGroupedRows && p->a_trans) || (how != kWhole && !offsets)) return FP8Q_ERR_INVALID_ARG;
+    if (p->k > 0) {
+        if (!p->a || !p->b) return FP8Q_ERR_INVALID_ARG;
+        if (p->lda < (p->a_trans ? p->m : p->k) || p->ldb < (p->b_trans ? p->n : p->k)) return FP8Q_ERR_INVALID_ARG;
+    }
+    const uintptr_t odd2 = (uintptr_t)(p->out == FP8Q_OUT_BF16 ? p->d : nullptr) | (uintptr_t)(p->out == FP8Q_OUT_BF16 ? p->residual : nullptr) |
+                           (uintptr_t)(p->bias_is_bf16 ? p->bias : nullptr);
+    const uintptr_t odd4 = (uintptr_t)(p->out == FP8Q_OUT_F32 ? p->d : nullptr) | (uintptr_t)(p->out == FP8Q_OUT_F32 ? p->residual : nullptr) |
+                           (uintptr_t)(p->bias_is_bf16 ? nullptr : p->bias) | (uintptr_t)p->a_scale | (uintptr_t)p->b_scale |
+                           (uintptr_t)p->q_scale | (uintptr_t)p->amax | (uintptr_t)offsets;
+    if ((odd2 & 1u) || (odd4 & 3u)) return FP8Q_ERR_INVALID_ARG;
+    if (p->k > 0 && ((((uintptr_t)p->a | (uintptr_t)p->b) & 15u) || ((p->lda | p->ldb) & 15))) return FP8Q_ERR_UNSUPPORTED;
+    // a tensor map's strides have 40 bits
+    if (p->k > 0 && (p->lda >= (1ll << 31) || p->ldb >= (1ll << 31) ||
+                     (how == kGroupedRows && groups > 1 && p->ldb * (p->b_trans ? p->k : p->n) >= (1ll << 40))))
+        return FP8Q_ERR_UNSUPPORTED;
+
+    ProductArgs a = {};
+#ifdef FP8Q_TEST_HOOKS
+    a.fail_role = g_pr_fail_role;
+    a.fail_at = g_pr_fail_at;
+    a.fail_cta = g_pr_fail_cta;
+#endif
+    Epilogue& e = a.e;
+    e.sa = p->a_scale;
+    e.sb = p->b_scale;
+    e.bias = p->bias;
+    e.residual = p->residual;
+    e.d = p->d;
+    e.q = p->q;
+    e.q_scale = p->q_scale;
+    e.amax = p->amax;
+    e.h = p->h;
+    e.h_sf = p->h_sf;
+    e.n = (int32_t)p->n;
+    e.blocks = (int32_t)((p->n + 31) / 32);
+    e.f32 = p->out == FP8Q_OUT_F32;
+    e.bias_bf16 = p->bias_is_bf16 != 0;
+    e.gelu = p->act == FP8Q_ACT_GELU;
+    e.e5m2 = p->q_fmt == FP8Q_E5M2;
+    // four columns at a time
+    const uintptr_t wide = (uintptr_t)p->d | (uintptr_t)p->residual;
+    e.vec = p->n % 4 == 0 && (wide & (e.f32 ? 15u : 7u)) == 0 && ((uintptr_t)p->bias & (e.bias_bf16 ? 7u : 15u)) == 0 &&
+            (((uintptr_t)p->q | (uintptr_t)p->h) & 3u) == 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    a.offsets = offsets;
+    a.groups = how == kWhole ? 1 : groups;
+    a.rows = (int32_t)(how == kGroupedK ? p->k : p->m);
+    a.m = (int32_t)p->m;
+    a.k = (int32_t)p->k;
+    const int fa = p->a_fmt == FP8Q_E5M2, fb = p->b_fmt == FP8Q_E5M2, ta = p->a_trans != 0, tb = p->b_trans != 0;
+    const int64_t b_groups = how == kGroupedRows ? groups : 1;
+    const int sms = sm_count();
+    const int64_t blocks = (p->m + 127) / 128 * ((p->n + 127) / 128);
+    const bool pairs = how == kGroupedK || (how == kGroupedRows ? p->m > 64 * (int64_t)groups : p->m > 128 && p->n > 128 && blocks > sms);
+    CUtensorMap mp = {}, mq = {};
+    if (pairs) {
+        a.idesc = mma_desc_fp8(256, 256, fa, fb, ta, tb);
+        a.p_across = ta;
+        a.q_across = tb;
+        a.split = 1;
+        a.p_tiles = (int32_t)((p->m + 255) / 256);
+        a.q_tiles = (int32_t)((p->n + 255) / 256);
+        const int64_t tiles = (how == kGroupedRows ? p->m / 256 + groups : (int64_t)a.p_tiles * (how == kGroupedK ? groups : 1)) * a.q_tiles;
+        if (tiles > 0x3FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
+        if (p->k > 0 && (!operand_map(&mp, p->a, p->m, p->k, p->lda, 1, ta, 128) || !operand_map(&mq, p->b, p->n, p->k, p->ldb, b_groups, tb, 128)))
+            return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_pair_kernel tensor map");
+        return how == kGroupedK ? launch_product_pairs<true>(mp, mq, a, tiles, s)
+                                : launch_product_pairs<false>(mp, mq, a, tiles, s);
+    }
+    // P is B and Q is A; a box of A across k is always 128 rows wide
+    const int64_t each = how == kGroupedRows ? (p->m + groups - 1) / groups : p->m;
+    const int bn = ta ? 128 : each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
+    const int steps = (int)((p->k + kStepK - 1) / kStepK);
+    a.idesc = mma_desc_fp8(128, bn, fb, fa, tb, ta);
+    a.p_across = tb;
+    a.q_across = ta;
+    a.p_tiles = (int32_t)((p->n + 127) / 128);
+    a.q_tiles = (int32_t)((p->m + bn - 1) / bn);
+    // a grouped call does not know its groups: at most as many tiles as full ones and one part of a tile in each
+    int64_t q_tiles = a.q_tiles;
+    if (how == kGroupedRows) q_tiles = p->m / bn + (groups < p->m ? groups : p->m);
+    const int64_t tiles = a.p_tiles * q_tiles, room = (bn <= 32 ? 2 : 1) * sms;
+    int split = 1, most = 1;
+    while (most < 8 && tiles * most * 2 <= room * (most == 1 ? 20 : most == 2 ? 19 : 16) / 20 && steps >= most * 4) most *= 2;
+    if (steps - steps / most > 3 + bn / 32) split = most;
+    a.split = split;
+    if (tiles * split > 0x7FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
+    if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, 128) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
+        return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_kernel tensor map");
+    const unsigned grid = (unsigned)(tiles * split);
+    switch (bn) {
+        case 16: return launch_product<16>(mp, mq, a, grid, s);
+        case 32: return launch_product<32>(mp, mq, a, grid, s);
+        case 64: return launch_product<64>(mp, mq, a, grid, s);
+        default: return launch_product<128>(mp, mq, a, grid, s);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+#ifdef FP8Q_TEST_HOOKS  // the wait of that role (PrWait) at that step or tile reports failure, in one CTA or (cta < 0) in all
+void fp8q_test_set_product_give_up(int role, int at, int cta) {
+    g_pr_fail_role = role;
+    g_pr_fail_at = at;
+    g_pr_fail_cta = cta;
+}
+#endif
+
+fp8q_status fp8q_matmul(const fp8q_product* args, void* stream) { return product(args, nullptr, 0, kWhole, stream); }
+
+fp8q_status fp8q_grouped_matmul(const fp8q_product* args, const int32_t* offsets, int32_t groups, void* stream) {
+    return product(args, offsets, groups, kGroupedRows, stream);
+}
+
+fp8q_status fp8q_grouped_weight_gradient(const fp8q_product* args, const int32_t* offsets, int32_t groups, void* stream) {
+    return product(args, offsets, groups, kGroupedK, stream);
+}
+
+}  // extern "C"

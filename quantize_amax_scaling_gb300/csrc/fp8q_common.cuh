@@ -1,8 +1,8 @@
 // fp8q_common.cuh -- what the kernels of libfp8q share: launch geometry,
 // bf16/FP8 conversions, the exact division by the scale, the CTA-wide amax
 // flush, and host-side error reporting.  The kernels and their C ABI entry
-// points live in quantize.cu, producers.cu, scale_update.cu, fp4_quantize.cu,
-// fp4_matmul.cu and residual_norm.cu; abi.cu holds the status strings.
+// points live in quantize.cu, producers.cu, scale_update.cu (and the status
+// strings), fp4_quantize.cu, fp4_matmul.cu, residual_norm.cu and fp8_matmul.cu.
 //
 // Sources (web pages, by title and section):
 //   "User Guide on Native XLA-FP8" (NVIDIA JAX-Toolbox), section "JAX":
@@ -13,8 +13,8 @@
 //   "Implement fused kernel for FP8 scale update" (TransformerEngine PR):
 //     the whole amax_and_scale_update in one in-place kernel, all layers.
 //
-// Every kernel but the 4-bit product (fp4_matmul.cu) streams HBM; that one runs
-// on the tensor cores.  Design points of quantize.cu, producers.cu and
+// Every kernel but the products (fp4_matmul.cu, fp8_matmul.cu) streams HBM; those
+// run on the tensor cores.  Design points of quantize.cu, producers.cu and
 // scale_update.cu (the others state their own):
 //   * quantize+amax reads each bf16 once (32-byte vector loads), writes each
 //     FP8 byte once (16-byte stores), and reduces |x| with packed
@@ -62,7 +62,7 @@
 #include <cstdint>
 #include <cstdio>
 
-// Host-side error reporting, shared by every translation unit (abi.cu).
+// Host-side error reporting, shared by every translation unit (scale_update.cu).
 namespace fp8q_detail {
 fp8q_status cuda_fail(cudaError_t e, const char* where);   // records the text, returns FP8Q_ERR_CUDA
 extern thread_local char g_last_error[256];

@@ -1,6 +1,6 @@
 // tcgen05.cuh -- the fifth-generation tensor core's instructions that the 4-bit
-// product uses: tensor memory, block-scaled multiply-add, and the copies that
-// feed it.  Documented PTX only.
+// and the 8-bit products use: tensor memory, the multiply-adds, and the copies
+// that feed them.  Documented PTX only.
 
 #pragma once
 
@@ -8,6 +8,8 @@
 #include "mbarrier.cuh"
 
 #include <cuda.h>
+
+#include <atomic>
 
 namespace {
 
@@ -187,6 +189,27 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 #undef FP8Q_MMA
 }
 
+// Instruction descriptor of the FP8 product: formats (0 e4m3, 1 e5m2), whether
+// an operand's rows lie along m or n (transposed) and not along k, N columns, M rows.
+__host__ __device__ constexpr uint32_t mma_desc_fp8(uint32_t m, uint32_t n, uint32_t fa, uint32_t fb, uint32_t ta, uint32_t tb) {
+    return (1u << 4) | (fa << 7) | (fb << 10) | (ta << 15) | (tb << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// d (+)= A B^T over 32 FP8 codes.
+template <int PAIR>
+__device__ __forceinline__ void tc_mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+#define FP8Q_MMA(group)                                                                                   \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                        \
+                 "tcgen05.mma.cta_group::" group ".kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),      \
+                 "l"(a), "l"(b), "r"(idesc), "r"(add)                                                     \
+                 : "memory")
+    if (PAIR == 2)
+        FP8Q_MMA("2");
+    else
+        FP8Q_MMA("1");
+#undef FP8Q_MMA
+}
+
 // *bar completes a phase when everything this thread has given to the tensor core is done.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -227,6 +250,23 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// arrive_cluster() that orders this thread's stores to shared memory as well.
+__device__ __forceinline__ void arrive_cluster_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A barrier of THREADS of the CTA's threads, whole warps.
+template <int THREADS>
+__device__ __forceinline__ void some_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
 __device__ __forceinline__ void arrive_local(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -258,6 +298,21 @@ __device__ __forceinline__ void tile_load_pair(uint32_t dst, const CUtensorMap* 
         : "memory");
 }
 
+// Of three dimensions.
+__device__ __forceinline__ void tile_load3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tile_load3_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void block_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                  "r"(bytes), "r"(smem_addr(bar))
@@ -278,5 +333,39 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 }
 __device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// ----------------------------------------------------------------------------
+// Tiles of 256 x 256, and tensor maps
+
+// Tiles go in bands of eight along P, along Q within a band, so that the tiles
+// under way at one time share rows of both operands in L2.
+struct PairTile {
+    int p, q;
+};
+__device__ __forceinline__ PairTile pair_tile(int tile, int p_tiles, int q_tiles) {
+    const int band = tile / (8 * q_tiles), in = tile - band * 8 * q_tiles;
+    const int high = min(8, p_tiles - band * 8);
+    return {(band * 8 + in % high) * 256, in / high * 256};
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static std::atomic<EncodeTiled> known{nullptr};
+    EncodeTiled f = known.load(std::memory_order_acquire);
+    if (!f) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            return nullptr;
+        }
+        f = reinterpret_cast<EncodeTiled>(p);
+        known.store(f, std::memory_order_release);
+    }
+    return f;
+}
 
 }  // namespace

@@ -3,8 +3,8 @@
 Argument marshalling only: every step of the path runs in the CUDA kernels of
 libfp8q.so.  Tensors are torch CUDA tensors (torch supplies device memory and
 streams); the functions keep the C names and raise Fp8qError on a non-OK
-status.  The 8-bit calls go through ctypes, the 4-bit and residual-norm calls
-through a compiled module (csrc/binding.cpp), which takes 2 to 3 us a call where
+status.  The first nine calls go through ctypes, the 4-bit calls and those behind
+them through a compiled module (csrc/binding.cpp), which takes 2 to 3 us a call where
 a single token's kernel takes 2 to 5; either lets other Python threads run
 meanwhile.  If the library has not been built, loading fails loudly -- there is
 no fallback.
@@ -18,6 +18,8 @@ E4M3FN = 0
 E5M2 = 1
 MXFP4 = 2
 NVFP4 = 3
+ACT_NONE = 0
+ACT_GELU = 1
 ALGO_MAX = 0
 ALGO_MOST_RECENT = 1
 MAX_TENSORS = 512
@@ -25,12 +27,14 @@ MAX_TENSORS = 512
 STATUS = {0: "FP8Q_OK", 1: "FP8Q_ERR_INVALID_ARG", 2: "FP8Q_ERR_UNSUPPORTED", 3: "FP8Q_ERR_CUDA",
           4: "FP8Q_ERR_TOO_MANY_TENSORS"}
 
-# Every symbol the header declares, but the three that only count bytes.
+# Every symbol the header declares, but the five that only count bytes.
 EXPORTS = ("fp8q_quantize_amax", "fp8q_multi_quantize_amax", "fp8q_dequantize",
            "fp8q_amax_scale_update", "fp8q_qdq_amax", "fp8q_amax_scale_update_ring",
            "fp8q_gelu_quantize_amax", "fp8q_layernorm_quantize_amax",
            "fp8q_amax_scale_update_ring_quantize", "fp8q_fp4_quantize_amax", "fp8q_fp4_dequantize",
            "fp8q_fp4_matmul", "fp8q_residual_norm_quantize_amax", "fp8q_residual_norm_backward",
+           "fp8q_matmul", "fp8q_grouped_matmul", "fp8q_grouped_weight_gradient", "fp8q_checkpoint_quantize",
+           "fp8q_checkpoint_dequantize", "fp8q_gelu_backward_quantize_amax",
            "fp8q_status_string", "fp8q_last_cuda_error")
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8q.so")
@@ -72,6 +76,23 @@ class ResidualNormGrad(ctypes.Structure):
                 ("d_gate", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+class Product(ctypes.Structure):
+    """fp8q_product: the arguments of fp8q_matmul, fp8q_grouped_matmul and fp8q_grouped_weight_gradient."""
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("a_fmt", ctypes.c_int), ("b_fmt", ctypes.c_int),
+                ("a_trans", ctypes.c_int32), ("b_trans", ctypes.c_int32), ("a_scale", ctypes.c_void_p), ("b_scale", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("bias_is_bf16", ctypes.c_int32), ("act", ctypes.c_int), ("residual", ctypes.c_void_p),
+                ("d", ctypes.c_void_p), ("out", ctypes.c_int), ("q_fmt", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("q_scale", ctypes.c_void_p), ("amax", ctypes.c_void_p), ("h", ctypes.c_void_p), ("h_sf", ctypes.c_void_p)]
+
+
+class GeluGrad(ctypes.Structure):
+    """fp8q_gelu_grad: the arguments of fp8q_gelu_backward_quantize_amax."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("fmt", ctypes.c_int), ("d_y", ctypes.c_void_p), ("h", ctypes.c_void_p),
+                ("h_sf", ctypes.c_void_p), ("d_x", ctypes.c_void_p), ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("amax", ctypes.c_void_p), ("d_bias", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -103,11 +124,23 @@ def lib() -> ctypes.CDLL:
         L.fp8q_residual_norm_backward.argtypes = [vp, vp]
         L.fp8q_residual_norm_backward_workspace.argtypes = [i64, i32, i64]
         L.fp8q_residual_norm_backward_workspace.restype = i64
+        L.fp8q_matmul.argtypes = [vp, vp]
+        L.fp8q_grouped_matmul.argtypes = [vp, vp, i32, vp]
+        L.fp8q_grouped_weight_gradient.argtypes = [vp, vp, i32, vp]
+        L.fp8q_checkpoint_scale_bytes.argtypes = [i64, i64]
+        L.fp8q_checkpoint_scale_bytes.restype = i64
+        L.fp8q_checkpoint_quantize.argtypes = [vp, vp, vp, i64, i64, vp]
+        L.fp8q_checkpoint_dequantize.argtypes = [vp, vp, vp, i64, i64, vp]
+        L.fp8q_gelu_backward_workspace.argtypes = [i64, i64]
+        L.fp8q_gelu_backward_workspace.restype = i64
+        L.fp8q_gelu_backward_quantize_amax.argtypes = [vp, vp]
         for f in ("fp8q_quantize_amax", "fp8q_multi_quantize_amax", "fp8q_dequantize",
                   "fp8q_amax_scale_update", "fp8q_qdq_amax", "fp8q_amax_scale_update_ring",
                   "fp8q_gelu_quantize_amax", "fp8q_layernorm_quantize_amax",
                   "fp8q_amax_scale_update_ring_quantize", "fp8q_fp4_quantize_amax", "fp8q_fp4_dequantize",
-                  "fp8q_fp4_matmul", "fp8q_residual_norm_quantize_amax", "fp8q_residual_norm_backward"):
+                  "fp8q_fp4_matmul", "fp8q_residual_norm_quantize_amax", "fp8q_residual_norm_backward", "fp8q_matmul",
+                  "fp8q_grouped_matmul", "fp8q_grouped_weight_gradient", "fp8q_checkpoint_quantize",
+                  "fp8q_checkpoint_dequantize", "fp8q_gelu_backward_quantize_amax"):
             getattr(L, f).restype = c_int
         L.fp8q_status_string.argtypes = [c_int]
         L.fp8q_status_string.restype = ctypes.c_char_p
@@ -121,7 +154,7 @@ _binding = None
 
 
 def _native():
-    """The compiled marshalling (csrc/binding.cpp) of the 4-bit and residual-norm calls, on libfp8q's entry points."""
+    """The compiled marshalling (csrc/binding.cpp) of the calls from the 4-bit ones on, on libfp8q's entry points."""
     global _binding
     if _binding is not None:
         return _binding
@@ -134,7 +167,9 @@ def _native():
     from . import _binding as b
     b.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
              (L.fp8q_fp4_quantize_amax, L.fp8q_fp4_dequantize, L.fp8q_fp4_matmul, L.fp8q_residual_norm_quantize_amax,
-              L.fp8q_residual_norm_backward, L.fp8q_residual_norm_backward_workspace)))
+              L.fp8q_residual_norm_backward, L.fp8q_residual_norm_backward_workspace, L.fp8q_matmul, L.fp8q_grouped_matmul,
+              L.fp8q_grouped_weight_gradient, L.fp8q_checkpoint_quantize, L.fp8q_checkpoint_dequantize,
+              L.fp8q_gelu_backward_quantize_amax, L.fp8q_gelu_backward_workspace)))
     _binding = b
     return b
 
@@ -486,6 +521,77 @@ def fp8q_residual_norm_backward(d_residual_out, d_h, residual_out, rstd_pre, pre
                                           d_block, d_post_weight, d_gate, workspace, stream)
     if st:
         _check(st, "fp8q_residual_norm_backward")
+
+
+def fp8q_matmul(a, b, d=None, a_fmt=E4M3FN, b_fmt=E4M3FN, a_scale=None, b_scale=None, a_trans=False, b_trans=False, bias=None,
+                act=ACT_NONE, residual=None, q=None, q_fmt=E4M3FN, q_scale=None, amax=None, h=None, h_sf=None, stream=None):
+    """d [m, n] = act(A B^T a_scale b_scale + bias) + residual, of A [m, k] (stored [k, m] with ``a_trans``) and
+    B [n, k] ([k, n] with ``b_trans``), both FP8 codes whose rows may lie any multiple of 16 bytes apart.
+
+    ``d`` is bf16 or float32; beside it or in its place q = FP8(bf16 result / q_scale), amax = max(amax, max|bf16
+    result|), and (h, h_sf), the checkpoint of what ``act`` is applied to.  ``bias`` is float32 or bf16 [n];
+    ``residual`` has d's type (bf16 without d) and may be d.
+    """
+    st = _native().matmul(a, b, d, a_fmt, b_fmt, a_scale, b_scale, a_trans, b_trans, bias, act, residual, q, q_fmt, q_scale,
+                          amax, h, h_sf, stream)
+    if st:
+        _check(st, "fp8q_matmul")
+
+
+def fp8q_grouped_matmul(a, b, offsets, d=None, a_fmt=E4M3FN, b_fmt=E4M3FN, a_scale=None, b_scale=None, b_trans=False, bias=None,
+                        act=ACT_NONE, residual=None, q=None, q_fmt=E4M3FN, q_scale=None, amax=None, h=None, h_sf=None,
+                        stream=None):
+    """fp8q_matmul of each group's rows of ``a`` [m, k] by its own matrix of ``b`` [groups, n, k] ([groups, k, n] with
+    ``b_trans``) and its own ``bias`` [groups, n].  Group g is rows offsets[g] to offsets[g + 1] - 1 (int32 on the
+    device, read by the kernel); rows of no group are left as they were."""
+    st = _native().grouped_matmul(a, b, d, a_fmt, b_fmt, a_scale, b_scale, False, b_trans, bias, act, residual, q, q_fmt, q_scale,
+                                  amax, h, h_sf, offsets, stream)
+    if st:
+        _check(st, "fp8q_grouped_matmul")
+
+
+def fp8q_grouped_weight_gradient(a, b, offsets, d, a_fmt=E5M2, b_fmt=E4M3FN, a_scale=None, b_scale=None, residual=None, stream=None):
+    """d [groups, m, n] (bf16 or float32): for each group the sum over its rows t of a[t]^T b[t] a_scale b_scale, plus
+    ``residual`` (d's type, may be d).  ``a`` is [rows, m], ``b`` [rows, n]; an empty group's sum is zeros."""
+    st = _native().grouped_weight_gradient(a, b, offsets, d, a_fmt, b_fmt, a_scale, b_scale, residual, stream)
+    if st:
+        _check(st, "fp8q_grouped_weight_gradient")
+
+
+def checkpoint_empty(rows, cols, device="cuda"):
+    """Room for the 8-bit checkpoint of an [rows, cols] activation: (codes [rows, cols], scales [rows, blocks of 32])."""
+    import torch
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+            torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=device))
+
+
+def fp8q_checkpoint_quantize(x, q, sf, stream=None):
+    """(q, sf) = the 8-bit checkpoint of x [rows, cols]: e4m3 codes under a power of two for each 32 columns of a row."""
+    st = _native().checkpoint_quantize(x, q, sf, stream)
+    if st:
+        _check(st, "fp8q_checkpoint_quantize")
+
+
+def fp8q_checkpoint_dequantize(q, sf, y, stream=None):
+    """y [rows, cols] = bf16 of what the checkpoint (q, sf) stands for."""
+    st = _native().checkpoint_dequantize(q, sf, y, stream)
+    if st:
+        _check(st, "fp8q_checkpoint_dequantize")
+
+
+def gelu_backward_workspace(rows, cols):
+    """Bytes of workspace of fp8q_gelu_backward_quantize_amax with d_bias."""
+    return _native().gelu_backward_workspace(rows, cols)
+
+
+def fp8q_gelu_backward_quantize_amax(d_y, h, h_sf, q=None, fmt=E5M2, scale=None, amax=None, d_x=None, d_bias=None, workspace=None,
+                                     stream=None):
+    """D = d_y GELU'(h) from the checkpoint (h, h_sf) of the GELU's input (both None: D = d_y); d_x = bf16(D), q = FP8(d_x /
+    scale), amax = max(amax, max|d_x|) and d_bias (float32 [cols]) = the sum of D over rows, each where it is given.
+    ``workspace``: gelu_backward_workspace bytes (uint8) with d_bias, for one call at a time."""
+    st = _native().gelu_backward_quantize_amax(d_y, h, h_sf, q, fmt, scale, amax, d_x, d_bias, workspace, stream)
+    if st:
+        _check(st, "fp8q_gelu_backward_quantize_amax")
 
 
 def status_string(status: int) -> str:
