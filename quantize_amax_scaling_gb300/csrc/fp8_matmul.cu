@@ -35,7 +35,9 @@ struct Epilogue {
     uint8_t *h, *h_sf;
     int32_t n;       // columns of D
     int32_t blocks;  // of 32, a row
-    bool f32, bias_bf16, gelu, e5m2, vec;
+    bool f32, bias_bf16, gelu, e5m2;
+    bool vec;   // four columns a vector, and
+    bool wide;  // sixteen bytes a vector, wherever a row starts
 };
 
 // P is the operand whose rows are the accumulator's lanes, Q the one whose rows are its columns.
@@ -220,6 +222,7 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
         for (int i = 0; i < ROWS; ++i) emit4(e, l, row + i * step, col, on >> i & 1, v[i], b, r[i]);
         return;
     }
+    const uint32_t here = (col & ~31) < e.n ? on : 0u;  // of a block's eight lanes the first may be the only one with columns
     if (col >= e.n) on = 0;
     const float2 alpha = splat2(l.alpha), b0 = make_float2(b[0], b[1]), b1 = make_float2(b[2], b[3]);
     float2 x[ROWS][2];
@@ -231,25 +234,28 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
     const int64_t at = row * e.n + col, next = (int64_t)step * e.n;
     uint32_t w[ROWS][2];
     if (e.h) {
-        uint32_t a[ROWS];
+        uint32_t a[ROWS], mine = 0;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             w[i][0] = cvt_bf16x2(x[i][0].x, x[i][0].y), w[i][1] = cvt_bf16x2(x[i][1].x, x[i][1].y);
-            const uint32_t m = bf16x2_absmax(w[i][0], w[i][1]);
-            a[i] = col < e.n ? max(m & 0x7FFFu, m >> 16 & 0x7FFFu) : 0u;
+            a[i] = col < e.n ? bf16x2_absmax(w[i][0], w[i][1]) : 0u;
         }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) a[i] = max(a[i], __shfl_xor_sync(0xFFFFFFFFu, a[i], o));
+            for (int i = 0; i < ROWS; ++i) a[i] = bf16x2_absmax(a[i], __shfl_xor_sync(0xFFFFFFFFu, a[i], o));
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const uint32_t code = ckpt_scale(a[i]), four = ckpt_codes4(w[i][0], w[i][1], ckpt_factor(code));
-            if (on >> i & 1) {
-                *reinterpret_cast<uint32_t*>(e.h + at + i * next) = four;
-                if ((threadIdx.x & 7) == 0) e.h_sf[(row + i * step) * e.blocks + (col >> 5)] = (uint8_t)code;
-            }
+            const uint32_t code = ckpt_scale(max(a[i] & 0x7FFFu, a[i] >> 16 & 0x7FFFu));
+            a[i] = ckpt_codes4(w[i][0], w[i][1], ckpt_factor(code));
+            if ((threadIdx.x & 7) == i) mine = code;
         }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (on >> i & 1) *reinterpret_cast<uint32_t*>(e.h + at + i * next) = a[i];
+        // each of the eight lanes of a block stores a row's scale
+        const int i = threadIdx.x & 7;
+        if (i < ROWS && (here >> i & 1)) e.h_sf[(row + i * step) * e.blocks + (col >> 5)] = (uint8_t)mine;
     }
     if (e.gelu) {
 #pragma unroll
@@ -291,6 +297,97 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
             if (on >> i & 1) *reinterpret_cast<uint32_t*>(e.q + at + i * next) = four[i];
+    }
+}
+
+// Thirty-two columns from col on, all there, of one row a lane, as tensor memory gives them: nothing passes between lanes, and a
+// block of the checkpoint is a lane's own.  For bf16, n a multiple of 16, 16-byte addresses and an ordinary scale.  (The
+// checkpoint's blocks over eight lanes each and codes through shared memory cost 105 us of 8192x16384x4096's 353, zeros for
+// operands; here 0.)
+__device__ __forceinline__ float2 as_f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
+__device__ __forceinline__ float2 bf16_f2(uint32_t w) { return as_f2(w << 16, w & 0xFFFF0000u); }
+
+__device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t row, int col, int64_t bias_at, const float (&v)[32], const uint4 (&r)[4]) {
+    float2 x[16];
+    const float2 alpha = splat2(l.alpha);
+    if (e.bias && e.bias_bf16) {
+        const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + bias_at + col);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 y = b[i];
+            x[4 * i] = fma2_rn(make_float2(v[8 * i], v[8 * i + 1]), alpha, bf16_f2(y.x));
+            x[4 * i + 1] = fma2_rn(make_float2(v[8 * i + 2], v[8 * i + 3]), alpha, bf16_f2(y.y));
+            x[4 * i + 2] = fma2_rn(make_float2(v[8 * i + 4], v[8 * i + 5]), alpha, bf16_f2(y.z));
+            x[4 * i + 3] = fma2_rn(make_float2(v[8 * i + 6], v[8 * i + 7]), alpha, bf16_f2(y.w));
+        }
+    } else if (e.bias) {
+        const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + bias_at + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 y = b[i];
+            x[2 * i] = fma2_rn(make_float2(v[4 * i], v[4 * i + 1]), alpha, make_float2(y.x, y.y));
+            x[2 * i + 1] = fma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), alpha, make_float2(y.z, y.w));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = mul2_rn(make_float2(v[2 * i], v[2 * i + 1]), alpha);
+    }
+    const int64_t at = row * e.n + col;
+    uint32_t w[16];
+    if (e.h) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(x[i].x, x[i].y);
+        uint32_t m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = bf16x2_absmax(w[i], w[i + 8]);
+#pragma unroll
+        for (int o = 4; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < o; ++i) m[i] = bf16x2_absmax(m[i], m[i + o]);
+        const uint32_t code = ckpt_scale(max(m[0] & 0x7FFFu, m[0] >> 16 & 0x7FFFu));
+        const float f = ckpt_factor(code);
+        uint4* h = reinterpret_cast<uint4*>(e.h + at);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            h[i] = make_uint4(ckpt_codes4(w[8 * i], w[8 * i + 1], f), ckpt_codes4(w[8 * i + 2], w[8 * i + 3], f),
+                              ckpt_codes4(w[8 * i + 4], w[8 * i + 5], f), ckpt_codes4(w[8 * i + 6], w[8 * i + 7], f));
+        e.h_sf[row * e.blocks + (col >> 5)] = (uint8_t)code;
+    }
+    if (e.gelu) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = gelu2(x[i]);
+    }
+    if (e.residual) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[4 * i] = add2_rn(x[4 * i], bf16_f2(r[i].x)), x[4 * i + 1] = add2_rn(x[4 * i + 1], bf16_f2(r[i].y));
+            x[4 * i + 2] = add2_rn(x[4 * i + 2], bf16_f2(r[i].z)), x[4 * i + 3] = add2_rn(x[4 * i + 3], bf16_f2(r[i].w));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(x[i].x, x[i].y);
+    if (e.amax) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) l.m2 = bf16x2_absmax(l.m2, w[i]);
+    }
+    if (e.d) {
+        uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.d) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    if (e.q) {
+        const Two s = two(l.c.s), mr = two(-l.c.r);
+        uint32_t o[8];
+        if (e.e5m2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = codes4_fast<FP8Q_E5M2>(w[2 * i], w[2 * i + 1], s, mr, l.c.t2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = codes4_fast<FP8Q_E4M3FN>(w[2 * i], w[2 * i + 1], s, mr, l.c.t2);
+        }
+        uint4* q = reinterpret_cast<uint4*>(e.q + at);
+        q[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        q[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
@@ -792,6 +889,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
         const uint32_t room = base + kPrOut + warp * 4096;
         const int sub = lane >> 3, c4 = (lane & 7) * 4;
         Lane l = make_lane(e);
+        const bool rows_in_lanes = e.wide && !e.f32 && (!e.q || l.c.fast);
         bool ok = true;
         uint32_t it = 0;
         for (int tile = first; tile < tiles; tile += stride, ++it) {
@@ -807,6 +905,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
             for (int c = 0; c < 128; c += 32) {
                 const int q = w.q0 + (warp >> 2) * 128 + c, col = q + c4;
                 float v[32];
+                uint4 before[4];
+                if (rows_in_lanes && e.residual && q + 32 <= e.n && p_first + lane < w.p_end) {
+                    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.residual) + (d_first + lane) * e.n + q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) before[i] = p[i];
+                }
                 if (w.k > 0) {
                     tmem_load32(from + set * 256 + c, v);
                 } else {
@@ -818,6 +922,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                     if (lane == 0) arrive_cluster(bar);
                 }
                 if (q >= e.n || p_first >= w.p_end) continue;
+                if (rows_in_lanes && q + 32 <= e.n) {
+                    if (!ok) {  // a wait that ran out shows as NaN
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7FFFFFFFu);
+                    }
+                    if (p_first + lane < w.p_end) emit_row32(e, l, d_first + lane, q, (int64_t)w.group * e.n, v, before);
+                    continue;
+                }
                 // through shared memory: a thread has a row's sums, and four of eight rows go out
                 __syncwarp();
 #pragma unroll
@@ -962,6 +1074,7 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     const uintptr_t wide = (uintptr_t)p->d | (uintptr_t)p->residual;
     e.vec = p->n % 4 == 0 && (wide & (e.f32 ? 15u : 7u)) == 0 && ((uintptr_t)p->bias & (e.bias_bf16 ? 7u : 15u)) == 0 &&
             (((uintptr_t)p->q | (uintptr_t)p->h) & 3u) == 0;
+    e.wide = e.vec && p->n % 16 == 0 && ((wide | (uintptr_t)p->bias | (uintptr_t)p->q | (uintptr_t)p->h) & 15u) == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.offsets = offsets;
     a.groups = how == kWhole ? 1 : groups;
