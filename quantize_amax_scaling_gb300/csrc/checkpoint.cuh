@@ -45,4 +45,19 @@ __device__ __forceinline__ void ckpt_decode4(uint32_t four, float s, float (&v)[
     v[0] = f16_lo(a) * s, v[1] = f16_hi(a) * s, v[2] = f16_lo(b) * s, v[3] = f16_hi(b) * s;
 }
 
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// quant_quad() at a scale that takes the exact quotient without a divide, two lanes at a time: the negative of -x's.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4_fast(uint32_t w0, uint32_t w1, Two s, Two mr, uint32_t t2) {
+    const Two a = minus_quotient(widen2(bf16x2_clamp(w0, t2) ^ 0x80008000u), s, mr), b = minus_quotient(widen2(bf16x2_clamp(w1, t2) ^ 0x80008000u), s, mr);
+    const uint32_t lo = cvt_fp8x2<FMT>(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)));
+    const uint32_t hi = cvt_fp8x2<FMT>(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32)));
+    return lo | hi << 16;
+}
+
 }  // namespace

@@ -20,7 +20,7 @@ struct CkptArgs {
     uint16_t* y;
     uint8_t *q, *sf;
     int64_t rows, cols, blocks;  // blocks of 32, a row
-    int64_t items;               // of sixteen elements (whole blocks), or of a block
+    int64_t items;               // of sixteen elements (whole blocks), or of four blocks of a row
 };
 
 constexpr int kCkptPer = 2;  // items a thread of the kernels of whole blocks, at a time
@@ -55,17 +55,36 @@ __global__ void __launch_bounds__(kThreads) checkpoint_quantize_kernel(const Ckp
     }
 }
 
-// Rows of any length, from anywhere: a block a warp, a column a lane.
+// Rows of any length, from anywhere: four blocks side by side a warp, a column of each a lane.
+struct CkptRow {
+    int64_t at;     // of the lane's first element
+    int64_t block;  // the first block
+    int blocks;     // there
+    int64_t left;   // elements of the row from the lane's first on
+};
+__device__ __forceinline__ CkptRow ckpt_row(const CkptArgs& a, int64_t item) {
+    const int64_t across = (a.blocks + 3) >> 2;
+    const int64_t row = a.items <= INT32_MAX ? (int64_t)((uint32_t)item / (uint32_t)across) : item / across, b = (item - row * across) * 4;
+    const int64_t col = b * 32 + (threadIdx.x & 31);
+    return {row * a.cols + col, row * a.blocks + b, (int)min(a.blocks - b, (int64_t)4), a.cols - col};
+}
+
 __global__ void __launch_bounds__(kThreads) checkpoint_quantize_rows_kernel(const CkptArgs a) {
     start_behind();
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; b < a.items; b += step) {
-        const int64_t row = b / a.blocks, col = (b - row * a.blocks) * 32 + lane;
-        const uint32_t w = col < a.cols ? a.x[row * a.cols + col] : 0u;
-        const uint32_t code = ckpt_scale(__reduce_max_sync(0xFFFFFFFFu, w & 0x7FFFu));
-        if (col < a.cols) a.q[row * a.cols + col] = (uint8_t)ckpt_codes4(w, 0u, ckpt_factor(code));
-        if (lane == 0) a.sf[b] = (uint8_t)code;
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; i < a.items; i += step) {
+        const CkptRow r = ckpt_row(a, i);
+        uint32_t w[4], mine = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = 32 * j < r.left ? a.x[r.at + 32 * j] : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t code = ckpt_scale(__reduce_max_sync(0xFFFFFFFFu, w[j] & 0x7FFFu));
+            if (32 * j < r.left) a.q[r.at + 32 * j] = (uint8_t)ckpt_codes4(w[j], 0u, ckpt_factor(code));
+            if (lane == j) mine = code;
+        }
+        if (lane < r.blocks) a.sf[r.block + lane] = (uint8_t)mine;
     }
 }
 
@@ -99,14 +118,20 @@ __global__ void __launch_bounds__(kThreads) checkpoint_dequantize_kernel(const C
 
 __global__ void __launch_bounds__(kThreads) checkpoint_dequantize_rows_kernel(const CkptArgs a) {
     start_behind();
-    const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t b = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; b < a.items; b += step) {
-        const int64_t row = b / a.blocks, col = (b - row * a.blocks) * 32 + lane;
-        if (col >= a.cols) continue;
-        float v[4];
-        ckpt_decode4(a.q[row * a.cols + col], ckpt_value(a.sf[b]), v);
-        a.y[row * a.cols + col] = (uint16_t)(cvt_bf16x2(v[0], 0.0f) & 0xFFFFu);
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; i < a.items; i += step) {
+        const CkptRow r = ckpt_row(a, i);
+        uint32_t q[4], sf[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (32 * j < r.left) q[j] = a.q[r.at + 32 * j], sf[j] = a.sf[r.block + j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (32 * j < r.left) {
+                float v[4];
+                ckpt_decode4(q[j], ckpt_value(sf[j]), v);
+                a.y[r.at + 32 * j] = (uint16_t)(cvt_bf16x2(v[0], 0.0f) & 0xFFFFu);
+            }
     }
 }
 
@@ -127,101 +152,144 @@ struct GeluBackArgs {
     int32_t strips;
 };
 
-// d/dx of x s(x), s(x) = 1 / (1 + t), t = exp(-2 sqrt(2 / pi) (x + 0.044715 x^3)):
-//   s + x s (t s) 2 sqrt(2 / pi) (1 + 3 0.044715 x^2)
-// Beyond +-10 it is 1 and 0 to 35 places, and given as such.
-__device__ __forceinline__ float gelu_slope(float x) {
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(10.0f));
-    const float x2 = x * x;
-    float t, s;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(x * fmaf(x2, -0.102943239f, -2.302208198f)));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.0f + t));
-    const float d = fmaf(x * fmaf(x2, 0.214064417f, 1.595769122f), s * (t * s), s);
-    return x < -10.0f ? 0.0f : d;
+// d/dx of x s(x), s(x) = 1 / (1 + t), t = exp(-2 sqrt(2 / pi) (x + 0.044715 x^3)), for two:
+//   s + x s (1 - s) 2 sqrt(2 / pi) (1 + 3 0.044715 x^2)
+// 1 - s is off by 2^-24, which counts up to x = 4.2 and makes 2^-20 there; beyond, s is 1 in binary32.  For |x| up to 2^50
+// nothing but t and its exponent overflows, and these into 0 and 1.
+__device__ __forceinline__ Two gelu_slope2(Two x) {
+    const Two x2 = mul_two(x, x);
+    const Two u = mul_two(x, fma_two(x2, two(-0.102943239f), two(-2.302208198f)));
+    float t0, t1, s0, s1;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(t0) : "f"(__uint_as_float((uint32_t)u)));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(t1) : "f"(__uint_as_float((uint32_t)(u >> 32))));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(s0) : "f"(t0 + 1.0f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(s1) : "f"(t1 + 1.0f));
+    const Two s = two(__float_as_uint(s0), __float_as_uint(s1));
+    const Two rest = fma_two(s, two(-1.0f), two(1.0f));
+    return fma_two(mul_two(mul_two(s, x), rest), fma_two(x2, two(0.214064417f), two(1.595769122f)), s);
+}
+// The same for any x.
+__device__ __noinline__ float gelu_slope(float x) {
+    if (x > 10.0f) return 1.0f;
+    if (x < -12.0f) return 0.0f;
+    return __uint_as_float((uint32_t)gelu_slope2(two(x)));  // NaN among them
 }
 
 constexpr int kGbCols = 256;  // columns a CTA: eight a lane, every eighth row a warp
 
-// VEC: eight columns side by side a lane, in one load each; otherwise every 32nd.
-template <int FMT, bool VEC>
-__global__ void __launch_bounds__(kThreads) gelu_backward_kernel(const GeluBackArgs a) {
+// Eight elements of a row: VEC, side by side; otherwise every 32nd of `left` from the lane's first on.
+template <bool VEC, bool GELU>
+struct GbRow {
+    uint32_t y[4], h[2];
+    uint32_t sf[VEC ? 1 : 8];
+    __device__ __forceinline__ void load(const GeluBackArgs& a, int64_t at, int64_t sf_at, int64_t left) {
+        if (VEC) {
+            const uint4 v = *reinterpret_cast<const uint4*>(a.dy + at);
+            y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+            if (GELU) {
+                const uint2 u = *reinterpret_cast<const uint2*>(a.h + at);
+                h[0] = u.x, h[1] = u.y;
+                sf[0] = a.h_sf[sf_at];
+            }
+        } else {
+            y[0] = y[1] = y[2] = y[3] = h[0] = h[1] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j * 32 < left) {
+                    y[j >> 1] |= (uint32_t)a.dy[at + j * 32] << (j & 1) * 16;
+                    if (GELU) {
+                        h[j >> 2] |= (uint32_t)a.h[at + j * 32] << (j & 3) * 8;
+                        sf[VEC ? 0 : j] = a.h_sf[sf_at + j];
+                    }
+                } else if (GELU) {
+                    sf[VEC ? 0 : j] = 127u;
+                }
+        }
+    }
+};
+
+template <int FMT, bool VEC, bool GELU, bool FAST>
+__device__ __forceinline__ void gb_rows(const GeluBackArgs& a, const QScale& c, int64_t r0, int64_t r1, int64_t col, Two (&sum)[4], uint32_t& m2) {
+    constexpr int kWarps = kThreads / 32;
+    const int64_t left = a.cols - col, blk = col >> 5;
+    GbRow<VEC, GELU> now, ahead;
+    if (r0 < r1) now.load(a, r0 * a.cols + col, r0 * a.blocks + blk, left);
+#pragma unroll 1
+    for (int64_t r = r0; r < r1; r += kWarps) {
+        if (r + kWarps < r1) ahead.load(a, (r + kWarps) * a.cols + col, (r + kWarps) * a.blocks + blk, left);
+        const int64_t at = r * a.cols + col;
+        Two d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = widen2(now.y[j]);
+        if (GELU) {
+            bool large = false;  // a scale whose values could leave gelu_slope2()'s range, or NaN
+#pragma unroll
+            for (int j = 0; j < (VEC ? 1 : 8); ++j) large |= now.sf[j] > 127u + 40u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t f = fp8x2_to_f16x2<FP8Q_E4M3FN>(now.h[j >> 1] >> (j & 1) * 16 & 0xFFFFu);
+                const Two s = two(__float_as_uint(ckpt_value(now.sf[VEC ? 0 : 2 * j])), __float_as_uint(ckpt_value(now.sf[VEC ? 0 : 2 * j + 1])));
+                const Two x = mul_two(two(__float_as_uint(f16_lo(f)), __float_as_uint(f16_hi(f))), s);
+                if (!large)
+                    d[j] = mul_two(d[j], gelu_slope2(x));
+                else
+                    d[j] = mul_two(d[j], two(__float_as_uint(gelu_slope(__uint_as_float((uint32_t)x))), __float_as_uint(gelu_slope(__uint_as_float((uint32_t)(x >> 32))))));
+            }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sum[j] = add_two(sum[j], d[j]);
+            w[j] = cvt_bf16x2(__uint_as_float((uint32_t)d[j]), __uint_as_float((uint32_t)(d[j] >> 32)));
+        }
+        m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(w[0], w[1]), bf16x2_absmax(w[2], w[3])));
+        uint2 o = make_uint2(0, 0);
+        if (FMT != kNoCodes) {
+            if (FAST) {
+                const Two s = two(c.s), mr = two(-c.r);
+                o = make_uint2(codes4_fast<FMT & 1>(w[0], w[1], s, mr, c.t2), codes4_fast<FMT & 1>(w[2], w[3], s, mr, c.t2));
+            } else {
+                o = make_uint2(quant_quad<FMT & 1, false>(w[0], w[1], c), quant_quad<FMT & 1, false>(w[2], w[3], c));
+            }
+        }
+        if (VEC) {
+            if (a.dx) st_v4(a.dx + at, make_uint4(w[0], w[1], w[2], w[3]));
+            if (FMT != kNoCodes) st_v2(a.q + at, o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j * 32 < left) {
+                    if (a.dx) a.dx[at + j * 32] = (uint16_t)(w[j >> 1] >> (j & 1) * 16);
+                    if (FMT != kNoCodes) a.q[at + j * 32] = (uint8_t)((j < 4 ? o.x : o.y) >> (j & 3) * 8);
+                }
+        }
+        now = ahead;
+    }
+}
+
+template <int FMT, bool VEC, bool GELU>
+__global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) gelu_backward_kernel(const GeluBackArgs a) {
     __shared__ float part[kThreads / 32][kGbCols];
     __shared__ uint32_t red[kThreads / 32];
     start_behind();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t col0 = (int64_t)blockIdx.x * kGbCols, strip = blockIdx.y;
     const int64_t col = col0 + (VEC ? lane * 8 : lane);
-    const int64_t r1 = min((strip + 1) * a.per_strip, a.rows);
+    const int64_t r0 = strip * a.per_strip + warp, r1 = min((strip + 1) * a.per_strip, a.rows);
     const QScale c = make_qscale_value(a.q ? *a.scale : 1.0f);
-    float sum[8] = {};
+    Two sum[4] = {};
     uint32_t m2 = 0;
     if (col < a.cols) {
-#pragma unroll 2
-        for (int64_t r = strip * a.per_strip + warp; r < r1; r += kThreads / 32) {
-            const int64_t at = r * a.cols + col;
-            uint32_t y[4] = {}, h[2] = {};
-            float s[VEC ? 1 : 8];
-            if (VEC) {
-                const uint4 v = *reinterpret_cast<const uint4*>(a.dy + at);
-                y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
-                if (a.h) {
-                    const uint2 u = *reinterpret_cast<const uint2*>(a.h + at);
-                    h[0] = u.x, h[1] = u.y;
-                    s[0] = ckpt_value(a.h_sf[r * a.blocks + (col >> 5)]);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + j * 32 < a.cols) {
-                        y[j >> 1] |= (uint32_t)a.dy[at + j * 32] << (j & 1) * 16;
-                        if (a.h) {
-                            h[j >> 2] |= (uint32_t)a.h[at + j * 32] << (j & 3) * 8;
-                            s[j] = ckpt_value(a.h_sf[r * a.blocks + (col >> 5) + j]);
-                        }
-                    } else if (!VEC) {
-                        s[j] = 0.0f;
-                    }
-            }
-            float d[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[2 * j] = __uint_as_float(y[j] << 16), d[2 * j + 1] = __uint_as_float(y[j] & 0xFFFF0000u);
-            if (a.h) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float v[4];
-                    ckpt_decode4(h[j], VEC ? s[0] : 1.0f, v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[4 * j + i] *= gelu_slope(VEC ? v[i] : v[i] * s[VEC ? 0 : 4 * j + i]);
-                }
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += d[j];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = cvt_bf16x2(d[2 * j], d[2 * j + 1]);
-            m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(w[0], w[1]), bf16x2_absmax(w[2], w[3])));
-            uint2 o = make_uint2(0, 0);
-            if (FMT != kNoCodes)
-                o = c.fast ? make_uint2(quant_quad<FMT & 1, true>(w[0], w[1], c), quant_quad<FMT & 1, true>(w[2], w[3], c))
-                           : make_uint2(quant_quad<FMT & 1, false>(w[0], w[1], c), quant_quad<FMT & 1, false>(w[2], w[3], c));
-            if (VEC) {
-                if (a.dx) st_v4(a.dx + at, make_uint4(w[0], w[1], w[2], w[3]));
-                if (FMT != kNoCodes) st_v2(a.q + at, o);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col + j * 32 < a.cols) {
-                        if (a.dx) a.dx[at + j * 32] = (uint16_t)(w[j >> 1] >> (j & 1) * 16);
-                        if (FMT != kNoCodes) a.q[at + j * 32] = (uint8_t)((j < 4 ? o.x : o.y) >> (j & 3) * 8);
-                    }
-            }
-        }
+        if (FMT == kNoCodes || c.fast)
+            gb_rows<FMT, VEC, GELU, true>(a, c, r0, r1, col, sum, m2);
+        else
+            gb_rows<FMT, VEC, GELU, false>(a, c, r0, r1, col, sum, m2);
     }
     if (a.amax) flush_amax(m2, 0, a.amax, red);
     if (!a.d_bias) return;
     // the eight warps' sums in their order
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[warp][VEC ? lane * 8 + j : lane + j * 32] = sum[j];
+    for (int j = 0; j < 8; ++j) part[warp][VEC ? lane * 8 + j : lane + j * 32] = __uint_as_float((uint32_t)(sum[j >> 1] >> (j & 1) * 32));
     __syncthreads();
     float v = 0.0f;
 #pragma unroll
@@ -265,8 +333,9 @@ GbStrips gb_strips(int64_t rows, int64_t cols) {
 template <int FMT>
 fp8q_status launch_gelu_backward(const GeluBackArgs& a, bool vec, cudaStream_t s) {
     const dim3 grid((unsigned)((a.cols + kGbCols - 1) / kGbCols), (unsigned)a.strips);
-    return launch_behind(vec ? gelu_backward_kernel<FMT, true> : gelu_backward_kernel<FMT, false>, grid, dim3(kThreads), 0, 1, s,
-                         "gelu_backward_kernel", a);
+    return launch_behind(a.h ? (vec ? gelu_backward_kernel<FMT, true, true> : gelu_backward_kernel<FMT, false, true>)
+                             : (vec ? gelu_backward_kernel<FMT, true, false> : gelu_backward_kernel<FMT, false, false>),
+                         grid, dim3(kThreads), 0, 1, s, "gelu_backward_kernel", a);
 }
 
 fp8q_status check_ckpt(const void* x, const uint8_t* q, const uint8_t* sf, int64_t rows, int64_t cols) {
@@ -288,7 +357,7 @@ fp8q_status launch_ckpt(CkptArgs a, bool back, cudaStream_t s) {
         return launch_behind(back ? checkpoint_dequantize_kernel : checkpoint_quantize_kernel, dim3((unsigned)grid), dim3(kThreads), 0, 1, s,
                              back ? "checkpoint_dequantize_kernel" : "checkpoint_quantize_kernel", a);
     }
-    a.items = a.rows * a.blocks;
+    a.items = a.rows * ((a.blocks + 3) / 4);
     const int64_t want = (a.items + kThreads / 32 - 1) / (kThreads / 32), most = 64 * (int64_t)sm_count();
     return launch_behind(back ? checkpoint_dequantize_rows_kernel : checkpoint_quantize_rows_kernel, dim3((unsigned)(want < most ? want : most)),
                          dim3(kThreads), 0, 1, s, back ? "checkpoint_dequantize_rows_kernel" : "checkpoint_quantize_rows_kernel", a);

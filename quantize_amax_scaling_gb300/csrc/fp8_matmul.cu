@@ -117,15 +117,6 @@ __device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, const QScal
     return c.fast ? quant_quad<FMT, true>(w0, w1, c) : quant_quad<FMT, false>(w0, w1, c);
 }
 
-// quant_quad() at a scale that takes the exact quotient without a divide, two lanes at a time: the negative of -x's.
-template <int FMT>
-__device__ __forceinline__ uint32_t codes4_fast(uint32_t w0, uint32_t w1, Two s, Two mr, uint32_t t2) {
-    const Two a = minus_quotient(widen2(bf16x2_clamp(w0, t2) ^ 0x80008000u), s, mr), b = minus_quotient(widen2(bf16x2_clamp(w1, t2) ^ 0x80008000u), s, mr);
-    const uint32_t lo = cvt_fp8x2<FMT>(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)));
-    const uint32_t hi = cvt_fp8x2<FMT>(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32)));
-    return lo | hi << 16;
-}
-
 // What a lane keeps over its columns.
 struct Lane {
     QScale c;
