@@ -160,124 +160,153 @@ __device__ __forceinline__ Two gelu_slope2(Two x) {
     const Two x2 = mul_two(x, x);
     const Two u = mul_two(x, fma_two(x2, two(-0.102943239f), two(-2.302208198f)));
     float t0, t1, s0, s1;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(t0) : "f"(__uint_as_float((uint32_t)u)));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(t1) : "f"(__uint_as_float((uint32_t)(u >> 32))));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(s0) : "f"(t0 + 1.0f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(s1) : "f"(t1 + 1.0f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(__uint_as_float((uint32_t)u)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(__uint_as_float((uint32_t)(u >> 32))));
+    const Two t = add_two(two(__float_as_uint(t0), __float_as_uint(t1)), two(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(__uint_as_float((uint32_t)t)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(__uint_as_float((uint32_t)(t >> 32))));
     const Two s = two(__float_as_uint(s0), __float_as_uint(s1));
     const Two rest = fma_two(s, two(-1.0f), two(1.0f));
     return fma_two(mul_two(mul_two(s, x), rest), fma_two(x2, two(0.214064417f), two(1.595769122f)), s);
 }
-// The same for any x.
-__device__ __noinline__ float gelu_slope(float x) {
-    if (x > 10.0f) return 1.0f;
-    if (x < -12.0f) return 0.0f;
-    return __uint_as_float((uint32_t)gelu_slope2(two(x)));  // NaN among them
+constexpr int kGbCtas = 2;  // of an SM
+
+// x held where gelu_slope2() is 1 and 0; NaN stays.
+__device__ __forceinline__ uint32_t near_zero(uint32_t x) {
+    float v;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(__uint_as_float(x)), "f"(64.0f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(v), "f"(-64.0f));
+    return __float_as_uint(v);
 }
 
-constexpr int kGbCols = 256;  // columns a CTA: eight a lane, every eighth row a warp
+// VEC: sixteen columns side by side a lane; otherwise eight of every 32nd.  Every eighth row a warp.
+template <bool VEC>
+struct GbGeom {
+    static constexpr int kPer = VEC ? 16 : 8;      // columns a lane
+    static constexpr int kCols = kPer * 32;        // a CTA
+};
 
-// Eight elements of a row: VEC, side by side; otherwise every 32nd of `left` from the lane's first on.
+// A lane's columns of one row, and where it finds those of its next.
 template <bool VEC, bool GELU>
 struct GbRow {
-    uint32_t y[4], h[2];
-    uint32_t sf[VEC ? 1 : 8];
-    __device__ __forceinline__ void load(const GeluBackArgs& a, int64_t at, int64_t sf_at, int64_t left) {
-        if (VEC) {
-            const uint4 v = *reinterpret_cast<const uint4*>(a.dy + at);
-            y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+    static constexpr int N = GbGeom<VEC>::kPer, S = VEC ? 1 : 8;
+    uint32_t y[N / 2], h[N / 4], sf[S];
+    __device__ __forceinline__ void load(const uint16_t* dy, const uint8_t* ph, const uint8_t* psf, int64_t left) {
+        if constexpr (VEC) {
+            uint4 u, v;
+            ld_once_v8(dy, u, v);
+            y[0] = u.x, y[1] = u.y, y[2] = u.z, y[3] = u.w, y[4] = v.x, y[5] = v.y, y[6] = v.z, y[7] = v.w;
             if (GELU) {
-                const uint2 u = *reinterpret_cast<const uint2*>(a.h + at);
-                h[0] = u.x, h[1] = u.y;
-                sf[0] = a.h_sf[sf_at];
+                const uint4 w = *reinterpret_cast<const uint4*>(ph);
+                h[0] = w.x, h[1] = w.y, h[2] = w.z, h[3] = w.w;
+                sf[0] = *psf;
             }
         } else {
-            y[0] = y[1] = y[2] = y[3] = h[0] = h[1] = 0;
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) y[j] = 0;
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j) h[j] = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (j * 32 < left) {
-                    y[j >> 1] |= (uint32_t)a.dy[at + j * 32] << (j & 1) * 16;
+                    y[j >> 1] |= (uint32_t)dy[j * 32] << (j & 1) * 16;
                     if (GELU) {
-                        h[j >> 2] |= (uint32_t)a.h[at + j * 32] << (j & 3) * 8;
-                        sf[VEC ? 0 : j] = a.h_sf[sf_at + j];
+                        h[j >> 2] |= (uint32_t)ph[j * 32] << (j & 3) * 8;
+                        sf[j] = psf[j];
                     }
                 } else if (GELU) {
-                    sf[VEC ? 0 : j] = 127u;
+                    sf[j] = 127u;
                 }
         }
     }
 };
 
 template <int FMT, bool VEC, bool GELU, bool FAST>
-__device__ __forceinline__ void gb_rows(const GeluBackArgs& a, const QScale& c, int64_t r0, int64_t r1, int64_t col, Two (&sum)[4], uint32_t& m2) {
-    constexpr int kWarps = kThreads / 32;
-    const int64_t left = a.cols - col, blk = col >> 5;
+__device__ __forceinline__ void gb_rows(const GeluBackArgs& a, const QScale& c, int64_t r0, int64_t r1, int64_t col,
+                                        Two (&sum)[GbGeom<VEC>::kPer / 2], uint32_t& m2) {
+    constexpr int kWarps = kThreads / 32, N = GbGeom<VEC>::kPer;
+    const int64_t left = a.cols - col, step = a.cols * kWarps, sf_step = a.blocks * kWarps;
+    const uint16_t* dy = a.dy + r0 * a.cols + col;
+    const uint8_t *ph = GELU ? a.h + r0 * a.cols + col : nullptr, *psf = GELU ? a.h_sf + r0 * a.blocks + (col >> 5) : nullptr;
+    int64_t at = r0 * a.cols + col;
     GbRow<VEC, GELU> now, ahead;
-    if (r0 < r1) now.load(a, r0 * a.cols + col, r0 * a.blocks + blk, left);
-#pragma unroll 1
-    for (int64_t r = r0; r < r1; r += kWarps) {
-        if (r + kWarps < r1) ahead.load(a, (r + kWarps) * a.cols + col, (r + kWarps) * a.blocks + blk, left);
-        const int64_t at = r * a.cols + col;
-        Two d[4];
+    int n = (int)((r1 - r0 + kWarps - 1) / kWarps);  // this warp's rows
+    if (r0 >= r1) return;
+    now.load(dy, ph, psf, left);
+#pragma unroll 2
+    for (; n > 0; --n, at += step) {
+        dy += step;
+        if (GELU) ph += step, psf += sf_step;
+        if (n > 1) ahead.load(dy, ph, psf, left);
+        Two d[N / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = widen2(now.y[j]);
+        for (int j = 0; j < N / 2; ++j) d[j] = widen2(now.y[j]);
         if (GELU) {
-            bool large = false;  // a scale whose values could leave gelu_slope2()'s range, or NaN
+            Two x[N / 2];
+            bool odd = false;  // a scale of 0 or NaN, or one whose values could leave gelu_slope2()'s range
 #pragma unroll
-            for (int j = 0; j < (VEC ? 1 : 8); ++j) large |= now.sf[j] > 127u + 40u;
+            for (int j = 0; j < (VEC ? 1 : 8); ++j) odd |= now.sf[j] - 1u > 127u + 39u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t f = fp8x2_to_f16x2<FP8Q_E4M3FN>(now.h[j >> 1] >> (j & 1) * 16 & 0xFFFFu);
-                const Two s = two(__float_as_uint(ckpt_value(now.sf[VEC ? 0 : 2 * j])), __float_as_uint(ckpt_value(now.sf[VEC ? 0 : 2 * j + 1])));
-                const Two x = mul_two(two(__float_as_uint(f16_lo(f)), __float_as_uint(f16_hi(f))), s);
-                if (!large)
-                    d[j] = mul_two(d[j], gelu_slope2(x));
-                else
-                    d[j] = mul_two(d[j], two(__float_as_uint(gelu_slope(__uint_as_float((uint32_t)x))), __float_as_uint(gelu_slope(__uint_as_float((uint32_t)(x >> 32))))));
+            for (int j = 0; j < N / 2; ++j) {
+                const uint32_t f = fp8x2_to_f16x2<FP8Q_E4M3FN>(j & 1 ? now.h[j >> 1] >> 16 : now.h[j >> 1]);
+                const Two s = VEC ? two(now.sf[0] << 23, now.sf[0] << 23) : two(now.sf[VEC ? 0 : 2 * j] << 23, now.sf[VEC ? 0 : 2 * j + 1] << 23);
+                x[j] = mul_two(two(__float_as_uint(f16_lo(f)), __float_as_uint(f16_hi(f))), s);
             }
-        }
-        uint32_t w[4];
+            if (odd) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < N / 2; ++j) {
+                    float v[4];
+                    ckpt_decode4(j & 1 ? now.h[j >> 1] >> 16 : now.h[j >> 1], 1.0f, v);
+                    x[j] = two(near_zero(__float_as_uint(v[0] * ckpt_value(now.sf[VEC ? 0 : 2 * j]))), near_zero(__float_as_uint(v[1] * ckpt_value(now.sf[VEC ? 0 : 2 * j + 1]))));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) d[j] = mul_two(d[j], gelu_slope2(x[j]));
+        }
+        uint32_t w[N / 2], o[N / 4];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
             sum[j] = add_two(sum[j], d[j]);
             w[j] = cvt_bf16x2(__uint_as_float((uint32_t)d[j]), __uint_as_float((uint32_t)(d[j] >> 32)));
         }
-        m2 = bf16x2_absmax(m2, bf16x2_absmax(bf16x2_absmax(w[0], w[1]), bf16x2_absmax(w[2], w[3])));
-        uint2 o = make_uint2(0, 0);
         if (FMT != kNoCodes) {
-            if (FAST) {
-                const Two s = two(c.s), mr = two(-c.r);
-                o = make_uint2(codes4_fast<FMT & 1>(w[0], w[1], s, mr, c.t2), codes4_fast<FMT & 1>(w[2], w[3], s, mr, c.t2));
-            } else {
-                o = make_uint2(quant_quad<FMT & 1, false>(w[0], w[1], c), quant_quad<FMT & 1, false>(w[2], w[3], c));
-            }
+            const Two s = two(c.s), mr = two(-c.r);
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                o[j] = FAST ? codes4_fast<FMT & 1>(w[2 * j], w[2 * j + 1], s, mr, c.t2) : quant_quad<FMT & 1, false>(w[2 * j], w[2 * j + 1], c);
         }
-        if (VEC) {
-            if (a.dx) st_v4(a.dx + at, make_uint4(w[0], w[1], w[2], w[3]));
-            if (FMT != kNoCodes) st_v2(a.q + at, o);
+        if constexpr (VEC) {
+            if (a.dx) {
+                st_v4(a.dx + at, make_uint4(w[0], w[1], w[2], w[3]));
+                st_v4(a.dx + at + 8, make_uint4(w[4], w[5], w[6], w[7]));
+            }
+            if (FMT != kNoCodes) st_v4(a.q + at, make_uint4(o[0], o[1], o[2], o[3]));
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (j * 32 < left) {
                     if (a.dx) a.dx[at + j * 32] = (uint16_t)(w[j >> 1] >> (j & 1) * 16);
-                    if (FMT != kNoCodes) a.q[at + j * 32] = (uint8_t)((j < 4 ? o.x : o.y) >> (j & 3) * 8);
+                    if (FMT != kNoCodes) a.q[at + j * 32] = (uint8_t)(o[j >> 2] >> (j & 3) * 8);
                 }
         }
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) m2 = bf16x2_absmax(m2, w[j]);
         now = ahead;
     }
 }
 
 template <int FMT, bool VEC, bool GELU>
-__global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) gelu_backward_kernel(const GeluBackArgs a) {
-    __shared__ float part[kThreads / 32][kGbCols];
+__global__ void __launch_bounds__(kThreads, kGbCtas) gelu_backward_kernel(const GeluBackArgs a) {
+    constexpr int N = GbGeom<VEC>::kPer, kCols = GbGeom<VEC>::kCols;
+    __shared__ float part[kThreads / 32][kCols];
     __shared__ uint32_t red[kThreads / 32];
     start_behind();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t col0 = (int64_t)blockIdx.x * kGbCols, strip = blockIdx.y;
-    const int64_t col = col0 + (VEC ? lane * 8 : lane);
+    const int64_t col0 = (int64_t)blockIdx.x * kCols, strip = blockIdx.y;
+    const int64_t col = col0 + (VEC ? lane * N : lane);
     const int64_t r0 = strip * a.per_strip + warp, r1 = min((strip + 1) * a.per_strip, a.rows);
     const QScale c = make_qscale_value(a.q ? *a.scale : 1.0f);
-    Two sum[4] = {};
+    Two sum[N / 2] = {};
     uint32_t m2 = 0;
     if (col < a.cols) {
         if (FMT == kNoCodes || c.fast)
@@ -289,12 +318,14 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) gelu_backward_kernel(co
     if (!a.d_bias) return;
     // the eight warps' sums in their order
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[warp][VEC ? lane * 8 + j : lane + j * 32] = __uint_as_float((uint32_t)(sum[j >> 1] >> (j & 1) * 32));
+    for (int j = 0; j < N; ++j) part[warp][VEC ? lane * N + j : lane + j * 32] = __uint_as_float((uint32_t)(sum[j >> 1] >> (j & 1) * 32));
     __syncthreads();
-    float v = 0.0f;
+    for (int i = threadIdx.x; i < kCols; i += kThreads) {
+        float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v += part[w][threadIdx.x];
-    if (col0 + threadIdx.x < a.cols) (a.strips > 1 ? a.space + strip * a.cols : a.d_bias)[col0 + threadIdx.x] = v;
+        for (int w = 0; w < kThreads / 32; ++w) v += part[w][i];
+        if (col0 + i < a.cols) (a.strips > 1 ? a.space + strip * a.cols : a.d_bias)[col0 + i] = v;
+    }
 }
 
 // The strips' sums, 32 columns a CTA, every 32nd strip a warp, all in a fixed order.
@@ -321,10 +352,11 @@ __global__ void __launch_bounds__(1024) gelu_backward_sum_kernel(const GeluBackA
 struct GbStrips {
     int64_t strips, per_strip;
 };
-// As many CTAs as four an SM, of 32 rows or more; by the sizes alone, so that the sums' order is.
+// As many CTAs as are resident, of 32 rows or more; by the sizes alone, so that the sums' order is (and the workspace).
 GbStrips gb_strips(int64_t rows, int64_t cols) {
-    const int64_t across = (cols + kGbCols - 1) / kGbCols;
-    int64_t strips = (4 * 152 + across - 1) / across;
+    const int64_t wide = cols % 16 == 0 ? GbGeom<true>::kCols : GbGeom<false>::kCols, across = (cols + wide - 1) / wide;
+    int64_t strips = kGbCtas * 152 / across;  // one CTA more than are resident would wait for all of them
+    if (strips < 1) strips = 1;
     if (strips > (rows + 31) / 32) strips = (rows + 31) / 32;
     const int64_t per = (rows + strips - 1) / strips;
     return {(rows + per - 1) / per, per};
@@ -332,7 +364,8 @@ GbStrips gb_strips(int64_t rows, int64_t cols) {
 
 template <int FMT>
 fp8q_status launch_gelu_backward(const GeluBackArgs& a, bool vec, cudaStream_t s) {
-    const dim3 grid((unsigned)((a.cols + kGbCols - 1) / kGbCols), (unsigned)a.strips);
+    const int64_t wide = vec ? GbGeom<true>::kCols : GbGeom<false>::kCols;
+    const dim3 grid((unsigned)((a.cols + wide - 1) / wide), (unsigned)a.strips);
     return launch_behind(a.h ? (vec ? gelu_backward_kernel<FMT, true, true> : gelu_backward_kernel<FMT, false, true>)
                              : (vec ? gelu_backward_kernel<FMT, true, false> : gelu_backward_kernel<FMT, false, false>),
                          grid, dim3(kThreads), 0, 1, s, "gelu_backward_kernel", a);
@@ -435,7 +468,7 @@ fp8q_status fp8q_gelu_backward_quantize_amax(const fp8q_gelu_grad* g, void* stre
     a.blocks = (g->cols + 31) / 32;
     a.per_strip = st.per_strip;
     a.strips = (int32_t)st.strips;
-    const bool vec = g->cols % 8 == 0 && (((uintptr_t)g->d_y | (uintptr_t)g->d_x) & 15u) == 0 && (((uintptr_t)g->h | (uintptr_t)g->q) & 7u) == 0;
+    const bool vec = g->cols % 16 == 0 && ((uintptr_t)g->d_y & 31u) == 0 && (((uintptr_t)g->d_x | (uintptr_t)g->h | (uintptr_t)g->q) & 15u) == 0;
     const fp8q_status rc = !g->q               ? launch_gelu_backward<kNoCodes>(a, vec, s)
                            : g->fmt == FP8Q_E4M3FN ? launch_gelu_backward<FP8Q_E4M3FN>(a, vec, s)
                                                    : launch_gelu_backward<FP8Q_E5M2>(a, vec, s);

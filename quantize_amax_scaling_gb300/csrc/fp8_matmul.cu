@@ -85,11 +85,11 @@ __device__ __forceinline__ int2 group_rows(const ProductArgs& a, int g) {
 __device__ __forceinline__ float2 gelu2(float2 x) {
     const float2 u = mul2_rn(x, fma2_rn(mul2_rn(x, x), splat2(-0.102943239f), splat2(-2.302208198f)));
     float2 t, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(t.x) : "f"(u.x));
-    asm("ex2.approx.f32 %0, %1;" : "=f"(t.y) : "f"(u.y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(u.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(u.y));
     t = add2_rn(t, splat2(1.0f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(t.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(t.y));
     return mul2_rn(x, r);
 }
 
