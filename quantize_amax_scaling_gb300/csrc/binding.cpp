@@ -506,36 +506,44 @@ int64_t workspace(PyObject* const* v, Py_ssize_t n) {
     return g_workspace(rows, (int32_t)(hidden > INT32_MAX ? INT32_MAX : hidden < 0 ? 0 : hidden), per);
 }
 
-// (rows, cols, fmt): room for a packed operand on the current CUDA device
+// Two contiguous byte tensors on the current CUDA device, in one allocation, the second behind the first (16-byte aligned).
+PyObject* pair_of(at::IntArrayRef first, at::IntArrayRef second) {
+    const auto o = at::TensorOptions().dtype(at::kByte).device(at::kCUDA, c10::cuda::current_device());
+    const int64_t from = (c10::multiply_integers(first) + 15) / 16 * 16;
+    const at::Tensor all = at::empty({from + c10::multiply_integers(second)}, o);
+    const auto part = [&](at::IntArrayRef sizes, int64_t at) {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+        t.unsafeGetTensorImpl()->set_storage_offset(at);
+        return t;
+    };
+    PyObject* q = THPVariable_Wrap(part(first, 0));
+    PyObject* sf = q ? THPVariable_Wrap(part(second, from)) : nullptr;
+    PyObject* both = sf ? PyTuple_Pack(2, q, sf) : nullptr;
+    Py_XDECREF(q);
+    Py_XDECREF(sf);
+    return both;
+}
+
+// (rows, cols, fmt): room for a packed operand; without fmt, for a checkpoint
+template <bool CHECKPOINT>
 PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
-        int64_t v[3];
-        for (int i = 0; i < 3; ++i) {
-            v[i] = n == 3 ? PyLong_AsLongLong(a[i]) : -1;
+        constexpr Py_ssize_t kWant = CHECKPOINT ? 2 : 3;
+        int64_t v[3] = {};
+        for (Py_ssize_t i = 0; i < kWant; ++i) {
+            v[i] = n == kWant ? PyLong_AsLongLong(a[i]) : -1;
             if (v[i] == -1 && PyErr_Occurred()) return nullptr;
         }
         // beyond what the calls take, the bytes of both arrays could pass 64 bits and come out as few
         constexpr int64_t kMax = 0x7FFFFC00;
-        if (n != 3 || v[0] < 0 || v[1] < 0 || v[0] > kMax || v[1] > kMax || !four_bits(v[2])) {
-            PyErr_SetString(PyExc_ValueError, "fp4_empty takes rows and cols from 0 to 2^31 - 1024 and MXFP4 or NVFP4");
+        if (n != kWant || v[0] < 0 || v[1] < 0 || v[0] > kMax || v[1] > kMax || (!CHECKPOINT && !four_bits(v[2]))) {
+            PyErr_SetString(PyExc_ValueError, CHECKPOINT ? "checkpoint_empty takes rows and cols from 0 to 2^31 - 1024"
+                                                         : "fp4_empty takes rows and cols from 0 to 2^31 - 1024 and MXFP4 or NVFP4");
             return nullptr;
         }
-        const auto o = at::TensorOptions().dtype(at::kByte).device(at::kCUDA, c10::cuda::current_device());
-        // one allocation for both, the scales behind the codes (a multiple of 16 bytes)
-        const int64_t codes = v[0] * row_bytes(v[1]), scales = scale_bytes(v[0], v[1], v[2]);
-        const at::Tensor all = at::empty({codes + scales}, o);
-        const auto part = [&](at::IntArrayRef sizes, int64_t from) {
-            at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
-            t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-            t.unsafeGetTensorImpl()->set_storage_offset(from);
-            return t;
-        };
-        PyObject* q = THPVariable_Wrap(part({v[0], row_bytes(v[1])}, 0));
-        PyObject* sf = q ? THPVariable_Wrap(part({scales}, codes)) : nullptr;
-        PyObject* both = sf ? PyTuple_Pack(2, q, sf) : nullptr;
-        Py_XDECREF(q);
-        Py_XDECREF(sf);
-        return both;
+        if (CHECKPOINT) return pair_of({v[0], v[1]}, {v[0], (v[1] + 31) / 32});
+        return pair_of({v[0], row_bytes(v[1])}, {scale_bytes(v[0], v[1], v[2])});
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
@@ -571,7 +579,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f))
 PyMethodDef g_methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
-                           {"fp4_empty", FAST(empty), METH_FASTCALL, nullptr},
+                           {"fp4_empty", FAST(empty<false>), METH_FASTCALL, nullptr},
+                           {"checkpoint_empty", FAST(empty<true>), METH_FASTCALL, nullptr},
                            {"fp4_quantize_amax", FAST(call<quantize>), METH_FASTCALL, nullptr},
                            {"fp4_dequantize", FAST(call<dequantize>), METH_FASTCALL, nullptr},
                            {"fp4_matmul", FAST(call<matmul>), METH_FASTCALL, nullptr},

@@ -51,6 +51,8 @@ struct ProductArgs {
     uint32_t idesc;
     int32_t p_across, q_across;  // P's, Q's rows do not lie along k
     int32_t p_tiles, q_tiles;    // tiles of a group where all have the same
+    int32_t p_high;              // rows of B a CTA (few tiles)
+    int32_t stages, stage_bytes;
     int32_t split;               // CTAs of a cluster that share a tile's k
 #ifdef FP8Q_TEST_HOOKS
     int32_t fail_role, fail_at, fail_cta;  // the wait that reports failure although what it waits for has come
@@ -132,11 +134,11 @@ __device__ __forceinline__ Lane make_lane(const Epilogue& e) {
     return l;
 }
 
-// Columns col to col + 3 of a row of D; eight lanes side by side hold a block of 32 columns.  `on`: the row is there.
+// Columns col to col + 3 of a row of D, before `end`; eight lanes side by side hold a block of 32 columns.  `on`: the row is there.
 // r: the residual.  All lanes of a warp come here.  (Any n, any addresses, any scale of q.)
-__device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, int col, bool on, const float (&sum)[4], const float (&b)[4],
+__device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, int col, int end, bool on, const float (&sum)[4], const float (&b)[4],
                                       const float (&r)[4]) {
-    const int left = e.n - col;
+    const int left = end - col;
     on = on && left > 0;
     float v[4];
 #pragma unroll
@@ -206,15 +208,15 @@ __device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, i
 // ordinary scale go through the stages all rows at a time, so that a stage's latencies overlap: row by row, with the
 // branches between, 8192x16384x4096 took 731 us with GELU, codes and checkpoint and 411 with bf16 alone.
 template <int ROWS>
-__device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t row, int step, uint32_t on, int col, float (&v)[ROWS][4],
+__device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t row, int step, uint32_t on, int col, int end, float (&v)[ROWS][4],
                                           const float (&b)[4], const float (&r)[ROWS][4]) {
     if (!e.vec || (e.q && !l.c.fast)) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) emit4(e, l, row + i * step, col, on >> i & 1, v[i], b, r[i]);
+        for (int i = 0; i < ROWS; ++i) emit4(e, l, row + i * step, col, end, on >> i & 1, v[i], b, r[i]);
         return;
     }
-    const uint32_t here = (col & ~31) < e.n ? on : 0u;  // of a block's eight lanes the first may be the only one with columns
-    if (col >= e.n) on = 0;
+    const uint32_t here = (col & ~31) < end ? on : 0u;  // of a block's eight lanes the first may be the only one with columns
+    if (col >= end) on = 0;
     const float2 alpha = splat2(l.alpha), b0 = make_float2(b[0], b[1]), b1 = make_float2(b[2], b[3]);
     float2 x[ROWS][2];
 #pragma unroll
@@ -229,7 +231,7 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             w[i][0] = cvt_bf16x2(x[i][0].x, x[i][0].y), w[i][1] = cvt_bf16x2(x[i][1].x, x[i][1].y);
-            a[i] = col < e.n ? bf16x2_absmax(w[i][0], w[i][1]) : 0u;
+            a[i] = col < end ? bf16x2_absmax(w[i][0], w[i][1]) : 0u;
         }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1)
@@ -406,49 +408,56 @@ __device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 
 template <int BN>
 struct PrGeom {
     static constexpr int kQBytes = BN * kStepK;
-    static constexpr int kStageBytes = kBoxBytes + kQBytes;
-    static constexpr int kStages = BN <= 32 ? 5 : 4;
-    static constexpr int kSmem = kStages * kStageBytes + 1024;  // and room to start on 1024 bytes
-    static constexpr int kCols = BN < 32 ? 32 : BN;             // of tensor memory
+    static constexpr int kSmem = (BN <= 64 ? 112 : 160) * 1024;  // two CTAs an SM, or one
+    static constexpr int kCols = BN < 32 ? 32 : BN;              // of tensor memory
 };
+constexpr int kMaxStages = 24;
 
-// This CTA's share of the tile's rows of A, over the SPLIT CTAs of the cluster whose sums are added in rank order.  A
-// warp takes a row of 128 columns at a time.
+// What the warps that carry a tile out know before its sums are there.
+struct TileLane {
+    Lane l;
+    float b[4];
+};
+__device__ __forceinline__ TileLane make_tile_lane(const ProductArgs& a, int64_t group, int col, int end) {
+    TileLane t = {make_lane(a.e), {}};
+    if (a.e.bias && col < end) read4(a.e.bias, group * a.e.n + col, end - col, !a.e.bias_bf16, a.e.vec, t.b);
+    return t;
+}
+
+// This CTA's share of the tile's rows of A, over the SPLIT CTAs of the cluster whose sums are added in rank order, by four
+// warps.  A warp takes four rows of 128 columns at a time.
 template <int SPLIT, int BN>
-__device__ __forceinline__ void emit_tile(const ProductArgs& a, uint32_t part, int rank, int64_t group, int p0, int q0, int q_end) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = p0 + lane * 4;
+__device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uint32_t part, int rank, int col, int end, int q0, int q_end) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Epilogue& e = a.e;
-    Lane l = make_lane(e);
-    float b[4] = {};
-    if (e.bias && col < e.n) read4(e.bias, group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
     constexpr int kShare = BN / SPLIT;
-    constexpr int kRows = kShare < 4 ? kShare : 4;  // of a warp at a time
+    constexpr int kRows = kShare < 4 ? kShare : 4;
 #pragma unroll 1
-    for (int t = rank * kShare + warp * kRows; t < (rank + 1) * kShare && q0 + t < q_end; t += 6 * kRows) {
-        const int row = q0 + t;
+    for (int i0 = rank * kShare + warp * kRows; i0 < (rank + 1) * kShare && q0 + i0 < q_end; i0 += 4 * kRows) {
+        const int row = q0 + i0;
         float r[kRows][4] = {}, v[kRows][4] = {};
         uint32_t on = 0;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             on |= (uint32_t)(row + i < q_end) << i;
-            if (e.residual && col < e.n && row + i < q_end) read4(e.residual, (int64_t)(row + i) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
+            if (e.residual && col < end && row + i < q_end) read4(e.residual, (int64_t)(row + i) * e.n + col, end - col, e.f32, e.vec, r[i]);
         }
         if (SPLIT == 1) {
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) ld_shared_v4(part + (t + i) * 512 + lane * 16, v[i]);
+            for (int i = 0; i < kRows; ++i) ld_shared_v4(part + (i0 + i) * 512 + lane * 16, v[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 float4 x[SPLIT];
 #pragma unroll
-                for (int j = 0; j < SPLIT; ++j) x[j] = ld_cluster_f32x4(in_cluster(part + (t + i) * 512 + lane * 16, j));
+                for (int j = 0; j < SPLIT; ++j) x[j] = ld_cluster_f32x4(in_cluster(part + (i0 + i) * 512 + lane * 16, j));
 #pragma unroll
                 for (int j = 0; j < SPLIT; ++j) v[i][0] += x[j].x, v[i][1] += x[j].y, v[i][2] += x[j].z, v[i][3] += x[j].w;
             }
         }
-        emit_rows<kRows>(e, l, row, 1, on, col, v, b, r);
+        emit_rows<kRows>(e, t.l, row, 1, on, col, end, v, t.b, r);
     }
-    flush_lane(e, l);
+    flush_lane(e, t.l);
 }
 
 template <int BN>
@@ -456,16 +465,21 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
                                                          const ProductArgs a) {
     using G = PrGeom<BN>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[G::kStages], empty[G::kStages], done;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
     __shared__ uint32_t tmem_slot, loads;
     __shared__ int gave_up;
+    const uint32_t stages = a.stages, stage_bytes = a.stage_bytes, p_bytes = stage_bytes - G::kQBytes;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
     const int tile = blockIdx.x / a.split;
 
     if (threadIdx.x == 128) {
-        for (int i = 0; i < G::kStages; ++i) {
+        if (a.k > 0) {
+            prefetch_map(&map_p);
+            prefetch_map(&map_q);
+        }
+        for (uint32_t i = 0; i < stages; ++i) {
             mbar_init(&full[i]);
             mbar_init(&empty[i]);
         }
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     if (a.offsets) {
         // this tile's group: tiles of B fastest, so that the tiles of a group's rows share its weights in L2
         const int t = tile / a.p_tiles;
-        p0 = tile % a.p_tiles * 128;
+        p0 = tile % a.p_tiles * a.p_high;
         int before = 0, g0 = 0;
         bool found = false;
         for (; g0 < a.groups; g0 += 32) {
@@ -510,7 +524,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             return;
         }
     } else {
-        p0 = tile / a.q_tiles * 128;
+        p0 = tile / a.q_tiles * a.p_high;
         q0 = tile % a.q_tiles * BN;
     }
     // this CTA's steps
@@ -520,6 +534,8 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
         tmem_alloc<1>(&tmem_slot, G::kCols);
         let_next_start();
     }
+    const int col = p0 + lane * 4, end = min(a.e.n, p0 + a.p_high);
+    TileLane t;
     uint32_t tmem = 0;
     if (warp != 4) {  // copies start without it
         tc_fence_before();
@@ -536,23 +552,23 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
                 ok = false;
                 break;
             }
-            const uint32_t at = base + st * G::kStageBytes;
+            const uint32_t at = base + st * stage_bytes;
             if (elect_lane()) {
-                expect_bytes(&full[st], G::kStageBytes);
+                expect_bytes(&full[st], stage_bytes);
                 if (a.p_across)
                     tile_load3(at, &map_p, p0, s * kStepK, group, &full[st]);
                 else
                     tile_load3(at, &map_p, s * kStepK, p0, group, &full[st]);
                 if (a.q_across)
-                    tile_load3(at + kBoxBytes, &map_q, q0, s * kStepK, 0, &full[st]);
+                    tile_load3(at + p_bytes, &map_q, q0, s * kStepK, 0, &full[st]);
                 else
-                    tile_load3(at + kBoxBytes, &map_q, s * kStepK, q0, 0, &full[st]);
+                    tile_load3(at + p_bytes, &map_q, s * kStepK, q0, 0, &full[st]);
             }
             __syncwarp();
-            if (++st == G::kStages) st = 0, ++round;
+            if (++st == stages) st = 0, ++round;
         }
         // the tensor core's last arrivals land before the CTA may go
-        for (uint32_t i = n > G::kStages ? n - G::kStages : 0; i < n && ok; ++i) ok = mbar_wait_all(&empty[i % G::kStages], (i / G::kStages) & 1);
+        for (uint32_t i = n > stages ? n - stages : 0; i < n && ok; ++i) ok = mbar_wait_all(&empty[i % stages], (i / stages) & 1);
         if (lane == 0) {
             if (!ok) gave_up = 1;
             loads = n;
@@ -568,8 +584,8 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             }
             tc_fence_after();
             const int nk = min(4, (a.k - s * kStepK + 31) / 32);
-            const uint32_t at = base + st * G::kStageBytes;
-            const uint64_t dp = desc_codes(at), dq = desc_codes(at + kBoxBytes);
+            const uint32_t at = base + st * stage_bytes;
+            const uint64_t dp = desc_codes(at), dq = desc_codes(at + p_bytes);
             if (elect_lane()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -577,13 +593,14 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
                 tc_commit(&empty[st]);
             }
             __syncwarp();
-            if (++st == G::kStages) st = 0, ++round;
+            if (++st == stages) st = 0, ++round;
         }
         if (elect_lane()) {
             tc_commit(&done);
             if (!ok) gave_up = 1;
         }
     } else {
+        t = make_tile_lane(a, group, col, end);
         if (!mbar_wait_warp(&done, 0, 0) || pr_made_to_fail(a, kPrOutDone, 0)) gave_up = 1;
     }
     __syncwarp();
@@ -592,7 +609,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     const int bad = gave_up;
     if (bad) {  // copies still under way end before the CTA does, and before sums (and NaN) lie where they go
         if (threadIdx.x == 0)
-            for (uint32_t n = loads > G::kStages ? loads - G::kStages : 0; n < loads; ++n) mbar_wait(&full[n % G::kStages], (n / G::kStages) & 1);
+            for (uint32_t n = loads > stages ? loads - stages : 0; n < loads; ++n) mbar_wait(&full[n % stages], (n / stages) & 1);
         __syncthreads();
     }
     // the sums in shared memory, a row of A's 128 columns side by side; a wait that ran out (correct operation never gets there)
@@ -611,13 +628,15 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     tc_fence_before();
     if (a.split == 1) {
         __syncthreads();
-        emit_tile<1, BN>(a, base, 0, group, p0, q0, q_end);
+        if (warp < 4) emit_tile<1, BN>(a, t, base, 0, col, end, q0, q_end);
     } else {
         cluster_sync_all();
-        switch (a.split) {
-            case 2: emit_tile<2, BN>(a, base, rank, group, p0, q0, q_end); break;
-            case 4: emit_tile<4, BN>(a, base, rank, group, p0, q0, q_end); break;
-            default: emit_tile<8, BN>(a, base, rank, group, p0, q0, q_end);
+        if (warp < 4) {
+            switch (a.split) {
+                case 2: emit_tile<2, BN>(a, t, base, rank, col, end, q0, q_end); break;
+                case 4: emit_tile<4, BN>(a, t, base, rank, col, end, q0, q_end); break;
+                default: emit_tile<8, BN>(a, t, base, rank, col, end, q0, q_end);
+            }
         }
         cluster_sync_all();  // no CTA's sums go away while another reads them
     }
@@ -702,6 +721,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
     const int stride = gridDim.x / 2, first = blockIdx.x / 2;
 
     if (threadIdx.x == 0) {
+        if (a.k > 0) {
+            prefetch_map(&map_p);
+            prefetch_map(&map_q);
+        }
         for (int i = 0; i < kPrPairStages; ++i) {
             mbar_init_count(&full[i], RAGGED_K ? 2 : 1);
             mbar_init(&landed[i]);
@@ -889,6 +912,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
             const uint32_t bar = in_cluster(smem_addr(&drained[set]), 0);
             const int p_first = w.p0 + (int)rank * 128 + (warp & 3) * 32;
             const int64_t d_first = (int64_t)p_first + (RAGGED_K ? (int64_t)w.group * a.m : 0);
+            if (e.residual && e.wide && p_first + lane < w.p_end) {  // on its way to L2 while the tensor cores work
+                const int q = w.q0 + (warp >> 2) * 128, there = min(128, e.n - q), size = e.f32 ? 4 : 2;
+                if (there > 0) block_prefetch(static_cast<const uint8_t*>(e.residual) + ((d_first + lane) * e.n + q) * size, there * size);
+            }
             ok = ok && mbar_wait_warp(&done[set], (it >> 1) & 1, 32) && !pr_made_to_fail(a, kPrOutDone, it);
             if (!ok) gave_up = 1;
             tc_fence_after();
@@ -946,7 +973,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = __uint_as_float(0x7FFFFFFFu);
                 }
-                emit_rows<8>(e, l, d_first + sub, 4, on, col, x, b, r);
+                emit_rows<8>(e, l, d_first + sub, 4, on, col, e.n, x, b, r);
             }
         }
         flush_lane(e, l);
@@ -984,12 +1011,21 @@ bool operand_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t k, in
 }
 
 template <int BN>
-fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, const ProductArgs& a, unsigned grid, cudaStream_t s) {
+fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, ProductArgs a, unsigned grid, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};
     auto kern = fp8_matmul_kernel<BN>;
     const cudaError_t e = allow_smem(kern, PrGeom<BN>::kSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_kernel setup");
-    return launch_behind(kern, dim3(grid), dim3(192), PrGeom<BN>::kSmem, (unsigned)a.split, s, "fp8_matmul_kernel", mp, mq, a);
+    // As many stages as there is room for: what is on its way has to cover the memory's latency however few rows a step has
+    // (4096 rows by 16384 with 16 rows a CTA: 34 us with five stages, whose step of 2 KB takes 0.25 us as one of 16 does).
+    // The multiply-adds read 128 rows of B, whatever lies behind a CTA's own, which ends in lanes that nobody reads.
+    a.stage_bytes = (a.p_across ? kBoxBytes : a.p_high * kStepK) + PrGeom<BN>::kQBytes;
+    const int behind = a.p_across ? 0 : kBoxBytes - a.p_high * kStepK, steps = ((a.k + kStepK - 1) / kStepK + a.split - 1) / a.split;
+    a.stages = (PrGeom<BN>::kSmem - 1024 - behind) / a.stage_bytes;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    if (a.stages > steps) a.stages = steps > 1 ? steps : 1;  // what a short k leaves free lets the next kernel start
+    const int need = a.stages * a.stage_bytes + behind;
+    return launch_behind(kern, dim3(grid), dim3(192), (need > BN * 512 ? need : BN * 512) + 1024, (unsigned)a.split, s, "fp8_matmul_kernel", mp, mq, a);
 }
 
 template <bool RAGGED_K>
@@ -1099,18 +1135,31 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     a.idesc = mma_desc_fp8(128, bn, fb, fa, tb, ta);
     a.p_across = tb;
     a.q_across = ta;
-    a.p_tiles = (int32_t)((p->n + 127) / 128);
     a.q_tiles = (int32_t)((p->m + bn - 1) / bn);
     // a grouped call does not know its groups: at most as many tiles as full ones and one part of a tile in each
-    int64_t q_tiles = a.q_tiles;
-    if (how == kGroupedRows) q_tiles = p->m / bn + (groups < p->m ? groups : p->m);
-    const int64_t tiles = a.p_tiles * q_tiles, room = (bn <= 32 ? 2 : 1) * sms;
-    int split = 1, most = 1;
-    while (most < 8 && tiles * most * 2 <= room * (most == 1 ? 20 : most == 2 ? 19 : 16) / 20 && steps >= most * 4) most *= 2;
-    if (steps - steps / most > 3 + bn / 32) split = most;
+    const int64_t q_tiles = how == kGroupedRows ? p->m / bn + (groups < p->m ? groups : p->m) : a.q_tiles;
+    // The rows of B that a CTA takes, and the CTAs of a cluster that share a tile's k, so that what the slowest SM reads is
+    // least: as many CTAs as are resident (two an SM up to 32 rows of A; clusters of 4 and 8 reach 19 and 16 of 20 of them),
+    // in units of a row's step.  A cluster's sums cost as much as some of them.
+    const int64_t room = (bn <= 64 ? 2 : 1) * sms;
+    const int grain = e.h ? 32 : 16;
+    int high = 128, split = 1;
+    int64_t least = INT64_MAX;
+    for (int t = 1; t <= 8 && (t == 1 || steps >= 2 * t); t *= 2) {
+        const int64_t slots = room * (t < 4 ? 20 : t == 4 ? 19 : 16) / 20 / t, across = slots / q_tiles;  // tiles of B a round
+        int64_t high_t = 128;
+        if (!tb && across > 0) high_t = ((p->n + across - 1) / across + grain - 1) / grain * grain;
+        if (high_t > 128) high_t = 128;
+        const int64_t rounds = ((p->n + high_t - 1) / high_t * q_tiles + slots - 1) / (slots > 0 ? slots : 1);
+        const int64_t cost = rounds * ((high_t + bn / 2 + 8) * ((steps + t - 1) / t) + 128) + (t > 1 ? 160 + 2 * bn : 0);
+        if (slots > 0 && cost < least) least = cost, high = (int)high_t, split = t;
+    }
+    a.p_high = high;
+    a.p_tiles = (int32_t)((p->n + high - 1) / high);
+    const int64_t tiles = a.p_tiles * q_tiles;
     a.split = split;
     if (tiles * split > 0x7FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
-    if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, 128) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
+    if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, high) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
         return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_kernel tensor map");
     const unsigned grid = (unsigned)(tiles * split);
     switch (bn) {

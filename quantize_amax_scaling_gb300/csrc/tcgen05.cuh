@@ -319,6 +319,11 @@ __device__ __forceinline__ void block_load(uint32_t dst, const void* src, uint32
                  : "memory");
 }
 
+// Bytes (a multiple of 16, from a 16-byte address) on their way to L2.
+__device__ __forceinline__ void block_prefetch(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // A box from shared memory, clipped at the tensor's edges; one thread's stores
 // are done reading shared memory after store_read_wait(), done altogether after
 // store_wait().

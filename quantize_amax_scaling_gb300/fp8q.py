@@ -559,8 +559,13 @@ def fp8q_grouped_weight_gradient(a, b, offsets, d, a_fmt=E5M2, b_fmt=E4M3FN, a_s
 
 
 def checkpoint_empty(rows, cols, device="cuda"):
-    """Room for the 8-bit checkpoint of an [rows, cols] activation: (codes [rows, cols], scales [rows, blocks of 32])."""
+    """Room for the 8-bit checkpoint of an [rows, cols] activation: (codes [rows, cols], scales [rows, blocks of 32]); on
+    the current CUDA device one allocation holds both."""
+    if device == "cuda":
+        return _native().checkpoint_empty(rows, cols)
     import torch
+    if not (0 <= rows <= _FP4_MAX_DIM and 0 <= cols <= _FP4_MAX_DIM):
+        raise ValueError("checkpoint_empty takes rows and cols from 0 to 2^31 - 1024")
     return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
             torch.empty((rows, (cols + 31) // 32), dtype=torch.uint8, device=device))
 
