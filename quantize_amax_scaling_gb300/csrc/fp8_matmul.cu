@@ -51,8 +51,7 @@ struct ProductArgs {
     uint32_t idesc;
     int32_t p_across, q_across;  // P's, Q's rows do not lie along k
     int32_t p_tiles, q_tiles;    // tiles of a group where all have the same
-    int32_t p_high;              // rows of B a CTA (few tiles)
-    int32_t stages, stage_bytes;
+    int32_t stages, per;         // stages of `per` steps
     int32_t split;               // CTAs of a cluster that share a tile's k
 #ifdef FP8Q_TEST_HOOKS
     int32_t fail_role, fail_at, fail_cta;  // the wait that reports failure although what it waits for has come
@@ -134,11 +133,11 @@ __device__ __forceinline__ Lane make_lane(const Epilogue& e) {
     return l;
 }
 
-// Columns col to col + 3 of a row of D, before `end`; eight lanes side by side hold a block of 32 columns.  `on`: the row is there.
+// Columns col to col + 3 of a row of D; eight lanes side by side hold a block of 32 columns.  `on`: the row is there.
 // r: the residual.  All lanes of a warp come here.  (Any n, any addresses, any scale of q.)
-__device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, int col, int end, bool on, const float (&sum)[4], const float (&b)[4],
+__device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, int col, bool on, const float (&sum)[4], const float (&b)[4],
                                       const float (&r)[4]) {
-    const int left = end - col;
+    const int left = e.n - col;
     on = on && left > 0;
     float v[4];
 #pragma unroll
@@ -208,15 +207,15 @@ __device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, i
 // ordinary scale go through the stages all rows at a time, so that a stage's latencies overlap: row by row, with the
 // branches between, 8192x16384x4096 took 731 us with GELU, codes and checkpoint and 411 with bf16 alone.
 template <int ROWS>
-__device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t row, int step, uint32_t on, int col, int end, float (&v)[ROWS][4],
+__device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t row, int step, uint32_t on, int col, float (&v)[ROWS][4],
                                           const float (&b)[4], const float (&r)[ROWS][4]) {
     if (!e.vec || (e.q && !l.c.fast)) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) emit4(e, l, row + i * step, col, end, on >> i & 1, v[i], b, r[i]);
+        for (int i = 0; i < ROWS; ++i) emit4(e, l, row + i * step, col, on >> i & 1, v[i], b, r[i]);
         return;
     }
-    const uint32_t here = (col & ~31) < end ? on : 0u;  // of a block's eight lanes the first may be the only one with columns
-    if (col >= end) on = 0;
+    const uint32_t here = (col & ~31) < e.n ? on : 0u;  // of a block's eight lanes the first may be the only one with columns
+    if (col >= e.n) on = 0;
     const float2 alpha = splat2(l.alpha), b0 = make_float2(b[0], b[1]), b1 = make_float2(b[2], b[3]);
     float2 x[ROWS][2];
 #pragma unroll
@@ -231,7 +230,7 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             w[i][0] = cvt_bf16x2(x[i][0].x, x[i][0].y), w[i][1] = cvt_bf16x2(x[i][1].x, x[i][1].y);
-            a[i] = col < end ? bf16x2_absmax(w[i][0], w[i][1]) : 0u;
+            a[i] = col < e.n ? bf16x2_absmax(w[i][0], w[i][1]) : 0u;
         }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1)
@@ -407,27 +406,27 @@ __device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 
 
 template <int BN>
 struct PrGeom {
-    static constexpr int kQBytes = BN * kStepK;
+    static constexpr int kBoxes = kBoxBytes + BN * kStepK;        // a step's codes of B and of A
     static constexpr int kSmem = (BN <= 64 ? 112 : 160) * 1024;  // two CTAs an SM, or one
+    static constexpr int kMaxStages = kSmem / kBoxes;
     static constexpr int kCols = BN < 32 ? 32 : BN;              // of tensor memory
 };
-constexpr int kMaxStages = 24;
 
 // What the warps that carry a tile out know before its sums are there.
 struct TileLane {
     Lane l;
     float b[4];
 };
-__device__ __forceinline__ TileLane make_tile_lane(const ProductArgs& a, int64_t group, int col, int end) {
+__device__ __forceinline__ TileLane make_tile_lane(const ProductArgs& a, int64_t group, int col) {
     TileLane t = {make_lane(a.e), {}};
-    if (a.e.bias && col < end) read4(a.e.bias, group * a.e.n + col, end - col, !a.e.bias_bf16, a.e.vec, t.b);
+    if (a.e.bias && col < a.e.n) read4(a.e.bias, group * a.e.n + col, a.e.n - col, !a.e.bias_bf16, a.e.vec, t.b);
     return t;
 }
 
 // This CTA's share of the tile's rows of A, over the SPLIT CTAs of the cluster whose sums are added in rank order, by four
 // warps.  A warp takes four rows of 128 columns at a time.
 template <int SPLIT, int BN>
-__device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uint32_t part, int rank, int col, int end, int q0, int q_end) {
+__device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uint32_t part, int rank, int col, int q0, int q_end) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Epilogue& e = a.e;
     constexpr int kShare = BN / SPLIT;
@@ -440,7 +439,7 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             on |= (uint32_t)(row + i < q_end) << i;
-            if (e.residual && col < end && row + i < q_end) read4(e.residual, (int64_t)(row + i) * e.n + col, end - col, e.f32, e.vec, r[i]);
+            if (e.residual && col < e.n && row + i < q_end) read4(e.residual, (int64_t)(row + i) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
         }
         if (SPLIT == 1) {
 #pragma unroll
@@ -455,7 +454,7 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
                 for (int j = 0; j < SPLIT; ++j) v[i][0] += x[j].x, v[i][1] += x[j].y, v[i][2] += x[j].z, v[i][3] += x[j].w;
             }
         }
-        emit_rows<kRows>(e, t.l, row, 1, on, col, end, v, t.b, r);
+        emit_rows<kRows>(e, t.l, row, 1, on, col, v, t.b, r);
     }
     flush_lane(e, t.l);
 }
@@ -465,10 +464,10 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
                                                          const ProductArgs a) {
     using G = PrGeom<BN>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint64_t full[G::kMaxStages], empty[G::kMaxStages], done;
     __shared__ uint32_t tmem_slot, loads;
     __shared__ int gave_up;
-    const uint32_t stages = a.stages, stage_bytes = a.stage_bytes, p_bytes = stage_bytes - G::kQBytes;
+    const uint32_t stages = a.stages, stage_bytes = a.per * G::kBoxes;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     if (a.offsets) {
         // this tile's group: tiles of B fastest, so that the tiles of a group's rows share its weights in L2
         const int t = tile / a.p_tiles;
-        p0 = tile % a.p_tiles * a.p_high;
+        p0 = tile % a.p_tiles * 128;
         int before = 0, g0 = 0;
         bool found = false;
         for (; g0 < a.groups; g0 += 32) {
@@ -524,7 +523,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             return;
         }
     } else {
-        p0 = tile / a.q_tiles * a.p_high;
+        p0 = tile / a.q_tiles * 128;
         q0 = tile % a.q_tiles * BN;
     }
     // this CTA's steps
@@ -534,7 +533,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
         tmem_alloc<1>(&tmem_slot, G::kCols);
         let_next_start();
     }
-    const int col = p0 + lane * 4, end = min(a.e.n, p0 + a.p_high);
+    const int col = p0 + lane * 4;
     TileLane t;
     uint32_t tmem = 0;
     if (warp != 4) {  // copies start without it
@@ -547,22 +546,25 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     if (warp == 4) {
         uint32_t st = 0, round = 0, n = 0;
         bool ok = true;
-        for (int s = s0; s < s1; ++s, ++n) {
+        for (int s = s0; s < s1; s += a.per, ++n) {
             if (!pr_wait(a, kPrCopyEmpty, n, &empty[st], (round & 1) ^ 1)) {
                 ok = false;
                 break;
             }
-            const uint32_t at = base + st * stage_bytes;
+            const int there = min(a.per, s1 - s);
             if (elect_lane()) {
-                expect_bytes(&full[st], stage_bytes);
-                if (a.p_across)
-                    tile_load3(at, &map_p, p0, s * kStepK, group, &full[st]);
-                else
-                    tile_load3(at, &map_p, s * kStepK, p0, group, &full[st]);
-                if (a.q_across)
-                    tile_load3(at + p_bytes, &map_q, q0, s * kStepK, 0, &full[st]);
-                else
-                    tile_load3(at + p_bytes, &map_q, s * kStepK, q0, 0, &full[st]);
+                uint32_t at = base + st * stage_bytes;
+                expect_bytes(&full[st], there * G::kBoxes);
+                for (int k = s * kStepK; k < (s + there) * kStepK; k += kStepK, at += G::kBoxes) {
+                    if (a.p_across)
+                        tile_load3(at, &map_p, p0, k, group, &full[st]);
+                    else
+                        tile_load3(at, &map_p, k, p0, group, &full[st]);
+                    if (a.q_across)
+                        tile_load3(at + kBoxBytes, &map_q, q0, k, 0, &full[st]);
+                    else
+                        tile_load3(at + kBoxBytes, &map_q, k, q0, 0, &full[st]);
+                }
             }
             __syncwarp();
             if (++st == stages) st = 0, ++round;
@@ -577,19 +579,22 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
         uint32_t st = 0, round = 0;
         bool ok = true;
         const uint64_t next_p = k_advance(a.p_across), next_q = k_advance(a.q_across);
-        for (int s = s0; s < s1; ++s) {
-            if (!pr_wait(a, kPrSumFull, s - s0, &full[st], round & 1)) {
+        for (int s = s0, n = 0; s < s1; s += a.per, ++n) {
+            if (!pr_wait(a, kPrSumFull, n, &full[st], round & 1)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const int nk = min(4, (a.k - s * kStepK + 31) / 32);
-            const uint32_t at = base + st * stage_bytes;
-            const uint64_t dp = desc_codes(at), dq = desc_codes(at + p_bytes);
+            const int end_k = min(a.k, min(s + a.per, s1) * kStepK);
+            uint32_t at = base + st * stage_bytes;
             if (elect_lane()) {
+                for (int k = s * kStepK; k < end_k; k += kStepK, at += G::kBoxes) {
+                    const int nk = (end_k - k + 31) / 32;
+                    const uint64_t dp = desc_codes(at), dq = desc_codes(at + kBoxBytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < nk) tc_mma_fp8<1>(tmem, dp + k * next_p, dq + k * next_q, a.idesc, (s - s0) | k);
+                    for (int i = 0; i < 4; ++i)
+                        if (i < nk) tc_mma_fp8<1>(tmem, dp + i * next_p, dq + i * next_q, a.idesc, (k - s0 * kStepK) | i);
+                }
                 tc_commit(&empty[st]);
             }
             __syncwarp();
@@ -600,7 +605,10 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             if (!ok) gave_up = 1;
         }
     } else {
-        t = make_tile_lane(a, group, col, end);
+        t = make_tile_lane(a, group, col);
+        const int row = q0 + rank * (BN / a.split) + (int)threadIdx.x;  // the residual on its way to L2
+        if (a.e.residual && a.e.wide && (int)threadIdx.x < BN / a.split && row < q_end)
+            block_prefetch(static_cast<const uint8_t*>(a.e.residual) + ((int64_t)row * a.e.n + p0) * (a.e.f32 ? 4 : 2), min(128, a.e.n - p0) * (a.e.f32 ? 4 : 2));
         if (!mbar_wait_warp(&done, 0, 0) || pr_made_to_fail(a, kPrOutDone, 0)) gave_up = 1;
     }
     __syncwarp();
@@ -628,14 +636,14 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     tc_fence_before();
     if (a.split == 1) {
         __syncthreads();
-        if (warp < 4) emit_tile<1, BN>(a, t, base, 0, col, end, q0, q_end);
+        if (warp < 4) emit_tile<1, BN>(a, t, base, 0, col, q0, q_end);
     } else {
         cluster_sync_all();
         if (warp < 4) {
             switch (a.split) {
-                case 2: emit_tile<2, BN>(a, t, base, rank, col, end, q0, q_end); break;
-                case 4: emit_tile<4, BN>(a, t, base, rank, col, end, q0, q_end); break;
-                default: emit_tile<8, BN>(a, t, base, rank, col, end, q0, q_end);
+                case 2: emit_tile<2, BN>(a, t, base, rank, col, q0, q_end); break;
+                case 4: emit_tile<4, BN>(a, t, base, rank, col, q0, q_end); break;
+                default: emit_tile<8, BN>(a, t, base, rank, col, q0, q_end);
             }
         }
         cluster_sync_all();  // no CTA's sums go away while another reads them
@@ -973,7 +981,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = __uint_as_float(0x7FFFFFFFu);
                 }
-                emit_rows<8>(e, l, d_first + sub, 4, on, col, e.n, x, b, r);
+                emit_rows<8>(e, l, d_first + sub, 4, on, col, x, b, r);
             }
         }
         flush_lane(e, l);
@@ -1016,15 +1024,15 @@ fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, Product
     auto kern = fp8_matmul_kernel<BN>;
     const cudaError_t e = allow_smem(kern, PrGeom<BN>::kSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_kernel setup");
-    // As many stages as there is room for: what is on its way has to cover the memory's latency however few rows a step has
-    // (4096 rows by 16384 with 16 rows a CTA: 34 us with five stages, whose step of 2 KB takes 0.25 us as one of 16 does).
-    // The multiply-adds read 128 rows of B, whatever lies behind a CTA's own, which ends in lanes that nobody reads.
-    a.stage_bytes = (a.p_across ? kBoxBytes : a.p_high * kStepK) + PrGeom<BN>::kQBytes;
-    const int behind = a.p_across ? 0 : kBoxBytes - a.p_high * kStepK, steps = ((a.k + kStepK - 1) / kStepK + a.split - 1) / a.split;
-    a.stages = (PrGeom<BN>::kSmem - 1024 - behind) / a.stage_bytes;
-    if (a.stages > kMaxStages) a.stages = kMaxStages;
-    if (a.stages > steps) a.stages = steps > 1 ? steps : 1;  // what a short k leaves free lets the next kernel start
-    const int need = a.stages * a.stage_bytes + behind;
+    // Stages of up to four steps, three stages or more: a stage's waits and its arrival take its issuers 150 cycles each, and
+    // a step 150 beside (24x4096x16384 with clusters of two: 16.3 us, 18.5 with a step a stage).
+    const int steps = ((a.k + kStepK - 1) / kStepK + a.split - 1) / a.split;
+    const int room = (PrGeom<BN>::kSmem - 1024) / PrGeom<BN>::kBoxes;
+    a.per = room >= 12 ? 4 : room >= 6 ? 2 : 1;
+    a.stages = room / a.per;
+    const int most = (steps + a.per - 1) / a.per;  // what a short k leaves free lets the next kernel start
+    if (a.stages > most) a.stages = most > 1 ? most : 1;
+    const int need = a.stages * a.per * PrGeom<BN>::kBoxes;
     return launch_behind(kern, dim3(grid), dim3(192), (need > BN * 512 ? need : BN * 512) + 1024, (unsigned)a.split, s, "fp8_matmul_kernel", mp, mq, a);
 }
 
@@ -1138,28 +1146,19 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     a.q_tiles = (int32_t)((p->m + bn - 1) / bn);
     // a grouped call does not know its groups: at most as many tiles as full ones and one part of a tile in each
     const int64_t q_tiles = how == kGroupedRows ? p->m / bn + (groups < p->m ? groups : p->m) : a.q_tiles;
-    // The rows of B that a CTA takes, and the CTAs of a cluster that share a tile's k, so that what the slowest SM reads is
-    // least: as many CTAs as are resident (two an SM up to 32 rows of A; clusters of 4 and 8 reach 19 and 16 of 20 of them),
-    // in units of a row's step.  A cluster's sums cost as much as some of them.
-    const int64_t room = (bn <= 64 ? 2 : 1) * sms;
-    const int grain = e.h ? 32 : 16;
-    int high = 128, split = 1;
-    int64_t least = INT64_MAX;
-    for (int t = 1; t <= 8 && (t == 1 || steps >= 2 * t); t *= 2) {
-        const int64_t slots = room * (t < 4 ? 20 : t == 4 ? 19 : 16) / 20 / t, across = slots / q_tiles;  // tiles of B a round
-        int64_t high_t = 128;
-        if (!tb && across > 0) high_t = ((p->n + across - 1) / across + grain - 1) / grain * grain;
-        if (high_t > 128) high_t = 128;
-        const int64_t rounds = ((p->n + high_t - 1) / high_t * q_tiles + slots - 1) / (slots > 0 ? slots : 1);
-        const int64_t cost = rounds * ((high_t + bn / 2 + 8) * ((steps + t - 1) / t) + 128) + (t > 1 ? 160 + 2 * bn : 0);
-        if (slots > 0 && cost < least) least = cost, high = (int)high_t, split = t;
-    }
-    a.p_high = high;
-    a.p_tiles = (int32_t)((p->n + high - 1) / high);
+    a.p_tiles = (int32_t)((p->n + 127) / 128);
     const int64_t tiles = a.p_tiles * q_tiles;
+    // The CTAs of a cluster share a tile's sums, as many as are resident at once (two an SM up to 64 rows of A; clusters
+    // of 4 and 8 reach 19 and 17 of 20 of them) and have four steps or more, where the steps that a CTA saves are worth the
+    // cluster and its sums: 1x4096x4096 7.2 us on clusters of 8, 7.9 on 2; 1x1024x4096 4.7, 5.6 on 4; but two rounds of
+    // CTAs cost more than they save, 1x16384x4096 18 us on clusters of 4, 13.9 on 2.
+    const int64_t room = (bn <= 64 ? 2 : 1) * sms;
+    int split = 1, most = 1;
+    while (most < 8 && tiles * most * 2 <= room * (most == 1 ? 20 : most == 2 ? 19 : 17) / 20 && steps >= most * 8) most *= 2;
+    if (steps - steps / most > 3 + bn / 32) split = most;
     a.split = split;
     if (tiles * split > 0x7FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
-    if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, high) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
+    if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, 128) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
         return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_kernel tensor map");
     const unsigned grid = (unsigned)(tiles * split);
     switch (bn) {
