@@ -550,35 +550,46 @@ PyObject* empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
-// Addresses of the entry points, in the order of the calls below.
-PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    constexpr int kEntries = 13;
-    void* p[kEntries] = {};
-    for (Py_ssize_t i = 0; i < kEntries; ++i) {
-        if (i < n) p[i] = PyLong_AsVoidPtr(a[i]);
-        if (!p[i]) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind takes thirteen addresses");
-            return nullptr;
-        }
+// Addresses of entry points, in the order of the calls below.
+template <size_t N>
+bool addresses(PyObject* const* a, Py_ssize_t n, void* (&p)[N]) {
+    for (size_t i = 0; i < N; ++i) {
+        p[i] = (Py_ssize_t)i < n ? PyLong_AsVoidPtr(a[i]) : nullptr;
+        if (p[i]) continue;
+        if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "bind takes %zu addresses", N);
+        return false;
     }
+    return true;
+}
+
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    void* p[6];
+    if (!addresses(a, n, p)) return nullptr;
     g_quantize = reinterpret_cast<decltype(g_quantize)>(p[0]);
     g_dequantize = reinterpret_cast<decltype(g_dequantize)>(p[1]);
     g_matmul = reinterpret_cast<decltype(g_matmul)>(p[2]);
     g_norm = reinterpret_cast<decltype(g_norm)>(p[3]);
     g_norm_backward = reinterpret_cast<decltype(g_norm_backward)>(p[4]);
     g_workspace = reinterpret_cast<decltype(g_workspace)>(p[5]);
-    g_product = reinterpret_cast<decltype(g_product)>(p[6]);
-    g_grouped = reinterpret_cast<decltype(g_grouped)>(p[7]);
-    g_grouped_gradient = reinterpret_cast<decltype(g_grouped_gradient)>(p[8]);
-    g_checkpoint = reinterpret_cast<decltype(g_checkpoint)>(p[9]);
-    g_checkpoint_back = reinterpret_cast<decltype(g_checkpoint_back)>(p[10]);
-    g_gelu_backward = reinterpret_cast<decltype(g_gelu_backward)>(p[11]);
-    g_gelu_workspace = reinterpret_cast<decltype(g_gelu_workspace)>(p[12]);
+    Py_RETURN_NONE;
+}
+
+PyObject* bind_products(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    void* p[7];
+    if (!addresses(a, n, p)) return nullptr;
+    g_product = reinterpret_cast<decltype(g_product)>(p[0]);
+    g_grouped = reinterpret_cast<decltype(g_grouped)>(p[1]);
+    g_grouped_gradient = reinterpret_cast<decltype(g_grouped_gradient)>(p[2]);
+    g_checkpoint = reinterpret_cast<decltype(g_checkpoint)>(p[3]);
+    g_checkpoint_back = reinterpret_cast<decltype(g_checkpoint_back)>(p[4]);
+    g_gelu_backward = reinterpret_cast<decltype(g_gelu_backward)>(p[5]);
+    g_gelu_workspace = reinterpret_cast<decltype(g_gelu_workspace)>(p[6]);
     Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f))
 PyMethodDef g_methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
+                           {"bind_products", FAST(bind_products), METH_FASTCALL, nullptr},
                            {"fp4_empty", FAST(empty<false>), METH_FASTCALL, nullptr},
                            {"checkpoint_empty", FAST(empty<true>), METH_FASTCALL, nullptr},
                            {"fp4_quantize_amax", FAST(call<quantize>), METH_FASTCALL, nullptr},

@@ -649,36 +649,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
 
 // Codes [rows, cols]: boxes of 128 bytes x box_rows rows, zeros beyond the edges.
 bool codes_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t cols, int box_rows) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const int64_t ld = fp4_row_bytes(cols);
-    const cuuint64_t dim[2] = {(cuuint64_t)ld, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {kStepBytes, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(q), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t ld = (cuuint64_t)fp4_row_bytes(cols);
+    return make_map<2>(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, {ld, (cuuint64_t)rows}, {ld}, {kStepBytes, (cuuint32_t)box_rows},
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // Block scales: rows of scale tiles along k, boxes of `tiles` of them x box_rows, zeros beyond the edges.
 bool scales_map(CUtensorMap* map, const uint8_t* sf, int64_t rows, int64_t across, int tiles, int box_rows) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const cuuint64_t dim[2] = {(cuuint64_t)across * 64, (cuuint64_t)((rows + 127) / 128)}, stride[1] = {(cuuint64_t)across * 512};
-    const cuuint32_t box[2] = {(cuuint32_t)tiles * 64, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(sf), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return make_map<2>(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, sf, {(cuuint64_t)across * 64, (cuuint64_t)((rows + 127) / 128)},
+                       {(cuuint64_t)across * 512}, {(cuuint32_t)tiles * 64, (cuuint32_t)box_rows}, CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // D: boxes of 32 rows of 128 bytes.
 template <bool F32>
 bool result_map(CUtensorMap* map, void* d, int64_t rows, int64_t cols) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
     constexpr int kBytes = F32 ? 4 : 2;
-    const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)cols * kBytes};
-    const cuuint32_t box[2] = {128 / kBytes, 32}, one[2] = {1, 1};
-    return f(map, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, d, dim, stride, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return make_map<2>(map, F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d, {(cuuint64_t)cols, (cuuint64_t)rows},
+                       {(cuuint64_t)cols * kBytes}, {128 / kBytes, 32}, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 template <int FMT, int BN, bool F32>

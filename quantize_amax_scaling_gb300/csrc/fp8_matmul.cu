@@ -1003,19 +1003,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
 // ----------------------------------------------------------------------------
 // Host
 
-// Codes: `lines` of `inner` bytes, `groups` times; boxes of 128 bytes x box_lines, zeros beyond the edges.
-bool fp8_map(CUtensorMap* map, const uint8_t* q, int64_t inner, int64_t lines, int64_t ld, int64_t groups, int box_lines) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const cuuint64_t dim[3] = {(cuuint64_t)inner, (cuuint64_t)lines, (cuuint64_t)groups}, stride[2] = {(cuuint64_t)ld, (cuuint64_t)(ld * lines)};
-    const cuuint32_t box[3] = {kStepK, (cuuint32_t)box_lines, 1}, one[3] = {1, 1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(q), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// An operand of `rows` rows; across: they do not lie along k.
+// An operand of `rows` rows, `groups` times; across: its rows do not lie along k.  Boxes of 128 bytes by 128 lines or box_rows
+// rows, zeros beyond the edges.
 bool operand_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t k, int64_t ld, int64_t groups, bool across, int box_rows) {
-    return fp8_map(map, q, across ? rows : k, across ? k : rows, ld, groups, across ? kStepK : box_rows);
+    const int64_t lines = across ? k : rows;
+    return make_map<3>(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, {(cuuint64_t)(across ? rows : k), (cuuint64_t)lines, (cuuint64_t)groups},
+                       {(cuuint64_t)ld, (cuuint64_t)(ld * lines)}, {kStepK, (cuuint32_t)(across ? kStepK : box_rows), 1},
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 template <int BN>

@@ -373,4 +373,29 @@ EncodeTiled encode_tiled() {
     return f;
 }
 
+// A tensor map of DIMS dimensions: sizes and strides (in bytes, of all but the first) and the box.  A thread that has made no
+// call of the runtime yet has no context, without which no map is made: the current device's is taken up then.
+template <int DIMS>
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, const cuuint64_t (&dim)[DIMS], const cuuint64_t (&stride)[DIMS - 1],
+              const cuuint32_t (&box)[DIMS], CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    cuuint32_t one[DIMS];
+    for (int i = 0; i < DIMS; ++i) one[i] = 1;
+    const auto make = [&] {
+        return f(map, type, DIMS, const_cast<void*>(p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = make();
+    if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED || r == CUDA_ERROR_CONTEXT_IS_DESTROYED) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return false;
+        }
+        r = make();
+    }
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace

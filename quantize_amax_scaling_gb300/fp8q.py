@@ -165,11 +165,11 @@ def _native():
         raise RuntimeError(f"_binding.so was made for {made_for or 'nothing yet'}, this is {runs or 'a Python without torch'}: "
                            "run python -m quantize_amax_scaling_gb300.build")
     from . import _binding as b
-    b.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-             (L.fp8q_fp4_quantize_amax, L.fp8q_fp4_dequantize, L.fp8q_fp4_matmul, L.fp8q_residual_norm_quantize_amax,
-              L.fp8q_residual_norm_backward, L.fp8q_residual_norm_backward_workspace, L.fp8q_matmul, L.fp8q_grouped_matmul,
-              L.fp8q_grouped_weight_gradient, L.fp8q_checkpoint_quantize, L.fp8q_checkpoint_dequantize,
-              L.fp8q_gelu_backward_quantize_amax, L.fp8q_gelu_backward_workspace)))
+    at = lambda *fs: (ctypes.cast(f, ctypes.c_void_p).value for f in fs)  # noqa: E731
+    b.bind(*at(L.fp8q_fp4_quantize_amax, L.fp8q_fp4_dequantize, L.fp8q_fp4_matmul, L.fp8q_residual_norm_quantize_amax,
+               L.fp8q_residual_norm_backward, L.fp8q_residual_norm_backward_workspace))
+    b.bind_products(*at(L.fp8q_matmul, L.fp8q_grouped_matmul, L.fp8q_grouped_weight_gradient, L.fp8q_checkpoint_quantize,
+                        L.fp8q_checkpoint_dequantize, L.fp8q_gelu_backward_quantize_amax, L.fp8q_gelu_backward_workspace))
     _binding = b
     return b
 
