@@ -37,7 +37,8 @@ struct Epilogue {
     int32_t blocks;  // of 32, a row
     bool f32, bias_bf16, gelu, e5m2;
     bool vec;   // four columns a vector, and
-    bool wide;  // sixteen bytes a vector, wherever a row starts
+    bool wide;   // sixteen bytes a vector, wherever a row starts, and
+    bool whole;  // thirty-two
 };
 
 // P is the operand whose rows are the accumulator's lanes, Q the one whose rows are its columns.
@@ -296,6 +297,18 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
 // block of the checkpoint is a lane's own.  For bf16, n a multiple of 16, 16-byte addresses and an ordinary scale.  (The
 // checkpoint's blocks over eight lanes each and codes through shared memory cost 105 us of 8192x16384x4096's 353, zeros for
 // operands; here 0.)
+// Thirty-two bytes of a row in one store where rows start on whole sectors (`whole`): each of the two halves is a request of
+// its own otherwise, in as many lines as there are lanes.
+__device__ __forceinline__ void st_row32(void* p, const uint4& a, const uint4& b, bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+                     "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = a;
+        static_cast<uint4*>(p)[1] = b;
+    }
+}
 __device__ __forceinline__ float2 as_f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 __device__ __forceinline__ float2 bf16_f2(uint32_t w) { return as_f2(w << 16, w & 0xFFFF0000u); }
 
@@ -338,11 +351,10 @@ __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t r
             for (int i = 0; i < o; ++i) m[i] = bf16x2_absmax(m[i], m[i + o]);
         const uint32_t code = ckpt_scale(max(m[0] & 0x7FFFu, m[0] >> 16 & 0x7FFFu));
         const float f = ckpt_factor(code);
-        uint4* h = reinterpret_cast<uint4*>(e.h + at);
+        uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            h[i] = make_uint4(ckpt_codes4(w[8 * i], w[8 * i + 1], f), ckpt_codes4(w[8 * i + 2], w[8 * i + 3], f),
-                              ckpt_codes4(w[8 * i + 4], w[8 * i + 5], f), ckpt_codes4(w[8 * i + 6], w[8 * i + 7], f));
+        for (int i = 0; i < 8; ++i) o[i] = ckpt_codes4(w[2 * i], w[2 * i + 1], f);
+        st_row32(e.h + at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), e.whole);
         e.h_sf[row * e.blocks + (col >> 5)] = (uint8_t)code;
     }
     if (e.gelu) {
@@ -363,9 +375,11 @@ __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t r
         for (int i = 0; i < 16; ++i) l.m2 = bf16x2_absmax(l.m2, w[i]);
     }
     if (e.d) {
-        uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.d) + at);
+        uint16_t* d = static_cast<uint16_t*>(e.d) + at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < 2; ++i)
+            st_row32(d + 16 * i, make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]),
+                     make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]), e.whole);
     }
     if (e.q) {
         const Two s = two(l.c.s), mr = two(-l.c.r);
@@ -377,9 +391,7 @@ __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t r
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = codes4_fast<FP8Q_E4M3FN>(w[2 * i], w[2 * i + 1], s, mr, l.c.t2);
         }
-        uint4* q = reinterpret_cast<uint4*>(e.q + at);
-        q[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        q[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        st_row32(e.q + at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), e.whole);
     }
 }
 
@@ -1104,6 +1116,7 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     e.vec = p->n % 4 == 0 && (wide & (e.f32 ? 15u : 7u)) == 0 && ((uintptr_t)p->bias & (e.bias_bf16 ? 7u : 15u)) == 0 &&
             (((uintptr_t)p->q | (uintptr_t)p->h) & 3u) == 0;
     e.wide = e.vec && p->n % 16 == 0 && ((wide | (uintptr_t)p->bias | (uintptr_t)p->q | (uintptr_t)p->h) & 15u) == 0;
+    e.whole = e.wide && p->n % 32 == 0 && (((uintptr_t)p->d | (uintptr_t)p->q | (uintptr_t)p->h) & 31u) == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.offsets = offsets;
     a.groups = how == kWhole ? 1 : groups;
