@@ -949,6 +949,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) before[i] = p[i];
                 }
+                const bool staged = !(rows_in_lanes && q + 32 <= e.n) && q < e.n && p_first < w.p_end;
+                float b[4] = {}, r[8][4] = {};
+                if (staged) {  // on their way while tensor memory is read
+                    if (e.bias && col < e.n) read4(e.bias, (int64_t)w.group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
+                    if (e.residual) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (col < e.n && p_first + i * 4 + sub < w.p_end)
+                                read4(e.residual, (d_first + i * 4 + sub) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
+                    }
+                }
                 if (w.k > 0) {
                     tmem_load32(from + set * 256 + c, v);
                 } else {
@@ -973,14 +984,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) st_shared_v4(room + lane * 128 + ((j ^ (lane & 7)) << 4), v + 4 * j);
                 __syncwarp();
-                float b[4] = {}, r[8][4] = {};
-                if (e.bias && col < e.n) read4(e.bias, (int64_t)w.group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
-                if (e.residual) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (col < e.n && p_first + i * 4 + sub < w.p_end)
-                            read4(e.residual, (d_first + i * 4 + sub) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
-                }
                 float x[8][4];
                 uint32_t on = 0;
 #pragma unroll
