@@ -136,13 +136,12 @@ __device__ __forceinline__ Lane make_lane(const Epilogue& e) {
 
 // Columns col to col + 3 of a row of D; eight lanes side by side hold a block of 32 columns.  `on`: the row is there.
 // r: the residual.  All lanes of a warp come here.  (Any n, any addresses, any scale of q.)
-__device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, int col, bool on, const float (&sum)[4], const float (&b)[4],
-                                      const float (&r)[4]) {
+// Out of line, so that the paths that most calls take stay short.  Returns the lane's largest.
+__device__ __noinline__ uint32_t emit4(const Epilogue& e, Lane l, int64_t row, int col, bool on, float4 sum, float4 b, float4 r4) {
     const int left = e.n - col;
     on = on && left > 0;
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = fmaf(sum[i], l.alpha, b[i]);
+    float v[4] = {fmaf(sum.x, l.alpha, b.x), fmaf(sum.y, l.alpha, b.y), fmaf(sum.z, l.alpha, b.z), fmaf(sum.w, l.alpha, b.w)};
+    const float r[4] = {r4.x, r4.y, r4.z, r4.w};
     if (e.h) {
         uint32_t w0 = cvt_bf16x2(v[0], v[1]), w1 = cvt_bf16x2(v[2], v[3]);
         if (left < 4) {  // beyond the row's end
@@ -163,7 +162,7 @@ __device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, i
             if ((threadIdx.x & 7) == 0) e.h_sf[row * e.blocks + (col >> 5)] = (uint8_t)code;
         }
     }
-    if (!on || !(e.d || e.q || e.amax)) return;
+    if (!on || !(e.d || e.q || e.amax)) return l.m2;
     if (e.gelu) {
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
@@ -183,7 +182,7 @@ __device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, i
             for (int i = 0; i < 4; ++i)
                 if (i < left) d[i] = v[i];
         }
-        return;
+        return l.m2;
     }
     uint32_t w0 = cvt_bf16x2(v[0], v[1]), w1 = cvt_bf16x2(v[2], v[3]);
     if (left < 4) w0 = left < 2 ? w0 & 0xFFFFu : w0, w1 = left < 3 ? 0u : w1 & 0xFFFFu;
@@ -202,7 +201,10 @@ __device__ __forceinline__ void emit4(const Epilogue& e, Lane& l, int64_t row, i
         else
             for (int i = 0; i < min(left, 4); ++i) e.q[at + i] = (uint8_t)(four >> 8 * i);
     }
+    return l.m2;
 }
+
+__device__ __forceinline__ float4 as_f4(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
 
 // emit4() for rows row, row + step, .. of which bit i of `on` says whether the i-th is there.  Whole vectors at an
 // ordinary scale go through the stages all rows at a time, so that a stage's latencies overlap: row by row, with the
@@ -212,7 +214,8 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
                                           const float (&b)[4], const float (&r)[ROWS][4]) {
     if (!e.vec || (e.q && !l.c.fast)) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) emit4(e, l, row + i * step, col, on >> i & 1, v[i], b, r[i]);
+        for (int i = 0; i < ROWS; ++i)
+            l.m2 = emit4(e, l, row + i * step, col, on >> i & 1, as_f4(v[i]), as_f4(b), as_f4(r[i]));
         return;
     }
     const uint32_t here = (col & ~31) < e.n ? on : 0u;  // of a block's eight lanes the first may be the only one with columns
