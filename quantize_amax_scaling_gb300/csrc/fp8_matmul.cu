@@ -170,8 +170,10 @@ __device__ __noinline__ uint32_t emit4(const Epilogue& e, Lane l, int64_t row, i
             v[i] = y.x, v[i + 1] = y.y;
         }
     }
+    if (e.residual) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += r[i];
+        for (int i = 0; i < 4; ++i) v[i] += r[i];
+    }
     const int64_t at = row * e.n + col;
     if (e.f32) {
         float* d = static_cast<float*>(e.d) + at;
@@ -257,13 +259,16 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) x[i][0] = gelu2(x[i][0]), x[i][1] = gelu2(x[i][1]);
     }
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-        x[i][0] = add2_rn(x[i][0], make_float2(r[i][0], r[i][1])), x[i][1] = add2_rn(x[i][1], make_float2(r[i][2], r[i][3]));
-    if (e.f32) {
+    if (e.residual) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
-            if (on >> i & 1) *reinterpret_cast<float4*>(static_cast<float*>(e.d) + at + i * next) = make_float4(x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y);
+            x[i][0] = add2_rn(x[i][0], make_float2(r[i][0], r[i][1])), x[i][1] = add2_rn(x[i][1], make_float2(r[i][2], r[i][3]));
+    }
+    if (e.f32) {
+        float* d = static_cast<float*>(e.d) + at;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i, d += next)
+            if (on >> i & 1) *reinterpret_cast<float4*>(d) = make_float4(x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y);
         return;
     }
 #pragma unroll
@@ -449,7 +454,7 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
 #pragma unroll 1
     for (int i0 = rank * kShare + warp * kRows; i0 < (rank + 1) * kShare && q0 + i0 < q_end; i0 += 4 * kRows) {
         const int row = q0 + i0;
-        float r[kRows][4] = {}, v[kRows][4] = {};
+        float r[kRows][4], v[kRows][4] = {};
         uint32_t on = 0;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -953,14 +958,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                     for (int i = 0; i < 4; ++i) before[i] = p[i];
                 }
                 const bool staged = !(rows_in_lanes && q + 32 <= e.n) && q < e.n && p_first < w.p_end;
-                float b[4] = {}, r[8][4] = {};
+                float b[4] = {}, r[8][4];
                 if (staged) {  // on their way while tensor memory is read
                     if (e.bias && col < e.n) read4(e.bias, (int64_t)w.group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
                     if (e.residual) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                        for (int i = 0; i < 8; ++i) {
                             if (col < e.n && p_first + i * 4 + sub < w.p_end)
                                 read4(e.residual, (d_first + i * 4 + sub) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
+                        }
                     }
                 }
                 if (w.k > 0) {
