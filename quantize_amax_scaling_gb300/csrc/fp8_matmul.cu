@@ -426,9 +426,8 @@ __device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 
 
 template <int BN>
 struct PrGeom {
-    static constexpr int kBoxes = kBoxBytes + BN * kStepK;        // a step's codes of B and of A
     static constexpr int kSmem = (BN <= 64 ? 112 : 160) * 1024;  // two CTAs an SM, or one
-    static constexpr int kMaxStages = kSmem / kBoxes;
+    static constexpr int kMaxStages = kSmem / (kBoxBytes + BN * kStepK);
     static constexpr int kCols = BN < 32 ? 32 : BN;              // of tensor memory
 };
 
@@ -451,6 +450,14 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
     const Epilogue& e = a.e;
     constexpr int kShare = BN / SPLIT;
     constexpr int kRows = kShare < 4 ? kShare : 4;
+    float next[kRows][4];
+    auto ask = [&](int i0) {  // the residual of a round, while the one before goes out
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (e.residual && col < e.n && i0 < (rank + 1) * kShare && q0 + i0 + i < q_end)
+                read4(e.residual, (int64_t)(q0 + i0 + i) * e.n + col, e.n - col, e.f32, e.vec, next[i]);
+    };
+    ask(rank * kShare + warp * kRows);
 #pragma unroll 1
     for (int i0 = rank * kShare + warp * kRows; i0 < (rank + 1) * kShare && q0 + i0 < q_end; i0 += 4 * kRows) {
         const int row = q0 + i0;
@@ -459,8 +466,10 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             on |= (uint32_t)(row + i < q_end) << i;
-            if (e.residual && col < e.n && row + i < q_end) read4(e.residual, (int64_t)(row + i) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[i][j] = next[i][j];
         }
+        ask(i0 + 4 * kRows);
         if (SPLIT == 1) {
 #pragma unroll
             for (int i = 0; i < kRows; ++i) ld_shared_v4(part + (i0 + i) * 512 + lane * 16, v[i]);
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     __shared__ uint64_t full[G::kMaxStages], empty[G::kMaxStages], done;
     __shared__ uint32_t tmem_slot, loads;
     __shared__ int gave_up;
-    const uint32_t stages = a.stages, stage_bytes = a.per * G::kBoxes;
+    const uint32_t stages = a.stages, boxes = kBoxBytes + (a.q_across ? kBoxBytes : BN * kStepK), stage_bytes = a.per * boxes;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const int rank = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
@@ -574,8 +583,8 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             const int there = min(a.per, s1 - s);
             if (elect_lane()) {
                 uint32_t at = base + st * stage_bytes;
-                expect_bytes(&full[st], there * G::kBoxes);
-                for (int k = s * kStepK; k < (s + there) * kStepK; k += kStepK, at += G::kBoxes) {
+                expect_bytes(&full[st], there * boxes);
+                for (int k = s * kStepK; k < (s + there) * kStepK; k += kStepK, at += boxes) {
                     if (a.p_across)
                         tile_load3(at, &map_p, p0, k, group, &full[st]);
                     else
@@ -608,7 +617,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             const int end_k = min(a.k, min(s + a.per, s1) * kStepK);
             uint32_t at = base + st * stage_bytes;
             if (elect_lane()) {
-                for (int k = s * kStepK; k < end_k; k += kStepK, at += G::kBoxes) {
+                for (int k = s * kStepK; k < end_k; k += kStepK, at += boxes) {
                     const int nk = (end_k - k + 31) / 32;
                     const uint64_t dp = desc_codes(at), dq = desc_codes(at + kBoxBytes);
 #pragma unroll
@@ -1045,12 +1054,12 @@ fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, Product
     // Stages of up to four steps, three stages or more: a stage's waits and its arrival take its issuers 150 cycles each, and
     // a step 150 beside (24x4096x16384 with clusters of two: 16.3 us, 18.5 with a step a stage).
     const int steps = ((a.k + kStepK - 1) / kStepK + a.split - 1) / a.split;
-    const int room = (PrGeom<BN>::kSmem - 1024) / PrGeom<BN>::kBoxes;
+    const int boxes = kBoxBytes + (a.q_across ? kBoxBytes : BN * kStepK), room = (PrGeom<BN>::kSmem - 1024) / boxes;
     a.per = room >= 12 ? 4 : room >= 6 ? 2 : 1;
     a.stages = room / a.per;
     const int most = (steps + a.per - 1) / a.per;  // what a short k leaves free lets the next kernel start
     if (a.stages > most) a.stages = most > 1 ? most : 1;
-    const int need = a.stages * a.per * PrGeom<BN>::kBoxes;
+    const int need = a.stages * a.per * boxes;
     return launch_behind(kern, dim3(grid), dim3(192), (need > BN * 512 ? need : BN * 512) + 1024, (unsigned)a.split, s, "fp8_matmul_kernel", mp, mq, a);
 }
 
@@ -1138,8 +1147,10 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     const int fa = p->a_fmt == FP8Q_E5M2, fb = p->b_fmt == FP8Q_E5M2, ta = p->a_trans != 0, tb = p->b_trans != 0;
     const int64_t b_groups = how == kGroupedRows ? groups : 1;
     const int sms = sm_count();
-    const int64_t blocks = (p->m + 127) / 128 * ((p->n + 127) / 128);
-    const bool pairs = how == kGroupedK || (how == kGroupedRows ? p->m > 64 * (int64_t)groups : p->m > 128 && p->n > 128 && blocks > sms);
+    // Pairs of CTAs where 128-row tiles of one CTA each would not all be resident at once.  (A grouped call does not know its
+    // groups: at most a part of a tile in each beside full ones.)
+    const int64_t across = (p->n + 127) / 128, blocks = (how == kGroupedRows ? p->m / 128 + groups : (p->m + 127) / 128) * across;
+    const bool pairs = how == kGroupedK || (blocks > sms && (how == kGroupedRows ? p->m > 64 * (int64_t)groups : p->m > 128 && p->n > 128));
     CUtensorMap mp = {}, mq = {};
     if (pairs) {
         a.idesc = mma_desc_fp8(256, 256, fa, fb, ta, tb);
@@ -1155,9 +1166,12 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
         return how == kGroupedK ? launch_product_pairs<true>(mp, mq, a, tiles, s)
                                 : launch_product_pairs<false>(mp, mq, a, tiles, s);
     }
-    // P is B and Q is A; a box of A across k is always 128 rows wide
+    // P is B and Q is A.  Fewer rows of A a CTA while two thirds of the SMs have room for all CTAs: a tile goes out sooner
+    // the smaller it is (300x1024x1024 5.3 us with 32 rows, 6.9 with 128; 278x208x64 5.5 and 14), but reads B once more, and
+    // takes the SMs that would share a longer k (1003x1040x2064 9.4 us with 128, 10.3 with 64).
     const int64_t each = how == kGroupedRows ? (p->m + groups - 1) / groups : p->m;
-    const int bn = ta ? 128 : each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
+    int bn = each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
+    while (bn > 32 && (how == kGroupedRows ? p->m * 2 / bn + groups : (p->m * 2 + bn - 1) / bn) * across * 3 <= sms * 2) bn /= 2;
     const int steps = (int)((p->k + kStepK - 1) / kStepK);
     a.idesc = mma_desc_fp8(128, bn, fb, fa, tb, ta);
     a.p_across = tb;
@@ -1165,8 +1179,8 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     a.q_tiles = (int32_t)((p->m + bn - 1) / bn);
     // a grouped call does not know its groups: at most as many tiles as full ones and one part of a tile in each
     const int64_t q_tiles = how == kGroupedRows ? p->m / bn + (groups < p->m ? groups : p->m) : a.q_tiles;
-    a.p_tiles = (int32_t)((p->n + 127) / 128);
-    const int64_t tiles = a.p_tiles * q_tiles;
+    a.p_tiles = (int32_t)across;
+    const int64_t tiles = across * q_tiles;
     // The CTAs of a cluster share a tile's sums, as many as are resident at once (two an SM up to 64 rows of A; clusters
     // of 4 and 8 reach 19 and 17 of 20 of them) and have four steps or more, where the steps that a CTA saves are worth the
     // cluster and its sums: 1x4096x4096 7.2 us on clusters of 8, 7.9 on 2; 1x1024x4096 4.7, 5.6 on 4; but two rounds of
