@@ -426,7 +426,7 @@ __device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 
 
 template <int BN>
 struct PrGeom {
-    static constexpr int kSmem = (BN <= 64 ? 112 : 160) * 1024;  // two CTAs an SM, or one
+    static constexpr int kSmem = (BN <= 64 ? 112 : 224) * 1024;  // two CTAs an SM, or one
     static constexpr int kMaxStages = kSmem / (kBoxBytes + BN * kStepK);
     static constexpr int kCols = BN < 32 ? 32 : BN;              // of tensor memory
 };
