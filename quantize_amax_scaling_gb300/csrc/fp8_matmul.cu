@@ -1051,11 +1051,11 @@ fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, Product
     auto kern = fp8_matmul_kernel<BN>;
     const cudaError_t e = allow_smem(kern, PrGeom<BN>::kSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_kernel setup");
-    // Stages of up to four steps, three stages or more: a stage's waits and its arrival take its issuers 150 cycles each, and
+    // Stages of up to four steps, two stages or more: a stage's waits and its arrival take its issuers 150 cycles each, and
     // a step 150 beside (24x4096x16384 with clusters of two: 16.3 us, 18.5 with a step a stage).
     const int steps = ((a.k + kStepK - 1) / kStepK + a.split - 1) / a.split;
     const int boxes = kBoxBytes + (a.q_across ? kBoxBytes : BN * kStepK), room = (PrGeom<BN>::kSmem - 1024) / boxes;
-    a.per = room >= 12 ? 4 : room >= 6 ? 2 : 1;
+    a.per = room >= 12 ? 4 : room >= 5 ? 2 : 1;
     a.stages = room / a.per;
     const int most = (steps + a.per - 1) / a.per;  // what a short k leaves free lets the next kernel start
     if (a.stages > most) a.stages = most > 1 ? most : 1;
