@@ -45,6 +45,13 @@ __device__ __forceinline__ void ckpt_decode4(uint32_t four, float s, float (&v)[
     v[0] = f16_lo(a) * s, v[1] = f16_hi(a) * s, v[2] = f16_lo(b) * s, v[3] = f16_hi(b) * s;
 }
 
+// A whole sector in one store.
+__device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+                 "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 __device__ __forceinline__ Two add_two(Two a, Two b) {
     Two d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));

@@ -309,9 +309,7 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
 // its own otherwise, in as many lines as there are lanes.
 __device__ __forceinline__ void st_row32(void* p, const uint4& a, const uint4& b, bool whole) {
     if (whole) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
-                     "r"(b.y), "r"(b.z), "r"(b.w)
-                     : "memory");
+        st_v8(p, a, b);
     } else {
         static_cast<uint4*>(p)[0] = a;
         static_cast<uint4*>(p)[1] = b;
