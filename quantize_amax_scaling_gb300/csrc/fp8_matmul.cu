@@ -11,10 +11,16 @@
 // core reads it across, so the products of a backward pass need no transposed copy.
 //
 // Two kernels.  Few tiles: 128 rows of B by 16 to 128 of A a CTA, k split over a
-// cluster while every CTA is resident.  Many tiles: pairs of CTAs with 256 x 256.
-// Both hand their sums to the same epilogue, four consecutive columns of a row a
-// lane: a row's stores are whole sectors wherever rows start, and any rows and
-// columns may be left out at a group's or the matrix's edge.
+// cluster while every CTA is resident; what bounds them is the operands' way from
+// HBM and 4 us until it flows and the sums are out: 1 x 16384 x 4096 (67 MB) 14.1 us,
+// 1 x 1024 x 4096 4.6; each megabyte more costs 0.15 us, 6.7 TB/s.  Many tiles: pairs
+// of CTAs with 256 x 256.  8192 x 16384 x 4096 takes 294 to 300 us in a burst, 3.7
+// PFLOP/s, and 325 in a loop at the 1400 W limit; with zeros for operands, which
+// cost little power, 239 us, 4.6 PFLOP/s, the multiply-adds' own 128 cycles for
+// 256 x 256 x 32 at 2070 MHz.  So the tensor cores' power bounds it, not their feeding.
+// Both take their sums through one epilogue, four columns of a row a lane, whose
+// stores are whole sectors wherever rows start and which leaves out any rows and
+// columns at a group's or the matrix's edge; pairs have a faster one beside it.
 
 #include "checkpoint_calls.cuh"
 #include "tcgen05.cuh"
@@ -301,12 +307,8 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
     }
 }
 
-// Thirty-two columns from col on, all there, of one row a lane, as tensor memory gives them: nothing passes between lanes, and a
-// block of the checkpoint is a lane's own.  For bf16, n a multiple of 16, 16-byte addresses and an ordinary scale.  (The
-// checkpoint's blocks over eight lanes each and codes through shared memory cost 105 us of 8192x16384x4096's 353, zeros for
-// operands; here 0.)
 // Thirty-two bytes of a row in one store where rows start on whole sectors (`whole`): each of the two halves is a request of
-// its own otherwise, in as many lines as there are lanes.
+// its own otherwise, in as many lines as there are lanes (8192x16384x4096 as below 394 us with halves, 340 whole).
 __device__ __forceinline__ void st_row32(void* p, const uint4& a, const uint4& b, bool whole) {
     if (whole) {
         st_v8(p, a, b);
@@ -318,6 +320,10 @@ __device__ __forceinline__ void st_row32(void* p, const uint4& a, const uint4& b
 __device__ __forceinline__ float2 as_f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 __device__ __forceinline__ float2 bf16_f2(uint32_t w) { return as_f2(w << 16, w & 0xFFFF0000u); }
 
+// Thirty-two columns from col on, all there, of one row a lane, as tensor memory gives them: nothing passes between lanes, and a
+// block of the checkpoint is a lane's own.  For bf16, n a multiple of 16, 16-byte addresses and an ordinary scale.  (8192x16384x4096
+// with GELU, codes and checkpoint 340 us, 477 with the checkpoint's blocks over eight lanes each and codes through
+// shared memory.  Binary32 goes through shared memory: a row a lane there is 128 bytes in four lines a store, no faster.)
 __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t row, int col, int64_t bias_at, const float (&v)[32], const uint4 (&r)[4]) {
     float2 x[16];
     const float2 alpha = splat2(l.alpha);
