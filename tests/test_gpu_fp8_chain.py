@@ -181,3 +181,25 @@ def test_experts_step(dev, rows, e, H, F):
     gr.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(out, again))
+
+
+def test_readme_example():
+    """The readme's MLP runs as written, behind the examples before it, and moves what it says."""
+    import os
+    import re
+
+    from conftest import ROOT
+    with open(os.path.join(ROOT, "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    ns = {}
+    for b in blocks[:3]:
+        exec(compile(b, "readme example", "exec"), ns)
+    torch.cuda.synchronize()
+    x, w1, s = R.values(ns["x8"], 0), R.values(ns["w1"], 0), 8.0 / 448
+    z = x @ w1.t() * s * s
+    a = R.values(ns["a8"], 0) * s
+    want = R.gelu(z).clamp(-8, 8)
+    assert ((a - want).abs() <= 0.07 * want.abs() + 2.0 ** -9 * s + 2.0 ** -16).all()  # half steps of bf16 and of e4m3
+    d1 = R.values(ns["d1"], 1)
+    check(ns["dw1"], d1.t() @ x * 1e-6 * s, (R.sum_bound(d1.t(), x.t()) + (d1.t() @ x).abs() * 2.0 ** -23) * 1e-6 * s)
+    assert ns["db1"].any() and torch.isfinite(ns["dw2"]).all() and ns["dw2"].any() and ns["y"].any()
