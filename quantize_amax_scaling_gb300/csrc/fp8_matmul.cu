@@ -84,12 +84,25 @@ __device__ __forceinline__ int2 group_rows(const ProductArgs& a, int g) {
     return make_int2(lo, max(lo, min(a.offsets[g + 1], a.rows)));
 }
 
+// Sums of the counts up to and with each lane's, held at kManyTiles: right offsets never come near, wrong ones must not
+// pass 32 bits (a tile before the tensor would be written there).
+constexpr int kManyTiles = 0x3FFFFFFF;
+__device__ __forceinline__ int sums_upto(int here) {
+    int upto = here;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if ((threadIdx.x & 31) >= o) upto = min(upto + v, kManyTiles);
+    }
+    return upto;
+}
+
 // ----------------------------------------------------------------------------
 // Epilogue
 
 // x / (1 + 2^u), u = -2 sqrt(2 / pi) log2(e) (x + 0.044715 x^3), for two: exp and the reciprocal by the hardware's
-// approximations, 2 and 1 units in the last place of binary32: the sum of all is 2^-18 of y beside a rounding to bf16 of
-// 2^-9.  At -infinity the formula is NaN.
+// approximations, 2 and 1 units in the last place of binary32, and u off by 2 roundings, |u| 2^-23 in y: 2^-18 of y at x = -5,
+// 2^-16 at -10, where y is 2^-120.  At -infinity the formula is NaN.
 __device__ __forceinline__ float2 gelu2(float2 x) {
     const float2 u = mul2_rn(x, fma2_rn(mul2_rn(x, x), splat2(-0.102943239f), splat2(-2.302208198f)));
     float2 t, r;
@@ -533,23 +546,18 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
         for (; g0 < a.groups; g0 += 32) {
             int2 r = make_int2(0, 0);
             if (g0 + lane < a.groups) r = group_rows(a, g0 + lane);
-            const int here = (r.y - r.x + BN - 1) / BN;
-            int upto = here;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-                if (lane >= o) upto += v;
-            }
+            const int upto = sums_upto((r.y - r.x + BN - 1) / BN);
             const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > t);
             if (past) {
                 const int i = __ffs(past) - 1;
                 group = g0 + i;
-                q0 = __shfl_sync(0xFFFFFFFFu, r.x, i) + (t - before - __shfl_sync(0xFFFFFFFFu, upto - here, i)) * BN;
+                const int ahead = __shfl_sync(0xFFFFFFFFu, upto, i - (i > 0));  // tiles of the groups before, at most t - before
+                q0 = __shfl_sync(0xFFFFFFFFu, r.x, i) + (t - before - (i > 0 ? ahead : 0)) * BN;
                 q_end = __shfl_sync(0xFFFFFFFFu, r.y, i);
                 found = true;
                 break;
             }
-            before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            before = min(before + __shfl_sync(0xFFFFFFFFu, upto, 31), kManyTiles);
         }
         if (!found) {  // the grid has room for a part of a tile in every group; the whole cluster ends here
             let_next_start();
@@ -793,19 +801,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                     const int2 r = group_rows(a, g0 + lane);
                     here = (r.y - r.x + 255) / 256;
                 }
-                int upto = here;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-                    if (lane >= o) upto += v;
-                }
-                if (g0 + lane <= a.groups) cum[g0 + lane] = before + upto - here;
-                before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+                const int upto = sums_upto(here), behind = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
+                if (g0 + lane <= a.groups) cum[g0 + lane] = min(before + (lane ? behind : 0), kManyTiles);
+                before = min(before + __shfl_sync(0xFFFFFFFFu, upto, 31), kManyTiles);
             }
         }
         __syncthreads();
     }
-    const int tiles = RAGGED_K ? a.groups * a.p_tiles * a.q_tiles : a.offsets ? cum[a.groups] * a.q_tiles : a.p_tiles * a.q_tiles;
+    const int tiles = RAGGED_K ? a.groups * a.p_tiles * a.q_tiles : a.offsets ? (int)min((int64_t)cum[a.groups] * a.q_tiles, (int64_t)kManyTiles)
+                                                                        : a.p_tiles * a.q_tiles;
     if (warp == 9) {
         tmem_alloc<2>(&tmem_slot, 512);
         let_next_start();
@@ -1164,7 +1168,7 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
         a.p_tiles = (int32_t)((p->m + 255) / 256);
         a.q_tiles = (int32_t)((p->n + 255) / 256);
         const int64_t tiles = (how == kGroupedRows ? p->m / 256 + groups : (int64_t)a.p_tiles * (how == kGroupedK ? groups : 1)) * a.q_tiles;
-        if (tiles > 0x3FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
+        if (tiles > kManyTiles) return FP8Q_ERR_UNSUPPORTED;
         if (p->k > 0 && (!operand_map(&mp, p->a, p->m, p->k, p->lda, 1, ta, 128) || !operand_map(&mq, p->b, p->n, p->k, p->ldb, b_groups, tb, 128)))
             return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_pair_kernel tensor map");
         return how == kGroupedK ? launch_product_pairs<true>(mp, mq, a, tiles, s)
@@ -1194,7 +1198,7 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     while (most < 8 && tiles * most * 2 <= room * (most == 1 ? 20 : most == 2 ? 19 : 17) / 20 && steps >= most * 8) most *= 2;
     if (steps - steps / most > 3 + bn / 32) split = most;
     a.split = split;
-    if (tiles * split > 0x7FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
+    if (tiles * split > kManyTiles) return FP8Q_ERR_UNSUPPORTED;
     if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, 128) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
         return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_kernel tensor map");
     const unsigned grid = (unsigned)(tiles * split);

@@ -172,6 +172,48 @@ def test_codes_amax_and_checkpoint(dev, m, n, k, q_fmt, scale):
     assert torch.equal(amax, want_amax)
 
 
+@pytest.mark.parametrize("m", [1, 40, 3000])
+def test_gelu_over_its_range(dev, m):
+    """The epilogue's GELU at every bf16, given by the bias of a product with an empty k: nothing else is rounded before it."""
+    z = torch.arange(65536, dtype=torch.int32, device=dev).to(torch.int16).view(torch.bfloat16).float()
+    z[:4096] = torch.linspace(-12, 12, 4096, device=dev)
+    a, b = torch.empty((m, 0), dtype=torch.uint8, device=dev), torch.empty((65536, 0), dtype=torch.uint8, device=dev)
+    d, y = torch.empty((m, 65536), device=dev), torch.empty((m, 65536), dtype=torch.bfloat16, device=dev)
+    fp8q.fp8q_matmul(a, b, d, bias=z, act=1)
+    fp8q.fp8q_matmul(a, b, y, bias=z, act=1)
+    assert torch.equal(y[0], d[0].to(torch.bfloat16)) or torch.equal(y[0].isnan(), d[0].isnan())
+    assert ((y == y[:1]) | y.isnan()).all() and ((d == d[:1]) | d.isnan()).all()
+    x = z.double()
+    want = torch.where(x < -30, torch.zeros_like(x), R.gelu(x))  # below, 0 in binary32 (and 1 + tanh 0 in 64 bits)
+    want = torch.where(x > 30, x, want)
+    # 1 + tanh loses what is left of it in 64 bits towards -6: there by exp
+    u = -2 * (2 / torch.pi) ** 0.5 * (x + 0.044715 * x ** 3)
+    want = torch.where((x < 0) & (x >= -30), x / (1 + torch.exp(u)), want)
+    fine = torch.isfinite(z)
+    rel = torch.where(x >= -5, 2.0 ** -18, 2.0 ** -16)
+    bound = torch.where(x >= -10, rel * want.abs() + 2.0 ** -130, torch.full_like(x, 2.0 ** -100))
+    assert ((d[0].double() - want).abs() <= bound)[fine].all()
+    assert ((y[0].double() - want).abs() <= bound + 2.0 ** -8 * (want.abs() + bound) + 2.0 ** -134)[fine & (x.abs() < 2.0 ** 127)].all()
+    assert d[0][z == float("inf")].eq(float("inf")).all() and d[0][z.isnan() | (z == -float("inf"))].isnan().all()
+
+
+@pytest.mark.parametrize("m,n,k", EPILOGUE)
+def test_checkpoint_beside_float32(dev, m, n, k):
+    a, b = operands(dev, m, n, k, 8)
+    A, B = stored(a, 0), stored(b, 0)
+    bias, s = torch.randn(n, generator=gen(dev, 3), device=dev), torch.full((1,), 1.0 / k ** 0.5, device=dev)
+    z = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+    fp8q.fp8q_matmul(A, B, z, a_scale=s, bias=bias)
+    want_h, want_sf = fp8q.checkpoint_empty(m, n)
+    fp8q.fp8q_checkpoint_quantize(z, want_h, want_sf)
+    for act in (0, 1):
+        h, sf = fp8q.checkpoint_empty(m, n)
+        d, ref = torch.empty((m, n), device=dev), torch.empty((m, n), device=dev)
+        fp8q.fp8q_matmul(A, B, d, a_scale=s, bias=bias, act=act, h=h, h_sf=sf)
+        fp8q.fp8q_matmul(A, B, ref, a_scale=s, bias=bias, act=act)
+        assert torch.equal(h, want_h) and torch.equal(sf, want_sf) and torch.equal(d, ref)
+
+
 @pytest.mark.parametrize("m,n,off", [(3, 200, 2), (130, 260, 1), (2600, 2304, 1), (2600, 2304, 2)])
 def test_outputs_from_any_address(dev, m, n, off):
     k = 64
