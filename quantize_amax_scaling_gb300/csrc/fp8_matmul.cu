@@ -44,7 +44,8 @@ struct Epilogue {
     bool f32, bias_bf16, gelu, e5m2;
     bool vec;   // four columns a vector, and
     bool wide;   // sixteen bytes a vector, wherever a row starts, and
-    bool whole;  // thirty-two
+    bool whole;   // thirty-two of d, and
+    bool whole8;  // of q and h
 };
 
 // P is the operand whose rows are the accumulator's lanes, Q the one whose rows are its columns.
@@ -322,29 +323,41 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t ro
 
 // Thirty-two bytes of a row in one store where rows start on whole sectors (`whole`): each of the two halves is a request of
 // its own otherwise, in as many lines as there are lanes (8192x16384x4096 as below 394 us with halves, 340 whole).
-__device__ __forceinline__ void st_row32(void* p, const uint4& a, const uint4& b, bool whole) {
+__device__ __forceinline__ void st_row32(void* p, const uint4& a, const uint4& b, bool whole, bool full) {
     if (whole) {
         st_v8(p, a, b);
     } else {
         static_cast<uint4*>(p)[0] = a;
-        static_cast<uint4*>(p)[1] = b;
+        if (full) static_cast<uint4*>(p)[1] = b;
     }
 }
 __device__ __forceinline__ float2 as_f2(uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); }
 __device__ __forceinline__ float2 bf16_f2(uint32_t w) { return as_f2(w << 16, w & 0xFFFF0000u); }
 
-// Thirty-two columns from col on, all there, of one row a lane, as tensor memory gives them: nothing passes between lanes, and a
-// block of the checkpoint is a lane's own.  For bf16, n a multiple of 16, 16-byte addresses and an ordinary scale.  (8192x16384x4096
-// with GELU, codes and checkpoint 340 us, 477 with the checkpoint's blocks over eight lanes each and codes through
-// shared memory.  Binary32 goes through shared memory: a row a lane there is 128 bytes in four lines a store, no faster.)
-__device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t row, int col, int64_t bias_at, const float (&v)[32], const uint4 (&r)[4]) {
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void copy_ahead16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// Thirty-two columns from col on, or the row's last sixteen, of one row a lane, as tensor memory gives them: nothing passes
+// between lanes, and a block of the checkpoint is a lane's own.  For n a multiple of 16, 16-byte addresses and an ordinary scale.
+// (8192x16384x4096 with GELU, codes and checkpoint 340 us, 477 with the checkpoint's blocks over eight lanes each and codes
+// through shared memory.)  Binary32 without a residual goes through shared memory: a row a lane there is 128 bytes in four
+// lines a store, no faster.  res: the warp's 32 rows of the residual's columns in shared memory, their 16-byte pieces swizzled.
+__device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t row, int col, int64_t bias_at, const float (&v)[32], uint32_t res) {
+    const int lane = threadIdx.x & 31;
+    const bool full = col + 32 <= e.n;
     float2 x[16];
     const float2 alpha = splat2(l.alpha);
     if (e.bias && e.bias_bf16) {
         const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + bias_at + col);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint4 y = b[i];
+            const uint4 y = i < 2 || full ? b[i] : make_uint4(0, 0, 0, 0);
             x[4 * i] = fma2_rn(make_float2(v[8 * i], v[8 * i + 1]), alpha, bf16_f2(y.x));
             x[4 * i + 1] = fma2_rn(make_float2(v[8 * i + 2], v[8 * i + 3]), alpha, bf16_f2(y.y));
             x[4 * i + 2] = fma2_rn(make_float2(v[8 * i + 4], v[8 * i + 5]), alpha, bf16_f2(y.z));
@@ -354,7 +367,7 @@ __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t r
         const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + bias_at + col);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float4 y = b[i];
+            const float4 y = i < 4 || full ? b[i] : make_float4(0, 0, 0, 0);
             x[2 * i] = fma2_rn(make_float2(v[4 * i], v[4 * i + 1]), alpha, make_float2(y.x, y.y));
             x[2 * i + 1] = fma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), alpha, make_float2(y.z, y.w));
         }
@@ -369,7 +382,7 @@ __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t r
         for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(x[i].x, x[i].y);
         uint32_t m[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = bf16x2_absmax(w[i], w[i + 8]);
+        for (int i = 0; i < 8; ++i) m[i] = full ? bf16x2_absmax(w[i], w[i + 8]) : bf16x2_absmax(w[i], 0u);
 #pragma unroll
         for (int o = 4; o; o >>= 1)
 #pragma unroll
@@ -379,32 +392,47 @@ __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t r
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = ckpt_codes4(w[2 * i], w[2 * i + 1], f);
-        st_row32(e.h + at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), e.whole);
+        st_row32(e.h + at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), e.whole8, full);
         e.h_sf[row * e.blocks + (col >> 5)] = (uint8_t)code;
     }
     if (e.gelu) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = gelu2(x[i]);
     }
+    if (e.f32) {
+        float* d = static_cast<float*>(e.d) + at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= 2 && !full) break;
+            const uint4 r0 = ld_shared_u4(res + lane * 128 + (((2 * i) ^ (lane & 7)) << 4)), r1 = ld_shared_u4(res + lane * 128 + (((2 * i + 1) ^ (lane & 7)) << 4));
+            const float2 a = add2_rn(x[4 * i], as_f2(r0.x, r0.y)), b = add2_rn(x[4 * i + 1], as_f2(r0.z, r0.w));
+            const float2 c = add2_rn(x[4 * i + 2], as_f2(r1.x, r1.y)), g = add2_rn(x[4 * i + 3], as_f2(r1.z, r1.w));
+            st_row32(d + 8 * i, make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)),
+                     make_uint4(__float_as_uint(c.x), __float_as_uint(c.y), __float_as_uint(g.x), __float_as_uint(g.y)), e.whole, true);
+        }
+        return;
+    }
     if (e.residual) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[4 * i] = add2_rn(x[4 * i], bf16_f2(r[i].x)), x[4 * i + 1] = add2_rn(x[4 * i + 1], bf16_f2(r[i].y));
-            x[4 * i + 2] = add2_rn(x[4 * i + 2], bf16_f2(r[i].z)), x[4 * i + 3] = add2_rn(x[4 * i + 3], bf16_f2(r[i].w));
+            const uint4 r = ld_shared_u4(res + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4));
+            x[4 * i] = add2_rn(x[4 * i], bf16_f2(r.x)), x[4 * i + 1] = add2_rn(x[4 * i + 1], bf16_f2(r.y));
+            x[4 * i + 2] = add2_rn(x[4 * i + 2], bf16_f2(r.z)), x[4 * i + 3] = add2_rn(x[4 * i + 3], bf16_f2(r.w));
         }
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(x[i].x, x[i].y);
     if (e.amax) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) l.m2 = bf16x2_absmax(l.m2, w[i]);
+        for (int i = 0; i < 16; ++i) l.m2 = i < 8 || full ? bf16x2_absmax(l.m2, w[i]) : l.m2;
     }
     if (e.d) {
         uint16_t* d = static_cast<uint16_t*>(e.d) + at;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            st_row32(d + 16 * i, make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]),
-                     make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]), e.whole);
+            if (i < 1 || full)
+                st_row32(d + 16 * i, make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]),
+                         make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]), e.whole, true);
     }
     if (e.q) {
         const Two s = two(l.c.s), mr = two(-l.c.r);
@@ -416,7 +444,7 @@ __device__ __forceinline__ void emit_row32(const Epilogue& e, Lane& l, int64_t r
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = codes4_fast<FP8Q_E4M3FN>(w[2 * i], w[2 * i + 1], s, mr, l.c.t2);
         }
-        st_row32(e.q + at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), e.whole);
+        st_row32(e.q + at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), e.whole8, full);
     }
 }
 
@@ -704,10 +732,15 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
 // arrive and, in the last, puts zeros over the lines that are not the group's (both
 // operands': zero times a NaN is none) before it tells the issuer.
 
-constexpr int kPrPairStages = 6;
+constexpr int kPrPairStages = 5;
 constexpr int kPrPairThreads = 352;  // warps 0-7 carry results out, 8 copies codes, 9 multiplies, 10 puts zeros (RAGGED_K)
-constexpr int kPrOut = kPrPairStages * 2 * kBoxBytes;  // 32 rows of 32 sums for each of eight warps
-constexpr int kPrState = kPrOut + 8 * 4096;
+constexpr int kPrOut = kPrPairStages * 2 * kBoxBytes;
+// Of each of the eight warps: 32 rows of 32 sums on their way out, or the residual of the next 64 (binary32) or 128 (bf16)
+// columns on its way in.  It takes the place of a sixth stage, which bought nothing (8192x4096x4096 74 us either way) and left
+// binary32 32 columns ahead: 3001 rows of 12 experts to weights of 2064x1040 on top of a residual 58 us, 46 with 64 ahead, 59
+// without; bf16 57 us without, 35.  (With a prefetch to L2 beside it 48 and 42: twice the requests.)
+constexpr int kPrRoom = 8192;
+constexpr int kPrState = kPrOut + 8 * kPrRoom;
 
 // Behind them in shared memory, which starts on 1024 bytes.  full: a stage's codes are there in both CTAs (the first
 // CTA's counts); landed: they are in this one; empty: the stage has been used; done, drained: a set of accumulators is
@@ -945,19 +978,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
     } else {
         const Epilogue& e = a.e;
         const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (warp >> 2) * 128;
-        const uint32_t room = base + kPrOut + warp * 4096;
+        const uint32_t room = base + kPrOut + warp * kPrRoom;
         const int sub = lane >> 3, c4 = (lane & 7) * 4;
         Lane l = make_lane(e);
-        const bool rows_in_lanes = e.wide && !e.f32 && (!e.q || l.c.fast);
+        const bool rows_in_lanes = e.wide && (!e.f32 || e.residual) && (!e.q || l.c.fast);
+        const bool ahead = rows_in_lanes && e.residual;
         bool ok = true;
         uint32_t it = 0;
-        for (int tile = first; tile < tiles; tile += stride, ++it) {
-            const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
+        const auto first_row = [&](const PairWhere& w) { return w.p0 + (int)rank * 128 + (warp & 3) * 32; };
+        const auto d_row = [&](const PairWhere& w) { return (int64_t)first_row(w) + (RAGGED_K ? (int64_t)w.group * a.m : 0); };
+        // 32 columns of a tile's residual on their way, by rows' lengths; a lane finds its row's as emit_row32() reads them
+        const auto ask = [&](const PairWhere& w, int c, uint32_t to) {
+            const int q = w.q0 + (warp >> 2) * 128 + c, rows = w.p_end - first_row(w);
+            const uint8_t* from = static_cast<const uint8_t*>(e.residual) + (d_row(w) * e.n + q) * (e.f32 ? 4 : 2);
+            if (e.f32) {
+                if (q + c4 < e.n) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = i * 4 + sub;
+                        if (row < rows) copy_ahead16(to + row * 128 + (((lane & 7) ^ (row & 7)) << 4), from + ((int64_t)row * e.n + c4) * 4);
+                    }
+                }
+            } else if (q + (lane & 3) * 8 < e.n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = i * 8 + (lane >> 2);
+                    if (row < rows) copy_ahead16(to + row * 64 + (((lane & 3) ^ (row >> 1 & 3)) << 4), from + ((int64_t)row * e.n + (lane & 3) * 8) * 2);
+                }
+            }
+        };
+        PairWhere w = {}, then = {};
+        if (first < tiles) w = pair_where<RAGGED_K>(a, cum, first);
+        if (ahead && first < tiles) {
+#pragma unroll
+            for (int c = 0; c < kPrRoom / 64; c += 32) {
+                if (e.f32 && c >= kPrRoom / 128) break;
+                ask(w, c, room + c * (e.f32 ? 128 : 64));
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+        }
+        for (int tile = first; tile < tiles; tile += stride, ++it, w = then) {
+            const bool more = tile + stride < tiles;
+            if (more) then = pair_where<RAGGED_K>(a, cum, tile + stride);
             const uint32_t set = it & 1;
             const uint32_t bar = in_cluster(smem_addr(&drained[set]), 0);
-            const int p_first = w.p0 + (int)rank * 128 + (warp & 3) * 32;
-            const int64_t d_first = (int64_t)p_first + (RAGGED_K ? (int64_t)w.group * a.m : 0);
-            if (e.residual && e.wide && p_first + lane < w.p_end) {  // on its way to L2 while the tensor cores work
+            const int p_first = first_row(w);
+            const int64_t d_first = d_row(w);
+            if (e.residual && !ahead && e.wide && p_first + lane < w.p_end) {  // on its way to L2 while the tensor cores work
                 const int q = w.q0 + (warp >> 2) * 128, there = min(128, e.n - q), size = e.f32 ? 4 : 2;
                 if (there > 0) block_prefetch(static_cast<const uint8_t*>(e.residual) + ((d_first + lane) * e.n + q) * size, there * size);
             }
@@ -968,13 +1035,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
             for (int c = 0; c < 128; c += 32) {
                 const int q = w.q0 + (warp >> 2) * 128 + c, col = q + c4;
                 float v[32];
-                uint4 before[4];
-                if (rows_in_lanes && e.residual && q + 32 <= e.n && p_first + lane < w.p_end) {
-                    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.residual) + (d_first + lane) * e.n + q);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) before[i] = p[i];
-                }
-                const bool staged = !(rows_in_lanes && q + 32 <= e.n) && q < e.n && p_first < w.p_end;
+                const bool staged = !rows_in_lanes && q < e.n && p_first < w.p_end;
                 float b[4] = {}, r[8][4];
                 if (staged) {  // on their way while tensor memory is read
                     if (e.bias && col < e.n) read4(e.bias, (int64_t)w.group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
@@ -996,15 +1057,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                     tc_fence_before();
                     if (lane == 0) arrive_cluster(bar);
                 }
-                if (q >= e.n || p_first >= w.p_end) continue;
-                if (rows_in_lanes && q + 32 <= e.n) {
+                if (rows_in_lanes) {
+                    const uint32_t res = room + (e.f32 ? c * 128 : c * 64) % kPrRoom;
+                    if (ahead) {
+                        if (e.f32)
+                            asm volatile("cp.async.wait_group %0;" ::"n"(kPrRoom / 4096 - 1) : "memory");
+                        else
+                            asm volatile("cp.async.wait_group %0;" ::"n"(kPrRoom / 2048 - 1) : "memory");
+                        __syncwarp();
+                    }
                     if (!ok) {  // a wait that ran out shows as NaN
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7FFFFFFFu);
                     }
-                    if (p_first + lane < w.p_end) emit_row32(e, l, d_first + lane, q, (int64_t)w.group * e.n, v, before);
+                    if (q < e.n && p_first + lane < w.p_end) emit_row32(e, l, d_first + lane, q, (int64_t)w.group * e.n, v, res);
+                    if (ahead) {
+                        __syncwarp();
+                        const int on = c + kPrRoom / (e.f32 ? 128 : 64);  // what this room holds next, of this tile or the one behind
+                        if (on < 128)
+                            ask(w, on, res);
+                        else if (more)
+                            ask(then, on - 128, res);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                    }
                     continue;
                 }
+                if (q >= e.n || p_first >= w.p_end) continue;
                 // through shared memory: a thread has a row's sums, and four of eight rows go out
                 __syncwarp();
 #pragma unroll
@@ -1145,7 +1223,8 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     e.vec = p->n % 4 == 0 && (wide & (e.f32 ? 15u : 7u)) == 0 && ((uintptr_t)p->bias & (e.bias_bf16 ? 7u : 15u)) == 0 &&
             (((uintptr_t)p->q | (uintptr_t)p->h) & 3u) == 0;
     e.wide = e.vec && p->n % 16 == 0 && ((wide | (uintptr_t)p->bias | (uintptr_t)p->q | (uintptr_t)p->h) & 15u) == 0;
-    e.whole = e.wide && p->n % 32 == 0 && (((uintptr_t)p->d | (uintptr_t)p->q | (uintptr_t)p->h) & 31u) == 0;
+    e.whole = e.wide && ((uintptr_t)p->d & 31u) == 0;
+    e.whole8 = e.wide && p->n % 32 == 0 && (((uintptr_t)p->q | (uintptr_t)p->h) & 31u) == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.offsets = offsets;
     a.groups = how == kWhole ? 1 : groups;

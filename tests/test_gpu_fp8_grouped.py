@@ -246,3 +246,33 @@ def test_refusals(dev):
     for bad in (dict(d=d[:2]), dict(d=d[0]), dict(b=b[:7]), dict(residual=d.bfloat16()), dict(offsets=None)):
         with pytest.raises(ValueError):
             fp8q.fp8q_grouped_weight_gradient(**{**dict(a=a, b=b, offsets=at, d=d), **bad})
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n", [(272, 1040), (1040, 2064)])
+def test_gradients_on_top_over_many_tiles(dev, m, n, dtype):
+    """Added to what is there: bit for bit the sum of it and of the call without it, over more tiles than pairs of CTAs, empty
+    groups among them; and rows by expert with a residual the same."""
+    off = [0, 0, 40, 41, 300, 300, 428, 700, 701, 1000, 1300, 1300, 1301, 1500, 1501, 1502, 2000, 2000, 2100]
+    e, rows = len(off) - 1, off[-1]
+    g = gen(dev, m + n)
+    a, b = R.random_codes((rows, m), 1, g), R.random_codes((rows, n), 0, g)
+    at = torch.tensor(off, dtype=torch.int32, device=dev)
+    s = torch.full((1,), 0.03, device=dev)
+    plain = torch.empty((e, m, n), device=dev)
+    fp8q.fp8q_grouped_weight_gradient(a, b, at, plain, 1, 0, s, None)
+    old = torch.randn((e, m, n), generator=g, device=dev).to(dtype)
+    buf, d = guarded((e, m, n), dtype, dev)
+    d.copy_(old)
+    fp8q.fp8q_grouped_weight_gradient(a, b, at, d, 1, 0, s, None, residual=d)
+    whole(buf)
+    assert torch.equal(d, (plain + old.float()).to(dtype))
+    few = torch.tensor([7, 7, 900, 901, 2093], dtype=torch.int32, device=dev)
+    w, wt = experts(4, n, m, 0, g)
+    y, old = torch.zeros((rows, n), device=dev), torch.randn((rows, n), generator=g, device=dev).to(dtype)
+    fp8q.fp8q_grouped_matmul(a, wt, few, y, 1, 0, s, None)
+    buf, d = guarded((rows, n), dtype, dev)
+    d.copy_(old)
+    fp8q.fp8q_grouped_matmul(a, wt, few, d, 1, 0, s, None, residual=d)
+    whole(buf)
+    assert torch.equal(d, (y + old.float()).to(dtype))

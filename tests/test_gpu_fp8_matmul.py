@@ -338,3 +338,45 @@ def test_refusals(dev):
         room = torch.empty(8 * 64 + 16, dtype=torch.uint8, device=dev)
         fp8q.fp8q_matmul(room[8: 8 + 8 * 64].view(8, 64), b, d)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("off", [0, 16])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n,k", [(2600, 2320, 160), (5000, 3344, 96), (2600, 2304, 0), (257, 20016, 48)])
+def test_residual_over_many_tiles(dev, m, n, k, out, off):
+    """The residual's columns run ahead of the tiles: bit for bit the sum of it and of the call without it, in place and not, with
+    rows that end within 32 columns, several tiles a CTA, and outputs on 16 and on 32 bytes."""
+    g = gen(dev, m + n + k)
+    a, b = R.random_codes((m, k), 0, g), R.random_codes((n, k), 0, g)
+    A, B = stored(a, 0), stored(b, 0)
+    bias = torch.randn(n, generator=g, device=dev)
+    s = torch.full((1,), 0.1, device=dev)
+    res = torch.randn((m, n), generator=g, device=dev).to(out)
+
+    def room(dtype):
+        size = torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((m * n * size + 256 + off,), CANARY, dtype=torch.uint8, device=dev)
+        return buf, buf[128 + off: 128 + off + m * n * size].view(dtype).view(m, n)
+
+    plain = torch.empty((m, n), device=dev)
+    for act in (0, 1):
+        fp8q.fp8q_matmul(A, B, plain, a_scale=s, bias=bias, act=act)
+        want = (plain + res.float()).to(out)
+        for same in (False, True):
+            buf, d = room(out)
+            if same:
+                d.copy_(res)
+            h, sf = fp8q.checkpoint_empty(m, n)
+            fp8q.fp8q_matmul(A, B, d, a_scale=s, bias=bias, act=act, residual=d if same else res, h=h, h_sf=sf)
+            assert torch.equal(d, want)
+            assert (buf[: 128 + off] == CANARY).all() and (buf[-128:] == CANARY).all()
+        h2, sf2 = fp8q.checkpoint_empty(m, n)
+        fp8q.fp8q_matmul(A, B, None, a_scale=s, bias=bias, h=h2, h_sf=sf2)
+        assert torch.equal(h, h2) and torch.equal(sf, sf2)
+        if out == torch.bfloat16:
+            buf, q = room(torch.uint8)
+            q2, amax, amax2 = torch.empty((m, n), dtype=torch.uint8, device=dev), torch.zeros(1, device=dev), torch.zeros(1, device=dev)
+            fp8q.fp8q_matmul(A, B, None, a_scale=s, bias=bias, act=act, residual=res, q=q, q_scale=s, amax=amax)
+            fp8q.fp8q_quantize_amax(want, q2, 0, s, amax2)
+            assert torch.equal(q, q2) and torch.equal(amax, amax2)
+            assert (buf[: 128 + off] == CANARY).all() and (buf[-128:] == CANARY).all()
