@@ -626,7 +626,7 @@ fp8q_status fp8q_grouped_weight_gradient(const fp8q_product* args, const int32_t
  * the block makes its scale NaN (0xFF).
  * q: [rows, cols] bytes, sf: fp8q_checkpoint_scale_bytes, [rows, ceil(cols / 32)]
  * bytes, both contiguous, from any address; on 16-byte and 4-byte boundaries, with
- * x_bf16 on a 32-byte one and whole blocks a row, they take the vectorised path.
+ * x_bf16 on a 32-byte one and cols a multiple of 16, they take the vectorised path.
  * Back: y = bf16(code * 2^e), the product exact.
  * Errors: INVALID_ARG for rows or cols < 0, a NULL or an odd bf16 pointer;
  *         UNSUPPORTED for rows or cols above 2^31 - 1024.

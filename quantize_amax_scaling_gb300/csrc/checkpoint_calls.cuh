@@ -20,41 +20,44 @@ struct CkptArgs {
     uint16_t* y;
     uint8_t *q, *sf;
     int64_t rows, cols, blocks;  // blocks of 32, a row
-    int64_t items;               // of sixteen elements (whole blocks), or stretches of rows
-    int64_t across;              // stretches a row
+    int64_t items;               // of sixteen elements, or stretches of rows
+    int64_t across;              // of them, a row
     int32_t stretch;             // blocks, a multiple of four
 };
 
-constexpr int kCkptPer = 1;  // items a thread of the kernels of whole blocks (two: 1% slower, four: 2%)
+// Rows of whole sixteens: sixteen elements a lane, two lanes a block (two or four of them a thread are 1% and 2% slower).
+// HALF: the last block of a row is one of sixteen columns, its second lane's item empty (8192x2064 9.5 us and 9.2 back; a column
+// a lane, as below, 31 and 21).
+template <bool HALF>
+__device__ __forceinline__ int64_t ckpt_at(const CkptArgs& a, int64_t item) {  // its first element; rows * cols for an empty one
+    if (!HALF) return item * 16;
+    const int64_t row = a.items <= INT32_MAX ? (int64_t)((uint32_t)item / (uint32_t)a.across) : item / a.across, col = (item - row * a.across) * 16;
+    return col < a.cols ? row * a.cols + col : a.rows * a.cols;
+}
 
-// Rows of whole blocks, which lie one behind another: sixteen elements a lane, two lanes a block.
+template <bool HALF>
 __global__ void __launch_bounds__(kThreads) checkpoint_quantize_kernel(const CkptArgs a) {
     start_behind();
-    const int64_t first = (int64_t)blockIdx.x * (kThreads * kCkptPer) + threadIdx.x;
-    uint4 w[kCkptPer][2];
-#pragma unroll
-    for (int u = 0; u < kCkptPer; ++u)
-        if (first + u * kThreads < a.items) ld_once_v8(a.x + (first + u * kThreads) * 16, w[u][0], w[u][1]);
-#pragma unroll
-    for (int u = 0; u < kCkptPer; ++u) {
-        const int64_t i = first + u * kThreads;
-        const uint32_t v[8] = {w[u][0].x, w[u][0].y, w[u][0].z, w[u][0].w, w[u][1].x, w[u][1].y, w[u][1].z, w[u][1].w};
-        uint32_t m = absmax16(v);
-        m = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        const uint32_t code = ckpt_scale(m);
-        const float f = ckpt_factor(code);
-        const uint32_t four = code | __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8 | __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16 |
-                              __shfl_down_sync(0xFFFFFFFFu, code, 6) << 24;
-        if (i < a.items) {
-            st_v4(a.q + i * 16, make_uint4(ckpt_codes4(v[0], v[1], f), ckpt_codes4(v[2], v[3], f), ckpt_codes4(v[4], v[5], f), ckpt_codes4(v[6], v[7], f)));
-            const int64_t blocks = a.items >> 1, b = i >> 1;
-            if ((threadIdx.x & 7) == 0 && b + 4 <= blocks)
-                *reinterpret_cast<uint32_t*>(a.sf + b) = four;
-            else if ((threadIdx.x & 1) == 0 && (b & ~(int64_t)3) + 4 > blocks)
-                a.sf[b] = (uint8_t)code;
-        }
-    }
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t at = i < a.items ? ckpt_at<HALF>(a, i) : a.rows * a.cols;
+    const bool on = at < a.rows * a.cols;
+    uint4 w[2] = {};
+    if (on) ld_once_v8(a.x + at, w[0], w[1]);
+    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    uint32_t m = absmax16(v);
+    m = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    const uint32_t code = ckpt_scale(m);
+    const float f = ckpt_factor(code);
+    const uint32_t four = code | __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8 | __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16 |
+                          __shfl_down_sync(0xFFFFFFFFu, code, 6) << 24;
+    if (i >= a.items) return;
+    if (on) st_v4(a.q + at, make_uint4(ckpt_codes4(v[0], v[1], f), ckpt_codes4(v[2], v[3], f), ckpt_codes4(v[4], v[5], f), ckpt_codes4(v[6], v[7], f)));
+    const int64_t blocks = a.items >> 1, b = i >> 1;
+    if ((threadIdx.x & 7) == 0 && b + 4 <= blocks)
+        *reinterpret_cast<uint32_t*>(a.sf + b) = four;
+    else if ((threadIdx.x & 1) == 0 && (b & ~(int64_t)3) + 4 > blocks)
+        a.sf[b] = (uint8_t)code;
 }
 
 // Rows of any length, from anywhere: a stretch of a row a warp, four blocks side by side at a time, a column of each a lane.
@@ -95,31 +98,24 @@ __global__ void __launch_bounds__(kThreads) checkpoint_quantize_rows_kernel(cons
     }
 }
 
+template <bool HALF>
 __global__ void __launch_bounds__(kThreads) checkpoint_dequantize_kernel(const CkptArgs a) {
     start_behind();
-    const int64_t first = (int64_t)blockIdx.x * (kThreads * kCkptPer) + threadIdx.x;
-    uint4 w[kCkptPer];
-    uint32_t code[kCkptPer];
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= a.items) return;
+    const int64_t at = ckpt_at<HALF>(a, i);
+    if (HALF && at >= a.rows * a.cols) return;
+    const uint4 w = *reinterpret_cast<const uint4*>(a.q + at);
+    const float s = ckpt_value(a.sf[i >> 1]);
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
 #pragma unroll
-    for (int u = 0; u < kCkptPer; ++u) {
-        const int64_t i = first + u * kThreads;
-        if (i < a.items) w[u] = *reinterpret_cast<const uint4*>(a.q + i * 16), code[u] = a.sf[i >> 1];
+    for (int j = 0; j < 4; ++j) {
+        float v[4];
+        ckpt_decode4(in[j], s, v);
+        o[2 * j] = cvt_bf16x2(v[0], v[1]), o[2 * j + 1] = cvt_bf16x2(v[2], v[3]);
     }
-#pragma unroll
-    for (int u = 0; u < kCkptPer; ++u) {
-        const int64_t i = first + u * kThreads;
-        if (i >= a.items) break;
-        const float s = ckpt_value(code[u]);
-        const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float v[4];
-            ckpt_decode4(in[j], s, v);
-            o[2 * j] = cvt_bf16x2(v[0], v[1]), o[2 * j + 1] = cvt_bf16x2(v[2], v[3]);
-        }
-        st_v8(a.y + i * 16, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
-    }
+    st_v8(a.y + at, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]));
 }
 
 __global__ void __launch_bounds__(kThreads) checkpoint_dequantize_rows_kernel(const CkptArgs a) {
@@ -389,13 +385,15 @@ fp8q_status check_ckpt(const void* x, const uint8_t* q, const uint8_t* sf, int64
 fp8q_status launch_ckpt(CkptArgs a, bool back, cudaStream_t s) {
     a.blocks = (a.cols + 31) / 32;
     const uintptr_t x = back ? (uintptr_t)a.y : (uintptr_t)a.x;
-    const bool whole = a.cols % 32 == 0 && (x & 31u) == 0 && ((uintptr_t)a.q & 15u) == 0 && ((uintptr_t)a.sf & 3u) == 0;
-    if (whole) {
-        a.items = a.rows * a.cols / 16;
-        const int64_t grid = (a.items + kThreads * kCkptPer - 1) / (kThreads * kCkptPer);
+    if (a.cols % 16 == 0 && (x & 31u) == 0 && ((uintptr_t)a.q & 15u) == 0 && ((uintptr_t)a.sf & 3u) == 0) {
+        const bool half = a.cols % 32 != 0;
+        a.across = 2 * a.blocks;
+        a.items = a.rows * a.across;
+        const int64_t grid = (a.items + kThreads - 1) / kThreads;
         if (grid > 0x7FFFFFFF) return FP8Q_ERR_UNSUPPORTED;
-        return launch_behind(back ? checkpoint_dequantize_kernel : checkpoint_quantize_kernel, dim3((unsigned)grid), dim3(kThreads), 0, 1, s,
-                             back ? "checkpoint_dequantize_kernel" : "checkpoint_quantize_kernel", a);
+        return launch_behind(back ? (half ? checkpoint_dequantize_kernel<true> : checkpoint_dequantize_kernel<false>)
+                                  : (half ? checkpoint_quantize_kernel<true> : checkpoint_quantize_kernel<false>),
+                             dim3((unsigned)grid), dim3(kThreads), 0, 1, s, back ? "checkpoint_dequantize_kernel" : "checkpoint_quantize_kernel", a);
     }
     // as many stretches as warps are resident, of four to 32 blocks (1187x2731 with 32: 11.4 us; 8192x4095 with four: 49.9)
     const int64_t fill = a.rows * a.blocks / (64 * (int64_t)sm_count()) / 4 * 4;

@@ -185,3 +185,27 @@ def test_refusals(dev):
         fp8q.fp8q_checkpoint_quantize(dy, h, sf[:3])
     with pytest.raises(ValueError):
         fp8q.fp8q_checkpoint_dequantize(h, sf, dy[:3])
+
+
+@pytest.mark.parametrize("cols", [1, 7, 8, 9, 40, 248, 255, 256, 257, 263, 265, 511, 784, 2047, 2049, 4101])
+def test_rows_and_outputs_from_any_address(dev, cols):
+    """Inputs and outputs at every offset from the vectors that hold them, rows of every length beside 256."""
+    for rows, x_off, q_off, y_off in ((1, 0, 0, 0), (3, 1, 1, 1), (5, 7, 7, 7), (4, 3, 2, 6), (9, 8, 3, 2), (2, 5, 4, 5), (40, 2, 5, 3), (33, 6, 6, 4), (7, 16, 0, 16), (70, 16, 16, 0)):
+        bits = inputs(rows, cols, rows + cols, rows % 2 == 0)
+        codes, sf, val, nan = R.checkpoint(bits)
+        n, blocks = rows * cols, (cols + 31) // 32
+        x = torch.zeros(x_off + n, dtype=torch.bfloat16, device=dev)[x_off:].view(rows, cols)
+        x.copy_(from_bits(bits, dev))
+        bq = torch.full((n + 64,), 0xEE, dtype=torch.uint8, device=dev)
+        bs = torch.full((rows * blocks + 64,), 0xEE, dtype=torch.uint8, device=dev)
+        by = torch.full((n + 64,), -7.0, dtype=torch.bfloat16, device=dev)
+        q, s = bq[16 + q_off: 16 + q_off + n].view(rows, cols), bs[16 + q_off: 16 + q_off + rows * blocks].view(rows, blocks)
+        y = by[16 + y_off: 16 + y_off + n].view(rows, cols)
+        fp8q.fp8q_checkpoint_quantize(x, q, s)
+        fp8q.fp8q_checkpoint_dequantize(q, s, y)
+        for buf, off, size, old in ((bq, 16 + q_off, n, 0xEE), (bs, 16 + q_off, rows * blocks, 0xEE), (by, 16 + y_off, n, -7.0)):
+            assert (buf[:off] == old).all() and (buf[off + size:] == old).all(), "write outside the output"
+        assert np.array_equal(s.cpu().numpy(), sf), "scales differ"
+        assert np.array_equal(q.cpu().numpy()[~nan], codes[~nan]), "codes differ"
+        want = torch.from_numpy(val).to(dev).to(torch.float32).to(torch.bfloat16)
+        assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y[~want.isnan()], want[~want.isnan()])
