@@ -58,7 +58,8 @@ struct ProductArgs {
     int32_t k;
     uint32_t idesc;
     int32_t p_across, q_across;  // P's, Q's rows do not lie along k
-    int32_t p_tiles, q_tiles;    // tiles of a group where all have the same
+    int32_t p_tiles, q_tiles;    // tiles of a group where all have the same (pairs: of 256 columns, the last narrow ones apart)
+    int32_t narrow;              // pairs: 1 where each row of tiles ends in one of half a tile's columns or fewer
     int32_t stages, per;         // stages of `per` steps
     int32_t split;               // CTAs of a cluster that share a tile's k
 #ifdef FP8Q_TEST_HOOKS
@@ -756,35 +757,48 @@ static_assert(kPrPairSmem <= 227 * 1024, "");
 
 struct PairWhere {
     int p0, p_end, q0;  // rows of A (of this CTA's pair's tile, absolute) and of B
+    int cols;           // of the tile that are multiplied, a multiple of 32
     int group, k0, k;   // codes of k from k0
 };
+// The rows of tiles of all groups.
+template <bool RAGGED_K>
+__device__ __forceinline__ int pair_rows(const ProductArgs& a, const int* cum) {
+    return RAGGED_K ? a.groups * a.p_tiles : a.offsets ? cum[a.groups] : a.p_tiles;
+}
+// Narrow tiles at the rows' ends come behind all others and are multiplied by their own width, so that a last round of them is
+// shorter (2304x2176x4096 21.8 us, 24.4 with all of 256 and in their places; 8192x1040x4096 29.0 and 31.5; 3001 rows of 12 experts, n
+// 1040, k 2064, 20.7 and 21.1).  Not for ragged k, which is short: there the stores bound (32.7 us, 30.9 in their places).
 template <bool RAGGED_K>
 __device__ __forceinline__ PairWhere pair_where(const ProductArgs& a, const int* cum, int tile) {
     PairWhere w;
-    w.k0 = 0, w.k = a.k, w.group = 0;
+    w.k0 = 0, w.k = a.k, w.group = 0, w.p_end = a.m;
+    const int rows = pair_rows<RAGGED_K>(a, cum);
+    const bool narrow = !RAGGED_K && a.narrow && tile >= (int64_t)rows * a.q_tiles;
+    const int q_tiles = narrow ? 1 : a.q_tiles;
+    if (narrow) tile -= rows * a.q_tiles;
+    PairTile t;
     if (RAGGED_K) {
-        const int each = a.p_tiles * a.q_tiles;
+        const int each = a.p_tiles * q_tiles;
         w.group = tile / each;
-        const PairTile t = pair_tile(tile - w.group * each, a.p_tiles, a.q_tiles);
+        t = pair_tile(tile - w.group * each, a.p_tiles, q_tiles);
         const int2 r = group_rows(a, w.group);
-        w.p0 = t.p, w.q0 = t.q, w.p_end = a.m;
-        w.k0 = r.x, w.k = r.y - r.x;
-        return w;
+        w.p0 = t.p, w.k0 = r.x, w.k = r.y - r.x;
+    } else if (!a.offsets) {
+        t = pair_tile(tile, a.p_tiles, q_tiles);
+        w.p0 = t.p;
+    } else {
+        const int at = tile / q_tiles;
+        int lo = 0, hi = a.groups;  // cum[lo] <= at < cum[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= at) lo = mid; else hi = mid;
+        }
+        t = pair_tile(tile - cum[lo] * q_tiles, cum[lo + 1] - cum[lo], q_tiles);
+        const int2 r = group_rows(a, lo);
+        w.group = lo, w.p0 = r.x + t.p, w.p_end = r.y;
     }
-    if (!a.offsets) {
-        const PairTile t = pair_tile(tile, a.p_tiles, a.q_tiles);
-        w.p0 = t.p, w.q0 = t.q, w.p_end = a.m;
-        return w;
-    }
-    const int at = tile / a.q_tiles;
-    int lo = 0, hi = a.groups;  // cum[lo] <= at < cum[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= at) lo = mid; else hi = mid;
-    }
-    const PairTile t = pair_tile(tile - cum[lo] * a.q_tiles, cum[lo + 1] - cum[lo], a.q_tiles);
-    const int2 r = group_rows(a, lo);
-    w.group = lo, w.p0 = r.x + t.p, w.p_end = r.y, w.q0 = t.q;
+    w.q0 = narrow ? a.q_tiles * 256 : t.q;
+    w.cols = min(256, (a.e.n - w.q0 + 31) & ~31);
     return w;
 }
 
@@ -841,8 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
         }
         __syncthreads();
     }
-    const int tiles = RAGGED_K ? a.groups * a.p_tiles * a.q_tiles : a.offsets ? (int)min((int64_t)cum[a.groups] * a.q_tiles, (int64_t)kManyTiles)
-                                                                        : a.p_tiles * a.q_tiles;
+    const int tiles = (int)min((int64_t)pair_rows<RAGGED_K>(a, cum) * (a.q_tiles + a.narrow), (int64_t)kManyTiles);
     if (warp == 9) {
         tmem_alloc<2>(&tmem_slot, 512);
         let_next_start();
@@ -862,7 +875,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
         const uint32_t bars = in_cluster(smem_addr(&full[0]), 0);
         for (int tile = first; tile < tiles && ok; tile += stride) {
             const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
-            const int p0 = w.p0 + (int)rank * 128, q0 = w.q0 + (int)rank * 128;
+            const int p0 = w.p0 + (int)rank * 128, q0 = w.q0 + (int)rank * (w.cols / 2);
             const int bg = RAGGED_K ? 0 : w.group;
             for (int k = 0; k < w.k; k += kStepK, ++n) {
                 if (!pr_wait(a, kPrCopyEmpty, n, &empty[st], (round & 1) ^ 1)) {
@@ -903,7 +916,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
             const uint64_t next_p = k_advance(a.p_across), next_q = k_advance(a.q_across);
             for (int tile = first; tile < tiles && ok; tile += stride, ++it) {
                 const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
-                const uint32_t set = it & 1, to = tmem + set * 256;
+                const uint32_t set = it & 1, to = tmem + set * 256, idesc = mma_desc_cols(a.idesc, w.cols);
                 if (it > 1 && !pr_wait(a, kPrSumDrained, it, &drained[set], ((it >> 1) - 1) & 1)) {
                     ok = false;
                     break;
@@ -921,7 +934,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                     if (elect_lane()) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (i < nk) tc_mma_fp8<2>(to, dp + i * next_p, dq + i * next_q, a.idesc, k | i);
+                            if (i < nk) tc_mma_fp8<2>(to, dp + i * next_p, dq + i * next_q, idesc, k | i);
                         tc_commit_pair(&empty[st], 3);
                     }
                     __syncwarp();
@@ -1245,8 +1258,9 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
         a.q_across = tb;
         a.split = 1;
         a.p_tiles = (int32_t)((p->m + 255) / 256);
-        a.q_tiles = (int32_t)((p->n + 255) / 256);
-        const int64_t tiles = (how == kGroupedRows ? p->m / 256 + groups : (int64_t)a.p_tiles * (how == kGroupedK ? groups : 1)) * a.q_tiles;
+        a.narrow = how != kGroupedK && p->n > 256 && p->n % 256 > 0 && p->n % 256 <= 128;
+        a.q_tiles = (int32_t)(a.narrow ? p->n / 256 : (p->n + 255) / 256);
+        const int64_t tiles = (how == kGroupedRows ? p->m / 256 + groups : (int64_t)a.p_tiles * (how == kGroupedK ? groups : 1)) * (a.q_tiles + a.narrow);
         if (tiles > kManyTiles) return FP8Q_ERR_UNSUPPORTED;
         if (p->k > 0 && (!operand_map(&mp, p->a, p->m, p->k, p->lda, 1, ta, 128) || !operand_map(&mq, p->b, p->n, p->k, p->ldb, b_groups, tb, 128)))
             return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_pair_kernel tensor map");

@@ -195,6 +195,9 @@ __host__ __device__ constexpr uint32_t mma_desc_fp8(uint32_t m, uint32_t n, uint
     return (1u << 4) | (fa << 7) | (fb << 10) | (ta << 15) | (tb << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// The same with another number of columns.
+__device__ __forceinline__ uint32_t mma_desc_cols(uint32_t idesc, uint32_t n) { return (idesc & ~(63u << 17)) | (n >> 3) << 17; }
+
 // d (+)= A B^T over 32 FP8 codes.
 template <int PAIR>
 __device__ __forceinline__ void tc_mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
