@@ -202,4 +202,4 @@ def test_readme_example():
     assert ((a - want).abs() <= 0.07 * want.abs() + 2.0 ** -9 * s + 2.0 ** -16).all()  # half steps of bf16 and of e4m3
     d1 = R.values(ns["d1"], 1)
     check(ns["dw1"], d1.t() @ x * 1e-6 * s, (R.sum_bound(d1.t(), x.t()) + (d1.t() @ x).abs() * 2.0 ** -23) * 1e-6 * s)
-    assert ns["db1"].any() and torch.isfinite(ns["dw2"]).all() and ns["dw2"].any() and ns["y"].any()
+    assert ns["db1"].any() and torch.isfinite(ns["dw2"]).all() and ns["dw2"].any() and ns["out"].any()
