@@ -18,9 +18,9 @@
 // PFLOP/s, and 325 in a loop at the 1400 W limit; with zeros for operands, which
 // cost little power, 239 us, 4.6 PFLOP/s, the multiply-adds' own 128 cycles for
 // 256 x 256 x 32 at 2070 MHz.  So the tensor cores' power bounds it, not their feeding.
-// Both take their sums through one epilogue, four columns of a row a lane, whose
-// stores are whole sectors wherever rows start and which leaves out any rows and
-// columns at a group's or the matrix's edge; pairs have a faster one beside it.
+// Sums go out four columns of a row a lane (emit_rows), in pairs a row a lane
+// (emit_row32), and a column a lane where n or an address holds no vectors
+// (emit_cols); rows and columns beyond a group's or the matrix's edge are left out.
 
 #include "checkpoint_calls.cuh"
 #include "tcgen05.cuh"
@@ -116,24 +116,18 @@ __device__ __forceinline__ float2 gelu2(float2 x) {
     return mul2_rn(x, r);
 }
 
-// Four consecutive elements of a row, `left` of them there.
-__device__ __forceinline__ void read4(const void* p, int64_t at, int left, bool f32, bool vec, float (&v)[4]) {
-    if (vec) {
-        if (f32) {
-            const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
-            v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-            v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
-        }
+// Four consecutive elements of a row.
+__device__ __forceinline__ void read4(const void* p, int64_t at, bool f32, float (&v)[4]) {
+    if (f32) {
+        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < left)
-                v[i] = f32 ? static_cast<const float*>(p)[at + i] : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[at + i] << 16);
+        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+        v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
     }
 }
+__device__ __forceinline__ float bf16_f(uint16_t w) { return __uint_as_float((uint32_t)w << 16); }
 
 template <int FMT>
 __device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, const QScale& c) {
@@ -145,6 +139,7 @@ struct Lane {
     QScale c;
     float alpha;
     uint32_t m2;  // the largest |bf16(D)|
+    bool any;     // n, an address or q's scale is such that only emit_cols() holds
 };
 
 __device__ __forceinline__ Lane make_lane(const Epilogue& e) {
@@ -152,95 +147,98 @@ __device__ __forceinline__ Lane make_lane(const Epilogue& e) {
     l.alpha = __fmul_rn(e.sa ? *e.sa : 1.0f, e.sb ? *e.sb : 1.0f);
     l.c = make_qscale_value(e.q ? *e.q_scale : 1.0f);
     l.m2 = 0;
+    l.any = !e.vec || (e.q && !l.c.fast);
     return l;
 }
 
-// Columns col to col + 3 of a row of D; eight lanes side by side hold a block of 32 columns.  `on`: the row is there.
-// r: the residual.  All lanes of a warp come here.  (Any n, any addresses, any scale of q.)
-// Out of line, so that the paths that most calls take stay short.  Returns the lane's largest.
-__device__ __noinline__ uint32_t emit4(const Epilogue& e, Lane l, int64_t row, int col, bool on, float4 sum, float4 b, float4 r4) {
-    const int left = e.n - col;
-    on = on && left > 0;
-    float v[4] = {fmaf(sum.x, l.alpha, b.x), fmaf(sum.y, l.alpha, b.y), fmaf(sum.z, l.alpha, b.z), fmaf(sum.w, l.alpha, b.w)};
-    const float r[4] = {r4.x, r4.y, r4.z, r4.w};
-    if (e.h) {
-        uint32_t w0 = cvt_bf16x2(v[0], v[1]), w1 = cvt_bf16x2(v[2], v[3]);
-        if (left < 4) {  // beyond the row's end
-            w0 = left < 1 ? 0u : left < 2 ? w0 & 0xFFFFu : w0;
-            w1 = left < 3 ? 0u : w1 & 0xFFFFu;
-        }
-        const uint32_t m = bf16x2_absmax(w0, w1);
-        uint32_t a = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
+// Eight rows from `row` on of one column a lane, the warp's a block of 32; bit i of `on` says whether the i-th is there.  For any n,
+// any addresses, any scale of q.  Returns the lane's largest.  (2600x2310x512 19.8 us; four columns a lane out of line, each its
+// own store into the others' sectors, 58.)
+__device__ __forceinline__ uint32_t emit_cols(const Epilogue& e, Lane l, int64_t row, uint32_t on, int col, int64_t bias_at, float4 v0, float4 v1) {
+    const bool in = col < e.n;
+    float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w}, r[8];
+    if (!in) on = 0;
+    const int64_t at = row * e.n + col;
+    float b = 0.0f;
+    if (in && e.bias) b = e.bias_bf16 ? bf16_f(static_cast<const uint16_t*>(e.bias)[bias_at + col]) : static_cast<const float*>(e.bias)[bias_at + col];
+    if (e.residual) {
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-        const uint32_t code = ckpt_scale(a), four = ckpt_codes4(w0, w1, ckpt_factor(code));
-        if (on) {
-            uint8_t* h = e.h + row * e.n + col;
-            if (e.vec)
-                *reinterpret_cast<uint32_t*>(h) = four;
-            else
-                for (int i = 0; i < min(left, 4); ++i) h[i] = (uint8_t)(four >> 8 * i);
-            if ((threadIdx.x & 7) == 0) e.h_sf[row * e.blocks + (col >> 5)] = (uint8_t)code;
+        for (int i = 0; i < 8; ++i) {
+            const int64_t p = at + (int64_t)i * e.n;
+            r[i] = !(on >> i & 1) ? 0.0f : e.f32 ? static_cast<const float*>(e.residual)[p] : bf16_f(static_cast<const uint16_t*>(e.residual)[p]);
         }
     }
-    if (!on || !(e.d || e.q || e.amax)) return l.m2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], l.alpha, b);
+    uint32_t w[4];
+    if (e.h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = in ? cvt_bf16x2(v[2 * i], v[2 * i + 1]) : 0u;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t x = w[i >> 1] >> 16 * (i & 1) & 0xFFFFu, code = ckpt_scale(__reduce_max_sync(0xFFFFFFFFu, x & 0x7FFFu));
+            if (on >> i & 1) e.h[at + (int64_t)i * e.n] = (uint8_t)cvt_fp8x2<FP8Q_E4M3FN>(__uint_as_float(x << 16) * ckpt_factor(code), 0.0f);
+            if ((col & 31) == i) mine = code;
+        }
+        const uint32_t there = __shfl_sync(0xFFFFFFFFu, on, 0);  // the block's first column is there if any is
+        if ((col & 31) < 8 && (there >> (col & 31) & 1)) e.h_sf[(row + (col & 31)) * e.blocks + (col >> 5)] = (uint8_t)mine;
+    }
+    if (!(e.d || e.q || e.amax)) return l.m2;
     if (e.gelu) {
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
+        for (int i = 0; i < 8; i += 2) {
             const float2 y = gelu2(make_float2(v[i], v[i + 1]));
             v[i] = y.x, v[i + 1] = y.y;
         }
     }
     if (e.residual) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += r[i];
+        for (int i = 0; i < 8; ++i) v[i] += r[i];
     }
-    const int64_t at = row * e.n + col;
     if (e.f32) {
         float* d = static_cast<float*>(e.d) + at;
-        if (e.vec) {
-            *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left) d[i] = v[i];
-        }
+        for (int i = 0; i < 8; ++i)
+            if (on >> i & 1) d[(int64_t)i * e.n] = v[i];
         return l.m2;
     }
-    uint32_t w0 = cvt_bf16x2(v[0], v[1]), w1 = cvt_bf16x2(v[2], v[3]);
-    if (left < 4) w0 = left < 2 ? w0 & 0xFFFFu : w0, w1 = left < 3 ? 0u : w1 & 0xFFFFu;
-    if (e.amax) l.m2 = bf16x2_absmax(l.m2, bf16x2_absmax(w0, w1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+    if (e.amax) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l.m2 = bf16x2_absmax(l.m2, w[i] & ((on >> 2 * i & 1 ? 0xFFFFu : 0u) | (on >> 2 * i & 2 ? 0xFFFF0000u : 0u)));
+    }
     if (e.d) {
         uint16_t* d = static_cast<uint16_t*>(e.d) + at;
-        if (e.vec)
-            *reinterpret_cast<uint2*>(d) = make_uint2(w0, w1);
-        else
-            for (int i = 0; i < min(left, 4); ++i) d[i] = (uint16_t)((i < 2 ? w0 : w1) >> 16 * (i & 1));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (on >> i & 1) d[(int64_t)i * e.n] = (uint16_t)(w[i >> 1] >> 16 * (i & 1));
     }
     if (e.q) {
-        const uint32_t four = e.e5m2 ? codes4<FP8Q_E5M2>(w0, w1, l.c) : codes4<FP8Q_E4M3FN>(w0, w1, l.c);
-        if (e.vec)
-            *reinterpret_cast<uint32_t*>(e.q + at) = four;
-        else
-            for (int i = 0; i < min(left, 4); ++i) e.q[at + i] = (uint8_t)(four >> 8 * i);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t four = e.e5m2 ? codes4<FP8Q_E5M2>(w[2 * j], w[2 * j + 1], l.c) : codes4<FP8Q_E4M3FN>(w[2 * j], w[2 * j + 1], l.c);
+#pragma unroll
+            for (int i = 4 * j; i < 4 * j + 4; ++i)
+                if (on >> i & 1) e.q[at + (int64_t)i * e.n] = (uint8_t)(four >> 8 * (i & 3));
+        }
     }
     return l.m2;
 }
 
-__device__ __forceinline__ float4 as_f4(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
+// The same out of line, for pairs whose scale of q turns out to be none of the ordinary ones.
+__device__ __noinline__ uint32_t emit_cols_apart(const Epilogue& e, Lane l, int64_t row, uint32_t on, int col, int64_t bias_at, float4 v0, float4 v1) {
+    return emit_cols(e, l, row, on, col, bias_at, v0, v1);
+}
 
-// emit4() for rows row, row + step, .. of which bit i of `on` says whether the i-th is there.  Whole vectors at an
-// ordinary scale go through the stages all rows at a time, so that a stage's latencies overlap: row by row, with the
-// branches between, 8192x16384x4096 took 731 us with GELU, codes and checkpoint and 411 with bf16 alone.
+// Columns col to col + 3 of rows row, row + step, .. of which bit i of `on` says whether the i-th is there; eight lanes side by
+// side hold a block of 32 columns.  r: the residual.  All lanes of a warp come here.  For whole vectors at an ordinary scale, which
+// go through the stages all rows at a time, so that a stage's latencies overlap: row by row, with the branches between,
+// 8192x16384x4096 took 731 us with GELU, codes and checkpoint and 411 with bf16 alone.
 template <int ROWS>
 __device__ __forceinline__ void emit_rows(const Epilogue& e, Lane& l, int64_t row, int step, uint32_t on, int col, float (&v)[ROWS][4],
                                           const float (&b)[4], const float (&r)[ROWS][4]) {
-    if (!e.vec || (e.q && !l.c.fast)) {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-            l.m2 = emit4(e, l, row + i * step, col, on >> i & 1, as_f4(v[i]), as_f4(b), as_f4(r[i]));
-        return;
-    }
     const uint32_t here = (col & ~31) < e.n ? on : 0u;  // of a block's eight lanes the first may be the only one with columns
     if (col >= e.n) on = 0;
     const float2 alpha = splat2(l.alpha), b0 = make_float2(b[0], b[1]), b1 = make_float2(b[2], b[3]);
@@ -463,6 +461,12 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t at, float (&v)[4]) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(at) : "memory");
 }
 
+__device__ __forceinline__ float ld_shared_f(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
 // A box of codes: 128 bytes along k by 128 rows, or 128 rows by 128 lines of k.  The multiply-adds of a step read 32 of k at
 // a time, 32 bytes on in a line or 32 lines on.
 __device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 : 2; }
@@ -484,15 +488,15 @@ struct TileLane {
 };
 __device__ __forceinline__ TileLane make_tile_lane(const ProductArgs& a, int64_t group, int col) {
     TileLane t = {make_lane(a.e), {}};
-    if (a.e.bias && col < a.e.n) read4(a.e.bias, group * a.e.n + col, a.e.n - col, !a.e.bias_bf16, a.e.vec, t.b);
+    if (a.e.bias && !t.l.any && col < a.e.n) read4(a.e.bias, group * a.e.n + col, !a.e.bias_bf16, t.b);
     return t;
 }
 
 // This CTA's share of the tile's rows of A, over the SPLIT CTAs of the cluster whose sums are added in rank order, by four
 // warps.  A warp takes four rows of 128 columns at a time.
 template <int SPLIT, int BN>
-__device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uint32_t part, int rank, int col, int q0, int q_end) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uint32_t part, int rank, int group, int p0, int q0, int q_end) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = p0 + lane * 4;
     const Epilogue& e = a.e;
     constexpr int kShare = BN / SPLIT;
     constexpr int kRows = kShare < 4 ? kShare : 4;
@@ -500,8 +504,8 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
     auto ask = [&](int i0) {  // the residual of a round, while the one before goes out
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
-            if (e.residual && col < e.n && i0 < (rank + 1) * kShare && q0 + i0 + i < q_end)
-                read4(e.residual, (int64_t)(q0 + i0 + i) * e.n + col, e.n - col, e.f32, e.vec, next[i]);
+            if (e.residual && !t.l.any && col < e.n && i0 < (rank + 1) * kShare && q0 + i0 + i < q_end)
+                read4(e.residual, (int64_t)(q0 + i0 + i) * e.n + col, e.f32, next[i]);
     };
     ask(rank * kShare + warp * kRows);
 #pragma unroll 1
@@ -528,6 +532,20 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
 #pragma unroll
                 for (int j = 0; j < SPLIT; ++j) v[i][0] += x[j].x, v[i][1] += x[j].y, v[i][2] += x[j].z, v[i][3] += x[j].w;
             }
+        }
+        if (t.l.any) {  // these rows of this CTA's sums are its own
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) st_shared_v4(part + (i0 + i) * 512 + lane * 16, v[i]);
+            __syncwarp();
+#pragma unroll 1
+            for (int c = lane; p0 + (c & ~31) < e.n && c < 128; c += 32) {
+                float x[4] = {};
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) x[i] = ld_shared_f(part + (i0 + i) * 512 + c * 4);
+                t.l.m2 = emit_cols(e, t.l, row, on, p0 + c, (int64_t)group * e.n, make_float4(x[0], x[1], x[2], x[3]), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+            }
+            continue;
         }
         emit_rows<kRows>(e, t.l, row, 1, on, col, v, t.b, r);
     }
@@ -706,14 +724,14 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     tc_fence_before();
     if (a.split == 1) {
         __syncthreads();
-        if (warp < 4) emit_tile<1, BN>(a, t, base, 0, col, q0, q_end);
+        if (warp < 4) emit_tile<1, BN>(a, t, base, 0, group, p0, q0, q_end);
     } else {
         cluster_sync_all();
         if (warp < 4) {
             switch (a.split) {
-                case 2: emit_tile<2, BN>(a, t, base, rank, col, q0, q_end); break;
-                case 4: emit_tile<4, BN>(a, t, base, rank, col, q0, q_end); break;
-                default: emit_tile<8, BN>(a, t, base, rank, col, q0, q_end);
+                case 2: emit_tile<2, BN>(a, t, base, rank, group, p0, q0, q_end); break;
+                case 4: emit_tile<4, BN>(a, t, base, rank, group, p0, q0, q_end); break;
+                default: emit_tile<8, BN>(a, t, base, rank, group, p0, q0, q_end);
             }
         }
         cluster_sync_all();  // no CTA's sums go away while another reads them
@@ -802,7 +820,10 @@ __device__ __forceinline__ PairWhere pair_where(const ProductArgs& a, const int*
     return w;
 }
 
-template <bool RAGGED_K>
+//
+// ANY: n or an address is such that only emit_cols() holds.  A kernel of its own: with both in one, 2600x2308x0 with a residual
+// takes 28.5 us for 23.9, and with emit_cols() out of line 2600x2310x512 43 for 19.8.
+template <bool RAGGED_K, bool ANY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
     fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const ProductArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -994,7 +1015,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
         const uint32_t room = base + kPrOut + warp * kPrRoom;
         const int sub = lane >> 3, c4 = (lane & 7) * 4;
         Lane l = make_lane(e);
-        const bool rows_in_lanes = e.wide && (!e.f32 || e.residual) && (!e.q || l.c.fast);
+        const bool rows_in_lanes = !ANY && e.wide && (!e.f32 || e.residual) && (!e.q || l.c.fast);
         const bool ahead = rows_in_lanes && e.residual;
         bool ok = true;
         uint32_t it = 0;
@@ -1050,13 +1071,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                 float v[32];
                 const bool staged = !rows_in_lanes && q < e.n && p_first < w.p_end;
                 float b[4] = {}, r[8][4];
-                if (staged) {  // on their way while tensor memory is read
-                    if (e.bias && col < e.n) read4(e.bias, (int64_t)w.group * e.n + col, e.n - col, !e.bias_bf16, e.vec, b);
+                if (!ANY && staged && !l.any) {  // on their way while tensor memory is read
+                    if (e.bias && col < e.n) read4(e.bias, (int64_t)w.group * e.n + col, !e.bias_bf16, b);
                     if (e.residual) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             if (col < e.n && p_first + i * 4 + sub < w.p_end)
-                                read4(e.residual, (d_first + i * 4 + sub) * e.n + col, e.n - col, e.f32, e.vec, r[i]);
+                                read4(e.residual, (d_first + i * 4 + sub) * e.n + col, e.f32, r[i]);
                         }
                     }
                 }
@@ -1101,6 +1122,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) st_shared_v4(room + lane * 128 + ((j ^ (lane & 7)) << 4), v + 4 * j);
                 __syncwarp();
+                if (ANY || l.any) {  // a column a lane, eight rows at a time
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 32 && p_first + i0 < w.p_end; i0 += 8) {
+                        float y[8];
+                        uint32_t on = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            y[i] = ld_shared_f(room + (i0 + i) * 128 + (((lane >> 2) ^ i) << 4) + (lane & 3) * 4);
+                            if (!ok) y[i] = __uint_as_float(0x7FFFFFFFu);  // a wait that ran out
+                            on |= (uint32_t)(p_first + i0 + i < w.p_end) << i;
+                        }
+                        const float4 y0 = make_float4(y[0], y[1], y[2], y[3]), y1 = make_float4(y[4], y[5], y[6], y[7]);
+                        l.m2 = ANY ? emit_cols(e, l, d_first + i0, on, q + lane, (int64_t)w.group * e.n, y0, y1)
+                                   : emit_cols_apart(e, l, d_first + i0, on, q + lane, (int64_t)w.group * e.n, y0, y1);
+                    }
+                    continue;
+                }
+                if (ANY) continue;
                 float x[8][4];
                 uint32_t on = 0;
 #pragma unroll
@@ -1162,10 +1201,10 @@ fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, Product
     return launch_behind(kern, dim3(grid), dim3(192), (need > BN * 512 ? need : BN * 512) + 1024, (unsigned)a.split, s, "fp8_matmul_kernel", mp, mq, a);
 }
 
-template <bool RAGGED_K>
+template <bool RAGGED_K, bool ANY>
 fp8q_status launch_product_pairs(const CUtensorMap& mp, const CUtensorMap& mq, const ProductArgs& a, int64_t tiles, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};
-    auto kern = fp8_matmul_pair_kernel<RAGGED_K>;
+    auto kern = fp8_matmul_pair_kernel<RAGGED_K, ANY>;
     const cudaError_t e = allow_smem(kern, kPrPairSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_pair_kernel setup");
     const int64_t pairs = sm_count() / 2;
@@ -1264,8 +1303,8 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
         if (tiles > kManyTiles) return FP8Q_ERR_UNSUPPORTED;
         if (p->k > 0 && (!operand_map(&mp, p->a, p->m, p->k, p->lda, 1, ta, 128) || !operand_map(&mq, p->b, p->n, p->k, p->ldb, b_groups, tb, 128)))
             return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_pair_kernel tensor map");
-        return how == kGroupedK ? launch_product_pairs<true>(mp, mq, a, tiles, s)
-                                : launch_product_pairs<false>(mp, mq, a, tiles, s);
+        if (how == kGroupedK) return e.vec ? launch_product_pairs<true, false>(mp, mq, a, tiles, s) : launch_product_pairs<true, true>(mp, mq, a, tiles, s);
+        return e.vec ? launch_product_pairs<false, false>(mp, mq, a, tiles, s) : launch_product_pairs<false, true>(mp, mq, a, tiles, s);
     }
     // P is B and Q is A.  Fewer rows of A a CTA while two thirds of the SMs have room for all CTAs: a tile goes out sooner
     // the smaller it is (300x1024x1024 5.3 us with 32 rows, 6.9 with 128; 278x208x64 5.5 and 14), but reads B once more, and
