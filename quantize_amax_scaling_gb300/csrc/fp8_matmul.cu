@@ -152,20 +152,23 @@ __device__ __forceinline__ Lane make_lane(const Epilogue& e) {
 }
 
 // Eight rows from `row` on of one column a lane, the warp's a block of 32; bit i of `on` says whether the i-th is there.  For any n,
-// any addresses, any scale of q.  Returns the lane's largest.  (2600x2310x512 19.8 us; four columns a lane out of line, each its
+// any addresses, any scale of q.  Returns the lane's largest.  (2600x2310x512 18.6 us; four columns a lane out of line, each its
 // own store into the others' sectors, 58.)
 __device__ __forceinline__ uint32_t emit_cols(const Epilogue& e, Lane l, int64_t row, uint32_t on, int col, int64_t bias_at, float4 v0, float4 v1) {
     const bool in = col < e.n;
-    float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w}, r[8];
+    float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     if (!in) on = 0;
     const int64_t at = row * e.n + col;
     float b = 0.0f;
     if (in && e.bias) b = e.bias_bf16 ? bf16_f(static_cast<const uint16_t*>(e.bias)[bias_at + col]) : static_cast<const float*>(e.bias)[bias_at + col];
-    if (e.residual) {
+    uint32_t raw[8];
+    if (e.residual) {  // all eight under way before the first is looked at (2600x2307x512 in bf16 28 us; 49 one after the other)
+        const int64_t size = e.f32 ? 4 : 2;
+        const uint8_t* p = static_cast<const uint8_t*>(e.residual) + at * size;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t p = at + (int64_t)i * e.n;
-            r[i] = !(on >> i & 1) ? 0.0f : e.f32 ? static_cast<const float*>(e.residual)[p] : bf16_f(static_cast<const uint16_t*>(e.residual)[p]);
+        for (int i = 0; i < 8; ++i, p += e.n * size) {
+            raw[i] = 0;
+            if (on >> i & 1) raw[i] = e.f32 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
         }
     }
 #pragma unroll
@@ -175,10 +178,11 @@ __device__ __forceinline__ uint32_t emit_cols(const Epilogue& e, Lane l, int64_t
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = in ? cvt_bf16x2(v[2 * i], v[2 * i + 1]) : 0u;
         uint32_t mine = 0;
+        uint8_t* h = e.h + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; ++i, h += e.n) {
             const uint32_t x = w[i >> 1] >> 16 * (i & 1) & 0xFFFFu, code = ckpt_scale(__reduce_max_sync(0xFFFFFFFFu, x & 0x7FFFu));
-            if (on >> i & 1) e.h[at + (int64_t)i * e.n] = (uint8_t)cvt_fp8x2<FP8Q_E4M3FN>(__uint_as_float(x << 16) * ckpt_factor(code), 0.0f);
+            if (on >> i & 1) *h = (uint8_t)cvt_fp8x2<FP8Q_E4M3FN>(__uint_as_float(x << 16) * ckpt_factor(code), 0.0f);
             if ((col & 31) == i) mine = code;
         }
         const uint32_t there = __shfl_sync(0xFFFFFFFFu, on, 0);  // the block's first column is there if any is
@@ -194,13 +198,13 @@ __device__ __forceinline__ uint32_t emit_cols(const Epilogue& e, Lane l, int64_t
     }
     if (e.residual) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
+        for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(e.f32 ? raw[i] : raw[i] << 16);
     }
     if (e.f32) {
         float* d = static_cast<float*>(e.d) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (on >> i & 1) d[(int64_t)i * e.n] = v[i];
+        for (int i = 0; i < 8; ++i, d += e.n)
+            if (on >> i & 1) *d = v[i];
         return l.m2;
     }
 #pragma unroll
@@ -212,17 +216,19 @@ __device__ __forceinline__ uint32_t emit_cols(const Epilogue& e, Lane l, int64_t
     if (e.d) {
         uint16_t* d = static_cast<uint16_t*>(e.d) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (on >> i & 1) d[(int64_t)i * e.n] = (uint16_t)(w[i >> 1] >> 16 * (i & 1));
+        for (int i = 0; i < 8; ++i, d += e.n)
+            if (on >> i & 1) *d = (uint16_t)(w[i >> 1] >> 16 * (i & 1));
     }
     if (e.q) {
+        uint32_t four[2];
+        if (e.e5m2)
+            four[0] = codes4<FP8Q_E5M2>(w[0], w[1], l.c), four[1] = codes4<FP8Q_E5M2>(w[2], w[3], l.c);
+        else
+            four[0] = codes4<FP8Q_E4M3FN>(w[0], w[1], l.c), four[1] = codes4<FP8Q_E4M3FN>(w[2], w[3], l.c);
+        uint8_t* q = e.q + at;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t four = e.e5m2 ? codes4<FP8Q_E5M2>(w[2 * j], w[2 * j + 1], l.c) : codes4<FP8Q_E4M3FN>(w[2 * j], w[2 * j + 1], l.c);
-#pragma unroll
-            for (int i = 4 * j; i < 4 * j + 4; ++i)
-                if (on >> i & 1) e.q[at + (int64_t)i * e.n] = (uint8_t)(four >> 8 * (i & 3));
-        }
+        for (int i = 0; i < 8; ++i, q += e.n)
+            if (on >> i & 1) *q = (uint8_t)(four[i >> 2] >> 8 * (i & 3));
     }
     return l.m2;
 }
@@ -822,7 +828,7 @@ __device__ __forceinline__ PairWhere pair_where(const ProductArgs& a, const int*
 
 //
 // ANY: n or an address is such that only emit_cols() holds.  A kernel of its own: with both in one, 2600x2308x0 with a residual
-// takes 28.5 us for 23.9, and with emit_cols() out of line 2600x2310x512 43 for 19.8.
+// takes 28.5 us for 23.9, and with emit_cols() out of line 2600x2310x512 43 for 18.6.
 template <bool RAGGED_K, bool ANY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
     fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const ProductArgs a) {
