@@ -599,7 +599,7 @@ fp8q_status fp8q_matmul(const fp8q_product* args, void* stream);
  * offsets: int32[groups + 1] (device), read by the kernel: they must not
  * decrease.  Any values are safe: one outside [0, m] counts as the bound, and a
  * group that would end before it starts is empty; rows that two groups hold
- * then get either's result.
+ * then get either's result (on a residual in place, possibly both's).
  * Errors: as for fp8q_matmul, and INVALID_ARG for groups < 0, NULL offsets or
  *         a_trans; UNSUPPORTED for groups > 512.  groups == 0 launches nothing.
  */
