@@ -558,6 +558,58 @@ __device__ __forceinline__ void emit_tile(const ProductArgs& a, TileLane& t, uin
     flush_lane(e, t.l);
 }
 
+// The rows of A of a tile, q0 < 0 for none.
+struct TileRows {
+    int q0, q_end, group;
+};
+
+// find_rows() below where offsets decrease.  Groups may overlap then and have more tiles than the grid has CTAs, so each gives up
+// the rows that a group which starts before it holds (of two that start together, the second): a row that any group holds stays with
+// one, and there are no more parts of tiles than groups.
+__device__ __noinline__ TileRows find_rows_apart(const int32_t* offsets, int groups, int rows, int tile_rows, int t) {
+    int before = 0;
+    for (int g = 0; g < groups; ++g) {
+        int lo = min(max(offsets[g], 0), rows), top = 0;
+        const int hi = min(offsets[g + 1], rows);
+        for (int h = 0; h < groups && lo < hi; ++h) {
+            const int from = min(max(offsets[h], 0), rows), to = min(offsets[h + 1], rows);
+            if (from < to && (from < lo || (from == lo && h < g))) top = max(top, to);
+        }
+        lo = max(lo, top);
+        const int here = lo < hi ? (hi - lo + tile_rows - 1) / tile_rows : 0;
+        if (t - before < here) return {lo + (t - before) * tile_rows, hi, g};
+        before += here;
+    }
+    return {-1, 0, 0};
+}
+
+// Those of the groups' t-th tile, by the whole warp.
+template <int BN>
+__device__ __forceinline__ TileRows find_rows(const ProductArgs& a, int t) {
+    const int lane = threadIdx.x & 31;
+    TileRows w = {-1, 0, 0};
+    int before = 0;
+    bool rise = true;
+    for (int g0 = 0; g0 < a.groups; g0 += 32) {
+        const int g = g0 + lane;
+        const int from = g < a.groups ? a.offsets[g] : 0, to = g < a.groups ? a.offsets[g + 1] : 0;
+        rise &= __all_sync(0xFFFFFFFFu, from <= to) != 0;
+        if (w.q0 >= 0) continue;
+        const int lo = min(max(from, 0), a.rows), hi = max(lo, min(to, a.rows));
+        const int upto = sums_upto((hi - lo + BN - 1) / BN);
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > t);
+        if (past) {
+            const int i = __ffs(past) - 1;
+            const int ahead = __shfl_sync(0xFFFFFFFFu, upto, i - (i > 0));  // tiles of the groups before, at most t - before
+            w.group = g0 + i;
+            w.q0 = __shfl_sync(0xFFFFFFFFu, lo, i) + (t - before - (i > 0 ? ahead : 0)) * BN;
+            w.q_end = __shfl_sync(0xFFFFFFFFu, hi, i);
+        }
+        before = min(before + __shfl_sync(0xFFFFFFFFu, upto, 31), kManyTiles);
+    }
+    return rise ? w : find_rows_apart(a.offsets, a.groups, a.rows, BN, t);
+}
+
 template <int BN>
 __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                                                          const ProductArgs a) {
@@ -589,37 +641,14 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     }
     __syncthreads();
     wait_behind();
-    int p0, q0, q_end = a.m, group = 0;
-    if (a.offsets) {
-        // this tile's group: tiles of B fastest, so that the tiles of a group's rows share its weights in L2
-        const int t = tile / a.p_tiles;
-        p0 = tile % a.p_tiles * 128;
-        int before = 0, g0 = 0;
-        bool found = false;
-        for (; g0 < a.groups; g0 += 32) {
-            int2 r = make_int2(0, 0);
-            if (g0 + lane < a.groups) r = group_rows(a, g0 + lane);
-            const int upto = sums_upto((r.y - r.x + BN - 1) / BN);
-            const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > t);
-            if (past) {
-                const int i = __ffs(past) - 1;
-                group = g0 + i;
-                const int ahead = __shfl_sync(0xFFFFFFFFu, upto, i - (i > 0));  // tiles of the groups before, at most t - before
-                q0 = __shfl_sync(0xFFFFFFFFu, r.x, i) + (t - before - (i > 0 ? ahead : 0)) * BN;
-                q_end = __shfl_sync(0xFFFFFFFFu, r.y, i);
-                found = true;
-                break;
-            }
-            before = min(before + __shfl_sync(0xFFFFFFFFu, upto, 31), kManyTiles);
-        }
-        if (!found) {  // the grid has room for a part of a tile in every group; the whole cluster ends here
-            let_next_start();
-            return;
-        }
-    } else {
-        p0 = tile / a.q_tiles * 128;
-        q0 = tile % a.q_tiles * BN;
+    // tiles of B fastest, so that the tiles of a group's rows share its weights in L2
+    const int p0 = (a.offsets ? tile % a.p_tiles : tile / a.q_tiles) * 128;
+    const TileRows w = a.offsets ? find_rows<BN>(a, tile / a.p_tiles) : TileRows{tile % a.q_tiles * BN, a.m, 0};
+    if (w.q0 < 0) {  // the grid has room for a part of a tile in every group; the whole cluster ends here
+        let_next_start();
+        return;
     }
+    const int q0 = w.q0, q_end = w.q_end, group = w.group;
     // this CTA's steps
     const int steps = (a.k + kStepK - 1) / kStepK;
     const int s0 = (int)((int64_t)steps * rank / a.split), s1 = (int)((int64_t)steps * (rank + 1) / a.split);
