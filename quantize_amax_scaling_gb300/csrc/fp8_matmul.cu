@@ -478,7 +478,8 @@ __device__ __forceinline__ float ld_shared_f(uint32_t at) {
 __device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 : 2; }
 
 // ----------------------------------------------------------------------------
-// Few tiles: one CTA a tile, 128 rows of B by BN of A
+// Few tiles: one CTA a tile, 128 rows of B by BN of A.  GROUPED: rows by expert, a kernel of its own (with both in one, what finds a
+// tile's group takes 0.1 us of one token's 14.4).
 
 template <int BN>
 struct PrGeom {
@@ -563,7 +564,7 @@ struct TileRows {
     int q0, q_end, group;
 };
 
-// find_rows() below where offsets decrease.  Groups may overlap then and have more tiles than the grid has CTAs, so each gives up
+// The groups' t-th tile where offsets decrease.  Groups may overlap then and have more tiles than the grid has CTAs, so each gives up
 // the rows that a group which starts before it holds (of two that start together, the second): a row that any group holds stays with
 // one, and there are no more parts of tiles than groups.
 __device__ __noinline__ TileRows find_rows_apart(const int32_t* offsets, int groups, int rows, int tile_rows, int t) {
@@ -583,34 +584,14 @@ __device__ __noinline__ TileRows find_rows_apart(const int32_t* offsets, int gro
     return {-1, 0, 0};
 }
 
-// Those of the groups' t-th tile, by the whole warp.
-template <int BN>
-__device__ __forceinline__ TileRows find_rows(const ProductArgs& a, int t) {
-    const int lane = threadIdx.x & 31;
-    TileRows w = {-1, 0, 0};
-    int before = 0;
-    bool rise = true;
-    for (int g0 = 0; g0 < a.groups; g0 += 32) {
-        const int g = g0 + lane;
-        const int from = g < a.groups ? a.offsets[g] : 0, to = g < a.groups ? a.offsets[g + 1] : 0;
-        rise &= __all_sync(0xFFFFFFFFu, from <= to) != 0;
-        if (w.q0 >= 0) continue;
-        const int lo = min(max(from, 0), a.rows), hi = max(lo, min(to, a.rows));
-        const int upto = sums_upto((hi - lo + BN - 1) / BN);
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > t);
-        if (past) {
-            const int i = __ffs(past) - 1;
-            const int ahead = __shfl_sync(0xFFFFFFFFu, upto, i - (i > 0));  // tiles of the groups before, at most t - before
-            w.group = g0 + i;
-            w.q0 = __shfl_sync(0xFFFFFFFFu, lo, i) + (t - before - (i > 0 ? ahead : 0)) * BN;
-            w.q_end = __shfl_sync(0xFFFFFFFFu, hi, i);
-        }
-        before = min(before + __shfl_sync(0xFFFFFFFFu, upto, 31), kManyTiles);
-    }
-    return rise ? w : find_rows_apart(a.offsets, a.groups, a.rows, BN, t);
+// Whether offsets decrease anywhere, by the whole warp.
+__device__ __forceinline__ bool offsets_fall(const ProductArgs& a) {
+    bool fall = false;
+    for (int g = threadIdx.x & 31; g < a.groups; g += 32) fall |= a.offsets[g] > a.offsets[g + 1];
+    return __any_sync(0xFFFFFFFFu, fall) != 0;
 }
 
-template <int BN>
+template <int BN, bool GROUPED>
 __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                                                          const ProductArgs a) {
     using G = PrGeom<BN>;
@@ -641,14 +622,42 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     }
     __syncthreads();
     wait_behind();
-    // tiles of B fastest, so that the tiles of a group's rows share its weights in L2
-    const int p0 = (a.offsets ? tile % a.p_tiles : tile / a.q_tiles) * 128;
-    const TileRows w = a.offsets ? find_rows<BN>(a, tile / a.p_tiles) : TileRows{tile % a.q_tiles * BN, a.m, 0};
-    if (w.q0 < 0) {  // the grid has room for a part of a tile in every group; the whole cluster ends here
-        let_next_start();
-        return;
+    int p0, q0, q_end = a.m, group = 0;
+    if (GROUPED) {
+        // this tile's group: tiles of B fastest, so that the tiles of a group's rows share its weights in L2
+        const int t = tile / a.p_tiles;
+        p0 = tile % a.p_tiles * 128;
+        int before = 0, g0 = 0;
+        bool found = false;
+        for (; g0 < a.groups; g0 += 32) {
+            int2 r = make_int2(0, 0);
+            if (g0 + lane < a.groups) r = group_rows(a, g0 + lane);
+            const int upto = sums_upto((r.y - r.x + BN - 1) / BN);
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > t);
+            if (past) {
+                const int i = __ffs(past) - 1;
+                group = g0 + i;
+                const int ahead = __shfl_sync(0xFFFFFFFFu, upto, i - (i > 0));  // tiles of the groups before, at most t - before
+                q0 = __shfl_sync(0xFFFFFFFFu, r.x, i) + (t - before - (i > 0 ? ahead : 0)) * BN;
+                q_end = __shfl_sync(0xFFFFFFFFu, r.y, i);
+                found = true;
+                break;
+            }
+            before = min(before + __shfl_sync(0xFFFFFFFFu, upto, 31), kManyTiles);
+        }
+        if (offsets_fall(a)) {
+            const TileRows w = find_rows_apart(a.offsets, a.groups, a.rows, BN, t);
+            q0 = w.q0, q_end = w.q_end, group = w.group;
+            found = q0 >= 0;
+        }
+        if (!found) {  // the grid has room for a part of a tile in every group; the whole cluster ends here
+            let_next_start();
+            return;
+        }
+    } else {
+        p0 = tile / a.q_tiles * 128;
+        q0 = tile % a.q_tiles * BN;
     }
-    const int q0 = w.q0, q_end = w.q_end, group = w.group;
     // this CTA's steps
     const int steps = (a.k + kStepK - 1) / kStepK;
     const int s0 = (int)((int64_t)steps * rank / a.split), s1 = (int)((int64_t)steps * (rank + 1) / a.split);
@@ -1218,10 +1227,10 @@ bool operand_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t k, in
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <int BN>
+template <int BN, bool GROUPED>
 fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, ProductArgs a, unsigned grid, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};
-    auto kern = fp8_matmul_kernel<BN>;
+    auto kern = fp8_matmul_kernel<BN, GROUPED>;
     const cudaError_t e = allow_smem(kern, PrGeom<BN>::kSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_kernel setup");
     // Stages of up to four steps, two stages or more: a stage's waits and its arrival take its issuers 150 cycles each, and
@@ -1369,11 +1378,12 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, 128) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
         return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_kernel tensor map");
     const unsigned grid = (unsigned)(tiles * split);
+    const bool grouped = how == kGroupedRows;
     switch (bn) {
-        case 16: return launch_product<16>(mp, mq, a, grid, s);
-        case 32: return launch_product<32>(mp, mq, a, grid, s);
-        case 64: return launch_product<64>(mp, mq, a, grid, s);
-        default: return launch_product<128>(mp, mq, a, grid, s);
+        case 16: return grouped ? launch_product<16, true>(mp, mq, a, grid, s) : launch_product<16, false>(mp, mq, a, grid, s);
+        case 32: return grouped ? launch_product<32, true>(mp, mq, a, grid, s) : launch_product<32, false>(mp, mq, a, grid, s);
+        case 64: return grouped ? launch_product<64, true>(mp, mq, a, grid, s) : launch_product<64, false>(mp, mq, a, grid, s);
+        default: return grouped ? launch_product<128, true>(mp, mq, a, grid, s) : launch_product<128, false>(mp, mq, a, grid, s);
     }
 }
 
