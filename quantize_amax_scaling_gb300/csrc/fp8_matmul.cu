@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
         const int row = q0 + rank * (BN / a.split) + (int)threadIdx.x;  // the residual on its way to L2
         if (a.e.residual && a.e.wide && (int)threadIdx.x < BN / a.split && row < q_end)
             block_prefetch(static_cast<const uint8_t*>(a.e.residual) + ((int64_t)row * a.e.n + p0) * (a.e.f32 ? 4 : 2), min(128, a.e.n - p0) * (a.e.f32 ? 4 : 2));
-        if (!mbar_wait_warp(&done, 0, 0) || pr_made_to_fail(a, kPrOutDone, 0)) gave_up = 1;
+        if (!(mbar_wait_warp(&done, 0, 0) || mbar_wait_on(&done, 0, empty, stages)) || pr_made_to_fail(a, kPrOutDone, 0)) gave_up = 1;
     }
     __syncwarp();
     __syncthreads();
@@ -1106,7 +1106,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                 const int q = w.q0 + (warp >> 2) * 128, there = min(128, e.n - q), size = e.f32 ? 4 : 2;
                 if (there > 0) block_prefetch(static_cast<const uint8_t*>(e.residual) + ((d_first + lane) * e.n + q) * size, there * size);
             }
-            ok = ok && mbar_wait_warp(&done[set], (it >> 1) & 1, 32) && !pr_made_to_fail(a, kPrOutDone, it);
+            ok = ok && (mbar_wait_warp(&done[set], (it >> 1) & 1, 32) || mbar_wait_on(&done[set], (it >> 1) & 1, empty, kPrPairStages)) &&
+                 !pr_made_to_fail(a, kPrOutDone, it);
             if (!ok) gave_up = 1;
             tc_fence_after();
 #pragma unroll 1

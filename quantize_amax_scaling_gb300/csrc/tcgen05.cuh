@@ -28,6 +28,25 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
     return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
+// For a wait that lasts as long as a loop over `stages` barriers does, once mbar_wait_warp() has given up: goes on while one of them
+// completes a phase within the limit.  Out of line, and with no count kept by the loop itself: a word in shared memory for each of
+// its steps took 1% of 8192x16384x4096.
+__device__ __noinline__ bool mbar_wait_on(uint64_t* bar, uint32_t parity, uint64_t* loop, uint32_t stages) {
+    uint32_t ok = 0;
+    if ((threadIdx.x & 31) == 0) {
+        WaitClock clock;
+        uint32_t seen = 0;
+        while (!(ok = mbar_try(bar, parity))) {
+            uint32_t now = 0;
+            for (uint32_t i = 0; i < stages; ++i) now |= (uint32_t)mbar_test(&loop[i], 0) << i;
+            if (now != seen) clock = WaitClock();
+            seen = now;
+            if (!clock.more()) break;
+        }
+    }
+    return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
 // mbar_wait() where each lane looks, with one verdict for the warp: every lane's
 // clock runs out for itself, and a warp of which some lanes went on and some
 // left would never come together again at the warp-wide instructions behind
