@@ -55,6 +55,23 @@ __device__ __forceinline__ bool mbar_wait_all(uint64_t* bar, uint32_t parity, bo
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity) && !fail_lane);
 }
 
+// The same for a barrier at which the cluster's other CTA arrives for what it has in its own shared memory (arrive_cluster_release()).
+__device__ __forceinline__ bool mbar_wait_all_cluster(uint64_t* bar, uint32_t parity, bool fail_lane = false) {
+    WaitClock clock;
+    uint32_t done;
+    for (;;) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done || !clock.more()) break;
+    }
+    return __all_sync(0xFFFFFFFFu, done && !fail_lane);
+}
+
 // One lane of a converged warp.  The warps that issue copies and multiply-adds
 // run their loops whole and let one lane issue: addresses and descriptors then
 // stay in uniform registers, and a step costs its issuer tens of cycles, not
@@ -278,7 +295,8 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
     return v;
 }
 
-// arrive_cluster() that orders this thread's stores to shared memory as well.
+// arrive_cluster() for what this CTA has in shared memory, copied there or stored: it happens before what follows
+// mbar_wait_all_cluster() in the other CTA.
 __device__ __forceinline__ void arrive_cluster_release(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
