@@ -170,6 +170,15 @@ void one(const at::Tensor* t, const char* name) {
     if (t && t->numel() != 1) Args::refuse("%s must have one element", name);
 }
 
+// Codes in a tensor whose type names another format than the call's argument does.
+void format(const at::Tensor* t, int64_t fmt, const char* name, const char* arg) {
+    if (!t) return;
+    const at::ScalarType s = t->scalar_type();
+    if (!(s == at::kFloat8_e4m3fn && fmt == FP8Q_E5M2) && !(s == at::kFloat8_e5m2 && fmt == FP8Q_E4M3FN)) return;
+    PyErr_Format(PyExc_ValueError, "%s has dtype %s but %s is %s", name, c10::toString(s), arg, fmt == FP8Q_E5M2 ? "E5M2" : "E4M3FN");
+    throw Refused();
+}
+
 void packed(const at::Tensor* q, const at::Tensor* sf, int64_t rows, int64_t cols, int64_t fmt, const char* name) {
     if (q && sf && q->numel() == rows * row_bytes(cols) && sf->numel() == scale_bytes(rows, cols, fmt)) return;
     PyErr_Format(PyExc_ValueError, "%s is not a packed operand of [%lld, %lld]: see fp4_empty", name, (long long)rows, (long long)cols);
@@ -385,6 +394,10 @@ int64_t product(PyObject* const* v, Py_ssize_t n) {
     one(qs, "q_scale");
     one(amax, "amax");
     if (residual && residual->scalar_type() != (d ? d->scalar_type() : at::kBFloat16)) Args::refuse("%s must have d's type", "residual");
+    format(x, p.a_fmt, "a", "a_fmt");
+    format(w, p.b_fmt, "b", "b_fmt");
+    format(q, p.q_fmt, "q", "q_fmt");
+    format(h, FP8Q_E4M3FN, "h", "a checkpoint");
     p.a = bytes(x);
     p.b = bytes(w);
     p.a_scale = floats(sa);
@@ -424,6 +437,8 @@ int64_t grouped_gradient(PyObject* const* v, Py_ssize_t n) {
     if (residual && residual->scalar_type() != d->scalar_type()) Args::refuse("%s must have d's type", "residual");
     one(sa, "a_scale");
     one(sb, "b_scale");
+    format(x, p.a_fmt, "a", "a_fmt");
+    format(w, p.b_fmt, "b", "b_fmt");
     p.a = bytes(x);
     p.b = bytes(w);
     p.a_trans = p.b_trans = 1;
@@ -446,6 +461,7 @@ int64_t checkpoint(PyObject* const* v, Py_ssize_t n) {
     if (!q || !sf) Args::refuse("%s must be a checkpoint: see checkpoint_empty", "(q, sf)");
     shaped(q, rows * cols, "q", "[rows, cols]");
     shaped(sf, rows * ((cols + 31) / 32), "sf", "[rows, ceil(cols / 32)]");
+    format(q, FP8Q_E4M3FN, "q", "a checkpoint");
     return BACK ? launch(g_checkpoint_back, bytes(q), bytes(sf), ptr(x), rows, cols, a.stream())
                 : launch(g_checkpoint, ptr(x), bytes(q), bytes(sf), rows, cols, a.stream());
 }
@@ -467,6 +483,8 @@ int64_t gelu_backward(PyObject* const* v, Py_ssize_t n) {
     shaped(db, g.cols, "d_bias", "[cols]");
     one(scale, "scale");
     one(amax, "amax");
+    format(h, FP8Q_E4M3FN, "h", "a checkpoint");
+    format(q, g.fmt, "q", "fmt");
     g.d_y = ptr(dy);
     g.h = bytes(h);
     g.h_sf = bytes(hs);

@@ -531,6 +531,7 @@ def fp8q_matmul(a, b, d=None, a_fmt=E4M3FN, b_fmt=E4M3FN, a_scale=None, b_scale=
     ``d`` is bf16 or float32; beside it or in its place q = FP8(bf16 result / q_scale), amax = max(amax, max|bf16
     result|), and (h, h_sf), the checkpoint of what ``act`` is applied to.  ``bias`` is float32 or bf16 [n];
     ``residual`` has d's type (bf16 without d) and may be d.
+    Codes are uint8 of either format, or of the float8 type that the call's format names.
     """
     st = _native().matmul(a, b, d, a_fmt, b_fmt, a_scale, b_scale, a_trans, b_trans, bias, act, residual, q, q_fmt, q_scale,
                           amax, h, h_sf, stream)
