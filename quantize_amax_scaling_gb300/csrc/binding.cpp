@@ -350,9 +350,11 @@ int64_t norm_backward(PyObject* const* v, Py_ssize_t n) {
     return launch(g_norm_backward, &g, a.stream());
 }
 
-void shaped(const at::Tensor* t, int64_t n, const char* name, const char* shape) {
-    if (!t || t->numel() == n) return;
-    PyErr_Format(PyExc_ValueError, "%s must be %s (%lld elements)", name, shape, (long long)n);
+// n elements in rows of `last`: their number alone would let a transposed result pass, to be filled in the wrong order.  Dimensions
+// ahead of the last may be split or flattened together, and so may all.
+void shaped(const at::Tensor* t, int64_t n, int64_t last, const char* name, const char* shape) {
+    if (!t || (t->numel() == n && (n == 0 || t->dim() < 2 || t->size(-1) == last))) return;
+    PyErr_Format(PyExc_ValueError, "%s must be %s (%lld elements in rows of %lld)", name, shape, (long long)n, (long long)last);
     throw Refused();
 }
 
@@ -383,12 +385,12 @@ int64_t product(PyObject* const* v, Py_ssize_t n) {
         throw Refused();
     }
     if (GROUPED && (!offsets || offsets->numel() != groups + 1)) Args::refuse("%s must have one element more than b has matrices", "offsets");
-    shaped(d, p.m * p.n, "d", "[m, n]");
-    shaped(residual, p.m * p.n, "residual", "[m, n]");
-    shaped(q, p.m * p.n, "q", "[m, n]");
-    shaped(h, p.m * p.n, "h", "[m, n]");
-    shaped(hs, p.m * ((p.n + 31) / 32), "h_sf", "[m, ceil(n / 32)]");
-    shaped(bias, groups * p.n, "bias", GROUPED ? "[groups, n]" : "[n]");
+    shaped(d, p.m * p.n, p.n, "d", "[m, n]");
+    shaped(residual, p.m * p.n, p.n, "residual", "[m, n]");
+    shaped(q, p.m * p.n, p.n, "q", "[m, n]");
+    shaped(h, p.m * p.n, p.n, "h", "[m, n]");
+    shaped(hs, p.m * ((p.n + 31) / 32), (p.n + 31) / 32, "h_sf", "[m, ceil(n / 32)]");
+    shaped(bias, groups * p.n, p.n, "bias", GROUPED ? "[groups, n]" : "[n]");
     one(sa, "a_scale");
     one(sb, "b_scale");
     one(qs, "q_scale");
@@ -433,7 +435,8 @@ int64_t grouped_gradient(PyObject* const* v, Py_ssize_t n) {
     if (w->size(0) != p.k) Args::refuse("%s must have as many rows as a", "b");
     if (d->size(1) != p.m || d->size(2) != p.n) Args::refuse("%s must be [groups, m, n]", "d");
     if (!offsets || offsets->numel() != groups + 1) Args::refuse("%s must have one element more than d has matrices", "offsets");
-    shaped(residual, groups * p.m * p.n, "residual", "[groups, m, n]");
+    shaped(residual, groups * p.m * p.n, p.n, "residual", "[groups, m, n]");
+    if (residual && residual->dim() == 3 && residual->sizes() != d->sizes()) Args::refuse("%s must be [groups, m, n]", "residual");
     if (residual && residual->scalar_type() != d->scalar_type()) Args::refuse("%s must have d's type", "residual");
     one(sa, "a_scale");
     one(sb, "b_scale");
@@ -459,8 +462,8 @@ int64_t checkpoint(PyObject* const* v, Py_ssize_t n) {
     if (BACK) x = a.tensor(kBf16, "y", "[rows, cols]");
     const int64_t rows = x->size(0), cols = x->size(1);
     if (!q || !sf) Args::refuse("%s must be a checkpoint: see checkpoint_empty", "(q, sf)");
-    shaped(q, rows * cols, "q", "[rows, cols]");
-    shaped(sf, rows * ((cols + 31) / 32), "sf", "[rows, ceil(cols / 32)]");
+    shaped(q, rows * cols, cols, "q", "[rows, cols]");
+    shaped(sf, rows * ((cols + 31) / 32), (cols + 31) / 32, "sf", "[rows, ceil(cols / 32)]");
     format(q, FP8Q_E4M3FN, "q", "a checkpoint");
     return BACK ? launch(g_checkpoint_back, bytes(q), bytes(sf), ptr(x), rows, cols, a.stream())
                 : launch(g_checkpoint, ptr(x), bytes(q), bytes(sf), rows, cols, a.stream());
@@ -476,11 +479,11 @@ int64_t gelu_backward(PyObject* const* v, Py_ssize_t n) {
                      *db = a.tensor(kF32, "d_bias"), *space = a.tensor(kByte, "workspace");
     g.rows = dy->size(0);
     g.cols = dy->size(1);
-    shaped(h, g.rows * g.cols, "h", "[rows, cols]");
-    shaped(hs, g.rows * ((g.cols + 31) / 32), "h_sf", "[rows, ceil(cols / 32)]");
-    shaped(q, g.rows * g.cols, "q", "[rows, cols]");
-    shaped(dx, g.rows * g.cols, "d_x", "[rows, cols]");
-    shaped(db, g.cols, "d_bias", "[cols]");
+    shaped(h, g.rows * g.cols, g.cols, "h", "[rows, cols]");
+    shaped(hs, g.rows * ((g.cols + 31) / 32), (g.cols + 31) / 32, "h_sf", "[rows, ceil(cols / 32)]");
+    shaped(q, g.rows * g.cols, g.cols, "q", "[rows, cols]");
+    shaped(dx, g.rows * g.cols, g.cols, "d_x", "[rows, cols]");
+    shaped(db, g.cols, g.cols, "d_bias", "[cols]");
     one(scale, "scale");
     one(amax, "amax");
     format(h, FP8Q_E4M3FN, "h", "a checkpoint");
