@@ -622,8 +622,10 @@ fp8q_status fp8q_grouped_weight_gradient(const fp8q_product* args, const int32_t
  * block, its scale is 2^e with the least e >= -127 for which a <= 448 * 2^e, kept
  * as the byte e + 127; code = e4m3(x / 2^e), the quotient exact.  So a value is
  * off by at most 2^-4 of itself, or 2^(e - 10) where that is more.  An infinity
- * counts as the largest finite bf16 in a and comes back as an infinity; a NaN in
- * the block makes its scale NaN (0xFF).
+ * counts as the largest finite bf16 in a and comes back as an infinity, and so do
+ * the eight finite bf16 from 248 * 2^120 on (0x7F78 to 0x7F7F, and their
+ * negatives): their code is that of 256, and 256 * 2^120 is beyond binary32.  A
+ * NaN in the block makes its scale NaN (0xFF).
  * q: [rows, cols] bytes, sf: fp8q_checkpoint_scale_bytes, [rows, ceil(cols / 32)]
  * bytes, both contiguous, from any address; on 16-byte and 4-byte boundaries, with
  * x_bf16 on a 32-byte one and cols a multiple of 16, they take the vectorised path.

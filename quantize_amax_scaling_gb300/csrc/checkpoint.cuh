@@ -7,7 +7,8 @@
 // The power of two makes the quotient exact, so a value is rounded once, by half a
 // step of e4m3 (2^-4 of it, or 2^-10 2^e where that is more).  The scale's byte is
 // e + 127; 255, NaN, where the block holds a NaN.  An infinity comes back as one
-// (448 2^120 is beyond binary32).
+// (448 2^120 is beyond binary32), and so does a finite value from 248 2^120 on, whose
+// code is 256's.
 //
 // Codes are [rows, cols] bytes, scales [rows, ceil(cols / 32)] bytes, both row-major.
 
