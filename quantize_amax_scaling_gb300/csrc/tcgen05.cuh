@@ -234,7 +234,8 @@ __host__ __device__ constexpr uint32_t mma_desc_fp8(uint32_t m, uint32_t n, uint
 // The same with another number of columns.
 __device__ __forceinline__ uint32_t mma_desc_cols(uint32_t idesc, uint32_t n) { return (idesc & ~(63u << 17)) | (n >> 3) << 17; }
 
-// d (+)= A B^T over 32 FP8 codes.
+// d (+)= A B^T over 32 FP8 codes.  Sums are binary32, but what lies below the last place of the largest addend is cut off, not
+// rounded: 8e-8 to 2.4e-7 of the results' root mean square over a k of 4096, three times what additions that round leave.
 template <int PAIR>
 __device__ __forceinline__ void tc_mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
 #define FP8Q_MMA(group)                                                                                   \
