@@ -14,10 +14,13 @@
 // cluster while every CTA is resident; what bounds them is the operands' way from
 // HBM and 4 us until it flows and the sums are out: 1 x 16384 x 4096 (67 MB) 14.1 us,
 // 1 x 1024 x 4096 4.6; each megabyte more costs 0.15 us, 6.7 TB/s.  Many tiles: pairs
-// of CTAs with 256 x 256.  8192 x 16384 x 4096 takes 294 to 300 us in a burst, 3.7
-// PFLOP/s, and 325 in a loop at the 1400 W limit; with zeros for operands, which
-// cost little power, 239 us, 4.6 PFLOP/s, the multiply-adds' own 128 cycles for
-// 256 x 256 x 32 at 2070 MHz.  So the tensor cores' power bounds it, not their feeding.
+// of CTAs with 256 x 256.  8192 x 16384 x 4096 is 27 rounds of tiles, 442 thousand
+// cycles of multiply-adds (128 for 256 x 256 x 32): 214 us at 2070 MHz.  It takes 294
+// to 301 us in a burst, 3.7 PFLOP/s, and 325 to 347 in a loop at the 1400 W limit,
+// where the clock falls to 1345 MHz: 466 thousand cycles, 95% of them multiply-adds.
+// With zeros for operands (940 W, 2070 MHz) 239 to 255 us, 4.6 to 4.3 PFLOP/s: at
+// that clock a tenth to a sixth goes to feeding them, to the start and to the end.
+// So power bounds it first, their feeding next.
 // Sums go out four columns of a row a lane (emit_rows), in pairs a row a lane
 // (emit_row32), and a column a lane where n or an address holds no vectors
 // (emit_cols); rows and columns beyond a group's or the matrix's edge are left out.
@@ -879,7 +882,7 @@ __device__ __forceinline__ PairWhere pair_where(const ProductArgs& a, const int*
 }
 
 //
-// ANY: n or an address is such that only emit_cols() holds.  A kernel of its own: with both in one, 2600x2308x0 with a residual
+// ANY: n or an address is such that only emit_cols() holds.  A kernel of its own (80 registers, of which it spills 40 bytes): with both in one, 2600x2308x0 with a residual
 // takes 28.5 us for 23.9, and with emit_cols() out of line 2600x2310x512 43 for 18.6.
 template <bool RAGGED_K, bool ANY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
