@@ -548,15 +548,16 @@ fp8q_status fp8q_residual_norm_backward(const fp8q_residual_norm_grad* args, voi
  * are held in binary32 by the tensor cores, which cut off, towards zero, what
  * lies below a sum's last place, once for 32 of k at most: measured, of the
  * results' root mean square, 3e-8 at k = 512, 1e-7 to 2.4e-7 at 4096 and 6e-7
- * to 1.5e-6 at 16384.  The rest is binary32, rounded to nearest, with the GELU
- * (tanh form) within 2^-16 of its value (2^-18 from z = -5 on; below z = -10,
- * where it is near 0, within 2^-100; NaN at -infinity, as in
- * fp8q_gelu_quantize_amax, whose bits are its own: these are not those).  Calls
- * with the same arguments give the same bits.  With k == 0 the sums are zeros
- * and a and b may be NULL.
+ * to 1.5e-6 at 16384; a longer k goes by parts of 8192 whose sums are added
+ * rounded to nearest, 6e-7 at any length.  The rest is binary32, rounded to
+ * nearest, with the GELU (tanh form) within 2^-16 of its value (2^-18 from z =
+ * -5 on; below z = -10, where it is near 0, within 2^-100; NaN at -infinity, as
+ * in fp8q_gelu_quantize_amax, whose bits are its own: these are not those).
+ * Calls with the same arguments give the same bits.  With k == 0 the sums are
+ * zeros and a and b may be NULL.
  * A wait inside the kernel that runs out, which only a fault elsewhere could
- * cause (one for a tile's sums lasts as long as its steps go on), ends the
- * kernel and shows as NaN in what it had not finished.
+ * cause (none has to last as long as a long k does), ends the kernel and shows
+ * as NaN in what it had not finished.
  */
 typedef enum {
     FP8Q_ACT_NONE = 0,

@@ -33,6 +33,9 @@ namespace {
 constexpr int kStepK = 128;       // codes of k a step
 constexpr int kBoxBytes = 16384;  // of 128 x 128 codes
 constexpr int kMaxGroups = 512;
+// A k of more than kLongSteps goes by parts of kPartSteps (a multiple of every stage's steps): sum_parts().
+constexpr int kPartSteps = 64, kLongSteps = 128;
+constexpr int kPartK = kPartSteps * kStepK, kLongK = kLongSteps * kStepK;
 
 struct Epilogue {
     const float *sa, *sb;
@@ -480,13 +483,67 @@ __device__ __forceinline__ float ld_shared_f(uint32_t at) {
     return v;
 }
 
+// A long k goes by parts, each with one of two sets of accumulators, and the parts' sums are added here, rounded to nearest: the tensor
+// cores cut off, towards zero, what lies below a sum's last place, and in one part the errors grow faster than k does.  Root mean
+// square of the errors over that of the results, for activations with a few large channels: k = 4096 2.4e-7, 8192 5.8e-7, 16384
+// 1.4e-6, 32768 3.7e-6 and by parts of 8192 5.8e-7, 100000 rows of a weight gradient 1.3e-5 and 4.6e-7, a million 3e-4 and 5e-7.
+// By parts 4096x4096x32768 takes 348 us, 325 without, 512x4096x65536 129 and 120, 200000 rows of two experts to 512x512 238 and 216:
+// the sums go through local memory, which meets the operands on their way out of shared memory.  (In registers, 128 of them, they
+// make the epilogue spill: 16384 rows of 8 experts on top of a residual 180 us for 123; in shared memory with a stage less 253 for
+// 216.)  Parts of 4096 from 8192 on halve the errors for twice the cost: 8192x4096x16384 343 us for 301.  So k up to 16384 is one part.
+// By a warp, for COLS columns of its 32 lanes from `at` on in the first set, those of the second `gap` behind.  The whole sums come to
+// lie where the last part's were.  first: the sets used before; done, drained: of both sets (PAIR: drained is the first CTA's).
+template <int COLS, bool PAIR>
+__device__ __forceinline__ bool sum_parts(uint32_t at, uint32_t gap, uint32_t first, int parts, uint64_t* done, uint64_t* drained, bool ok) {
+    alignas(16) float sum[COLS];
+    for (int j = 0; j < parts; ++j) {
+        const uint32_t set = (first + j) & 1, parity = ((first + j) >> 1) & 1, from = at + set * gap;
+        ok = ok && mbar_wait_warp(&done[set], parity, 32);
+        tc_fence_after();
+        constexpr int kAt = COLS < 32 ? COLS : 32;
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += kAt) {
+            float4* const held = reinterpret_cast<float4*>(sum + c);
+            float4 y[kAt / 4];
+#pragma unroll
+            for (int i = 0; i < kAt / 4; ++i) y[i] = j ? held[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float v[kAt];
+            if constexpr (kAt == 32)
+                tmem_load32(from + c, v);
+            else
+                tmem_load16(from + c, v);
+#pragma unroll
+            for (int i = 0; i < kAt; i += 4) v[i] += y[i / 4].x, v[i + 1] += y[i / 4].y, v[i + 2] += y[i / 4].z, v[i + 3] += y[i / 4].w;
+            if (j + 1 < parts) {
+#pragma unroll
+                for (int i = 0; i < kAt; i += 4) held[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kAt; i += 16) tmem_store16(from + c + i, v + i);
+            }
+        }
+        if (j + 1 < parts) {
+            tc_fence_before();
+            if ((threadIdx.x & 31) == 0) {
+                if (PAIR)
+                    arrive_cluster(in_cluster(smem_addr(&drained[set]), 0));
+                else
+                    arrive_local(&drained[set]);
+            }
+            __syncwarp();
+        }
+    }
+    tmem_stored();
+    return ok;
+}
+
 // A box of codes: 128 bytes along k by 128 rows, or 128 rows by 128 lines of k.  The multiply-adds of a step read 32 of k at
 // a time, 32 bytes on in a line or 32 lines on.
 __device__ __forceinline__ uint64_t k_advance(int across) { return across ? 256 : 2; }
 
 // ----------------------------------------------------------------------------
 // Few tiles: one CTA a tile, 128 rows of B by BN of A.  GROUPED: rows by expert, a kernel of its own (with both in one, what finds a
-// tile's group takes 0.1 us of one token's 14.4).
+// tile's group takes 0.1 us of one token's 14.4).  LONG: k may be so long that it goes by parts; with GROUPED, for either.
 
 template <int BN>
 struct PrGeom {
@@ -598,12 +655,12 @@ __device__ __forceinline__ bool offsets_fall(const ProductArgs& a) {
     return __any_sync(0xFFFFFFFFu, fall) != 0;
 }
 
-template <int BN, bool GROUPED>
+template <int BN, bool GROUPED, bool LONG>
 __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                                                          const ProductArgs a) {
     using G = PrGeom<BN>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[G::kMaxStages], empty[G::kMaxStages], done;
+    __shared__ uint64_t full[G::kMaxStages], empty[G::kMaxStages], done[2], drained[2];
     __shared__ uint32_t tmem_slot, loads;
     __shared__ int gave_up;
     const uint32_t stages = a.stages, boxes = kBoxBytes + (a.q_across ? kBoxBytes : BN * kStepK), stage_bytes = a.per * boxes;
@@ -621,7 +678,10 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             mbar_init(&full[i]);
             mbar_init(&empty[i]);
         }
-        mbar_init(&done);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i]);
+            mbar_init_count(&drained[i], 4);
+        }
         loads = 0;
         gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -630,7 +690,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     __syncthreads();
     wait_behind();
     int p0, q0, q_end = a.m, group = 0;
-    if (GROUPED) {
+    if (GROUPED && (!LONG || a.offsets)) {
         // this tile's group: tiles of B fastest, so that the tiles of a group's rows share its weights in L2
         const int t = tile / a.p_tiles;
         p0 = tile % a.p_tiles * 128;
@@ -668,8 +728,10 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     // this CTA's steps
     const int steps = (a.k + kStepK - 1) / kStepK;
     const int s0 = (int)((int64_t)steps * rank / a.split), s1 = (int)((int64_t)steps * (rank + 1) / a.split);
+    const int parts = LONG && s1 - s0 > kLongSteps ? (s1 - s0 + kPartSteps - 1) / kPartSteps : 1;
+    const uint32_t cols = LONG ? 2 * G::kCols : G::kCols;
     if (warp == 5) {
-        tmem_alloc<1>(&tmem_slot, G::kCols);
+        tmem_alloc<1>(&tmem_slot, cols);
         let_next_start();
     }
     const int col = p0 + lane * 4;
@@ -715,10 +777,21 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             loads = n;
         }
     } else if (warp == 5) {
-        uint32_t st = 0, round = 0;
+        uint32_t st = 0, round = 0, part = 0, to = tmem;
         bool ok = true;
         const uint64_t next_p = k_advance(a.p_across), next_q = k_advance(a.q_across);
         for (int s = s0, n = 0; s < s1; s += a.per, ++n) {
+            if (LONG && parts > 1 && (s - s0) % kPartSteps == 0 && s > s0) {  // the next part; stages hold 1, 2 or 4 steps
+                if (elect_lane()) tc_commit(&done[part & 1]);
+                __syncwarp();
+                ++part;
+                to = tmem + (part & 1) * G::kCols;
+                if (part > 1 && !pr_wait(a, kPrSumDrained, part, &drained[part & 1], ((part >> 1) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+            }
             if (!pr_wait(a, kPrSumFull, n, &full[st], round & 1)) {
                 ok = false;
                 break;
@@ -732,7 +805,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
                     const uint64_t dp = desc_codes(at), dq = desc_codes(at + kBoxBytes);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < nk) tc_mma_fp8<1>(tmem, dp + i * next_p, dq + i * next_q, a.idesc, (k - s0 * kStepK) | i);
+                        if (i < nk) tc_mma_fp8<1>(to, dp + i * next_p, dq + i * next_q, a.idesc, (LONG && parts > 1 ? (k - s0 * kStepK) % kPartK : k - s0 * kStepK) | i);
                 }
                 tc_commit(&empty[st]);
             }
@@ -740,7 +813,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
             if (++st == stages) st = 0, ++round;
         }
         if (elect_lane()) {
-            tc_commit(&done);
+            tc_commit(&done[part & 1]);
             if (!ok) gave_up = 1;
         }
     } else {
@@ -748,7 +821,9 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
         const int row = q0 + rank * (BN / a.split) + (int)threadIdx.x;  // the residual on its way to L2
         if (a.e.residual && a.e.wide && (int)threadIdx.x < BN / a.split && row < q_end)
             block_prefetch(static_cast<const uint8_t*>(a.e.residual) + ((int64_t)row * a.e.n + p0) * (a.e.f32 ? 4 : 2), min(128, a.e.n - p0) * (a.e.f32 ? 4 : 2));
-        if (!(mbar_wait_warp(&done, 0, 0) || mbar_wait_on(&done, 0, empty, stages)) || pr_made_to_fail(a, kPrOutDone, 0)) gave_up = 1;
+        const bool ok = parts > 1 ? sum_parts<BN, false>(tmem + ((uint32_t)(warp * 32) << 16), G::kCols, 0, parts, done, drained, true)
+                                  : mbar_wait_warp(&done[0], 0, 0);
+        if (!ok || pr_made_to_fail(a, kPrOutDone, 0)) gave_up = 1;
     }
     __syncwarp();
     __syncthreads();
@@ -763,7 +838,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
     // shows as NaN in the whole tile
     if (warp < 4) {
         float* part = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
-        const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t row = tmem + ((uint32_t)(warp * 32) << 16) + ((parts - 1) & 1) * G::kCols;
 #pragma unroll 1
         for (int c = 0; c < BN; c += 16) {
             float v[16] = {};
@@ -787,7 +862,7 @@ __global__ void __launch_bounds__(192) fp8_matmul_kernel(const __grid_constant__
         }
         cluster_sync_all();  // no CTA's sums go away while another reads them
     }
-    if (warp == 5) tmem_free<1>(tmem, G::kCols);
+    if (warp == 5) tmem_free<1>(tmem, cols);
 }
 
 // ----------------------------------------------------------------------------
@@ -882,9 +957,10 @@ __device__ __forceinline__ PairWhere pair_where(const ProductArgs& a, const int*
 }
 
 //
-// ANY: n or an address is such that only emit_cols() holds.  A kernel of its own (80 registers, of which it spills 40 bytes): with both in one, 2600x2308x0 with a residual
-// takes 28.5 us for 23.9, and with emit_cols() out of line 2600x2310x512 43 for 18.6.
-template <bool RAGGED_K, bool ANY>
+// ANY: n or an address is such that only emit_cols() holds.  A kernel of its own (80 registers, and 40 bytes spilled): with both in
+// one, 2600x2308x0 with a residual takes 28.5 us for 23.9, and with emit_cols() out of line 2600x2310x512 43 for 18.6.  LONG: k may be
+// so long that it goes by parts.
+template <bool RAGGED_K, bool ANY, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
     fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const ProductArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -1007,13 +1083,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
             const uint64_t next_p = k_advance(a.p_across), next_q = k_advance(a.q_across);
             for (int tile = first; tile < tiles && ok; tile += stride, ++it) {
                 const PairWhere w = pair_where<RAGGED_K>(a, cum, tile);
-                const uint32_t set = it & 1, to = tmem + set * 256, idesc = mma_desc_cols(a.idesc, w.cols);
+                const uint32_t idesc = mma_desc_cols(a.idesc, w.cols);
+                uint32_t set = it & 1, to = tmem + set * 256;
                 if (it > 1 && !pr_wait(a, kPrSumDrained, it, &drained[set], ((it >> 1) - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 for (int k = 0; k < w.k; k += kStepK, ++n) {
+                    if (LONG && w.k > kLongK && k % kPartK == 0 && k > 0) {  // the next part
+                        if (elect_lane()) tc_commit_pair(&done[set], 3);
+                        __syncwarp();
+                        set = ++it & 1, to = tmem + set * 256;
+                        if (it > 1 && !pr_wait(a, kPrSumDrained, it, &drained[set], ((it >> 1) - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
                     if (!(group_ends<RAGGED_K>(w.k - k) ? pr_wait_cluster(a, kPrSumFull, n, &full[st], round & 1) : pr_wait(a, kPrSumFull, n, &full[st], round & 1))) {
                         ok = false;
                         break;
@@ -1025,7 +1112,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                     if (elect_lane()) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (i < nk) tc_mma_fp8<2>(to, dp + i * next_p, dq + i * next_q, idesc, k | i);
+                            if (i < nk) tc_mma_fp8<2>(to, dp + i * next_p, dq + i * next_q, idesc, (LONG && w.k > kLongK ? k % kPartK : k) | i);
                         tc_commit_pair(&empty[st], 3);
                     }
                     __syncwarp();
@@ -1057,7 +1144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                 for (int k = 0; k < w.k; k += kStepK, ++n) {
                     const int there = w.k - k, upto = (there + 31) & ~31;  // lines of the group, and those that are multiplied
                     const bool ends = group_ends<RAGGED_K>(there);
-                    // all steps of the group go by meanwhile
+                    // all steps of the group go by meanwhile, which may take longer than a wait
                     if (pr_made_to_fail(a, kPrMaskFull, n) ||
                         (ends && !mbar_wait_warp(&landed[st], phase >> st & 1, 32) && !mbar_wait_on(&landed[st], phase >> st & 1, empty, kPrPairStages))) {
                         ok = false;
@@ -1126,6 +1213,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
         for (int tile = first; tile < tiles; tile += stride, ++it, w = then) {
             const bool more = tile + stride < tiles;
             if (more) then = pair_where<RAGGED_K>(a, cum, tile + stride);
+            const int parts = LONG && w.k > kLongK ? (w.k + kPartK - 1) / kPartK : 1;
+            const uint32_t before = it;
+            it += parts - 1;
             const uint32_t set = it & 1;
             const uint32_t bar = in_cluster(smem_addr(&drained[set]), 0);
             const int p_first = first_row(w);
@@ -1134,8 +1224,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPrPairThreads)
                 const int q = w.q0 + (warp >> 2) * 128, there = min(128, e.n - q), size = e.f32 ? 4 : 2;
                 if (there > 0) block_prefetch(static_cast<const uint8_t*>(e.residual) + ((d_first + lane) * e.n + q) * size, there * size);
             }
-            ok = ok && (mbar_wait_warp(&done[set], (it >> 1) & 1, 32) || mbar_wait_on(&done[set], (it >> 1) & 1, empty, kPrPairStages)) &&
-                 !pr_made_to_fail(a, kPrOutDone, it);
+            if (parts > 1)
+                ok = sum_parts<128, true>(from, 256, before, parts, done, drained, ok);
+            else
+                ok = ok && mbar_wait_warp(&done[set], (it >> 1) & 1, 32);
+            ok = ok && !pr_made_to_fail(a, kPrOutDone, it);
             if (!ok) gave_up = 1;
             tc_fence_after();
 #pragma unroll 1
@@ -1260,10 +1353,10 @@ bool operand_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t k, in
                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <int BN, bool GROUPED>
+template <int BN, bool GROUPED, bool LONG>
 fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, ProductArgs a, unsigned grid, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};
-    auto kern = fp8_matmul_kernel<BN, GROUPED>;
+    auto kern = fp8_matmul_kernel<BN, GROUPED, LONG>;
     const cudaError_t e = allow_smem(kern, PrGeom<BN>::kSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_kernel setup");
     // Stages of up to four steps, two stages or more: a stage's waits and its arrival take its issuers 150 cycles each, and
@@ -1278,10 +1371,15 @@ fp8q_status launch_product(const CUtensorMap& mp, const CUtensorMap& mq, Product
     return launch_behind(kern, dim3(grid), dim3(192), (need > BN * 512 ? need : BN * 512) + 1024, (unsigned)a.split, s, "fp8_matmul_kernel", mp, mq, a);
 }
 
-template <bool RAGGED_K, bool ANY>
+template <int BN>
+auto launch_product_of(bool grouped, bool parts) {
+    return parts ? launch_product<BN, true, true> : grouped ? launch_product<BN, true, false> : launch_product<BN, false, false>;
+}
+
+template <bool RAGGED_K, bool ANY, bool LONG>
 fp8q_status launch_product_pairs(const CUtensorMap& mp, const CUtensorMap& mq, const ProductArgs& a, int64_t tiles, cudaStream_t s) {
     static std::atomic<uint64_t> devices{0};
-    auto kern = fp8_matmul_pair_kernel<RAGGED_K, ANY>;
+    auto kern = fp8_matmul_pair_kernel<RAGGED_K, ANY, LONG>;
     const cudaError_t e = allow_smem(kern, kPrPairSmem, devices);
     if (e != cudaSuccess) return cuda_fail(e, "fp8_matmul_pair_kernel setup");
     const int64_t pairs = sm_count() / 2;
@@ -1380,8 +1478,11 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
         if (tiles > kManyTiles) return FP8Q_ERR_UNSUPPORTED;
         if (p->k > 0 && (!operand_map(&mp, p->a, p->m, p->k, p->lda, 1, ta, 128) || !operand_map(&mq, p->b, p->n, p->k, p->ldb, b_groups, tb, 128)))
             return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_pair_kernel tensor map");
-        if (how == kGroupedK) return e.vec ? launch_product_pairs<true, false>(mp, mq, a, tiles, s) : launch_product_pairs<true, true>(mp, mq, a, tiles, s);
-        return e.vec ? launch_product_pairs<false, false>(mp, mq, a, tiles, s) : launch_product_pairs<false, true>(mp, mq, a, tiles, s);
+        const auto launch = how == kGroupedK ? (a.k > kLongK ? (e.vec ? launch_product_pairs<true, false, true> : launch_product_pairs<true, true, true>)
+                                                            : (e.vec ? launch_product_pairs<true, false, false> : launch_product_pairs<true, true, false>))
+                                             : (a.k > kLongK ? (e.vec ? launch_product_pairs<false, false, true> : launch_product_pairs<false, true, true>)
+                                                            : (e.vec ? launch_product_pairs<false, false, false> : launch_product_pairs<false, true, false>));
+        return launch(mp, mq, a, tiles, s);
     }
     // P is B and Q is A.  Fewer rows of A a CTA while two thirds of the SMs have room for all CTAs: a tile goes out sooner
     // the smaller it is (300x1024x1024 5.3 us with 32 rows, 6.9 with 128; 278x208x64 5.5 and 14), but reads B once more, and
@@ -1411,12 +1512,12 @@ fp8q_status product(const fp8q_product* p, const int32_t* offsets, int32_t group
     if (p->k > 0 && (!operand_map(&mp, p->b, p->n, p->k, p->ldb, b_groups, tb, 128) || !operand_map(&mq, p->a, p->m, p->k, p->lda, 1, ta, bn)))
         return cuda_fail(cudaErrorInvalidValue, "fp8_matmul_kernel tensor map");
     const unsigned grid = (unsigned)(tiles * split);
-    const bool grouped = how == kGroupedRows;
+    const bool grouped = how == kGroupedRows, parts = steps > kLongSteps * split;
     switch (bn) {
-        case 16: return grouped ? launch_product<16, true>(mp, mq, a, grid, s) : launch_product<16, false>(mp, mq, a, grid, s);
-        case 32: return grouped ? launch_product<32, true>(mp, mq, a, grid, s) : launch_product<32, false>(mp, mq, a, grid, s);
-        case 64: return grouped ? launch_product<64, true>(mp, mq, a, grid, s) : launch_product<64, false>(mp, mq, a, grid, s);
-        default: return grouped ? launch_product<128, true>(mp, mq, a, grid, s) : launch_product<128, false>(mp, mq, a, grid, s);
+        case 16: return launch_product_of<16>(grouped, parts)(mp, mq, a, grid, s);
+        case 32: return launch_product_of<32>(grouped, parts)(mp, mq, a, grid, s);
+        case 64: return launch_product_of<64>(grouped, parts)(mp, mq, a, grid, s);
+        default: return launch_product_of<128>(grouped, parts)(mp, mq, a, grid, s);
     }
 }
 

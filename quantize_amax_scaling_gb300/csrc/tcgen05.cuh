@@ -29,8 +29,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
 }
 
 // For a wait that lasts as long as a loop over `stages` barriers does, once mbar_wait_warp() has given up: goes on while one of them
-// completes a phase within the limit.  Out of line, and with no count kept by the loop itself: a word in shared memory for each of
-// its steps took 1% of 8192x16384x4096.
+// completes a phase within the limit.  Out of line: no short loop comes here.
 __device__ __noinline__ bool mbar_wait_on(uint64_t* bar, uint32_t parity, uint64_t* loop, uint32_t stages) {
     uint32_t ok = 0;
     if ((threadIdx.x & 31) == 0) {
@@ -141,6 +140,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+
+// Sixteen columns back; they are there after tmem_stored().
+__device__ __forceinline__ void tmem_store16(uint32_t at, const float* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]),
+        "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------
 // Shared-memory descriptors
